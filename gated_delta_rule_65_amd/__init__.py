@@ -28,7 +28,10 @@ __all__ = ["chunk_fwd", "chunk_fwd_noalloc", "chunk_fwd_noalloc_raw", "varlen_fw
            "chunk_fwd_raw", "varlen_fwd_raw", "decode_step_raw", "chunk_workspace_bytes",
            "varlen_workspace_bytes", "DTYPE", "Prologue", "prologue", "chunk_bwd", "varlen_bwd", "chunk_bwd_raw",
            "varlen_bwd_raw", "chunk_bwd_workspace_bytes", "varlen_bwd_workspace_bytes", "ChunkKDA",
-           "calib_copy_raw", "calib_mfma_raw"]
+           "calib_copy_raw", "calib_mfma_raw", "layer", "Packed8", "ckpt8_pack", "ckpt8_unpack", "scan_fwd",
+           "scan_varlen_fwd", "scan_bwd", "scan_varlen_bwd", "scan_step", "scan_workspace_bytes", "scan_carry_bytes",
+           "GatedScan", "VarlenGatedScan", "qk_norm_rope_fwd", "qk_norm_rope_bwd", "qk_norm_rope_workspace_bytes",
+           "NormChunkKDA"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libkda.so")
@@ -101,6 +104,7 @@ def load_library():
     L.kda_calib_copy.restype = ci
     L.kda_calib_mfma.argtypes = [vp, ci, i64, ci, vp]
     L.kda_calib_mfma.restype = ci
+    layer.declare(L)
     L.kda_last_error.restype = ctypes.c_char_p
     L.kda_version.restype = ctypes.c_char_p
     _lib = L
@@ -454,3 +458,9 @@ class ChunkKDA(torch.autograd.Function):
         d_sf = None if d_sf is None else d_sf.float().contiguous()
         dq, dk, dv, dg, dbeta, ds0 = chunk_bwd(q, k, v, g, beta, d_o, s0, d_sf)
         return dq.to(q.dtype), dk.to(k.dtype), dv.to(v.dtype), dg, dbeta, (ds0 if s0 is not None else None)
+
+
+from . import layer  # noqa: E402
+from .layer import (GatedScan, NormChunkKDA, Packed8, VarlenGatedScan, ckpt8_pack, ckpt8_unpack,  # noqa: E402
+                    qk_norm_rope_bwd, qk_norm_rope_fwd, qk_norm_rope_workspace_bytes, scan_bwd, scan_carry_bytes,
+                    scan_fwd, scan_step, scan_varlen_bwd, scan_varlen_fwd, scan_workspace_bytes)
