@@ -187,6 +187,9 @@ kda_status scan_form(kda::ScanArgs& a, int64_t D, const kda_scan_form* f) {
 }
 
 kda_status scan_ws(kda::ScanArgs& a, void* ws, size_t bytes, const char* what) {
+    if (kda::scan_places(a) > 0x7fffffffLL)
+        return fail(KDA_ERR_BAD_SHAPE, "%s: %lld tokens of %lld channels exceed the grid limit", what,
+                    (long long)a.total, (long long)a.D);
     const int64_t need = a.total ? kda::scan_workspace_bytes(a.N, a.total, a.D) : 0;
     if (need > 0 && !ws)
         return fail(KDA_ERR_NULL_ARG, "%s: workspace is NULL (%lld bytes needed)", what, (long long)need);

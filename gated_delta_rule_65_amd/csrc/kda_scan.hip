@@ -1,5 +1,24 @@
 // Gated scan over channels: h_t = a_t h_{t-1} + w_t x_t, its gradients and its single-token step
 // (mathematics and layouts: include/kda_layer.h).
+//
+// A step of the scan is the map s -> A s + b of the state; steps compose to (A2 A1, A2 b1 + b2), so a run of tokens is
+// one such pair per channel.  Time is cut into segments of 64 tokens, a segment and 64 * CPL channels to a workgroup:
+//   1. each wave takes 8 of the tokens, reads its rows (all loads in flight at once), and folds them to its pair;
+//   2. the waves' pairs meet in LDS and give the segment's pair, which is published in the workspace;
+//   3. the state before the segment is folded from what the earlier segments of the sequence published: the pairs of
+//      the up to 7 segments of its own group of 8, of the up to 7 whole groups before in its own block of 64, and
+//      the state at the end of the block before.  The last segment of a group publishes the group's pair, the
+//      last of a block the state behind it;
+//   4. each wave runs its tokens again from its own state, with the gates and inputs still in registers.
+// Every input is read once and every output written once; the pairs add 8 bytes for 64 tokens of a channel, and
+// are read about 8 times, from the cache behind the L2s.  What waits is a chain of one hop for each 4096 tokens.
+// All sums are in a fixed order, so results do not depend on the timing.
+//
+// Why every wait ends: a workgroup takes its place in the order of work from a counter when it starts, and only waits for
+// segments whose places were taken earlier, by workgroups that are therefore running or done.  The one
+// with the lowest place among those not done waits for nobody.
+//
+// The backward pass is the same scan with time reversed, of e_t = a_t (dy_t + e_{t+1}).
 #include "kda_ckpt8.h"
 #include "kda_layer_launch.h"
 
@@ -7,19 +26,81 @@ namespace kda {
 
 namespace {
 
-template <bool F32>
-__device__ __forceinline__ float load1(const void* p, int64_t i) {
-    if constexpr (F32) return static_cast<const float*>(p)[i];
-    else return __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
-}
-template <bool F32>
-__device__ __forceinline__ void store1(void* p, int64_t i, float v) {
-    if constexpr (F32) static_cast<float*>(p)[i] = v;
-    else static_cast<__bf16*>(p)[i] = (__bf16)v;
-}
+typedef unsigned long long u64;
+
+constexpr int kWaves = 8, kRows = 8, kThreads = kWaves * 64;
+static_assert(kWaves * kRows == kScanSeg, "a wave's rows");
+constexpr int kGroup = 8, kBlock = 64;  // segments of a group and of a block
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// ---------------------------------------------------------------------------- rows in registers
+// CPL consecutive elements of a row as they come from memory.
+template <bool F32, int CPL>
+struct Raw {
+    static constexpr int WORDS = F32 ? CPL : (CPL + 1) / 2;
+    uint32_t w[WORDS];
+};
+template <int WORDS>
+__device__ __forceinline__ void load_words(const void* p, uint32_t* w) {
+    if constexpr (WORDS % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < WORDS; i += 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint32_t*>(p) + i);
+            w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
+        }
+    } else if constexpr (WORDS == 2) {
+        const uint2 v = *static_cast<const uint2*>(p);
+        w[0] = v.x; w[1] = v.y;
+    } else {
+        w[0] = *static_cast<const uint32_t*>(p);
+    }
+}
+template <bool F32, int CPL>
+__device__ __forceinline__ Raw<F32, CPL> load_raw(const void* base, int64_t i) {
+    Raw<F32, CPL> r;
+    if constexpr (F32) load_words<CPL>(static_cast<const float*>(base) + i, r.w);
+    else if constexpr (CPL == 1) r.w[0] = static_cast<const uint16_t*>(base)[i];
+    else load_words<CPL / 2>(static_cast<const uint16_t*>(base) + i, r.w);
+    return r;
+}
+template <bool F32, int CPL>
+__device__ __forceinline__ float raw_get(const Raw<F32, CPL>& r, int k) {
+    if constexpr (F32) return __uint_as_float(r.w[k]);
+    else return __uint_as_float(k % 2 ? r.w[k / 2] & 0xffff0000u : r.w[k / 2] << 16);
+}
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+    typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+    const bf2 v = {(__bf16)a, (__bf16)b};
+    return __builtin_bit_cast(uint32_t, v);
+}
+template <bool F32, int CPL>
+__device__ __forceinline__ void store_row(void* base, int64_t i, const float v[CPL]) {
+    if constexpr (F32) {
+        float* p = static_cast<float*>(base) + i;
+        if constexpr (CPL % 4 == 0) {
+#pragma unroll
+            for (int k = 0; k < CPL; k += 4) *reinterpret_cast<float4*>(p + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+        } else if constexpr (CPL == 2) {
+            *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+        } else {
+            *p = v[0];
+        }
+    } else {
+        uint16_t* p = static_cast<uint16_t*>(base) + i;
+        if constexpr (CPL == 8)
+            *reinterpret_cast<uint4*>(p) = make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]),
+                                                      bf16_pair(v[6], v[7]));
+        else if constexpr (CPL == 4)
+            *reinterpret_cast<uint2*>(p) = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
+        else if constexpr (CPL == 2)
+            *reinterpret_cast<uint32_t*>(p) = bf16_pair(v[0], v[1]);
+        else
+            *reinterpret_cast<__bf16*>(p) = (__bf16)v[0];
+    }
+}
+
+// ---------------------------------------------------------------------------- gates
 // 1 - e^l for l in [-5, 0]: by its series where the difference would cancel.
 __device__ __forceinline__ float one_minus_exp(float l, float a) {
     // l (1 + l/2 (1 + l/3 (1 + ...))) to l^8 / 8!: below 2^-24 of the result for |l| <= 0.4
@@ -58,141 +139,697 @@ __device__ __forceinline__ float gate_slope(float g, float rest, bool logit) {
     return (g < -5.f || g > 0.f) ? 0.f : 1.f;
 }
 
-struct Span {
-    int64_t first, end, slot;  // rows of sequence n, and the segment index of its first row (equal lengths)
+// ---------------------------------------------------------------------------- places in the order of work
+struct ScanPlan {
+    uint32_t cols;      // groups of 64 * CPL channels
+    uint32_t chains;    // sequences with segments of their own; 1 for packed rows
+    uint32_t per_chain; // segments of a chain
+    uint32_t* counter;  // nullptr: no chain is longer than a segment
+    u64 *pairs, *groups, *states;
 };
-__device__ __forceinline__ Span span_of(const ScanArgs& a, int64_t n) {
-    if (!a.cu) return {n * a.T_fixed, (n + 1) * a.T_fixed, n * ((a.T_fixed + kScanSeg - 1) / kScanSeg)};
-    // offsets outside [0, total] are cut there: no access leaves the buffers whatever they hold
-    const int64_t lo = a.cu[n], hi = a.cu[n + 1];
-    const int64_t f = lo < 0 ? 0 : lo > a.total ? a.total : lo, e = hi < f ? f : hi > a.total ? a.total : hi;
-    return {f, e, 0};
-}
-// Index of the segment that begins at row r of a sequence, or -1 where none does.
-__device__ __forceinline__ int64_t segment_at(const ScanArgs& a, const Span& s, int64_t r) {
-    if (a.cu) return r % kScanSeg ? -1 : r / kScanSeg;
-    return (r - s.first) % kScanSeg ? -1 : s.slot + (r - s.first) / kScanSeg;
+
+struct Tile {
+    int64_t chain, at;   // segment `at` of its chain, in the direction of the scan
+    int64_t id;          // index of the segment
+    int64_t row0;        // its first row, and how many rows it has
+    int rows;
+    int64_t col;
+};
+
+template <bool FLAT, bool BACK>
+__device__ __forceinline__ Tile tile_of(const ScanArgs& a, const ScanPlan& p, uint32_t place, int64_t total) {
+    Tile t;
+    t.col = place % p.cols;
+    const uint32_t s = place / p.cols;
+    t.chain = FLAT ? 0 : s % p.chains;
+    t.at = FLAT ? s : s / p.chains;
+    const int64_t q = BACK ? (int64_t)p.per_chain - 1 - t.at : t.at;
+    t.id = t.chain * p.per_chain + q;
+    t.row0 = t.chain * a.T_fixed + q * kScanSeg;
+    const int64_t end = FLAT ? total : (t.chain + 1) * a.T_fixed;
+    const int64_t left = end - t.row0;
+    t.rows = left < 0 ? 0 : left < kScanSeg ? (int)left : kScanSeg;
+    return t;
 }
 
-// A channel of a sequence to a lane, one token after the other.
-template <bool XF, bool GF>
-__global__ __launch_bounds__(64) void scan_fwd_kernel(ScanArgs a) {
-    const int64_t cols = (a.D + 63) / 64, n = blockIdx.x / cols;
-    const int64_t c = (blockIdx.x - n * cols) * 64 + threadIdx.x;
-    const bool in = c < a.D;
-    const int64_t cc = in ? c : a.D - 1;
-    const Span s = span_of(a, n);
-    float h = a.h0 ? a.h0[n * a.D + cc] : 0.f;
-    const int64_t blocks = (a.D + kCkptBlock - 1) / kCkptBlock;
-    for (int64_t r = s.first; r < s.end; ++r) {
-        const int64_t i = r * a.D + cc;
-        if (a.carry_out) {
-            const int64_t seg = segment_at(a, s, r);
-            if (seg >= 0 && in) a.carry_out[seg * a.D + c] = h;
-        }
-        const Gate q = gate_of(load1<GF>(a.g, i), a.logit, a.complement);
-        const float x = load1<XF>(a.x, i);
-        if (a.u_out) {
-            const float u = a.complement ? h - x : h;
-            uint32_t top = in ? finite_abs_bits(u) : 0u;
+// The place of this workgroup, the same in all its threads.
+__device__ __forceinline__ uint32_t take_place(uint32_t* counter, uint32_t* shared) {
+    if (!counter) return blockIdx.x;
+    if (threadIdx.x == 0)
+        *shared = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    return (uint32_t)__builtin_amdgcn_readfirstlane((int)*shared);
+}
+
+// The sequence that holds row r of packed rows: the last n with cu[n] <= r, by 64 candidates at a time.
+__device__ __forceinline__ int64_t seq_of(const int32_t* cu, int64_t N, int64_t r) {
+    int64_t lo = 0, len = N;
+    while (len > 1) {
+        const int64_t step = (len + 63) / 64;
+        const int64_t i = lo + (int64_t)(threadIdx.x & 63) * step;
+        const bool le = i < lo + len && cu[i] <= r;
+        const int c = __popcll(__ballot(le));
+        const int64_t at = lo + (c > 0 ? c - 1 : 0) * step;
+        len = lo + len - at < step ? lo + len - at : step;
+        lo = at;
+    }
+    return lo;
+}
+
+// ---------------------------------------------------------------------------- published words
+// A pair (A, b) in one 64-bit word that is valid as a whole: kEmpty until it is written, so that neither a flag nor
+// a fence is needed.  A word that happens to look empty is written with another NaN.  A = -0 says that a sequence
+// begins inside: whatever the state before is, even infinite, it has no part in what follows.
+constexpr u64 kEmpty = ~0ull;
+constexpr uint32_t kBegins = 0x80000000u;
+
+struct Pair {
+    float A, b;
+};
+__device__ __forceinline__ Pair then(Pair first, Pair second) {
+    if (__float_as_uint(second.A) == kBegins) return second;
+    const bool begun = __float_as_uint(first.A) == kBegins;
+    return {begun ? first.A : first.A * second.A, fmaf(second.A, first.b, second.b)};
+}
+__device__ __forceinline__ float apply(Pair p, float s) {
+    return __float_as_uint(p.A) == kBegins ? p.b : fmaf(p.A, s, p.b);
+}
+__device__ __forceinline__ void publish(u64* at, Pair p) {
+    u64 w = (u64)__float_as_uint(p.A) << 32 | __float_as_uint(p.b);
+    if (w == kEmpty) w ^= 1;
+    __hip_atomic_store(at, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ u64 peek(const u64* at) {
+    return __hip_atomic_load(const_cast<u64*>(at), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// Waits for a word that an earlier place publishes.  The bound (some seconds) is never reached by the argument above; behind
+// it the word reads as NaN, so that a broken promise shows and does not hang.
+__device__ __forceinline__ Pair await(const u64* at, u64 w) {
+    for (int i = 0; w == kEmpty && i < (1 << 22); ++i) {
+        __builtin_amdgcn_s_sleep(1);
+        w = peek(at);
+    }
+    return {__uint_as_float((uint32_t)(w >> 32)), __uint_as_float((uint32_t)w)};
+}
+
+// The state of channel c before segment t.at of its chain, from what its predecessors published; `reach` of them back at
+// most have a part in it (packed rows: those from the sequence's first on).
+__device__ __forceinline__ float state_before(const ScanArgs& a, const ScanPlan& p, const Tile& t, int64_t c, int64_t reach,
+                                              Pair own) {
+    const int64_t first = t.at - reach;
+    const int n1 = (int)(t.at % kGroup), n2 = (int)(t.at / kGroup % (kBlock / kGroup));
+    const int64_t base1 = t.chain * p.per_chain + t.at - n1;                                 // of this group
+    const int64_t groups = (p.per_chain + kGroup - 1) / kGroup, blocks = (p.per_chain + kBlock - 1) / kBlock;
+    const int64_t base2 = t.chain * groups + t.at / kGroup - n2;                             // of this block
+    const bool wait3 = t.at >= kBlock && first < t.at / kBlock * kBlock;
+    u64 w1[kGroup - 1], w2[kBlock / kGroup - 1], w3 = 0;
+    if (wait3) w3 = peek(p.states + (t.chain * blocks + t.at / kBlock - 1) * a.D + c);
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) {
-                const uint32_t o = (uint32_t)__shfl_xor((int)top, off);
-                top = top > o ? top : o;
-            }
-            const int sc = ckpt_scale(top);
-            if (in) {
-                a.u_out[i] = (uint8_t)ckpt_code2(u, 0.f, ckpt_inverse(sc));
-                if ((c & 31) == 0) a.us_out[r * blocks + c / kCkptBlock] = (uint8_t)sc;
-            }
-        }
-        h = fmaf(q.a, h, a.complement ? q.rest * x : x);
-        if (in) store1<XF>(a.y, i, h);
-    }
-    if (in && a.h_final) a.h_final[n * a.D + c] = h;
+    for (int i = 0; i < kBlock / kGroup - 1; ++i) w2[i] = i < n2 ? peek(p.groups + (base2 + i) * a.D + c) : 0;
+#pragma unroll
+    for (int i = 0; i < kGroup - 1; ++i) w1[i] = i < n1 ? peek(p.pairs + (base1 + i) * a.D + c) : 0;
+    Pair group = {1.f, 0.f};
+    // the segments of the group first: the group's own pair waits for nothing further back
+#pragma unroll
+    for (int i = 0; i < kGroup - 1; ++i)
+        if (i < n1) group = then(group, await(p.pairs + (base1 + i) * a.D + c, w1[i]));
+    if (n1 == kGroup - 1) publish(p.groups + (t.chain * groups + t.at / kGroup) * a.D + c, then(group, own));
+    Pair before = {1.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < kBlock / kGroup - 1; ++i)
+        if (i < n2) before = then(before, await(p.groups + (base2 + i) * a.D + c, w2[i]));
+    before = then(before, group);
+    float s = 0.f;
+    if (wait3) s = await(p.states + (t.chain * blocks + t.at / kBlock - 1) * a.D + c, w3).b;
+    s = apply(before, s);
+    if (t.at % kBlock == kBlock - 1)
+        publish(p.states + (t.chain * blocks + t.at / kBlock) * a.D + c, Pair{0.f, apply(own, s)});
+    return s;
 }
 
-template <bool XF, bool GF>
-__global__ __launch_bounds__(64) void scan_bwd_kernel(ScanArgs a) {
-    const int64_t cols = (a.D + 63) / 64, n = blockIdx.x / cols;
-    const int64_t c = (blockIdx.x - n * cols) * 64 + threadIdx.x;
-    if (c >= a.D) return;
-    const Span s = span_of(a, n);
-    float e = a.dh_final ? a.dh_final[n * a.D + c] : 0.f;
+// The waves' pairs, then the states before the waves, of the workgroup's channels.
+template <int CPL>
+struct Exchange {
+    float A[kWaves][64 * CPL], b[kWaves][64 * CPL];
+};
+template <int CPL>
+__device__ __forceinline__ void put(float* row, const float v[CPL]) {
+    if constexpr (CPL % 4 == 0) {
+#pragma unroll
+        for (int k = 0; k < CPL; k += 4)
+            *reinterpret_cast<float4*>(row + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < CPL; ++k) row[k] = v[k];
+    }
+}
+template <int CPL>
+__device__ __forceinline__ void take(const float* row, float v[CPL]) {
+    if constexpr (CPL % 4 == 0) {
+#pragma unroll
+        for (int k = 0; k < CPL; k += 4) {
+            const float4 u = *reinterpret_cast<const float4*>(row + k);
+            v[k] = u.x; v[k + 1] = u.y; v[k + 2] = u.z; v[k + 3] = u.w;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < CPL; ++k) v[k] = row[k];
+    }
+}
+
+// From the waves' pairs (in the scan's direction: wave `order(i)` is the i-th) to the state before each wave, in x.b;
+// `start`: the state before the chain's first segment.  Each thread has channels of its own throughout.
+template <bool BACK, int CPL>
+__device__ __forceinline__ void join_waves(const ScanArgs& a, const ScanPlan& p, const Tile& t, Exchange<CPL>& x,
+                                           const float* start, int64_t reach, float* carry) {
+    for (int ch = threadIdx.x; ch < 64 * CPL; ch += kThreads) {
+        const int64_t c = t.col * 64 * CPL + ch;
+        if (c >= a.D) continue;
+        Pair own = {1.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) {
+            const int w = BACK ? kWaves - 1 - i : i;
+            own = then(own, Pair{x.A[w][ch], x.b[w][ch]});
+        }
+        float s;
+        if (reach < 0) {  // the chain's first segment: what lies before it is known, so its pair holds for any state
+            s = start ? start[c] : 0.f;
+            own = {__uint_as_float(kBegins), apply(own, s)};
+        }
+        if (p.counter) publish(p.pairs + (t.chain * p.per_chain + t.at) * a.D + c, own);
+        if (p.counter) {
+            const float before = state_before(a, p, t, c, reach < 0 ? 0 : reach, own);
+            if (reach >= 0) s = before;
+        } else if (reach >= 0) {
+            s = 0.f;
+        }
+        if (carry) carry[t.id * a.D + c] = s;
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) {
+            const int w = BACK ? kWaves - 1 - i : i;
+            const Pair q = {x.A[w][ch], x.b[w][ch]};
+            x.b[w][ch] = s;
+            s = apply(q, s);
+        }
+    }
+}
+
+// Where sequences begin or end among a wave's rows of packed rows (bit i: row i), and their numbers.
+struct Marks {
+    uint32_t begins, ends;
+    int n[kRows];
+};
+__device__ __forceinline__ Marks marks_of(const ScanArgs& a, int64_t r0, int rows) {
+    Marks m{0, 0, {}};
+    if (rows <= 0) return m;
+    int64_t n = seq_of(a.cu, a.N, r0);
+    int64_t next = a.cu[n + 1];
+    bool begins = a.cu[n] == r0;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        if (i < rows) {
+            while (r0 + i >= next && n + 1 < a.N) {
+                ++n;
+                next = a.cu[n + 1];
+                begins = true;
+            }
+            m.n[i] = __builtin_amdgcn_readfirstlane((int)n);
+            if (begins) m.begins |= 1u << i;
+            if (r0 + i + 1 == next) m.ends |= 1u << i;
+            begins = false;
+        }
+    }
+    m.begins = __builtin_amdgcn_readfirstlane(m.begins);
+    m.ends = __builtin_amdgcn_readfirstlane(m.ends);
+    return m;
+}
+
+// Largest of the lanes that share a block of 32 channels.
+template <int CPL>
+__device__ __forceinline__ uint32_t block_max(uint32_t v) {
+    auto dpp = [](uint32_t x, auto ctrl) {
+        return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, decltype(ctrl)::value, 0xf, 0xf, true);
+    };
+    v = max(v, dpp(v, std::integral_constant<int, 0xB1>()));            // lane ^ 1
+    v = max(v, dpp(v, std::integral_constant<int, 0x4E>()));            // lane ^ 2: quads agree
+    if constexpr (CPL <= 4) v = max(v, dpp(v, std::integral_constant<int, 0x141>()));  // the other quad of eight
+    if constexpr (CPL <= 2) v = max(v, dpp(v, std::integral_constant<int, 0x140>()));  // the other eight of sixteen
+    if constexpr (CPL == 1) v = max(v, (uint32_t)__shfl_xor((int)v, 16));
+    return v;
+}
+
+// ---------------------------------------------------------------------------- forward
+template <bool XF, bool GF, int CPL, bool FLAT>
+__global__ __launch_bounds__(kThreads) void scan_fwd_kernel(ScanArgs a, ScanPlan p) {
+    __shared__ Exchange<CPL> x;
+    __shared__ uint32_t place;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t pl = take_place(p.counter, &place);
+    int64_t total = a.total;
+    if constexpr (FLAT) {
+        const int64_t used = a.cu[a.N];
+        total = used < 0 ? 0 : used < total ? used : total;
+    }
+    const Tile t = tile_of<FLAT, false>(a, p, pl, total);
+    const int64_t c = t.col * 64 * CPL + lane * CPL;
+    const bool in = c < a.D;
+    const int64_t cc = in ? c : 0;
+    const int64_t r0 = t.row0 + wave * kRows;
+    const int rows = t.rows - wave * kRows < 0 ? 0 : t.rows - wave * kRows < kRows ? t.rows - wave * kRows : kRows;
+
+    Raw<XF, CPL> xr[kRows];
+    Raw<GF, CPL> gr[kRows];
+    const int64_t last = total > 0 ? (t.row0 + t.rows > 0 ? t.row0 + t.rows - 1 : 0) : 0;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int64_t r = r0 + i < last ? r0 + i : last;
+        const int64_t at = (t.rows > 0 ? r : 0) * a.D + cc;
+        gr[i] = load_raw<GF, CPL>(a.g, at);
+        xr[i] = load_raw<XF, CPL>(a.x, at);
+    }
+    Marks m{0, 0, {}};
+    if constexpr (FLAT) m = marks_of(a, r0, rows);
+
+    float al[kRows][CPL], b[kRows][CPL];
+    float A[CPL], h[CPL];
+#pragma unroll
+    for (int k = 0; k < CPL; ++k) A[k] = 1.f, h[k] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+#pragma unroll
+        for (int k = 0; k < CPL; ++k) {
+            const Gate q = gate_of(raw_get(gr[i], k), a.logit, a.complement);
+            const float v = raw_get(xr[i], k);
+            al[i][k] = q.a;
+            b[i][k] = a.complement ? q.rest * v : v;
+        }
+        if (i >= rows) {
+#pragma unroll
+            for (int k = 0; k < CPL; ++k) al[i][k] = 1.f, b[i][k] = 0.f;
+        }
+        bool begins = false;
+        if constexpr (FLAT) begins = m.begins >> i & 1;
+        if (begins) {
+#pragma unroll
+            for (int k = 0; k < CPL; ++k) {
+                A[k] = __uint_as_float(kBegins);
+                const float s = a.h0 && in ? a.h0[m.n[i] * a.D + c + k] : 0.f;
+                h[k] = fmaf(al[i][k], s, b[i][k]);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < CPL; ++k) {
+                A[k] *= al[i][k];
+                h[k] = fmaf(al[i][k], h[k], b[i][k]);
+            }
+        }
+    }
+    put<CPL>(&x.A[wave][lane * CPL], A);
+    put<CPL>(&x.b[wave][lane * CPL], h);
+    __syncthreads();
+    int64_t reach = t.at > 0 ? t.at : -1;
+    if constexpr (FLAT) {
+        // segments back to the one where the sequence of the first row begins
+        if (t.rows > 0) {
+            const int64_t n = seq_of(a.cu, a.N, t.row0);
+            const int64_t begin = a.cu[n] < 0 ? 0 : a.cu[n];
+            reach = t.at - begin / kScanSeg;
+            if (reach < 0) reach = 0;
+        } else {
+            reach = 0;
+        }
+    }
+    join_waves<false, CPL>(a, p, t, x, a.h0 && !FLAT ? a.h0 + t.chain * a.D : nullptr, reach, a.carry_out);
+    __syncthreads();
+    take<CPL>(&x.b[wave][lane * CPL], h);
+
     const int64_t blocks = (a.D + kCkptBlock - 1) / kCkptBlock;
-    int64_t end = s.end;
-    while (end > s.first) {
-        // the segment's rows, and the states before them from the carry
-        int64_t from = a.cu ? (end - 1) / kScanSeg * kScanSeg
-                            : s.first + (end - 1 - s.first) / kScanSeg * kScanSeg;
-        const bool head = from <= s.first;
-        if (head) from = s.first;
-        float before[kScanSeg];
-        if (!a.u) {
-            float h = head ? (a.h0 ? a.h0[n * a.D + c] : 0.f) : a.carry[segment_at(a, s, from) * a.D + c];
-            for (int64_t r = from; r < end; ++r) {
-                before[r - from] = h;
-                const Gate q = gate_of(load1<GF>(a.g, r * a.D + c), a.logit, a.complement);
-                const float x = load1<XF>(a.x, r * a.D + c);
-                h = fmaf(q.a, h, a.complement ? q.rest * x : x);
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        if (i >= rows) break;
+        const int64_t r = r0 + i;
+        if constexpr (FLAT) {
+            if (m.begins >> i & 1) {
+#pragma unroll
+                for (int k = 0; k < CPL; ++k) h[k] = a.h0 && in ? a.h0[m.n[i] * a.D + c + k] : 0.f;
             }
         }
-        for (int64_t r = end - 1; r >= from; --r) {
-            const int64_t i = r * a.D + c;
-            const float g = load1<GF>(a.g, i);
-            const Gate q = gate_of(g, a.logit, true);
-            float u;
-            if (a.u) u = ckpt_value<0>(a.u[i], a.us[r * blocks + c / kCkptBlock]);
-            else u = before[r - from] - (a.complement ? load1<XF>(a.x, i) : 0.f);
-            const float dh = load1<XF>(a.dy, i) + e;
-            e = q.a * dh;
-            store1<XF>(a.dx, i, a.complement ? q.rest * dh : dh);
-            store1<GF>(a.dg, i, u * e * gate_slope(g, q.rest, a.logit));
+        if (a.u_out) {
+            float u[CPL];
+            uint32_t top = 0;
+#pragma unroll
+            for (int k = 0; k < CPL; ++k) {
+                u[k] = a.complement ? h[k] - raw_get(xr[i], k) : h[k];
+                top = max(top, finite_abs_bits(u[k]));
+            }
+            const int s = ckpt_scale(block_max<CPL>(in ? top : 0));
+            const float inv = ckpt_inverse(s);
+            if (in) {
+                uint8_t* codes = a.u_out + r * a.D + c;
+                if constexpr (CPL == 1) {
+                    *codes = (uint8_t)ckpt_code2(u[0], 0.f, inv);
+                } else if constexpr (CPL == 2) {
+                    *reinterpret_cast<uint16_t*>(codes) = (uint16_t)ckpt_code2(u[0], u[1], inv);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < CPL; k += 4)
+                        *reinterpret_cast<uint32_t*>(codes + k) =
+                            ckpt_code2(u[k], u[k + 1], inv) | ckpt_code2(u[k + 2], u[k + 3], inv) << 16;
+                }
+                if (c % kCkptBlock == 0) a.us_out[r * blocks + c / kCkptBlock] = (uint8_t)s;
+            }
         }
-        end = from;
+#pragma unroll
+        for (int k = 0; k < CPL; ++k) h[k] = fmaf(al[i][k], h[k], b[i][k]);
+        if (in) store_row<XF, CPL>(a.y, r * a.D + c, h);
+        if (a.h_final && in) {
+            bool ends;
+            int64_t n;
+            if constexpr (FLAT) ends = m.ends >> i & 1, n = m.n[i];
+            else ends = r + 1 == (t.chain + 1) * a.T_fixed, n = t.chain;
+            if (ends) store_row<true, CPL>(a.h_final, n * a.D + c, h);
+        }
     }
-    if (a.dh0) a.dh0[n * a.D + c] = e;
 }
 
-template <bool XF, bool GF>
+// ---------------------------------------------------------------------------- backward
+// PACKED: the factor u of the gate's gradient comes from its 8-bit codes; else the states of the segment are made again
+// from the carry and x.
+template <bool XF, bool GF, int CPL, bool FLAT, bool PACKED>
+__global__ __launch_bounds__(kThreads) void scan_bwd_kernel(ScanArgs a, ScanPlan p) {
+    __shared__ Exchange<CPL> x;
+    __shared__ uint32_t place;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t pl = take_place(p.counter, &place);
+    int64_t total = a.total;
+    if constexpr (FLAT) {
+        const int64_t used = a.cu[a.N];
+        total = used < 0 ? 0 : used < total ? used : total;
+    }
+    const Tile t = tile_of<FLAT, true>(a, p, pl, total);
+    const int64_t c = t.col * 64 * CPL + lane * CPL;
+    const bool in = c < a.D;
+    const int64_t cc = in ? c : 0;
+    const int64_t r0 = t.row0 + wave * kRows;
+    const int rows = t.rows - wave * kRows < 0 ? 0 : t.rows - wave * kRows < kRows ? t.rows - wave * kRows : kRows;
+    const int64_t blocks = (a.D + kCkptBlock - 1) / kCkptBlock;
+
+    Raw<GF, CPL> gr[kRows];
+    Raw<XF, CPL> dr[kRows], xr[PACKED ? 1 : kRows];
+    uint32_t code[PACKED ? kRows : 1][(CPL + 3) / 4];
+    int scale[PACKED ? kRows : 1];
+    const int64_t last = t.rows > 0 ? t.row0 + t.rows - 1 : 0;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int64_t r = r0 + i < last ? r0 + i : last;
+        const int64_t at = r * a.D + cc;
+        gr[i] = load_raw<GF, CPL>(a.g, at);
+        dr[i] = load_raw<XF, CPL>(a.dy, at);
+        if constexpr (PACKED) {
+            if constexpr (CPL == 1) code[i][0] = a.u[at];
+            else if constexpr (CPL == 2) code[i][0] = *reinterpret_cast<const uint16_t*>(a.u + at);
+            else load_words<CPL / 4>(a.u + at, code[i]);
+            scale[i] = a.us[r * blocks + cc / kCkptBlock];
+        } else {
+            xr[i] = load_raw<XF, CPL>(a.x, at);
+        }
+    }
+    Marks m{0, 0, {}};
+    if constexpr (FLAT) m = marks_of(a, r0, rows);
+
+    float al[kRows][CPL], rest[kRows][CPL];
+    float A[CPL], s[CPL];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+#pragma unroll
+        for (int k = 0; k < CPL; ++k) {
+            const Gate q = gate_of(raw_get(gr[i], k), a.logit, a.complement);
+            al[i][k] = i < rows ? q.a : 1.f;
+            rest[i][k] = q.rest;
+        }
+    }
+    float u[PACKED ? 1 : kRows][CPL];
+    if constexpr (!PACKED) {
+        // the states again: the waves' pairs from x, joined from the carry
+#pragma unroll
+        for (int k = 0; k < CPL; ++k) A[k] = 1.f, s[k] = 0.f;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            if (i >= rows) break;
+            const bool begins = FLAT && (m.begins >> i & 1);
+#pragma unroll
+            for (int k = 0; k < CPL; ++k) {
+                const float v = raw_get(xr[i], k), b = a.complement ? rest[i][k] * v : v;
+                if (begins) {
+                    A[k] = __uint_as_float(kBegins);
+                    s[k] = fmaf(al[i][k], a.h0 && in ? a.h0[m.n[i] * a.D + c + k] : 0.f, b);
+                } else {
+                    A[k] *= al[i][k];
+                    s[k] = fmaf(al[i][k], s[k], b);
+                }
+            }
+        }
+        put<CPL>(&x.A[wave][lane * CPL], A);
+        put<CPL>(&x.b[wave][lane * CPL], s);
+        __syncthreads();
+        for (int ch = threadIdx.x; ch < 64 * CPL; ch += kThreads) {
+            const int64_t cf = t.col * 64 * CPL + ch;
+            if (cf >= a.D) continue;
+            float h;
+            if (!FLAT && t.id == t.chain * p.per_chain) h = a.h0 ? a.h0[t.chain * a.D + cf] : 0.f;
+            else h = a.carry[t.id * a.D + cf];  // not used where the segment's first row begins a sequence
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                const Pair q = {x.A[w][ch], x.b[w][ch]};
+                x.b[w][ch] = h;
+                h = apply(q, h);
+            }
+        }
+        __syncthreads();
+        take<CPL>(&x.b[wave][lane * CPL], s);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const bool begins = FLAT && (m.begins >> i & 1);
+#pragma unroll
+            for (int k = 0; k < CPL; ++k) {
+                if (begins) s[k] = a.h0 && in ? a.h0[m.n[i] * a.D + c + k] : 0.f;
+                const float v = raw_get(xr[i], k);
+                u[i][k] = a.complement ? s[k] - v : s[k];
+                s[k] = fmaf(al[i][k], s[k], a.complement ? rest[i][k] * v : v);
+            }
+        }
+    }
+    // the reversed scan
+#pragma unroll
+    for (int k = 0; k < CPL; ++k) A[k] = 1.f, s[k] = 0.f;
+#pragma unroll
+    for (int i = kRows - 1; i >= 0; --i) {
+        if (i >= rows) continue;
+        const bool ends = FLAT && (m.ends >> i & 1);
+#pragma unroll
+        for (int k = 0; k < CPL; ++k) {
+            if (ends) {
+                A[k] = __uint_as_float(kBegins);
+                s[k] = al[i][k] * (raw_get(dr[i], k) + (a.dh_final && in ? a.dh_final[m.n[i] * a.D + c + k] : 0.f));
+            } else {
+                A[k] *= al[i][k];
+                s[k] = al[i][k] * (raw_get(dr[i], k) + s[k]);
+            }
+        }
+    }
+    put<CPL>(&x.A[wave][lane * CPL], A);
+    put<CPL>(&x.b[wave][lane * CPL], s);
+    __syncthreads();
+    int64_t reach = t.at > 0 ? t.at : -1;
+    if constexpr (FLAT) {
+        reach = 0;
+        if (t.rows == kScanSeg) {  // segments on to the one where the sequence of the last row ends
+            const int64_t n = seq_of(a.cu, a.N, last);
+            const int64_t end = a.cu[n + 1] < total ? a.cu[n + 1] : total;
+            reach = end > last ? (end - 1) / kScanSeg - t.id : 0;
+        }
+    }
+    join_waves<true, CPL>(a, p, t, x, a.dh_final && !FLAT ? a.dh_final + t.chain * a.D : nullptr, reach, nullptr);
+    __syncthreads();
+    take<CPL>(&x.b[wave][lane * CPL], s);
+#pragma unroll
+    for (int i = kRows - 1; i >= 0; --i) {
+        if (i >= rows) continue;
+        const int64_t r = r0 + i;
+        if constexpr (FLAT) {
+            if (m.ends >> i & 1) {
+#pragma unroll
+                for (int k = 0; k < CPL; ++k) s[k] = a.dh_final && in ? a.dh_final[m.n[i] * a.D + c + k] : 0.f;
+            }
+        }
+        float dx[CPL], dg[CPL];
+#pragma unroll
+        for (int k = 0; k < CPL; ++k) {
+            const float dh = raw_get(dr[i], k) + s[k];
+            s[k] = al[i][k] * dh;
+            dx[k] = a.complement ? rest[i][k] * dh : dh;
+            float f;
+            if constexpr (PACKED) {
+                const uint32_t w = code[i][k / 4];
+                f = k % 4 == 0 ? ckpt_value<0>(w, scale[i]) : k % 4 == 1 ? ckpt_value<1>(w, scale[i])
+                    : k % 4 == 2 ? ckpt_value<2>(w, scale[i]) : ckpt_value<3>(w, scale[i]);
+            } else {
+                f = u[i][k];
+            }
+            dg[k] = f * s[k] * gate_slope(raw_get(gr[i], k), rest[i][k], a.logit);
+        }
+        if (in) {
+            store_row<XF, CPL>(a.dx, r * a.D + c, dx);
+            store_row<GF, CPL>(a.dg, r * a.D + c, dg);
+            if (a.dh0) {
+                bool begins;
+                int64_t n;
+                if constexpr (FLAT) begins = m.begins >> i & 1, n = m.n[i];
+                else begins = r == t.chain * a.T_fixed, n = t.chain;
+                if (begins) store_row<true, CPL>(a.dh0, n * a.D + c, s);
+            }
+        }
+    }
+}
+
+// Empties the published words and the counter; sequences without tokens pass their state through.
+__global__ __launch_bounds__(256) void scan_begin_kernel(u64* words, int64_t count, uint32_t* counter, const int32_t* cu,
+                                                         int64_t N, int64_t T_fixed, int64_t total, int64_t D,
+                                                         const float* from, float* to) {
+    const int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
+    for (int64_t i = i0; i < count; i += step) words[i] = kEmpty;
+    if (counter && i0 == 0) *counter = 0;
+    if (!to) return;
+    for (int64_t n = blockIdx.x; n < N; n += gridDim.x) {
+        int64_t rows = T_fixed;
+        if (cu) rows = cu[n] < total ? (int64_t)cu[n + 1] - cu[n] : 0;
+        if (rows > 0) continue;
+        for (int64_t c = threadIdx.x; c < D; c += 256) to[n * D + c] = from ? from[n * D + c] : 0.f;
+    }
+}
+
+template <bool XF, bool GF, int CPL>
 __global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs a, const float* h_in, float* h_out, int64_t count) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * CPL;
     if (i >= count) return;
-    const Gate q = gate_of(load1<GF>(a.g, i), a.logit, a.complement);
-    const float x = load1<XF>(a.x, i);
-    const float h = fmaf(q.a, h_in[i], a.complement ? q.rest * x : x);
-    store1<XF>(a.y, i, h);
-    h_out[i] = h;
+    const Raw<GF, CPL> g = load_raw<GF, CPL>(a.g, i);
+    const Raw<XF, CPL> x = load_raw<XF, CPL>(a.x, i);
+    const Raw<true, CPL> h = load_raw<true, CPL>(h_in, i);
+    float v[CPL];
+#pragma unroll
+    for (int k = 0; k < CPL; ++k) {
+        const Gate q = gate_of(raw_get(g, k), a.logit, a.complement);
+        const float u = raw_get(x, k);
+        v[k] = fmaf(q.a, raw_get(h, k), a.complement ? q.rest * u : u);
+    }
+    store_row<XF, CPL>(a.y, i, v);
+    store_row<true, CPL>(h_out, i, v);
+}
+
+// ---------------------------------------------------------------------------- launches
+int64_t words_of(int64_t chains, int64_t per_chain, int64_t D) {
+    return chains * D * (per_chain + (per_chain + kGroup - 1) / kGroup + (per_chain + kBlock - 1) / kBlock);
+}
+
+// The plan, with the workspace emptied; `from` and `to`: the states that sequences without tokens pass through.
+template <int CPL>
+ScanPlan plan_of(const ScanArgs& a, const float* from, float* to, hipStream_t st) {
+    ScanPlan p{};
+    p.cols = (uint32_t)((a.D + 64 * CPL - 1) / (64 * CPL));
+    p.chains = a.cu ? 1 : (uint32_t)a.N;
+    p.per_chain = (uint32_t)(a.cu ? scan_segments(a) : (a.T_fixed + kScanSeg - 1) / kScanSeg);
+    int64_t words = 0;
+    if (p.per_chain > 1) {
+        p.counter = static_cast<uint32_t*>(a.ws);
+        p.pairs = static_cast<u64*>(a.ws) + 32;
+        p.groups = p.pairs + (int64_t)p.chains * p.per_chain * a.D;
+        p.states = p.groups + (int64_t)p.chains * ((p.per_chain + kGroup - 1) / kGroup) * a.D;
+        words = words_of(p.chains, p.per_chain, a.D);
+    }
+    const bool pass = to && (a.cu || a.T_fixed == 0);
+    if (words > 0 || pass) {
+        int64_t groups = (words + 1023) / 1024;
+        if (pass && groups < a.N) groups = a.N;
+        if (groups > 2048) groups = 2048;
+        hipLaunchKernelGGL(scan_begin_kernel, dim3((unsigned)groups), dim3(256), 0, st, p.pairs, words, p.counter, a.cu,
+                           a.N, a.T_fixed, a.total, a.D, from, pass ? to : nullptr);
+    }
+    return p;
+}
+
+template <bool XF, bool GF, int CPL>
+void fwd(const ScanArgs& a, hipStream_t st) {
+    const ScanPlan p = plan_of<CPL>(a, a.h0, a.h_final, st);
+    if (a.total == 0) return;
+    const dim3 grid(p.cols * p.chains * p.per_chain), block(kThreads);
+    if (a.cu) hipLaunchKernelGGL((scan_fwd_kernel<XF, GF, CPL, true>), grid, block, 0, st, a, p);
+    else hipLaunchKernelGGL((scan_fwd_kernel<XF, GF, CPL, false>), grid, block, 0, st, a, p);
+}
+
+template <bool XF, bool GF, int CPL>
+void bwd(const ScanArgs& a, hipStream_t st) {
+    const ScanPlan p = plan_of<CPL>(a, a.dh_final, a.dh0, st);
+    if (a.total == 0) return;
+    const dim3 grid(p.cols * p.chains * p.per_chain), block(kThreads);
+    if (a.u && a.cu) hipLaunchKernelGGL((scan_bwd_kernel<XF, GF, CPL, true, true>), grid, block, 0, st, a, p);
+    else if (a.u) hipLaunchKernelGGL((scan_bwd_kernel<XF, GF, CPL, false, true>), grid, block, 0, st, a, p);
+    else if (a.cu) hipLaunchKernelGGL((scan_bwd_kernel<XF, GF, CPL, true, false>), grid, block, 0, st, a, p);
+    else hipLaunchKernelGGL((scan_bwd_kernel<XF, GF, CPL, false, false>), grid, block, 0, st, a, p);
+}
+
+template <bool XF, bool GF, int CPL>
+void step(const ScanArgs& a, const float* h_in, float* h_out, hipStream_t st) {
+    const int64_t count = a.N * a.D;
+    const dim3 grid((unsigned)((count + 256 * CPL - 1) / (256 * CPL)));
+    hipLaunchKernelGGL((scan_step_kernel<XF, GF, CPL>), grid, dim3(256), 0, st, a, h_in, h_out, count);
+}
+
+// `f` with the types of x and g.
+template <class F>
+void by_type(const ScanArgs& a, F f) {
+    if (a.x_f32 && a.g_f32) f(std::true_type(), std::true_type());
+    else if (a.x_f32) f(std::true_type(), std::false_type());
+    else if (a.g_f32) f(std::false_type(), std::true_type());
+    else f(std::false_type(), std::false_type());
 }
 
 }  // namespace
 
-int64_t scan_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
+int64_t scan_places(const ScanArgs& a) {
+    const int64_t wide = a.D % 4 == 0 ? 256 : 64;
+    return (a.D + wide - 1) / wide * scan_segments(a);
+}
 
-#define KDA_SCAN_TYPES(KERNEL, GRID, BLOCK, ...)                                                            \
-    do {                                                                                                    \
-        if (a.x_f32 && a.g_f32) hipLaunchKernelGGL((KERNEL<true, true>), GRID, BLOCK, 0, st, __VA_ARGS__);  \
-        else if (a.x_f32) hipLaunchKernelGGL((KERNEL<true, false>), GRID, BLOCK, 0, st, __VA_ARGS__);       \
-        else if (a.g_f32) hipLaunchKernelGGL((KERNEL<false, true>), GRID, BLOCK, 0, st, __VA_ARGS__);       \
-        else hipLaunchKernelGGL((KERNEL<false, false>), GRID, BLOCK, 0, st, __VA_ARGS__);                   \
-    } while (0)
+// For N sequences and total tokens, packed or of equal lengths: at most total/64 + N segments in all, each group and
+// block started anew for each sequence.
+int64_t scan_workspace_bytes(int64_t N, int64_t total, int64_t D) {
+    if (total <= kScanSeg) return 0;
+    const int64_t s = total / kScanSeg + N;
+    return 256 + 8 * D * (s + s / kGroup + N + s / kBlock + N);
+}
 
 hipError_t launch_scan_fwd(const ScanArgs& a, hipStream_t st) {
-    const dim3 grid((unsigned)((a.D + 63) / 64 * a.N));
-    KDA_SCAN_TYPES(scan_fwd_kernel, grid, dim3(64), a);
+    by_type(a, [&](auto xf, auto gf) {
+        if (a.D % 4 == 0) fwd<decltype(xf)::value, decltype(gf)::value, 4>(a, st);
+        else fwd<decltype(xf)::value, decltype(gf)::value, 1>(a, st);
+    });
     return hipGetLastError();
 }
 
 hipError_t launch_scan_bwd(const ScanArgs& a, hipStream_t st) {
-    const dim3 grid((unsigned)((a.D + 63) / 64 * a.N));
-    KDA_SCAN_TYPES(scan_bwd_kernel, grid, dim3(64), a);
+    by_type(a, [&](auto xf, auto gf) {
+        if (a.D % 4 == 0) bwd<decltype(xf)::value, decltype(gf)::value, 4>(a, st);
+        else bwd<decltype(xf)::value, decltype(gf)::value, 1>(a, st);
+    });
     return hipGetLastError();
 }
 
 hipError_t launch_scan_step(const ScanArgs& a, const float* h_in, float* h_out, hipStream_t st) {
-    const int64_t count = a.N * a.D;
-    const dim3 grid((unsigned)((count + 255) / 256));
-    KDA_SCAN_TYPES(scan_step_kernel, grid, dim3(256), a, h_in, h_out, count);
+    by_type(a, [&](auto xf, auto gf) {
+        if (a.N * a.D % 4 == 0) step<decltype(xf)::value, decltype(gf)::value, 4>(a, h_in, h_out, st);
+        else step<decltype(xf)::value, decltype(gf)::value, 1>(a, h_in, h_out, st);
+    });
     return hipGetLastError();
 }
 

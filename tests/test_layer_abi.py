@@ -83,6 +83,7 @@ def test_scan_validation(name, defaults, kw, status, msg):
 @pytest.mark.parametrize("name,defaults,kw,status,msg", [
     ("kda_scan_fwd", FWD, dict(y=None), 1, "y"), ("kda_scan_fwd", FWD, dict(B=-1), 2, "B"),
     ("kda_scan_fwd", FWD, dict(T=-1), 2, "T"), ("kda_scan_fwd", FWD, dict(B=1 << 30, T=1 << 30), 2, "2^40"),
+    ("kda_scan_fwd", FWD, dict(B=1 << 22, T=1, D=(1 << 17) + 1), 2, "grid limit"),
     ("kda_scan_fwd", FWD, dict(u=FAKE), 1, "u_scales"), ("kda_scan_fwd", FWD, dict(us=FAKE), 1, "u_codes"),
     ("kda_scan_fwd", FWD, dict(carry=FAKE + 4), 4, "carry"),
     ("kda_scan_fwd", FWD, dict(h0=FAKE, h_final=FAKE), 2, "overlap"),
@@ -112,8 +113,7 @@ def test_scan_entry_validation(name, defaults, kw, status, msg):
 def test_scan_workspace_validation(name, defaults):
     N, total = (defaults["B"], defaults["B"] * defaults["T"]) if "B" in defaults else (2, 4096)
     need = kda.scan_workspace_bytes(N, total, 64)
-    if need == 0:
-        pytest.skip("no workspace needed")
+    assert need > 0
     expect(name, defaults, dict(ws=None), 1, "workspace")
     expect(name, defaults, dict(ws_bytes=need - 1), 2, "workspace")
     expect(name, defaults, dict(ws=FAKE + 8), 4, "workspace")
