@@ -142,6 +142,7 @@ kda_status check_ckpt8(int64_t rows, int64_t cols, kda_dtype dtype) {
     if ((st = check_dtype(dtype)) != KDA_OK) return st;
     if (rows < 0 || cols < 0) return fail(KDA_ERR_BAD_SHAPE, "rows and cols must be >= 0");
     if (cols > 0 && rows > kMostElements / cols) return fail(KDA_ERR_BAD_SHAPE, "rows*cols exceeds 2^40");
+    if (cols > 0x7fffffff) return fail(KDA_ERR_BAD_SHAPE, "cols must be below 2^31");
     return KDA_OK;
 }
 

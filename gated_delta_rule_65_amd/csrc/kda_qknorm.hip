@@ -1,5 +1,10 @@
 // Norm of queries and keys per head with the position rotation in the same pass, forward and backward
 // (mathematics and layouts: include/kda_layer.h).
+//
+// A row (token, head) of D channels goes to D/16 lanes of 16 channels, both channels of a turned pair in one lane, so that
+// only the row's sums cross lanes.  A workgroup takes a few whole tokens with all their heads: the angles, 64-bit products
+// with a sine and a cosine each, are made once a token and shared by its heads through LDS, while the first rows'
+// loads are in flight.  Both passes move their bytes once; what bounds them is HBM.
 #include "kda_ckpt8.h"
 #include "kda_layer_launch.h"
 
@@ -7,30 +12,100 @@ namespace kda {
 
 namespace {
 
+constexpr int kThreads = 256;
+constexpr int kAngles = 2048;  // pairs of a workgroup's tokens at most: 16 KiB of cosines and sines
+
 // The two chunks of eight channels that a lane of a row holds, such that both channels of every pair that is
 // turned are in one lane: lane j of D/16 holds channels first(j) .. +7 and second(j) .. +7.  In halves,
 // pair i is (i, i + rot/2); with adjacent pairs, and behind the turned channels, sixteen in a row.
 struct Place {
     int first, second;
-    bool turned;
-    int pair;  // the first of the lane's eight pairs
+    bool turned;  // in halves lane j holds pairs 8j .. +7, and so it does with adjacent pairs
 };
 __device__ __forceinline__ Place place_of(int j, int rot, bool interleaved) {
     const bool t = j < rot / 16;
-    if (t && !interleaved) return {8 * j, rot / 2 + 8 * j, true, 8 * j};
-    return {16 * j, 16 * j + 8, t, 8 * j};
+    if (t && !interleaved) return {8 * j, rot / 2 + 8 * j, true};
+    return {16 * j, 16 * j + 8, t};
 }
 
+// The sum over the lanes of a row (4 or 8 neighbours), the same bits in each of them.
+template <int LANES>
+__device__ __forceinline__ float row_sum(float v) {
+    static_assert(LANES == 4 || LANES == 8, "lanes of a row");
+    const auto from = [](float x, auto ctrl) {
+        return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), decltype(ctrl)::value, 0xf, 0xf, true));
+    };
+    v += from(v, std::integral_constant<int, 0xB1>());  // lane ^ 1
+    v += from(v, std::integral_constant<int, 0x4E>());  // lane ^ 2
+    if constexpr (LANES == 8) v += from(v, std::integral_constant<int, 0x141>());  // the other quad
+    return v;
+}
+
+// (s |x|^2 + eps)^(-1/2) of a row, 0 where that is 0.  Rows whose sum of squares leaves float32's comfortable
+// range are summed again at a power of two of their own size.
+template <int LANES>
+__device__ __forceinline__ float row_rsqrt(const float x[16], float s, float eps) {
+    float ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) ss = fmaf(x[k], x[k], ss);
+    ss = row_sum<LANES>(ss);
+    if (ss > 0x1p-100f && ss < 0x1p100f) return __builtin_amdgcn_rsqf(fmaf(ss, s, eps));
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) top = max(top, abs_bits(x[k]));
+    top = lanes_max<LANES>(top);
+    if (top >= kInfBits) return __uint_as_float(0x7fc00000u);  // a row that holds infinity or NaN has no norm
+    if (top == 0) return eps > 0.f ? rsqrtf(eps) : 0.f;
+    int e;
+    frexpf(__uint_as_float(top), &e);
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        const float u = ldexpf(x[k], -e);
+        sum = fmaf(u, u, sum);
+    }
+    sum = row_sum<LANES>(sum);
+    const double total = (double)sum * s * ldexp(1.0, 2 * e) + eps;
+    return total < 0x1p-252 ? 0.f : (float)(1.0 / sqrt(total));
+}
+
+// Sixteen channels of a row as they come from memory: two chunks of eight.
+template <bool F32, bool PACKED>
+struct Chunks {
+    uint4 a[F32 ? 2 : 1], b[F32 ? 2 : 1];
+};
 template <bool F32>
-__device__ __forceinline__ void load8(const void* p, int64_t i, float x[8]) {
-    if constexpr (F32) {
-        const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-        const float4 u = s[0], v = s[1];
-        x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
-        x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+struct Chunks<F32, true> {
+    uint2 a, b;
+    uint8_t sa, sb;
+};
+template <bool F32, bool PACKED>
+__device__ __forceinline__ void load_chunks(const void* p, const uint8_t* scales, int64_t row, const Place& at,
+                                            Chunks<F32, PACKED>& c) {
+    if constexpr (PACKED) {
+        const uint8_t* s = static_cast<const uint8_t*>(p) + row;
+        c.a = *reinterpret_cast<const uint2*>(s + at.first);
+        c.b = *reinterpret_cast<const uint2*>(s + at.second);
+        c.sa = scales[(row + at.first) / kCkptBlock];
+        c.sb = scales[(row + at.second) / kCkptBlock];
     } else {
-        const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        const char* s = static_cast<const char*>(p) + row * (F32 ? 4 : 2);
+#pragma unroll
+        for (int i = 0; i < (F32 ? 2 : 1); ++i) {
+            c.a[i] = *reinterpret_cast<const uint4*>(s + at.first * (F32 ? 4 : 2) + 16 * i);
+            c.b[i] = *reinterpret_cast<const uint4*>(s + at.second * (F32 ? 4 : 2) + 16 * i);
+        }
+    }
+}
+template <bool F32>
+__device__ __forceinline__ void chunk_values(const uint4* c, float x[8]) {
+    if constexpr (F32) {
+        x[0] = __uint_as_float(c[0].x); x[1] = __uint_as_float(c[0].y);
+        x[2] = __uint_as_float(c[0].z); x[3] = __uint_as_float(c[0].w);
+        x[4] = __uint_as_float(c[1].x); x[5] = __uint_as_float(c[1].y);
+        x[6] = __uint_as_float(c[1].z); x[7] = __uint_as_float(c[1].w);
+    } else {
+        const uint32_t u[4] = {c[0].x, c[0].y, c[0].z, c[0].w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             x[2 * k] = __uint_as_float(u[k] << 16);
@@ -38,298 +113,353 @@ __device__ __forceinline__ void load8(const void* p, int64_t i, float x[8]) {
         }
     }
 }
-template <bool F32>
-__device__ __forceinline__ void store8(void* p, int64_t i, const float x[8]) {
-    if constexpr (F32) {
-        float4* d = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
-        d[0] = make_float4(x[0], x[1], x[2], x[3]);
-        d[1] = make_float4(x[4], x[5], x[6], x[7]);
+template <bool F32, bool PACKED>
+__device__ __forceinline__ void values_of(const Chunks<F32, PACKED>& c, float x[16]) {
+    if constexpr (PACKED) {
+        const float ua = ckpt_unit(c.sa), ub = ckpt_unit(c.sb);
+        ckpt_value4(c.a.x, ua, x);
+        ckpt_value4(c.a.y, ua, x + 4);
+        ckpt_value4(c.b.x, ub, x + 8);
+        ckpt_value4(c.b.y, ub, x + 12);
     } else {
-        typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
-        bf8 w;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) w[k] = (__bf16)x[k];
-        *reinterpret_cast<bf8*>(static_cast<uint16_t*>(p) + i) = w;
+        chunk_values<F32>(c.a, x);
+        chunk_values<F32>(c.b, x + 8);
     }
 }
-// Eight packed values of one block.
-__device__ __forceinline__ void load8_packed(const uint8_t* codes, int64_t i, int scale, float x[8]) {
-    const uint2 w = *reinterpret_cast<const uint2*>(codes + i);
-    x[0] = ckpt_value<0>(w.x, scale); x[1] = ckpt_value<1>(w.x, scale);
-    x[2] = ckpt_value<2>(w.x, scale); x[3] = ckpt_value<3>(w.x, scale);
-    x[4] = ckpt_value<0>(w.y, scale); x[5] = ckpt_value<1>(w.y, scale);
-    x[6] = ckpt_value<2>(w.y, scale); x[7] = ckpt_value<3>(w.y, scale);
+template <bool F32>
+__device__ __forceinline__ void store_chunks(void* p, int64_t row, const Place& at, const float x[16]) {
+    if constexpr (F32) {
+        float* d = static_cast<float*>(p) + row;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<float4*>(d + (i < 2 ? at.first : at.second) + 4 * (i & 1)) =
+                make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    } else {
+        typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+        bf8 u, v;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) u[k] = (__bf16)x[k], v[k] = (__bf16)x[8 + k];
+        uint16_t* d = static_cast<uint16_t*>(p) + row;
+        *reinterpret_cast<bf8*>(d + at.first) = u;
+        *reinterpret_cast<bf8*>(d + at.second) = v;
+    }
 }
 
-// Cosine and sine of pos * freq radians.  The product is taken in 64 bits and reduced to a fraction of a turn
-// there, so that far positions keep float32's accuracy.
-__device__ __forceinline__ void turn(double pos, double freq, float& c, float& s) {
+// Cosine and sine of pos * freq radians.  The product is taken in 64 bits and reduced to a fraction of a turn there, so that
+// far positions keep float32's accuracy.
+__device__ __forceinline__ void angle(double pos, double freq, float& c, float& s) {
     constexpr double inv_2pi = 0.15915494309189533577;
     const double t = pos * (freq * inv_2pi);
     sincospif(2.f * (float)(t - rint(t)), &s, &c);
 }
-// z = (x0 c - x1 s, x1 c + x0 s) on the lane's eight pairs; sign -1 turns back.
-__device__ __forceinline__ void turn8(float a[8], float b[8], const float c[8], const float s[8], bool interleaved,
-                                      float sign) {
-    if (!interleaved) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float x = a[k], y = b[k], t = sign * s[k];
-            a[k] = x * c[k] - y * t;
-            b[k] = y * c[k] + x * t;
+
+// The tables of a workgroup's tokens in LDS, in the order in which lanes read them: a lane's eight values of a token as two
+// 16-byte reads, the lanes of a row side by side.
+template <int D>
+struct Tables {
+    static constexpr int LANES = D / 16;
+    float c[kAngles], s[kAngles];
+    float w[2][D];
+
+    // value `pair` of a token with `lanes` turned lanes
+    static __device__ __forceinline__ int slot(int token, int pair, int lanes) {
+        return token * lanes * 8 + (pair & 4) * lanes + (pair >> 3) * 4 + (pair & 3);
+    }
+    __device__ __forceinline__ void weights(const QkArgs& a) {
+        for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+            const int side = i / D, at = i % D, m = at / (4 * LANES), j = at / 4 % LANES, k = (m & 1) * 4 + at % 4;
+            const Place p = place_of(j, a.rot, a.interleaved);
+            const float* src = side ? a.wk : a.wq;
+            w[side][at] = src ? src[(m < 2 ? p.first : p.second) + k] : 1.f;
         }
-        return;
     }
+    __device__ __forceinline__ void angles(const QkArgs& a, int64_t t0, int tokens) {
+        const int pairs = a.rot / 2, lanes = a.rot / 16;
+        for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
+            const int t = i / pairs, q = i - t * pairs;
+            const double pos = a.pos64 ? (double)static_cast<const int64_t*>(a.pos)[t0 + t]
+                                       : (double)static_cast<const int32_t*>(a.pos)[t0 + t];
+            const int at = slot(t, q, lanes);
+            angle(pos, a.freqs[q], c[at], s[at]);
+        }
+    }
+    __device__ __forceinline__ void weight(int side, int j, float v[16]) const {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        float x = a[2 * k], y = a[2 * k + 1], t = sign * s[k];
-        a[2 * k] = x * c[k] - y * t;
-        a[2 * k + 1] = y * c[k] + x * t;
-        x = b[2 * k], y = b[2 * k + 1], t = sign * s[k + 4];
-        b[2 * k] = x * c[k + 4] - y * t;
-        b[2 * k + 1] = y * c[k + 4] + x * t;
+        for (int m = 0; m < 4; ++m) {
+            const float4 u = *reinterpret_cast<const float4*>(&w[side][m * 4 * LANES + 4 * j]);
+            v[4 * m] = u.x; v[4 * m + 1] = u.y; v[4 * m + 2] = u.z; v[4 * m + 3] = u.w;
+        }
     }
+    // z = (x0 c - x1 s, x1 c + x0 s) on the lane's eight pairs; sign -1 turns back.
+    __device__ __forceinline__ void turn(float x[16], int token, int j, int lanes, bool interleaved, float sign) const {
+        float cv[8], sv[8];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            const int at = token * lanes * 8 + m * 4 * lanes + 4 * j;
+            const float4 u = *reinterpret_cast<const float4*>(c + at), v = *reinterpret_cast<const float4*>(s + at);
+            cv[4 * m] = u.x; cv[4 * m + 1] = u.y; cv[4 * m + 2] = u.z; cv[4 * m + 3] = u.w;
+            sv[4 * m] = v.x; sv[4 * m + 1] = v.y; sv[4 * m + 2] = v.z; sv[4 * m + 3] = v.w;
+        }
+        if (interleaved) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float p = x[2 * k], q = x[2 * k + 1], t = sign * sv[k];
+                x[2 * k] = p * cv[k] - q * t;
+                x[2 * k + 1] = q * cv[k] + p * t;
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float p = x[k], q = x[8 + k], t = sign * sv[k];
+                x[k] = p * cv[k] - q * t;
+                x[8 + k] = q * cv[k] + p * t;
+            }
+        }
+    }
+};
+
+// The row's channels packed in 8 bits, from the raw values.  The lanes of a block: the quad of each chunk where pairs lie
+// half of the turned channels apart (in halves of whole blocks), two neighbours where the lane's channels follow one another;
+// other halves exchange each block's largest over the whole row.
+template <int D>
+__device__ __forceinline__ void pack_row(const float x[16], const Place& p, int j, int rot, bool interleaved,
+                                         uint8_t* codes, uint8_t* scales) {
+    constexpr int LANES = D / 16, BLOCKS = D / kCkptBlock;
+    int s0, s1;
+    bool any0, any1;
+    if (interleaved || rot % 64 == 0) {
+        const bool halves = p.turned && !interleaved;
+        const auto tops = [&](uint32_t a, uint32_t b, uint32_t& t0, uint32_t& t1) {
+            const uint32_t both = lanes_max<2>(max(a, b));
+            t0 = halves ? lanes_max<4>(a) : both;
+            t1 = halves ? lanes_max<4>(b) : both;
+        };
+        uint32_t t0, t1;
+        tops(ckpt_amax<8>(x), ckpt_amax<8>(x + 8), t0, t1);
+        any0 = t0 > kCkptTopBits;
+        any1 = t1 > kCkptTopBits;
+        if (__any(any0 || any1)) tops(ckpt_amax_finite<8>(x), ckpt_amax_finite<8>(x + 8), t0, t1);
+        s0 = ckpt_scale(t0);
+        s1 = ckpt_scale(t1);
+    } else {
+        const uint32_t m0 = ckpt_amax_finite<8>(x), m1 = ckpt_amax_finite<8>(x + 8);
+        s0 = s1 = 0;
+        any0 = any1 = true;
+#pragma unroll
+        for (int b = 0; b < BLOCKS; ++b) {
+            const bool in0 = p.first / kCkptBlock == b, in1 = p.second / kCkptBlock == b;
+            const int s = ckpt_scale(lanes_max<LANES>(max(in0 ? m0 : 0u, in1 ? m1 : 0u)));
+            if (in0) s0 = s;
+            if (in1) s1 = s;
+        }
+    }
+    const float i0 = ckpt_inverse(s0), i1 = ckpt_inverse(s1);
+    *reinterpret_cast<uint2*>(codes + p.first) = make_uint2(ckpt_code4(x, i0, any0), ckpt_code4(x + 4, i0, any0));
+    *reinterpret_cast<uint2*>(codes + p.second) = make_uint2(ckpt_code4(x + 8, i1, any1), ckpt_code4(x + 12, i1, any1));
+    // a block's first channels are the start of some lane's chunk
+    if (p.first % kCkptBlock == 0) scales[p.first / kCkptBlock] = (uint8_t)s0;
+    if (p.second % kCkptBlock == 0) scales[p.second / kCkptBlock] = (uint8_t)s1;
 }
 
-template <int LANES>
-__device__ __forceinline__ float row_sum(float v) {
-#pragma unroll
-    for (int off = LANES / 2; off > 0; off >>= 1) v += __shfl_xor(v, off);
-    return v;
-}
-
-// (s |x|^2 + eps)^(-1/2) of a row, 0 where that is 0.  Rows whose sum of squares leaves float32's comfortable
-// range are summed again at a power of two of their own size.
-template <int LANES>
-__device__ __forceinline__ float row_rsqrt(const float a[8], const float b[8], float s, float eps) {
-    float ss = 0.f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) ss = fmaf(a[k], a[k], fmaf(b[k], b[k], ss));
-    ss = row_sum<LANES>(ss);
-    if (ss > 0x1p-100f && ss < 0x1p100f) return __builtin_amdgcn_rsqf(fmaf(ss, s, eps));
-    uint32_t top = 0;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        top = max(top, abs_bits(a[k]));
-        top = max(top, abs_bits(b[k]));
-    }
-#pragma unroll
-    for (int off = LANES / 2; off > 0; off >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off));
-    if (top >= kInfBits) return __uint_as_float(0x7fc00000u);  // a row that holds infinity or NaN has no norm
-    if (top == 0) return eps > 0.f ? rsqrtf(eps) : 0.f;
-    int e;
-    frexpf(__uint_as_float(top), &e);
-    float sum = 0.f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const float u = ldexpf(a[k], -e), v = ldexpf(b[k], -e);
-        sum = fmaf(u, u, fmaf(v, v, sum));
-    }
-    sum = row_sum<LANES>(sum);
-    const double total = (double)sum * s * ldexp(1.0, 2 * e) + eps;
-    return total < 0x1p-252 ? 0.f : (float)(1.0 / sqrt(total));
-}
-
-// A row (token, head) to D/16 lanes.
+// `per` tokens to a workgroup, their rows (queries, then keys, of a token) by passes of 256 / LANES; PASSES passes are
+// loaded before the first of them is used.
 template <int D, bool F32, bool PACKED>
-__global__ __launch_bounds__(256) void qknorm_fwd_kernel(QkArgs a) {
-    constexpr int LANES = D / 16;
-    const int H = a.Hq + a.Hk;
-    const int64_t rows = a.tokens * H;
+__global__ __launch_bounds__(kThreads) void qknorm_fwd_kernel(QkArgs a, int per) {
+    constexpr int LANES = D / 16, ROWS = kThreads / LANES, PASSES = F32 ? 2 : 4;
+    __shared__ __align__(16) Tables<D> tab;
+    const int H = a.Hq + a.Hk, j = threadIdx.x % LANES;
+    const Place p = place_of(j, a.rot, a.interleaved);
+    const int64_t t0 = (int64_t)blockIdx.x * per;
+    const int tokens = a.tokens - t0 < per ? (int)(a.tokens - t0) : per, rows = tokens * H;
+    for (int base = 0; base < rows; base += PASSES * ROWS) {
+        Chunks<F32, PACKED> c[PASSES];
+        int tok[PASSES], head[PASSES];
+#pragma unroll
+        for (int i = 0; i < PASSES; ++i) {
+            int r = base + i * ROWS + threadIdx.x / LANES;
+            r = r < rows ? r : rows - 1;
+            tok[i] = (uint32_t)r / (uint32_t)H;
+            head[i] = r - tok[i] * H;
+            const bool key = head[i] >= a.Hq;
+            const int64_t t = t0 + tok[i];
+            if (key) load_chunks(a.k, a.ks, t * a.k_stride + (head[i] - a.Hq) * D, p, c[i]);
+            else load_chunks(a.q, a.qs, t * a.q_stride + head[i] * D, p, c[i]);
+        }
+        if (base == 0) {
+            if (a.wq || a.wk) tab.weights(a);
+            tab.angles(a, t0, tokens);
+            __syncthreads();
+        }
+#pragma unroll
+        for (int i = 0; i < PASSES; ++i) {
+            if (base + i * ROWS + (int)threadIdx.x / LANES >= rows) continue;
+            const bool key = head[i] >= a.Hq;
+            const int64_t out = key ? ((t0 + tok[i]) * a.Hk + head[i] - a.Hq) * D : ((t0 + tok[i]) * a.Hq + head[i]) * D;
+            float x[16];
+            values_of(c[i], x);
+            if constexpr (!PACKED) {
+                if (a.q8)
+                    pack_row<D>(x, p, j, a.rot, a.interleaved, (key ? a.k8 : a.q8) + out,
+                                (key ? a.k8s : a.q8s) + out / kCkptBlock);
+            }
+            const float r = row_rsqrt<LANES>(x, a.rms ? 1.f / D : 1.f, a.eps);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) x[k] *= r;
+            if (a.wq || a.wk) {
+                float w[16];
+                tab.weight(key, j, w);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) x[k] *= w[k];
+            }
+            if (p.turned) tab.turn(x, tok[i], j, a.rot / 16, a.interleaved, 1.f);
+            store_chunks<F32>(key ? a.k_out : a.q_out, out, p, x);
+        }
+    }
+}
+
+// Gradients of the rows, queries and keys in turn.  With weights, a workgroup goes on over the tokens with its lanes' sums
+// in registers and writes them, added up in LDS, to its line of the workspace.
+template <int D, bool F32, bool PACKED, bool GF32>
+__global__ __launch_bounds__(kThreads) void qknorm_bwd_kernel(QkArgs a, int per, int64_t tiles) {
+    constexpr int LANES = D / 16, ROWS = kThreads / LANES, PASSES = 2;
+    __shared__ __align__(16) Tables<D> tab;
+    __shared__ __align__(16) float part[ROWS][D];
     const int j = threadIdx.x % LANES;
     const Place p = place_of(j, a.rot, a.interleaved);
-    for (int64_t row = (int64_t)blockIdx.x * (256 / LANES) + threadIdx.x / LANES; row < rows;
-         row += (int64_t)gridDim.x * (256 / LANES)) {
-        const int64_t t = row / H;
-        int h = (int)(row - t * H);
-        const bool key = h >= a.Hq;
-        if (key) h -= a.Hq;
-        const void* src = key ? a.k : a.q;
-        const int64_t in = t * (key ? a.k_stride : a.q_stride) + h * D;
-        const int64_t out = (t * (key ? a.Hk : a.Hq) + h) * D;
-        float x0[8], x1[8];
-        if constexpr (PACKED) {
-            const uint8_t* sc = (key ? a.ks : a.qs) + out / kCkptBlock;
-            load8_packed(static_cast<const uint8_t*>(src), in + p.first, sc[p.first / kCkptBlock], x0);
-            load8_packed(static_cast<const uint8_t*>(src), in + p.second, sc[p.second / kCkptBlock], x1);
-        } else {
-            load8<F32>(src, in + p.first, x0);
-            load8<F32>(src, in + p.second, x1);
-        }
-        if constexpr (!PACKED) {
-            if (a.q8) {
-                // the lanes that share a block are not neighbours in halves; each takes its block's largest
-                // magnitude over the whole row's exchange
-                uint32_t m0 = 0, m1 = 0;
+    const float sc = a.rms ? 1.f / D : 1.f;
+    const bool weighted = a.wq || a.wk || a.dwq;
+    if (weighted) tab.weights(a);
+    float dw[2][16] = {};
+    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        const int64_t t0 = tile * per;
+        const int tokens = a.tokens - t0 < per ? (int)(a.tokens - t0) : per;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    m0 = max(m0, finite_abs_bits(x0[k]));
-                    m1 = max(m1, finite_abs_bits(x1[k]));
+        for (int side = 0; side < 2; ++side) {
+            const int Hs = side ? a.Hk : a.Hq, rows = tokens * Hs;
+            const void* src = side ? a.k : a.q;
+            const uint8_t* scales = side ? a.ks : a.qs;
+            const int64_t stride = side ? a.k_stride : a.q_stride;
+            for (int base = 0; base < rows; base += PASSES * ROWS) {
+                Chunks<F32, PACKED> c[PASSES];
+                Chunks<GF32, false> g[PASSES];
+                int tok[PASSES];
+                int64_t out[PASSES];
+#pragma unroll
+                for (int i = 0; i < PASSES; ++i) {
+                    int r = base + i * ROWS + threadIdx.x / LANES;
+                    r = r < rows ? r : rows - 1;
+                    tok[i] = (uint32_t)r / (uint32_t)Hs;
+                    out[i] = (t0 * Hs + r) * D;
+                    load_chunks(src, scales, (t0 + tok[i]) * stride + (r - tok[i] * Hs) * D, p, c[i]);
+                    load_chunks(side ? a.d_k : a.d_q, nullptr, out[i], p, g[i]);
                 }
-                uint32_t top[D / kCkptBlock] = {};
-#pragma unroll
-                for (int b = 0; b < D / kCkptBlock; ++b) {
-                    if (p.first / kCkptBlock == b) top[b] = m0;
-                    if (p.second / kCkptBlock == b) top[b] = max(top[b], m1);
-#pragma unroll
-                    for (int off = LANES / 2; off > 0; off >>= 1)
-                        top[b] = max(top[b], (uint32_t)__shfl_xor((int)top[b], off));
+                if (side == 0 && base == 0) {
+                    __syncthreads();  // the tables of the tile before are done with
+                    tab.angles(a, t0, tokens);
+                    __syncthreads();
                 }
-                uint8_t* codes = (key ? a.k8 : a.q8) + out;
-                uint8_t* sc = (key ? a.k8s : a.q8s) + out / kCkptBlock;
 #pragma unroll
-                for (int b = 0; b < D / kCkptBlock; ++b) {
-                    const int s = ckpt_scale(top[b]);
-                    const float inv = ckpt_inverse(s);
-                    if (j == b) sc[b] = (uint8_t)s;
+                for (int i = 0; i < PASSES; ++i) {
+                    if (base + i * ROWS + (int)threadIdx.x / LANES >= rows) continue;
+                    float x[16], d[16];
+                    values_of(c[i], x);
+                    values_of(g[i], d);
+                    const float r = row_rsqrt<LANES>(x, sc, a.eps);
+                    if (p.turned) tab.turn(d, tok[i], j, a.rot / 16, a.interleaved, -1.f);
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int at = half ? p.second : p.first;
-                        const float* x = half ? x1 : x0;
-                        if (at / kCkptBlock == b) {
-                            uint2 w;
-                            w.x = ckpt_code2(x[0], x[1], inv) | ckpt_code2(x[2], x[3], inv) << 16;
-                            w.y = ckpt_code2(x[4], x[5], inv) | ckpt_code2(x[6], x[7], inv) << 16;
-                            *reinterpret_cast<uint2*>(codes + at) = w;
+                    for (int k = 0; k < 16; ++k) x[k] *= r;
+                    if (weighted) {
+                        float w[16];
+                        tab.weight(side, j, w);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            dw[side][k] = fmaf(d[k], x[k], dw[side][k]);
+                            d[k] *= w[k];
                         }
                     }
+                    float dot = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) dot = fmaf(d[k], x[k], dot);
+                    dot = row_sum<LANES>(dot) * sc;
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) x[k] = r * fmaf(-dot, x[k], d[k]);
+                    store_chunks<F32>(side ? a.dk : a.dq, out[i], p, x);
                 }
             }
         }
-        const float r = row_rsqrt<LANES>(x0, x1, a.rms ? 1.f / D : 1.f, a.eps);
-        const float* w = key ? a.wk : a.wq;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            x0[k] *= r * (w ? w[p.first + k] : 1.f);
-            x1[k] *= r * (w ? w[p.second + k] : 1.f);
-        }
-        if (p.turned) {
-            const double pos = a.pos64 ? (double)static_cast<const int64_t*>(a.pos)[t]
-                                       : (double)static_cast<const int32_t*>(a.pos)[t];
-            float c[8], s[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) turn(pos, a.freqs[p.pair + k], c[k], s[k]);
-            turn8(x0, x1, c, s, a.interleaved, 1.f);
-        }
-        void* dst = key ? a.k_out : a.q_out;
-        store8<F32>(dst, out + p.first, x0);
-        store8<F32>(dst, out + p.second, x1);
     }
-}
-
-// Gradients of the rows; a workgroup's sums for the weights go to its line of the workspace.
-template <int D, bool F32, bool PACKED, bool GF32>
-__global__ __launch_bounds__(256) void qknorm_bwd_kernel(QkArgs a) {
-    constexpr int LANES = D / 16, ROWS = 256 / LANES;
-    __shared__ float part[ROWS][D];
-    const int H = a.Hq + a.Hk;
-    const int j = threadIdx.x % LANES;
-    const Place p = place_of(j, a.rot, a.interleaved);
+    if (!a.dwq) return;
     float* line = static_cast<float*>(a.ws) + (int64_t)blockIdx.x * 2 * D;
+#pragma unroll
     for (int side = 0; side < 2; ++side) {
-        const int Hs = side ? a.Hk : a.Hq;
-        const int64_t rows = a.tokens * Hs;
-        const void* src = side ? a.k : a.q;
-        const void* grad = side ? a.d_k : a.d_q;
-        const float* w = side ? a.wk : a.wq;
-        float dw0[8] = {}, dw1[8] = {};
-        for (int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / LANES; row < rows;
-             row += (int64_t)gridDim.x * ROWS) {
-            const int64_t t = row / Hs;
-            const int h = (int)(row - t * Hs);
-            const int64_t in = t * (side ? a.k_stride : a.q_stride) + h * D, out = row * D;
-            float x0[8], x1[8], d0[8], d1[8];
-            if constexpr (PACKED) {
-                const uint8_t* sc = (side ? a.ks : a.qs) + out / kCkptBlock;
-                load8_packed(static_cast<const uint8_t*>(src), in + p.first, sc[p.first / kCkptBlock], x0);
-                load8_packed(static_cast<const uint8_t*>(src), in + p.second, sc[p.second / kCkptBlock], x1);
-            } else {
-                load8<F32>(src, in + p.first, x0);
-                load8<F32>(src, in + p.second, x1);
-            }
-            load8<GF32>(grad, out + p.first, d0);
-            load8<GF32>(grad, out + p.second, d1);
-            const float sc = a.rms ? 1.f / D : 1.f;
-            const float r = row_rsqrt<LANES>(x0, x1, sc, a.eps);
-            if (p.turned) {
-                const double pos = a.pos64 ? (double)static_cast<const int64_t*>(a.pos)[t]
-                                           : (double)static_cast<const int32_t*>(a.pos)[t];
-                float c[8], s[8];
+        __syncthreads();
+        float* mine = part[threadIdx.x / LANES];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) turn(pos, a.freqs[p.pair + k], c[k], s[k]);
-                turn8(d0, d1, c, s, a.interleaved, -1.f);
-            }
-            float dot = 0.f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                x0[k] *= r;
-                x1[k] *= r;
-                dw0[k] = fmaf(d0[k], x0[k], dw0[k]);
-                dw1[k] = fmaf(d1[k], x1[k], dw1[k]);
-                d0[k] *= w ? w[p.first + k] : 1.f;
-                d1[k] *= w ? w[p.second + k] : 1.f;
-                dot = fmaf(d0[k], x0[k], fmaf(d1[k], x1[k], dot));
-            }
-            dot = row_sum<LANES>(dot) * sc;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                x0[k] = r * fmaf(-dot, x0[k], d0[k]);
-                x1[k] = r * fmaf(-dot, x1[k], d1[k]);
-            }
-            void* dst = side ? a.dk : a.dq;
-            store8<F32>(dst, out + p.first, x0);
-            store8<F32>(dst, out + p.second, x1);
-        }
-        if (a.dwq) {
-            float* mine = part[threadIdx.x / LANES];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                mine[p.first + k] = dw0[k];
-                mine[p.second + k] = dw1[k];
-            }
-            __syncthreads();
-            if (threadIdx.x < D) {
-                float sum = 0.f;
-                for (int i = 0; i < ROWS; ++i) sum += part[i][threadIdx.x];
-                line[side * D + threadIdx.x] = sum;
-            }
-            __syncthreads();
+        for (int m = 0; m < 4; ++m)
+            *reinterpret_cast<float4*>(mine + (m < 2 ? p.first : p.second) + 4 * (m & 1)) =
+                make_float4(dw[side][4 * m], dw[side][4 * m + 1], dw[side][4 * m + 2], dw[side][4 * m + 3]);
+        __syncthreads();
+        if (threadIdx.x < D) {
+            float sum = 0.f;
+            for (int i = 0; i < ROWS; ++i) sum += part[i][threadIdx.x];
+            line[side * D + threadIdx.x] = sum;
         }
     }
 }
 
-// The workgroups' lines added up in their order.
-__global__ __launch_bounds__(256) void qknorm_dw_kernel(const float* __restrict__ lines, int count, int D,
-                                                        float* __restrict__ dwq, float* __restrict__ dwk) {
-    const int c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= 2 * D) return;
+// The workgroups' lines added up in a fixed order: 32 threads to a column, each every 32nd line, then those in their
+// order.  Columns in groups of 32.
+__global__ __launch_bounds__(1024) void qknorm_dw_kernel(const float* __restrict__ lines, int count, int D,
+                                                         float* __restrict__ dwq, float* __restrict__ dwk) {
+    __shared__ float part[32][33];
+    const int col = threadIdx.x % 32, at = threadIdx.x / 32, c = blockIdx.x * 32 + col;
     float sum = 0.f;
-    for (int i = 0; i < count; ++i) sum += lines[(int64_t)i * 2 * D + c];
-    if (c < D) dwq[c] = sum;
-    else dwk[c - D] = sum;
+#pragma unroll 8
+    for (int i = at; i < count; i += 32) sum += lines[(int64_t)i * 2 * D + c];
+    part[at][col] = sum;
+    __syncthreads();
+    if (at == 0) {
+        float all = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) all += part[i][col];
+        if (c < D) dwq[c] = all;
+        else dwk[c - D] = all;
+    }
 }
 
-constexpr int kBwdGroups = 1024;
-int bwd_groups(int64_t tokens, int Hq, int Hk, int D) {
-    const int64_t need = (tokens * (Hq > Hk ? Hq : Hk) + 4095 / D) / (4096 / D);
-    return (int)(need < kBwdGroups ? need : kBwdGroups);
+// Tokens of a workgroup: enough rows of their H heads to fill `passes` passes, as far as their angles fit.
+int tokens_of(int H, int D, int rot, int passes) {
+    const int rows = passes * kThreads / (D / 16);
+    int per = (rows + H - 1) / H;
+    if (rot && per > kAngles / (rot / 2)) per = kAngles / (rot / 2);
+    return per;
+}
+
+constexpr int kBwdGroups = 1024;  // four workgroups a CU
+
+int64_t bwd_tiles(int64_t tokens, int Hq, int Hk, int D, int rot) {
+    const int per = tokens_of(Hq > Hk ? Hq : Hk, D, rot, 2);
+    return (tokens + per - 1) / per;
 }
 
 }  // namespace
 
-int64_t qknorm_bwd_workspace_bytes(int64_t tokens, int Hq, int Hk, int D) {
-    return (int64_t)bwd_groups(tokens, Hq, Hk, D) * 2 * D * 4;
+// At most as many lines as workgroups (rot only cuts the tiles smaller).
+int64_t qknorm_bwd_workspace_bytes(int64_t tokens, int, int, int D) {
+    return (tokens < kBwdGroups ? tokens : kBwdGroups) * 2 * D * 4;
 }
 
 hipError_t launch_qknorm_fwd(const QkArgs& a, hipStream_t st) {
-    const int64_t groups = (a.tokens * (a.Hq + a.Hk) + 4096 / a.D - 1) / (4096 / a.D);
-    const dim3 grid((unsigned)(groups < 16384 ? groups : 16384)), block(256);
+    const int per = tokens_of(a.Hq + a.Hk, a.D, a.rot, 4);
+    const int64_t tiles = (a.tokens + per - 1) / per;
+    if (tiles > 0x7fffffff) return hipErrorInvalidConfiguration;
+    const dim3 grid((unsigned)tiles), block(kThreads);
     const bool packed = a.qs != nullptr;
-#define KDA_FWD(DIM)                                                                                          \
-    if (a.f32 && packed) hipLaunchKernelGGL((qknorm_fwd_kernel<DIM, true, true>), grid, block, 0, st, a);     \
-    else if (a.f32) hipLaunchKernelGGL((qknorm_fwd_kernel<DIM, true, false>), grid, block, 0, st, a);         \
-    else if (packed) hipLaunchKernelGGL((qknorm_fwd_kernel<DIM, false, true>), grid, block, 0, st, a);        \
-    else hipLaunchKernelGGL((qknorm_fwd_kernel<DIM, false, false>), grid, block, 0, st, a);
+#define KDA_FWD(DIM)                                                                                             \
+    if (a.f32 && packed) hipLaunchKernelGGL((qknorm_fwd_kernel<DIM, true, true>), grid, block, 0, st, a, per);   \
+    else if (a.f32) hipLaunchKernelGGL((qknorm_fwd_kernel<DIM, true, false>), grid, block, 0, st, a, per);       \
+    else if (packed) hipLaunchKernelGGL((qknorm_fwd_kernel<DIM, false, true>), grid, block, 0, st, a, per);      \
+    else hipLaunchKernelGGL((qknorm_fwd_kernel<DIM, false, false>), grid, block, 0, st, a, per);
     if (a.D == 128) {
         KDA_FWD(128)
     } else {
@@ -340,22 +470,30 @@ hipError_t launch_qknorm_fwd(const QkArgs& a, hipStream_t st) {
 }
 
 template <int D, bool GF32>
-static void launch_bwd_types(const QkArgs& a, int groups, hipStream_t st) {
-    const dim3 grid((unsigned)groups), block(256);
+static void launch_bwd_types(const QkArgs& a, int groups, int per, int64_t tiles, hipStream_t st) {
+    const dim3 grid((unsigned)groups), block(kThreads);
     const bool packed = a.qs != nullptr;
-    if (a.f32 && packed) hipLaunchKernelGGL((qknorm_bwd_kernel<D, true, true, GF32>), grid, block, 0, st, a);
-    else if (a.f32) hipLaunchKernelGGL((qknorm_bwd_kernel<D, true, false, GF32>), grid, block, 0, st, a);
-    else if (packed) hipLaunchKernelGGL((qknorm_bwd_kernel<D, false, true, GF32>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((qknorm_bwd_kernel<D, false, false, GF32>), grid, block, 0, st, a);
+    if (a.f32 && packed) hipLaunchKernelGGL((qknorm_bwd_kernel<D, true, true, GF32>), grid, block, 0, st, a, per, tiles);
+    else if (a.f32) hipLaunchKernelGGL((qknorm_bwd_kernel<D, true, false, GF32>), grid, block, 0, st, a, per, tiles);
+    else if (packed) hipLaunchKernelGGL((qknorm_bwd_kernel<D, false, true, GF32>), grid, block, 0, st, a, per, tiles);
+    else hipLaunchKernelGGL((qknorm_bwd_kernel<D, false, false, GF32>), grid, block, 0, st, a, per, tiles);
 }
 
 hipError_t launch_qknorm_bwd(const QkArgs& a, hipStream_t st) {
-    const int groups = bwd_groups(a.tokens, a.Hq, a.Hk, a.D);
+    const int per = tokens_of(a.Hq > a.Hk ? a.Hq : a.Hk, a.D, a.rot, 2);
+    const int64_t tiles = bwd_tiles(a.tokens, a.Hq, a.Hk, a.D, a.rot);
+    const int64_t most = a.dwq ? kBwdGroups : 0x7fffffff;
+    const int groups = (int)(tiles < most ? tiles : most);
     if (groups == 0) {  // no tokens: only the weights' zero gradients are written
-    } else if (a.D == 128) a.grad_f32 ? launch_bwd_types<128, true>(a, groups, st) : launch_bwd_types<128, false>(a, groups, st);
-    else a.grad_f32 ? launch_bwd_types<64, true>(a, groups, st) : launch_bwd_types<64, false>(a, groups, st);
+    } else if (a.D == 128) {
+        a.grad_f32 ? launch_bwd_types<128, true>(a, groups, per, tiles, st)
+                   : launch_bwd_types<128, false>(a, groups, per, tiles, st);
+    } else {
+        a.grad_f32 ? launch_bwd_types<64, true>(a, groups, per, tiles, st)
+                   : launch_bwd_types<64, false>(a, groups, per, tiles, st);
+    }
     if (a.dwq)
-        hipLaunchKernelGGL(qknorm_dw_kernel, dim3((unsigned)((2 * a.D + 255) / 256)), dim3(256), 0, st,
+        hipLaunchKernelGGL(qknorm_dw_kernel, dim3((unsigned)(2 * a.D / 32)), dim3(1024), 0, st,
                            static_cast<const float*>(a.ws), groups, a.D, a.dwq, a.dwk);
     return hipGetLastError();
 }

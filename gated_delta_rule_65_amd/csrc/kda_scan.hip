@@ -81,8 +81,6 @@ __device__ __forceinline__ void store_row(void* base, int64_t i, const float v[C
         if constexpr (CPL % 4 == 0) {
 #pragma unroll
             for (int k = 0; k < CPL; k += 4) *reinterpret_cast<float4*>(p + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
-        } else if constexpr (CPL == 2) {
-            *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
         } else {
             *p = v[0];
         }
@@ -93,8 +91,6 @@ __device__ __forceinline__ void store_row(void* base, int64_t i, const float v[C
                                                       bf16_pair(v[6], v[7]));
         else if constexpr (CPL == 4)
             *reinterpret_cast<uint2*>(p) = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
-        else if constexpr (CPL == 2)
-            *reinterpret_cast<uint32_t*>(p) = bf16_pair(v[0], v[1]);
         else
             *reinterpret_cast<__bf16*>(p) = (__bf16)v[0];
     }
@@ -364,20 +360,6 @@ __device__ __forceinline__ Marks marks_of(const ScanArgs& a, int64_t r0, int row
     return m;
 }
 
-// Largest of the lanes that share a block of 32 channels.
-template <int CPL>
-__device__ __forceinline__ uint32_t block_max(uint32_t v) {
-    auto dpp = [](uint32_t x, auto ctrl) {
-        return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, decltype(ctrl)::value, 0xf, 0xf, true);
-    };
-    v = max(v, dpp(v, std::integral_constant<int, 0xB1>()));            // lane ^ 1
-    v = max(v, dpp(v, std::integral_constant<int, 0x4E>()));            // lane ^ 2: quads agree
-    if constexpr (CPL <= 4) v = max(v, dpp(v, std::integral_constant<int, 0x141>()));  // the other quad of eight
-    if constexpr (CPL <= 2) v = max(v, dpp(v, std::integral_constant<int, 0x140>()));  // the other eight of sixteen
-    if constexpr (CPL == 1) v = max(v, (uint32_t)__shfl_xor((int)v, 16));
-    return v;
-}
-
 // ---------------------------------------------------------------------------- forward
 template <bool XF, bool GF, int CPL, bool FLAT>
 __global__ __launch_bounds__(kThreads) void scan_fwd_kernel(ScanArgs a, ScanPlan p) {
@@ -476,25 +458,18 @@ __global__ __launch_bounds__(kThreads) void scan_fwd_kernel(ScanArgs a, ScanPlan
         }
         if (a.u_out) {
             float u[CPL];
-            uint32_t top = 0;
 #pragma unroll
-            for (int k = 0; k < CPL; ++k) {
-                u[k] = a.complement ? h[k] - raw_get(xr[i], k) : h[k];
-                top = max(top, finite_abs_bits(u[k]));
-            }
-            const int s = ckpt_scale(block_max<CPL>(in ? top : 0));
+            for (int k = 0; k < CPL; ++k) u[k] = a.complement ? h[k] - raw_get(xr[i], k) : h[k];
+            bool any;
+            const int s = ckpt_block<kCkptBlock / CPL, CPL>(u, in, any);
             const float inv = ckpt_inverse(s);
             if (in) {
                 uint8_t* codes = a.u_out + r * a.D + c;
                 if constexpr (CPL == 1) {
-                    *codes = (uint8_t)ckpt_code2(u[0], 0.f, inv);
-                } else if constexpr (CPL == 2) {
-                    *reinterpret_cast<uint16_t*>(codes) = (uint16_t)ckpt_code2(u[0], u[1], inv);
+                    *codes = (uint8_t)ckpt_code_any(u[0], inv);
                 } else {
 #pragma unroll
-                    for (int k = 0; k < CPL; k += 4)
-                        *reinterpret_cast<uint32_t*>(codes + k) =
-                            ckpt_code2(u[k], u[k + 1], inv) | ckpt_code2(u[k + 2], u[k + 3], inv) << 16;
+                    for (int k = 0; k < CPL; k += 4) *reinterpret_cast<uint32_t*>(codes + k) = ckpt_code4(u + k, inv, any);
                 }
                 if (c % kCkptBlock == 0) a.us_out[r * blocks + c / kCkptBlock] = (uint8_t)s;
             }
@@ -547,7 +522,6 @@ __global__ __launch_bounds__(kThreads) void scan_bwd_kernel(ScanArgs a, ScanPlan
         dr[i] = load_raw<XF, CPL>(a.dy, at);
         if constexpr (PACKED) {
             if constexpr (CPL == 1) code[i][0] = a.u[at];
-            else if constexpr (CPL == 2) code[i][0] = *reinterpret_cast<const uint16_t*>(a.u + at);
             else load_words<CPL / 4>(a.u + at, code[i]);
             scale[i] = a.us[r * blocks + cc / kCkptBlock];
         } else {
@@ -663,21 +637,21 @@ __global__ __launch_bounds__(kThreads) void scan_bwd_kernel(ScanArgs a, ScanPlan
                 for (int k = 0; k < CPL; ++k) s[k] = a.dh_final && in ? a.dh_final[m.n[i] * a.D + c + k] : 0.f;
             }
         }
-        float dx[CPL], dg[CPL];
+        float dx[CPL], dg[CPL], f[PACKED ? (CPL + 3) / 4 * 4 : CPL];
+        if constexpr (PACKED) {
+            const float unit = ckpt_unit(scale[i]);
+#pragma unroll
+            for (int k = 0; k < CPL; k += 4) ckpt_value4(code[i][k / 4], unit, f + k);
+        } else {
+#pragma unroll
+            for (int k = 0; k < CPL; ++k) f[k] = u[i][k];
+        }
 #pragma unroll
         for (int k = 0; k < CPL; ++k) {
             const float dh = raw_get(dr[i], k) + s[k];
             s[k] = al[i][k] * dh;
             dx[k] = a.complement ? rest[i][k] * dh : dh;
-            float f;
-            if constexpr (PACKED) {
-                const uint32_t w = code[i][k / 4];
-                f = k % 4 == 0 ? ckpt_value<0>(w, scale[i]) : k % 4 == 1 ? ckpt_value<1>(w, scale[i])
-                    : k % 4 == 2 ? ckpt_value<2>(w, scale[i]) : ckpt_value<3>(w, scale[i]);
-            } else {
-                f = u[i][k];
-            }
-            dg[k] = f * s[k] * gate_slope(raw_get(gr[i], k), rest[i][k], a.logit);
+            dg[k] = f[k] * s[k] * gate_slope(raw_get(gr[i], k), rest[i][k], a.logit);
         }
         if (in) {
             store_row<XF, CPL>(a.dx, r * a.D + c, dx);

@@ -465,6 +465,23 @@ def test_qk_leading_dimensions_and_one_weight():
     near(dwk, dw, "f32", "dwk")
 
 
+def test_qk_gradient_of_absent_weights_is_that_of_ones():
+    import ctypes
+    d, angle = qk_data(70, 2, 1, 64, 32, "f32", False, 9)
+    out = [torch.empty_like(d["q"]), torch.empty_like(d["k"]), *(torch.full((64,), 7.0, device="cuda") for _ in range(2))]
+    ws = torch.empty(kda.qk_norm_rope_workspace_bytes(70, 2, 1, 64), dtype=torch.uint8, device="cuda")
+    form = kda.layer.QkNormForm(0, 0.0, 32, 0, 8)
+    rc = kda.load_library().kda_qknorm_bwd(
+        d["q"].data_ptr(), d["k"].data_ptr(), None, None, 128, 64, None, None, d["pos"].data_ptr(), d["freqs"].data_ptr(),
+        d["dq"].data_ptr(), d["dk"].data_ptr(), *(t.data_ptr() for t in out), 70, 2, 1, 64, 0, 0, ctypes.byref(form),
+        ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    for i, n in enumerate("qk"):
+        _, dx, dw = ref.qk_norm(host(d[n]), None, angle, False, 0.0, False, host(d["d" + n]))
+        near(out[i], dx, "f32", "d" + n)
+        near(out[2 + i], dw, "f32", "dw" + n)
+
+
 def test_qk_rows_of_any_size():
     """Zero rows stay zero; rows whose squares overflow or vanish in float32 are normed all the same; infinity and
     NaN stay in their row."""

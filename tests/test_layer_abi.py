@@ -37,7 +37,7 @@ PACK = dict(x=FAKE, codes=FAKE, scales=FAKE, rows=3, cols=40, dtype=1, stream=No
 @pytest.mark.parametrize("name", ["kda_ckpt8_pack", "kda_ckpt8_unpack"])
 @pytest.mark.parametrize("kw,status,msg", [
     (dict(x=None), 1, "x"), (dict(codes=None), 1, "codes"), (dict(scales=None), 1, "scales"),
-    (dict(rows=-1), 2, "rows"), (dict(cols=-1), 2, "cols"), (dict(rows=1 << 40, cols=2), 2, "2^40"),
+    (dict(rows=-1), 2, "rows"), (dict(cols=-1), 2, "cols"), (dict(rows=1 << 40, cols=2), 2, "2^40"), (dict(rows=1, cols=1 << 31), 2, "2^31"),
     (dict(dtype=2), 3, "dtype"), (dict(codes=FAKE + 1), 4, "codes"), (dict(x=FAKE + 8), 4, "x"),
 ])
 def test_ckpt8_validation(name, kw, status, msg):
