@@ -147,7 +147,7 @@ kda_status check_ckpt8(int64_t rows, int64_t cols, kda_dtype dtype) {
 }
 
 bool scan_sizes(int64_t N, int64_t total, int64_t D) {
-    return N >= 1 && N <= 0x7fffffff && total >= 0 && D >= 1 && D <= 0x7fffffff && total <= kMostElements / D &&
+    return N >= 1 && N <= 0x7fffffff && total >= 0 && D >= 1 && D <= kda::kMaxChannels && total <= kMostElements / D &&
            N <= kMostElements / D;
 }
 

@@ -13,6 +13,7 @@ hipError_t launch_ckpt8_unpack(const uint8_t* codes, const uint8_t* scales, void
 
 // ---- gated scan (kda_scan.hip)
 constexpr int kScanSeg = 64;  // tokens of a segment
+constexpr int64_t kMaxChannels = 1 << 24;
 
 struct ScanArgs {
     const void *x, *g;

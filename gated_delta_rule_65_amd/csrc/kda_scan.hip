@@ -19,6 +19,8 @@
 // with the lowest place among those not done waits for nobody.
 //
 // The backward pass is the same scan with time reversed, of e_t = a_t (dy_t + e_{t+1}).
+#include <type_traits>
+
 #include "kda_ckpt8.h"
 #include "kda_layer_launch.h"
 
@@ -32,8 +34,6 @@ constexpr int kWaves = 8, kRows = 8, kThreads = kWaves * 64;
 static_assert(kWaves * kRows == kScanSeg, "a wave's rows");
 constexpr int kGroup = 8, kBlock = 64;  // segments of a group and of a block
 
-constexpr float kLog2e = 1.4426950408889634f;
-
 // ---------------------------------------------------------------------------- rows in registers
 // CPL consecutive elements of a row as they come from memory.
 template <bool F32, int CPL>
@@ -41,19 +41,21 @@ struct Raw {
     static constexpr int WORDS = F32 ? CPL : (CPL + 1) / 2;
     uint32_t w[WORDS];
 };
+// Rows are read once and written once: past the caches.  (B = 4, T = 8192, D = 2048 in bf16, rows moved in this pattern and
+// nothing else: 90 us, and 84 non-temporal.)
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 template <int WORDS>
 __device__ __forceinline__ void load_words(const void* p, uint32_t* w) {
-    if constexpr (WORDS % 4 == 0) {
-#pragma unroll
-        for (int i = 0; i < WORDS; i += 4) {
-            const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint32_t*>(p) + i);
-            w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
-        }
+    if constexpr (WORDS == 4) {
+        const u32x4 v = __builtin_nontemporal_load(static_cast<const u32x4*>(p));
+        w[0] = v[0]; w[1] = v[1]; w[2] = v[2]; w[3] = v[3];
     } else if constexpr (WORDS == 2) {
-        const uint2 v = *static_cast<const uint2*>(p);
-        w[0] = v.x; w[1] = v.y;
+        const u32x2 v = __builtin_nontemporal_load(static_cast<const u32x2*>(p));
+        w[0] = v[0]; w[1] = v[1];
     } else {
-        w[0] = *static_cast<const uint32_t*>(p);
+        w[0] = __builtin_nontemporal_load(static_cast<const uint32_t*>(p));
     }
 }
 template <bool F32, int CPL>
@@ -65,9 +67,9 @@ __device__ __forceinline__ Raw<F32, CPL> load_raw(const void* base, int64_t i) {
     return r;
 }
 template <bool F32, int CPL>
-__device__ __forceinline__ float raw_get(const Raw<F32, CPL>& r, int k) {
+__device__ __forceinline__ float raw_get(const Raw<F32, CPL>& r, int k, uint32_t shift = 16, uint32_t mask = 0xffff0000u) {
     if constexpr (F32) return __uint_as_float(r.w[k]);
-    else return __uint_as_float(k % 2 ? r.w[k / 2] & 0xffff0000u : r.w[k / 2] << 16);
+    else return __uint_as_float(k % 2 ? r.w[k / 2] & mask : r.w[k / 2] << shift);
 }
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
     typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
@@ -78,21 +80,13 @@ template <bool F32, int CPL>
 __device__ __forceinline__ void store_row(void* base, int64_t i, const float v[CPL]) {
     if constexpr (F32) {
         float* p = static_cast<float*>(base) + i;
-        if constexpr (CPL % 4 == 0) {
-#pragma unroll
-            for (int k = 0; k < CPL; k += 4) *reinterpret_cast<float4*>(p + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
-        } else {
-            *p = v[0];
-        }
+        if constexpr (CPL == 4) __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4*>(p));
+        else *p = v[0];
     } else {
         uint16_t* p = static_cast<uint16_t*>(base) + i;
-        if constexpr (CPL == 8)
-            *reinterpret_cast<uint4*>(p) = make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]),
-                                                      bf16_pair(v[6], v[7]));
-        else if constexpr (CPL == 4)
-            *reinterpret_cast<uint2*>(p) = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
-        else
-            *reinterpret_cast<__bf16*>(p) = (__bf16)v[0];
+        if constexpr (CPL == 4)
+            __builtin_nontemporal_store(u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])}, reinterpret_cast<u32x2*>(p));
+        else *reinterpret_cast<__bf16*>(p) = (__bf16)v[0];
     }
 }
 
@@ -119,19 +113,32 @@ constexpr float kLogitEdge = 4.993239165f;  // ln(e^5 - 1)
 struct Gate {
     float a, rest;
 };
-__device__ __forceinline__ Gate gate_of(float g, bool logit, bool need_rest) {
-    if (logit) {
-        const float t = __builtin_amdgcn_exp2f(__builtin_elementwise_minimum(g, kLogitEdge) * kLog2e);
+// The constants of one run over a wave's rows.  A later run takes the same ones through again(), where the compiler cannot
+// see that they are the same: it would keep every decay and input of the first run in registers otherwise.
+struct Run {
+    uint32_t shift = 16, mask = 0xffff0000u;
+    float low = -5.f, edge = kLogitEdge, log2e = 1.4426950408889634f;
+};
+__device__ __forceinline__ Run again() {
+    Run r;
+    __asm__ volatile("" : "+s"(r.shift), "+s"(r.mask), "+s"(r.low), "+s"(r.edge), "+s"(r.log2e));
+    return r;
+}
+template <bool LOGIT, bool REST>
+__device__ __forceinline__ Gate gate_of(float g, const Run& run) {
+    if constexpr (LOGIT) {
+        const float t = __builtin_amdgcn_exp2f(__builtin_elementwise_minimum(g, run.edge) * run.log2e);
         const float a = __builtin_amdgcn_rcpf(1.f + t);
         return {a, t * a};
     }
-    const float l = __builtin_elementwise_minimum(__builtin_elementwise_maximum(g, -5.f), 0.f);
-    const float a = __builtin_amdgcn_exp2f(l * kLog2e);
-    return {a, need_rest ? one_minus_exp(l, a) : 0.f};
+    const float l = __builtin_elementwise_minimum(__builtin_elementwise_maximum(g, run.low), 0.f);
+    const float a = __builtin_amdgcn_exp2f(l * run.log2e);
+    return {a, REST ? one_minus_exp(l, a) : 0.f};
 }
 // The derivative of l by g: 1 inside the clamp (ends included) and 0 outside; with logits -sigmoid(g) = -(1 - a).
-__device__ __forceinline__ float gate_slope(float g, float rest, bool logit) {
-    if (logit) return g > kLogitEdge ? 0.f : -rest;
+template <bool LOGIT>
+__device__ __forceinline__ float gate_slope(float g, float rest) {
+    if constexpr (LOGIT) return g > kLogitEdge ? 0.f : -rest;
     return (g < -5.f || g > 0.f) ? 0.f : 1.f;
 }
 
@@ -177,17 +184,18 @@ __device__ __forceinline__ uint32_t take_place(uint32_t* counter, uint32_t* shar
     return (uint32_t)__builtin_amdgcn_readfirstlane((int)*shared);
 }
 
-// The sequence that holds row r of packed rows: the last n with cu[n] <= r, by 64 candidates at a time.
+// An offset of packed rows, read through the scalar cache (the kernels do not write them).
+__device__ __forceinline__ int64_t offset_of(const int32_t* cu, int64_t n) {
+    typedef const __attribute__((address_space(4))) int32_t* scalar;
+    return ((scalar)cu)[__builtin_amdgcn_readfirstlane((int)n)];
+}
+// The sequence that holds row r of packed rows: the last n with cu[n] <= r.
 __device__ __forceinline__ int64_t seq_of(const int32_t* cu, int64_t N, int64_t r) {
-    int64_t lo = 0, len = N;
-    while (len > 1) {
-        const int64_t step = (len + 63) / 64;
-        const int64_t i = lo + (int64_t)(threadIdx.x & 63) * step;
-        const bool le = i < lo + len && cu[i] <= r;
-        const int c = __popcll(__ballot(le));
-        const int64_t at = lo + (c > 0 ? c - 1 : 0) * step;
-        len = lo + len - at < step ? lo + len - at : step;
-        lo = at;
+    int lo = 0, hi = (int)N - 1;
+    while (lo < hi) {
+        const int mid = lo + (hi - lo + 1) / 2;
+        if (offset_of(cu, mid) <= r) lo = mid;
+        else hi = mid - 1;
     }
     return lo;
 }
@@ -228,45 +236,56 @@ __device__ __forceinline__ Pair await(const u64* at, u64 w) {
     return {__uint_as_float((uint32_t)(w >> 32)), __uint_as_float((uint32_t)w)};
 }
 
-// The state of channel c before segment t.at of its chain, from what its predecessors published; `reach` of them back at
-// most have a part in it (packed rows: those from the sequence's first on).
-__device__ __forceinline__ float state_before(const ScanArgs& a, const ScanPlan& p, const Tile& t, int64_t c, int64_t reach,
-                                              Pair own) {
-    const int64_t first = t.at - reach;
-    const int n1 = (int)(t.at % kGroup), n2 = (int)(t.at / kGroup % (kBlock / kGroup));
-    const int64_t base1 = t.chain * p.per_chain + t.at - n1;                                 // of this group
-    const int64_t groups = (p.per_chain + kGroup - 1) / kGroup, blocks = (p.per_chain + kBlock - 1) / kBlock;
-    const int64_t base2 = t.chain * groups + t.at / kGroup - n2;                             // of this block
-    const bool wait3 = t.at >= kBlock && first < t.at / kBlock * kBlock;
-    u64 w1[kGroup - 1], w2[kBlock / kGroup - 1], w3 = 0;
-    if (wait3) w3 = peek(p.states + (t.chain * blocks + t.at / kBlock - 1) * a.D + c);
+// The pair of the segments of t.at's group before it, for channel c; the group's last segment publishes the group's.
+__device__ __forceinline__ Pair group_before(const ScanArgs& a, const ScanPlan& p, const Tile& t, int64_t c, Pair own) {
+    const int n = (int)(t.at % kGroup);
+    const u64* at = p.pairs + (t.chain * p.per_chain + t.at - n) * a.D + c;
+    u64 w[kGroup - 1];
 #pragma unroll
-    for (int i = 0; i < kBlock / kGroup - 1; ++i) w2[i] = i < n2 ? peek(p.groups + (base2 + i) * a.D + c) : 0;
-#pragma unroll
-    for (int i = 0; i < kGroup - 1; ++i) w1[i] = i < n1 ? peek(p.pairs + (base1 + i) * a.D + c) : 0;
+    for (int i = 0; i < kGroup - 1; ++i) w[i] = i < n ? peek(at + i * a.D) : 0;
     Pair group = {1.f, 0.f};
-    // the segments of the group first: the group's own pair waits for nothing further back
 #pragma unroll
     for (int i = 0; i < kGroup - 1; ++i)
-        if (i < n1) group = then(group, await(p.pairs + (base1 + i) * a.D + c, w1[i]));
-    if (n1 == kGroup - 1) publish(p.groups + (t.chain * groups + t.at / kGroup) * a.D + c, then(group, own));
-    Pair before = {1.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < kBlock / kGroup - 1; ++i)
-        if (i < n2) before = then(before, await(p.groups + (base2 + i) * a.D + c, w2[i]));
-    before = then(before, group);
-    float s = 0.f;
-    if (wait3) s = await(p.states + (t.chain * blocks + t.at / kBlock - 1) * a.D + c, w3).b;
-    s = apply(before, s);
-    if (t.at % kBlock == kBlock - 1)
-        publish(p.states + (t.chain * blocks + t.at / kBlock) * a.D + c, Pair{0.f, apply(own, s)});
-    return s;
+        if (i < n) group = then(group, await(at + i * a.D, w[i]));
+    if (n == kGroup - 1) {
+        const int64_t groups = (p.per_chain + kGroup - 1) / kGroup;
+        publish(p.groups + (t.chain * groups + t.at / kGroup) * a.D + c, then(group, own));
+    }
+    return group;
 }
 
-// The waves' pairs, then the states before the waves, of the workgroup's channels.
+// The state of channel c before t.at's group, from the groups of its block and the state before the block; `reach` segments
+// back at most have a part in it (packed rows: those from the sequence's first on).
+__device__ __forceinline__ float state_before_group(const ScanArgs& a, const ScanPlan& p, const Tile& t, int64_t c,
+                                                    int64_t reach) {
+    constexpr int most = kBlock / kGroup - 1;
+    const int64_t groups = (p.per_chain + kGroup - 1) / kGroup, blocks = (p.per_chain + kBlock - 1) / kBlock;
+    const int n = (int)(t.at / kGroup % (most + 1));
+    const bool further = t.at >= kBlock && t.at - reach < t.at / kBlock * kBlock;
+    const u64* at = p.groups + (t.chain * groups + t.at / kGroup - n) * a.D + c;
+    const u64* state = p.states + (t.chain * blocks + t.at / kBlock - 1) * a.D + c;
+    u64 w[most], ws = 0;
+    if (further) ws = peek(state);
+#pragma unroll
+    for (int i = 0; i < most; ++i) w[i] = i < n ? peek(at + i * a.D) : 0;
+    Pair before = {1.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < most; ++i)
+        if (i < n) before = then(before, await(at + i * a.D, w[i]));
+    return apply(before, further ? await(state, ws).b : 0.f);
+}
+
+// What the waves of a workgroup tell one another of its channels: their pairs, then the states before them, and
+// the state before the segment's group.
 template <int CPL>
 struct Exchange {
-    float A[kWaves][64 * CPL], b[kWaves][64 * CPL];
+    float A[kWaves][64 * CPL], b[kWaves][64 * CPL], before[64 * CPL];
+};
+// Half of what a lane keeps of its rows in the backward pass, so that two workgroups' registers fit a CU.
+constexpr int kKept = kRows / 2;
+template <int CPL, bool USED>
+struct Kept {
+    float rows[USED ? kKept : 1][USED ? kWaves : 1][USED ? 64 * CPL : 1];
 };
 template <int CPL>
 __device__ __forceinline__ void put(float* row, const float v[CPL]) {
@@ -293,40 +312,48 @@ __device__ __forceinline__ void take(const float* row, float v[CPL]) {
     }
 }
 
-// From the waves' pairs (in the scan's direction: wave `order(i)` is the i-th) to the state before each wave, in x.b;
-// `start`: the state before the chain's first segment.  Each thread has channels of its own throughout.
+// From the waves' pairs (taken in the scan's direction) to the state before each wave, in x.b.  `start`: the state before the
+// chain's first segment, where reach < 0 names it.  A thread of the first part has a channel of its own and folds
+// its group, one of the second part folds what lies before the group at the same time.
 template <bool BACK, int CPL>
 __device__ __forceinline__ void join_waves(const ScanArgs& a, const ScanPlan& p, const Tile& t, Exchange<CPL>& x,
                                            const float* start, int64_t reach, float* carry) {
-    for (int ch = threadIdx.x; ch < 64 * CPL; ch += kThreads) {
-        const int64_t c = t.col * 64 * CPL + ch;
-        if (c >= a.D) continue;
-        Pair own = {1.f, 0.f};
+    constexpr int C = 64 * CPL;
+    static_assert(2 * C <= kThreads, "two threads a channel");
+    const int part = __builtin_amdgcn_readfirstlane(threadIdx.x / C), ch = threadIdx.x % C;
+    const int64_t c = t.col * C + ch;
+    const bool mine = c < a.D;
+    Pair own = {1.f, 0.f}, group = {1.f, 0.f};
+    if (part == 0 && mine) {
 #pragma unroll
         for (int i = 0; i < kWaves; ++i) {
             const int w = BACK ? kWaves - 1 - i : i;
             own = then(own, Pair{x.A[w][ch], x.b[w][ch]});
         }
-        float s;
-        if (reach < 0) {  // the chain's first segment: what lies before it is known, so its pair holds for any state
-            s = start ? start[c] : 0.f;
-            own = {__uint_as_float(kBegins), apply(own, s)};
-        }
-        if (p.counter) publish(p.pairs + (t.chain * p.per_chain + t.at) * a.D + c, own);
+        // before the chain's first segment the state is known: its pair holds for any
+        if (reach < 0) own = {__uint_as_float(kBegins), apply(own, start ? start[c] : 0.f)};
         if (p.counter) {
-            const float before = state_before(a, p, t, c, reach < 0 ? 0 : reach, own);
-            if (reach >= 0) s = before;
-        } else if (reach >= 0) {
-            s = 0.f;
+            publish(p.pairs + (t.chain * p.per_chain + t.at) * a.D + c, own);
+            group = group_before(a, p, t, c, own);
         }
-        if (carry) carry[t.id * a.D + c] = s;
+    }
+    if (part == 1 && mine && p.counter) x.before[ch] = state_before_group(a, p, t, c, reach);
+    if (p.counter) __syncthreads();
+    if (part != 0 || !mine) return;
+    float s;
+    if (reach < 0) s = start ? start[c] : 0.f;
+    else s = p.counter ? apply(group, x.before[ch]) : 0.f;
+    if (p.counter && t.at % kBlock == kBlock - 1) {
+        const int64_t blocks = (p.per_chain + kBlock - 1) / kBlock;
+        publish(p.states + (t.chain * blocks + t.at / kBlock) * a.D + c, Pair{0.f, apply(own, s)});
+    }
+    if (carry) carry[t.id * a.D + c] = s;
 #pragma unroll
-        for (int i = 0; i < kWaves; ++i) {
-            const int w = BACK ? kWaves - 1 - i : i;
-            const Pair q = {x.A[w][ch], x.b[w][ch]};
-            x.b[w][ch] = s;
-            s = apply(q, s);
-        }
+    for (int i = 0; i < kWaves; ++i) {
+        const int w = BACK ? kWaves - 1 - i : i;
+        const Pair q = {x.A[w][ch], x.b[w][ch]};
+        x.b[w][ch] = s;
+        s = apply(q, s);
     }
 }
 
@@ -339,127 +366,92 @@ __device__ __forceinline__ Marks marks_of(const ScanArgs& a, int64_t r0, int row
     Marks m{0, 0, {}};
     if (rows <= 0) return m;
     int64_t n = seq_of(a.cu, a.N, r0);
-    int64_t next = a.cu[n + 1];
-    bool begins = a.cu[n] == r0;
+    int64_t next = offset_of(a.cu, n + 1);
+    bool begins = offset_of(a.cu, n) == r0;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
         if (i < rows) {
             while (r0 + i >= next && n + 1 < a.N) {
                 ++n;
-                next = a.cu[n + 1];
+                next = offset_of(a.cu, n + 1);
                 begins = true;
             }
-            m.n[i] = __builtin_amdgcn_readfirstlane((int)n);
+            m.n[i] = (int)n;
             if (begins) m.begins |= 1u << i;
             if (r0 + i + 1 == next) m.ends |= 1u << i;
             begins = false;
         }
     }
-    m.begins = __builtin_amdgcn_readfirstlane(m.begins);
-    m.ends = __builtin_amdgcn_readfirstlane(m.ends);
     return m;
 }
 
 // ---------------------------------------------------------------------------- forward
-template <bool XF, bool GF, int CPL, bool FLAT>
-__global__ __launch_bounds__(kThreads) void scan_fwd_kernel(ScanArgs a, ScanPlan p) {
-    __shared__ Exchange<CPL> x;
-    __shared__ uint32_t place;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const uint32_t pl = take_place(p.counter, &place);
-    int64_t total = a.total;
-    if constexpr (FLAT) {
-        const int64_t used = a.cu[a.N];
-        total = used < 0 ? 0 : used < total ? used : total;
-    }
-    const Tile t = tile_of<FLAT, false>(a, p, pl, total);
-    const int64_t c = t.col * 64 * CPL + lane * CPL;
-    const bool in = c < a.D;
-    const int64_t cc = in ? c : 0;
-    const int64_t r0 = t.row0 + wave * kRows;
-    const int rows = t.rows - wave * kRows < 0 ? 0 : t.rows - wave * kRows < kRows ? t.rows - wave * kRows : kRows;
+// The rows of a wave with what a row gives: its decay and its input's share.  The gates are made again in the second run
+// rather than kept: as they come, in 16 bits, the rows of a wave take half the registers of decays and inputs in 32,
+// and twice the workgroups are on a CU while they wait for memory and for one another.
+template <bool XF, bool GF, int CPL>
+struct Rows {
+    Raw<XF, CPL> x[kRows];
+    Raw<GF, CPL> g[kRows];
+};
+template <bool LOGIT, bool MIX, bool XF, bool GF, int CPL>
+__device__ __forceinline__ void step_of(const Rows<XF, GF, CPL>& rows, int i, int k, const Run& run, float& a, float& b) {
+    const Gate q = gate_of<LOGIT, MIX>(raw_get(rows.g[i], k, run.shift, run.mask), run);
+    const float v = raw_get(rows.x[i], k, run.shift, run.mask);
+    a = q.a;
+    b = MIX ? q.rest * v : v;
+}
 
-    Raw<XF, CPL> xr[kRows];
-    Raw<GF, CPL> gr[kRows];
-    const int64_t last = total > 0 ? (t.row0 + t.rows > 0 ? t.row0 + t.rows - 1 : 0) : 0;
+// The state before a sequence, or zeros.
+template <int CPL>
+__device__ __forceinline__ void state_of(const float* h0, int64_t at, bool in, float h[CPL]) {
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const int64_t r = r0 + i < last ? r0 + i : last;
-        const int64_t at = (t.rows > 0 ? r : 0) * a.D + cc;
-        gr[i] = load_raw<GF, CPL>(a.g, at);
-        xr[i] = load_raw<XF, CPL>(a.x, at);
-    }
-    Marks m{0, 0, {}};
-    if constexpr (FLAT) m = marks_of(a, r0, rows);
+    for (int k = 0; k < CPL; ++k) h[k] = h0 && in ? h0[at + k] : 0.f;
+}
 
-    float al[kRows][CPL], b[kRows][CPL];
+template <bool LOGIT, bool MIX, bool XF, bool GF, int CPL, bool FLAT, bool PACK>
+__device__ __forceinline__ void fwd_body(const ScanArgs& a, const ScanPlan& p, const Tile& t, const Marks& m,
+                                         const Rows<XF, GF, CPL>& raw, int rows, int64_t r0, int64_t c, bool in,
+                                         int64_t reach, Exchange<CPL>& x) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     float A[CPL], h[CPL];
+    Run run = again();
 #pragma unroll
     for (int k = 0; k < CPL; ++k) A[k] = 1.f, h[k] = 0.f;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
+        if (i >= rows) break;
+        if (FLAT && (m.begins >> i & 1)) {
+            state_of<CPL>(a.h0, m.n[i] * a.D + c, in, h);
+#pragma unroll
+            for (int k = 0; k < CPL; ++k) A[k] = __uint_as_float(kBegins);
+        }
 #pragma unroll
         for (int k = 0; k < CPL; ++k) {
-            const Gate q = gate_of(raw_get(gr[i], k), a.logit, a.complement);
-            const float v = raw_get(xr[i], k);
-            al[i][k] = q.a;
-            b[i][k] = a.complement ? q.rest * v : v;
-        }
-        if (i >= rows) {
-#pragma unroll
-            for (int k = 0; k < CPL; ++k) al[i][k] = 1.f, b[i][k] = 0.f;
-        }
-        bool begins = false;
-        if constexpr (FLAT) begins = m.begins >> i & 1;
-        if (begins) {
-#pragma unroll
-            for (int k = 0; k < CPL; ++k) {
-                A[k] = __uint_as_float(kBegins);
-                const float s = a.h0 && in ? a.h0[m.n[i] * a.D + c + k] : 0.f;
-                h[k] = fmaf(al[i][k], s, b[i][k]);
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < CPL; ++k) {
-                A[k] *= al[i][k];
-                h[k] = fmaf(al[i][k], h[k], b[i][k]);
-            }
+            float al, b;
+            step_of<LOGIT, MIX>(raw, i, k, run, al, b);
+            A[k] *= al;  // -0 stays -0
+            h[k] = fmaf(al, h[k], b);
         }
     }
     put<CPL>(&x.A[wave][lane * CPL], A);
     put<CPL>(&x.b[wave][lane * CPL], h);
     __syncthreads();
-    int64_t reach = t.at > 0 ? t.at : -1;
-    if constexpr (FLAT) {
-        // segments back to the one where the sequence of the first row begins
-        if (t.rows > 0) {
-            const int64_t n = seq_of(a.cu, a.N, t.row0);
-            const int64_t begin = a.cu[n] < 0 ? 0 : a.cu[n];
-            reach = t.at - begin / kScanSeg;
-            if (reach < 0) reach = 0;
-        } else {
-            reach = 0;
-        }
-    }
     join_waves<false, CPL>(a, p, t, x, a.h0 && !FLAT ? a.h0 + t.chain * a.D : nullptr, reach, a.carry_out);
     __syncthreads();
     take<CPL>(&x.b[wave][lane * CPL], h);
 
+    run = again();
     const int64_t blocks = (a.D + kCkptBlock - 1) / kCkptBlock;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
         if (i >= rows) break;
         const int64_t r = r0 + i;
-        if constexpr (FLAT) {
-            if (m.begins >> i & 1) {
-#pragma unroll
-                for (int k = 0; k < CPL; ++k) h[k] = a.h0 && in ? a.h0[m.n[i] * a.D + c + k] : 0.f;
-            }
-        }
-        if (a.u_out) {
+        if (FLAT && (m.begins >> i & 1)) state_of<CPL>(a.h0, m.n[i] * a.D + c, in, h);
+        if constexpr (PACK) {
             float u[CPL];
 #pragma unroll
-            for (int k = 0; k < CPL; ++k) u[k] = a.complement ? h[k] - raw_get(xr[i], k) : h[k];
+            for (int k = 0; k < CPL; ++k) u[k] = MIX ? h[k] - raw_get(raw.x[i], k, run.shift, run.mask) : h[k];
             bool any;
             const int s = ckpt_block<kCkptBlock / CPL, CPL>(u, in, any);
             const float inv = ckpt_inverse(s);
@@ -475,7 +467,11 @@ __global__ __launch_bounds__(kThreads) void scan_fwd_kernel(ScanArgs a, ScanPlan
             }
         }
 #pragma unroll
-        for (int k = 0; k < CPL; ++k) h[k] = fmaf(al[i][k], h[k], b[i][k]);
+        for (int k = 0; k < CPL; ++k) {
+            float al, b;
+            step_of<LOGIT, MIX>(raw, i, k, run, al, b);
+            h[k] = fmaf(al, h[k], b);
+        }
         if (in) store_row<XF, CPL>(a.y, r * a.D + c, h);
         if (a.h_final && in) {
             bool ends;
@@ -487,80 +483,109 @@ __global__ __launch_bounds__(kThreads) void scan_fwd_kernel(ScanArgs a, ScanPlan
     }
 }
 
-// ---------------------------------------------------------------------------- backward
-// PACKED: the factor u of the gate's gradient comes from its 8-bit codes; else the states of the segment are made again
-// from the carry and x.
-template <bool XF, bool GF, int CPL, bool FLAT, bool PACKED>
-__global__ __launch_bounds__(kThreads) void scan_bwd_kernel(ScanArgs a, ScanPlan p) {
+// Rows in use: all of them, or those up to the last sequence's end.
+template <bool FLAT>
+__device__ __forceinline__ int64_t rows_used(const ScanArgs& a) {
+    if constexpr (!FLAT) return a.total;
+    const int64_t used = offset_of(a.cu, a.N);
+    return used < 0 ? 0 : used < a.total ? used : a.total;
+}
+// Of the segment's rows, how many are the wave's.
+__device__ __forceinline__ int rows_of_wave(const Tile& t, int wave) {
+    const int left = t.rows - wave * kRows;
+    return left < 0 ? 0 : left < kRows ? left : kRows;
+}
+
+// `f` with the form of the gates, the same in all threads.
+template <class F>
+__device__ __forceinline__ void by_form(const ScanArgs& a, F f) {
+    if (a.logit) {
+        if (a.complement) f(std::true_type(), std::true_type());
+        else f(std::true_type(), std::false_type());
+    } else {
+        if (a.complement) f(std::false_type(), std::true_type());
+        else f(std::false_type(), std::false_type());
+    }
+}
+
+// Waves of a SIMD that the registers are cut to: two to a workgroup.
+constexpr int fwd_waves(bool xf, bool gf) { return xf && gf ? 4 : xf || gf ? 5 : 7; }
+constexpr int bwd_waves(bool xf, bool gf, bool packed) { return packed && !xf && !gf ? 5 : 4; }
+
+template <bool XF, bool GF, int CPL, bool FLAT, bool PACK>
+__global__ __launch_bounds__(kThreads, fwd_waves(XF, GF)) void scan_fwd_kernel(ScanArgs a, ScanPlan p) {
     __shared__ Exchange<CPL> x;
     __shared__ uint32_t place;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t pl = take_place(p.counter, &place);
-    int64_t total = a.total;
-    if constexpr (FLAT) {
-        const int64_t used = a.cu[a.N];
-        total = used < 0 ? 0 : used < total ? used : total;
-    }
-    const Tile t = tile_of<FLAT, true>(a, p, pl, total);
+    const Tile t = tile_of<FLAT, false>(a, p, pl, rows_used<FLAT>(a));
     const int64_t c = t.col * 64 * CPL + lane * CPL;
     const bool in = c < a.D;
-    const int64_t cc = in ? c : 0;
-    const int64_t r0 = t.row0 + wave * kRows;
-    const int rows = t.rows - wave * kRows < 0 ? 0 : t.rows - wave * kRows < kRows ? t.rows - wave * kRows : kRows;
-    const int64_t blocks = (a.D + kCkptBlock - 1) / kCkptBlock;
+    const int64_t r0 = t.row0 + wave * kRows, last = t.rows > 0 ? t.row0 + t.rows - 1 : 0;
+    const int rows = rows_of_wave(t, wave);
 
-    Raw<GF, CPL> gr[kRows];
-    Raw<XF, CPL> dr[kRows], xr[PACKED ? 1 : kRows];
-    uint32_t code[PACKED ? kRows : 1][(CPL + 3) / 4];
-    int scale[PACKED ? kRows : 1];
-    const int64_t last = t.rows > 0 ? t.row0 + t.rows - 1 : 0;
+    Rows<XF, GF, CPL> raw;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-        const int64_t r = r0 + i < last ? r0 + i : last;
-        const int64_t at = r * a.D + cc;
-        gr[i] = load_raw<GF, CPL>(a.g, at);
-        dr[i] = load_raw<XF, CPL>(a.dy, at);
-        if constexpr (PACKED) {
-            if constexpr (CPL == 1) code[i][0] = a.u[at];
-            else load_words<CPL / 4>(a.u + at, code[i]);
-            scale[i] = a.us[r * blocks + cc / kCkptBlock];
-        } else {
-            xr[i] = load_raw<XF, CPL>(a.x, at);
-        }
+        const int64_t at = (r0 + i < last ? r0 + i : last) * a.D + (in ? c : 0);
+        raw.g[i] = load_raw<GF, CPL>(a.g, at);
+        raw.x[i] = load_raw<XF, CPL>(a.x, at);
     }
     Marks m{0, 0, {}};
-    if constexpr (FLAT) m = marks_of(a, r0, rows);
-
-    float al[kRows][CPL], rest[kRows][CPL];
-    float A[CPL], s[CPL];
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-#pragma unroll
-        for (int k = 0; k < CPL; ++k) {
-            const Gate q = gate_of(raw_get(gr[i], k), a.logit, a.complement);
-            al[i][k] = i < rows ? q.a : 1.f;
-            rest[i][k] = q.rest;
+    int64_t reach = t.at > 0 ? t.at : -1;
+    if constexpr (FLAT) {
+        m = marks_of(a, r0, rows);
+        // segments back to the one where the sequence of the first row begins
+        reach = 0;
+        if (t.rows > 0) {
+            const int64_t begin = offset_of(a.cu, seq_of(a.cu, a.N, t.row0));
+            reach = begin < t.row0 ? t.at - (begin < 0 ? 0 : begin) / kScanSeg : 0;
         }
     }
-    float u[PACKED ? 1 : kRows][CPL];
+    by_form(a, [&](auto logit, auto mix) {
+        fwd_body<decltype(logit)::value, decltype(mix)::value, XF, GF, CPL, FLAT, PACK>(a, p, t, m, raw, rows, r0, c, in,
+                                                                                       reach, x);
+    });
+}
+
+// ---------------------------------------------------------------------------- backward
+// PACKED: the factor u of the gate's gradient comes from its 8-bit codes; else the states of the segment are made again
+// from the carry and x.
+template <bool XF, bool GF, int CPL, bool PACKED>
+struct BackRows {
+    Raw<GF, CPL> g[kRows];
+    Raw<XF, CPL> dy[kRows], x[PACKED ? 1 : kRows];
+    uint32_t code[PACKED ? kRows : 1][(CPL + 3) / 4];
+    uint32_t scale[PACKED ? kRows / 4 : 1];  // a byte a row
+    __device__ __forceinline__ int scale_of(int i) const { return scale[i / 4] >> (i % 4 * 8) & 0xff; }
+};
+
+template <bool LOGIT, bool MIX, bool XF, bool GF, int CPL, bool FLAT, bool PACKED>
+__device__ __forceinline__ void bwd_body(const ScanArgs& a, const ScanPlan& p, const Tile& t, const Marks& m,
+                                         const BackRows<XF, GF, CPL, PACKED>& raw, int rows, int64_t r0, int64_t c,
+                                         bool in, int64_t reach, Exchange<CPL>& x, Kept<CPL, !PACKED>& kept) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    float A[CPL], s[CPL];
+    float u[PACKED ? 1 : kRows - kKept][CPL];
     if constexpr (!PACKED) {
         // the states again: the waves' pairs from x, joined from the carry
+        Run run = again();
 #pragma unroll
         for (int k = 0; k < CPL; ++k) A[k] = 1.f, s[k] = 0.f;
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
             if (i >= rows) break;
-            const bool begins = FLAT && (m.begins >> i & 1);
+            if (FLAT && (m.begins >> i & 1)) {
+                state_of<CPL>(a.h0, m.n[i] * a.D + c, in, s);
+#pragma unroll
+                for (int k = 0; k < CPL; ++k) A[k] = __uint_as_float(kBegins);
+            }
 #pragma unroll
             for (int k = 0; k < CPL; ++k) {
-                const float v = raw_get(xr[i], k), b = a.complement ? rest[i][k] * v : v;
-                if (begins) {
-                    A[k] = __uint_as_float(kBegins);
-                    s[k] = fmaf(al[i][k], a.h0 && in ? a.h0[m.n[i] * a.D + c + k] : 0.f, b);
-                } else {
-                    A[k] *= al[i][k];
-                    s[k] = fmaf(al[i][k], s[k], b);
-                }
+                const Gate q = gate_of<LOGIT, MIX>(raw_get(raw.g[i], k, run.shift, run.mask), run);
+                const float v = raw_get(raw.x[i], k, run.shift, run.mask);
+                A[k] *= q.a;
+                s[k] = fmaf(q.a, s[k], MIX ? q.rest * v : v);
             }
         }
         put<CPL>(&x.A[wave][lane * CPL], A);
@@ -582,76 +607,76 @@ __global__ __launch_bounds__(kThreads) void scan_bwd_kernel(ScanArgs a, ScanPlan
         __syncthreads();
         take<CPL>(&x.b[wave][lane * CPL], s);
         __syncthreads();
+        run = again();
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            const bool begins = FLAT && (m.begins >> i & 1);
+            if (FLAT && (m.begins >> i & 1)) state_of<CPL>(a.h0, m.n[i] * a.D + c, in, s);
+            float f[CPL];
 #pragma unroll
             for (int k = 0; k < CPL; ++k) {
-                if (begins) s[k] = a.h0 && in ? a.h0[m.n[i] * a.D + c + k] : 0.f;
-                const float v = raw_get(xr[i], k);
-                u[i][k] = a.complement ? s[k] - v : s[k];
-                s[k] = fmaf(al[i][k], s[k], a.complement ? rest[i][k] * v : v);
+                const Gate q = gate_of<LOGIT, MIX>(raw_get(raw.g[i], k, run.shift, run.mask), run);
+                const float v = raw_get(raw.x[i], k, run.shift, run.mask);
+                f[k] = MIX ? s[k] - v : s[k];
+                s[k] = fmaf(q.a, s[k], MIX ? q.rest * v : v);
+            }
+            if (i < kKept) {
+                put<CPL>(&kept.rows[i < kKept ? i : 0][wave][lane * CPL], f);
+            } else {
+#pragma unroll
+                for (int k = 0; k < CPL; ++k) u[i < kKept ? 0 : i - kKept][k] = f[k];
             }
         }
     }
     // the reversed scan
+    const Run back = again();
 #pragma unroll
     for (int k = 0; k < CPL; ++k) A[k] = 1.f, s[k] = 0.f;
 #pragma unroll
     for (int i = kRows - 1; i >= 0; --i) {
         if (i >= rows) continue;
-        const bool ends = FLAT && (m.ends >> i & 1);
+        if (FLAT && (m.ends >> i & 1)) {
+            state_of<CPL>(a.dh_final, m.n[i] * a.D + c, in, s);
+#pragma unroll
+            for (int k = 0; k < CPL; ++k) A[k] = __uint_as_float(kBegins);
+        }
 #pragma unroll
         for (int k = 0; k < CPL; ++k) {
-            if (ends) {
-                A[k] = __uint_as_float(kBegins);
-                s[k] = al[i][k] * (raw_get(dr[i], k) + (a.dh_final && in ? a.dh_final[m.n[i] * a.D + c + k] : 0.f));
-            } else {
-                A[k] *= al[i][k];
-                s[k] = al[i][k] * (raw_get(dr[i], k) + s[k]);
-            }
+            const float al = gate_of<LOGIT, false>(raw_get(raw.g[i], k, back.shift, back.mask), back).a;
+            A[k] *= al;
+            s[k] = al * (raw_get(raw.dy[i], k, back.shift, back.mask) + s[k]);
         }
     }
     put<CPL>(&x.A[wave][lane * CPL], A);
     put<CPL>(&x.b[wave][lane * CPL], s);
     __syncthreads();
-    int64_t reach = t.at > 0 ? t.at : -1;
-    if constexpr (FLAT) {
-        reach = 0;
-        if (t.rows == kScanSeg) {  // segments on to the one where the sequence of the last row ends
-            const int64_t n = seq_of(a.cu, a.N, last);
-            const int64_t end = a.cu[n + 1] < total ? a.cu[n + 1] : total;
-            reach = end > last ? (end - 1) / kScanSeg - t.id : 0;
-        }
-    }
     join_waves<true, CPL>(a, p, t, x, a.dh_final && !FLAT ? a.dh_final + t.chain * a.D : nullptr, reach, nullptr);
     __syncthreads();
     take<CPL>(&x.b[wave][lane * CPL], s);
+    const Run run = again();
 #pragma unroll
     for (int i = kRows - 1; i >= 0; --i) {
         if (i >= rows) continue;
         const int64_t r = r0 + i;
-        if constexpr (FLAT) {
-            if (m.ends >> i & 1) {
-#pragma unroll
-                for (int k = 0; k < CPL; ++k) s[k] = a.dh_final && in ? a.dh_final[m.n[i] * a.D + c + k] : 0.f;
-            }
-        }
-        float dx[CPL], dg[CPL], f[PACKED ? (CPL + 3) / 4 * 4 : CPL];
+        if (FLAT && (m.ends >> i & 1)) state_of<CPL>(a.dh_final, m.n[i] * a.D + c, in, s);
+        float dx[CPL], dg[CPL], f[(CPL + 3) / 4 * 4];
         if constexpr (PACKED) {
-            const float unit = ckpt_unit(scale[i]);
+            const float unit = ckpt_unit(raw.scale_of(i));
 #pragma unroll
-            for (int k = 0; k < CPL; k += 4) ckpt_value4(code[i][k / 4], unit, f + k);
+            for (int k = 0; k < CPL; k += 4) ckpt_value4(raw.code[i][k / 4], unit, f + k);
+        } else if (i < kKept) {
+            take<CPL>(&kept.rows[i < kKept ? i : 0][wave][lane * CPL], f);
         } else {
 #pragma unroll
-            for (int k = 0; k < CPL; ++k) f[k] = u[i][k];
+            for (int k = 0; k < CPL; ++k) f[k] = u[i < kKept ? 0 : i - kKept][k];
         }
 #pragma unroll
         for (int k = 0; k < CPL; ++k) {
-            const float dh = raw_get(dr[i], k) + s[k];
-            s[k] = al[i][k] * dh;
-            dx[k] = a.complement ? rest[i][k] * dh : dh;
-            dg[k] = f[k] * s[k] * gate_slope(raw_get(gr[i], k), rest[i][k], a.logit);
+            const float g = raw_get(raw.g[i], k, run.shift, run.mask);
+            const Gate q = gate_of<LOGIT, MIX>(g, run);
+            const float dh = raw_get(raw.dy[i], k, run.shift, run.mask) + s[k];
+            s[k] = q.a * dh;
+            dx[k] = MIX ? q.rest * dh : dh;
+            dg[k] = f[k] * s[k] * gate_slope<LOGIT>(g, q.rest);
         }
         if (in) {
             store_row<XF, CPL>(a.dx, r * a.D + c, dx);
@@ -665,6 +690,57 @@ __global__ __launch_bounds__(kThreads) void scan_bwd_kernel(ScanArgs a, ScanPlan
             }
         }
     }
+}
+
+template <bool XF, bool GF, int CPL, bool FLAT, bool PACKED>
+__global__ __launch_bounds__(kThreads, bwd_waves(XF, GF, PACKED)) void scan_bwd_kernel(ScanArgs a, ScanPlan p) {
+    __shared__ __align__(16) Exchange<CPL> x;
+    __shared__ __align__(16) Kept<CPL, !PACKED> kept;
+    __shared__ uint32_t place;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t pl = take_place(p.counter, &place);
+    const int64_t total = rows_used<FLAT>(a);
+    const Tile t = tile_of<FLAT, true>(a, p, pl, total);
+    const int64_t c = t.col * 64 * CPL + lane * CPL;
+    const bool in = c < a.D;
+    const int64_t r0 = t.row0 + wave * kRows, last = t.rows > 0 ? t.row0 + t.rows - 1 : 0;
+    const int rows = rows_of_wave(t, wave);
+    const int64_t blocks = (a.D + kCkptBlock - 1) / kCkptBlock;
+
+    BackRows<XF, GF, CPL, PACKED> raw;
+    uint32_t scales[PACKED ? kRows : 1];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int64_t r = r0 + i < last ? r0 + i : last, cc = in ? c : 0, at = r * a.D + cc;
+        raw.g[i] = load_raw<GF, CPL>(a.g, at);
+        raw.dy[i] = load_raw<XF, CPL>(a.dy, at);
+        if constexpr (PACKED) {
+            if constexpr (CPL == 1) raw.code[i][0] = a.u[at];
+            else load_words<CPL / 4>(a.u + at, raw.code[i]);
+            scales[i] = a.us[r * blocks + cc / kCkptBlock];
+        } else {
+            raw.x[i] = load_raw<XF, CPL>(a.x, at);
+        }
+    }
+    if constexpr (PACKED) {
+#pragma unroll
+        for (int i = 0; i < kRows; i += 4)
+            raw.scale[i / 4] = scales[i] | scales[i + 1] << 8 | scales[i + 2] << 16 | scales[i + 3] << 24;
+    }
+    Marks m{0, 0, {}};
+    int64_t reach = t.at > 0 ? t.at : -1;
+    if constexpr (FLAT) {
+        m = marks_of(a, r0, rows);
+        reach = 0;
+        if (t.rows == kScanSeg) {  // segments on to the one where the sequence of the last row ends
+            const int64_t next = offset_of(a.cu, seq_of(a.cu, a.N, last) + 1), end = next < total ? next : total;
+            reach = end > last ? (end - 1) / kScanSeg - t.id : 0;
+        }
+    }
+    by_form(a, [&](auto logit, auto mix) {
+        bwd_body<decltype(logit)::value, decltype(mix)::value, XF, GF, CPL, FLAT, PACKED>(a, p, t, m, raw, rows, r0, c, in,
+                                                                                         reach, x, kept);
+    });
 }
 
 // Empties the published words and the counter; sequences without tokens pass their state through.
@@ -693,9 +769,11 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs a, const float*
     float v[CPL];
 #pragma unroll
     for (int k = 0; k < CPL; ++k) {
-        const Gate q = gate_of(raw_get(g, k), a.logit, a.complement);
         const float u = raw_get(x, k);
-        v[k] = fmaf(q.a, raw_get(h, k), a.complement ? q.rest * u : u);
+        by_form(a, [&](auto logit, auto mix) {
+            const Gate q = gate_of<decltype(logit)::value, decltype(mix)::value>(raw_get(g, k), Run());
+            v[k] = fmaf(q.a, raw_get(h, k), decltype(mix)::value ? q.rest * u : u);
+        });
     }
     store_row<XF, CPL>(a.y, i, v);
     store_row<true, CPL>(h_out, i, v);
@@ -737,8 +815,10 @@ void fwd(const ScanArgs& a, hipStream_t st) {
     const ScanPlan p = plan_of<CPL>(a, a.h0, a.h_final, st);
     if (a.total == 0) return;
     const dim3 grid(p.cols * p.chains * p.per_chain), block(kThreads);
-    if (a.cu) hipLaunchKernelGGL((scan_fwd_kernel<XF, GF, CPL, true>), grid, block, 0, st, a, p);
-    else hipLaunchKernelGGL((scan_fwd_kernel<XF, GF, CPL, false>), grid, block, 0, st, a, p);
+    if (a.u_out && a.cu) hipLaunchKernelGGL((scan_fwd_kernel<XF, GF, CPL, true, true>), grid, block, 0, st, a, p);
+    else if (a.u_out) hipLaunchKernelGGL((scan_fwd_kernel<XF, GF, CPL, false, true>), grid, block, 0, st, a, p);
+    else if (a.cu) hipLaunchKernelGGL((scan_fwd_kernel<XF, GF, CPL, true, false>), grid, block, 0, st, a, p);
+    else hipLaunchKernelGGL((scan_fwd_kernel<XF, GF, CPL, false, false>), grid, block, 0, st, a, p);
 }
 
 template <bool XF, bool GF, int CPL>
