@@ -14,7 +14,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libkda.so")
 OBJ_DIR = os.path.join(PKG, "_build")
 SOURCES = ["kda_api.hip", "kda_chunk.hip", "kda_chunk2.hip", "kda_fwd16.hip", "kda_decode.hip", "kda_bwd.hip",
-           "kda_calib.hip", "kda_ckpt8.hip", "kda_scan.hip", "kda_qknorm.hip"]
+           "kda_calib.hip", "kda_ckpt8.hip", "kda_scan.hip", "kda_scan_fwd_bf16.hip", "kda_scan_fwd_f32.hip",
+           "kda_scan_bwd_bf16.hip", "kda_scan_bwd_f32.hip", "kda_qknorm.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

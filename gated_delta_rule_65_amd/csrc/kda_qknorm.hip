@@ -5,6 +5,8 @@
 // only the row's sums cross lanes.  A workgroup takes a few whole tokens with all their heads: the angles, 64-bit products
 // with a sine and a cosine each, are made once a token and shared by its heads through LDS, while the first rows'
 // loads are in flight.  Both passes move their bytes once; what bounds them is HBM.
+#include <type_traits>
+
 #include "kda_ckpt8.h"
 #include "kda_layer_launch.h"
 
@@ -15,17 +17,22 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kAngles = 2048;  // pairs of a workgroup's tokens at most: 16 KiB of cosines and sines
 
-// The two chunks of eight channels that a lane of a row holds, such that both channels of every pair that is
-// turned are in one lane: lane j of D/16 holds channels first(j) .. +7 and second(j) .. +7.  In halves,
-// pair i is (i, i + rot/2); with adjacent pairs, and behind the turned channels, sixteen in a row.
+// The two chunks of eight channels that a lane of a row holds, such that both channels of every pair that is turned are in
+// one lane: lane j of D/16 holds channels first .. +7 and second .. +7.
+//   Spread (adjacent pairs, no rotation, or halves of the whole head): 8j and D/2 + 8j.  Pairs (2i, 2i + 1) lie in a
+//     chunk, pairs (i, i + D/2) in the two of a lane, and the lanes' chunks are side by side: whole lines at a time.
+//   Else (halves of part of the head, pairs (i, i + rot/2)): 8j and rot/2 + 8j for the lanes j < rot/16, and
+//     sixteen in a row for those behind the turned channels.
 struct Place {
     int first, second;
-    bool turned;  // in halves lane j holds pairs 8j .. +7, and so it does with adjacent pairs
+    bool turned0, turned1;  // the chunks lie in the turned channels
 };
+__host__ __device__ __forceinline__ bool is_spread(int D, int rot, bool interleaved) { return interleaved || rot == 0 || rot == D; }
+template <int D>
 __device__ __forceinline__ Place place_of(int j, int rot, bool interleaved) {
-    const bool t = j < rot / 16;
-    if (t && !interleaved) return {8 * j, rot / 2 + 8 * j, true};
-    return {16 * j, 16 * j + 8, t};
+    const bool spread = is_spread(D, rot, interleaved), half = spread || j < rot / 16;
+    const int first = (half ? 8 : 16) * j, apart = spread ? D / 2 : half ? rot / 2 : 8;
+    return {first, first + apart, first < rot, first + apart < rot};
 }
 
 // The sum over the lanes of a row (4 or 8 neighbours), the same bits in each of them.
@@ -70,78 +77,83 @@ __device__ __forceinline__ float row_rsqrt(const float x[16], float s, float eps
 }
 
 // Sixteen channels of a row as they come from memory: two chunks of eight.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 template <bool F32, bool PACKED>
 struct Chunks {
-    uint4 a[F32 ? 2 : 1], b[F32 ? 2 : 1];
+    u32x4 a[F32 ? 2 : 1], b[F32 ? 2 : 1];
 };
 template <bool F32>
 struct Chunks<F32, true> {
-    uint2 a, b;
+    u32x2 a, b;
     uint8_t sa, sb;
 };
-template <bool F32, bool PACKED>
+template <class T, bool STREAM>
+__device__ __forceinline__ T load_as(const void* p) {
+    if constexpr (STREAM) return __builtin_nontemporal_load(static_cast<const T*>(p));
+    else return *static_cast<const T*>(p);
+}
+template <bool STREAM, class T>
+__device__ __forceinline__ void store_as(void* p, T v) {
+    if constexpr (STREAM) __builtin_nontemporal_store(v, static_cast<T*>(p));
+    else *static_cast<T*>(p) = v;
+}
+template <bool STREAM, bool F32, bool PACKED>
 __device__ __forceinline__ void load_chunks(const void* p, const uint8_t* scales, int64_t row, const Place& at,
                                             Chunks<F32, PACKED>& c) {
     if constexpr (PACKED) {
         const uint8_t* s = static_cast<const uint8_t*>(p) + row;
-        c.a = *reinterpret_cast<const uint2*>(s + at.first);
-        c.b = *reinterpret_cast<const uint2*>(s + at.second);
+        c.a = load_as<u32x2, STREAM>(s + at.first);
+        c.b = load_as<u32x2, STREAM>(s + at.second);
         c.sa = scales[(row + at.first) / kCkptBlock];
         c.sb = scales[(row + at.second) / kCkptBlock];
     } else {
         const char* s = static_cast<const char*>(p) + row * (F32 ? 4 : 2);
 #pragma unroll
         for (int i = 0; i < (F32 ? 2 : 1); ++i) {
-            c.a[i] = *reinterpret_cast<const uint4*>(s + at.first * (F32 ? 4 : 2) + 16 * i);
-            c.b[i] = *reinterpret_cast<const uint4*>(s + at.second * (F32 ? 4 : 2) + 16 * i);
+            c.a[i] = load_as<u32x4, STREAM>(s + at.first * (F32 ? 4 : 2) + 16 * i);
+            c.b[i] = load_as<u32x4, STREAM>(s + at.second * (F32 ? 4 : 2) + 16 * i);
         }
     }
 }
 template <bool F32>
-__device__ __forceinline__ void chunk_values(const uint4* c, float x[8]) {
-    if constexpr (F32) {
-        x[0] = __uint_as_float(c[0].x); x[1] = __uint_as_float(c[0].y);
-        x[2] = __uint_as_float(c[0].z); x[3] = __uint_as_float(c[0].w);
-        x[4] = __uint_as_float(c[1].x); x[5] = __uint_as_float(c[1].y);
-        x[6] = __uint_as_float(c[1].z); x[7] = __uint_as_float(c[1].w);
-    } else {
-        const uint32_t u[4] = {c[0].x, c[0].y, c[0].z, c[0].w};
+__device__ __forceinline__ void chunk_values(const u32x4* c, float x[8]) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            x[2 * k] = __uint_as_float(u[k] << 16);
-            x[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
-        }
+    for (int k = 0; k < 8; ++k) {
+        if constexpr (F32) x[k] = __uint_as_float(c[k / 4][k % 4]);
+        else x[k] = __uint_as_float(k % 2 ? c[0][k / 2] & 0xffff0000u : c[0][k / 2] << 16);
     }
 }
 template <bool F32, bool PACKED>
 __device__ __forceinline__ void values_of(const Chunks<F32, PACKED>& c, float x[16]) {
     if constexpr (PACKED) {
         const float ua = ckpt_unit(c.sa), ub = ckpt_unit(c.sb);
-        ckpt_value4(c.a.x, ua, x);
-        ckpt_value4(c.a.y, ua, x + 4);
-        ckpt_value4(c.b.x, ub, x + 8);
-        ckpt_value4(c.b.y, ub, x + 12);
+        ckpt_value4(c.a[0], ua, x);
+        ckpt_value4(c.a[1], ua, x + 4);
+        ckpt_value4(c.b[0], ub, x + 8);
+        ckpt_value4(c.b[1], ub, x + 12);
     } else {
         chunk_values<F32>(c.a, x);
         chunk_values<F32>(c.b, x + 8);
     }
 }
-template <bool F32>
+template <bool STREAM, bool F32>
 __device__ __forceinline__ void store_chunks(void* p, int64_t row, const Place& at, const float x[16]) {
     if constexpr (F32) {
         float* d = static_cast<float*>(p) + row;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<float4*>(d + (i < 2 ? at.first : at.second) + 4 * (i & 1)) =
-                make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            store_as<STREAM>(d + (i < 2 ? at.first : at.second) + 4 * (i & 1),
+                             f32x4{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]});
     } else {
         typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
         bf8 u, v;
 #pragma unroll
         for (int k = 0; k < 8; ++k) u[k] = (__bf16)x[k], v[k] = (__bf16)x[8 + k];
         uint16_t* d = static_cast<uint16_t*>(p) + row;
-        *reinterpret_cast<bf8*>(d + at.first) = u;
-        *reinterpret_cast<bf8*>(d + at.second) = v;
+        store_as<STREAM>(d + at.first, u);
+        store_as<STREAM>(d + at.second, v);
     }
 }
 
@@ -154,33 +166,60 @@ __device__ __forceinline__ void angle(double pos, double freq, float& c, float& 
 }
 
 // The tables of a workgroup's tokens in LDS, in the order in which lanes read them: a lane's eight values of a token as two
-// 16-byte reads, the lanes of a row side by side.
+// 16-byte reads, the lanes of a row side by side.  With adjacent pairs that is the pairs' own order.
 template <int D>
 struct Tables {
     static constexpr int LANES = D / 16;
     float c[kAngles], s[kAngles];
     float w[2][D];
 
-    // value `pair` of a token with `lanes` turned lanes
-    static __device__ __forceinline__ int slot(int token, int pair, int lanes) {
-        return token * lanes * 8 + (pair & 4) * lanes + (pair >> 3) * 4 + (pair & 3);
+    // value `pair` of a token, rot/2 to a token
+    static __device__ __forceinline__ int slot(int token, int pair, int rot, bool interleaved) {
+        const int lanes = rot / 16;
+        return token * lanes * 8 + (interleaved ? pair : (pair & 4) * lanes + (pair >> 3) * 4 + (pair & 3));
     }
-    __device__ __forceinline__ void weights(const QkArgs& a) {
-        for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
-            const int side = i / D, at = i % D, m = at / (4 * LANES), j = at / 4 % LANES, k = (m & 1) * 4 + at % 4;
-            const Place p = place_of(j, a.rot, a.interleaved);
-            const float* src = side ? a.wk : a.wq;
-            w[side][at] = src ? src[(m < 2 ? p.first : p.second) + k] : 1.f;
+    // What the tables are made from is asked for before the rows, and used while those are on their way: loads come
+    // back in order.
+    struct Source {
+        double pos, freq;
+        float w;
+    };
+    static __device__ __forceinline__ double position(const QkArgs& a, int64_t t) {
+        return a.pos64 ? (double)static_cast<const int64_t*>(a.pos)[t] : (double)static_cast<const int32_t*>(a.pos)[t];
+    }
+    static __device__ __forceinline__ Source first_of(const QkArgs& a, int64_t t0, int tokens, bool weighted) {
+        Source s{0.0, 0.0, 1.f};
+        const int pairs = a.rot / 2, i = threadIdx.x;
+        if (i < tokens * pairs) {
+            const int t = (uint32_t)i / (uint32_t)pairs;
+            s.pos = position(a, t0 + t);
+            s.freq = a.freqs[i - t * pairs];
         }
+        if (weighted && i < 2 * D) s.w = weight_at(a, i);
+        return s;
     }
-    __device__ __forceinline__ void angles(const QkArgs& a, int64_t t0, int tokens) {
-        const int pairs = a.rot / 2, lanes = a.rot / 16;
+    static __device__ __forceinline__ float weight_at(const QkArgs& a, int i) {
+        const int side = i / D, at = i % D, m = at / (4 * LANES), j = at / 4 % LANES, k = (m & 1) * 4 + at % 4;
+        const Place p = place_of<D>(j, a.rot, a.interleaved);
+        const int first = p.first, second = p.second;
+        const float* src = side ? a.wk : a.wq;
+        return src ? src[(m < 2 ? first : second) + k] : 1.f;
+    }
+    __device__ __forceinline__ void fill_weights(float first) {
+        static_assert(2 * D <= kThreads, "a weight a thread");
+        if (threadIdx.x < 2 * D) (&w[0][0])[threadIdx.x] = first;
+    }
+    __device__ __forceinline__ void fill_angles(const QkArgs& a, int64_t t0, int tokens, const Source& first) {
+        const int pairs = a.rot / 2;
+        double pos = first.pos, freq = first.freq;
         for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
-            const int t = i / pairs, q = i - t * pairs;
-            const double pos = a.pos64 ? (double)static_cast<const int64_t*>(a.pos)[t0 + t]
-                                       : (double)static_cast<const int32_t*>(a.pos)[t0 + t];
-            const int at = slot(t, q, lanes);
-            angle(pos, a.freqs[q], c[at], s[at]);
+            const int t = (uint32_t)i / (uint32_t)pairs, q = i - t * pairs;
+            if (i != (int)threadIdx.x) {
+                pos = position(a, t0 + t);
+                freq = a.freqs[q];
+            }
+            const int at = slot(t, q, a.rot, a.interleaved);
+            angle(pos, freq, c[at], s[at]);
         }
     }
     __device__ __forceinline__ void weight(int side, int j, float v[16]) const {
@@ -190,45 +229,58 @@ struct Tables {
             v[4 * m] = u.x; v[4 * m + 1] = u.y; v[4 * m + 2] = u.z; v[4 * m + 3] = u.w;
         }
     }
-    // z = (x0 c - x1 s, x1 c + x0 s) on the lane's eight pairs; sign -1 turns back.
-    __device__ __forceinline__ void turn(float x[16], int token, int j, int lanes, bool interleaved, float sign) const {
-        float cv[8], sv[8];
+    __device__ __forceinline__ void four(int at, float cv[4], float sv[4]) const {
+        const float4 u = *reinterpret_cast<const float4*>(c + at), v = *reinterpret_cast<const float4*>(s + at);
+        cv[0] = u.x; cv[1] = u.y; cv[2] = u.z; cv[3] = u.w;
+        sv[0] = v.x; sv[1] = v.y; sv[2] = v.z; sv[3] = v.w;
+    }
+    // The four adjacent pairs of a chunk.
+    __device__ __forceinline__ void adjacent(float* x, int at, float sign) const {
+        float cv[4], sv[4];
+        four(at, cv, sv);
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-            const int at = token * lanes * 8 + m * 4 * lanes + 4 * j;
-            const float4 u = *reinterpret_cast<const float4*>(c + at), v = *reinterpret_cast<const float4*>(s + at);
-            cv[4 * m] = u.x; cv[4 * m + 1] = u.y; cv[4 * m + 2] = u.z; cv[4 * m + 3] = u.w;
-            sv[4 * m] = v.x; sv[4 * m + 1] = v.y; sv[4 * m + 2] = v.z; sv[4 * m + 3] = v.w;
+        for (int k = 0; k < 4; ++k) {
+            const float u = x[2 * k], v = x[2 * k + 1], t = sign * sv[k];
+            x[2 * k] = u * cv[k] - v * t;
+            x[2 * k + 1] = v * cv[k] + u * t;
         }
+        __asm__ volatile("; a chunk of adjacent pairs");
+    }
+    // z = (x0 c - x1 s, x1 c + x0 s) on the lane's pairs; sign -1 turns back.
+    __device__ __forceinline__ void turn(float x[16], int token, int j, const Place& p, int rot, bool interleaved,
+                                         float sign) const {
+        const int lanes = rot / 16, base = token * lanes * 8;
         if (interleaved) {
+            if (p.turned0) adjacent(x, base + p.first / 2, sign);
+            if (p.turned1) adjacent(x + 8, base + p.second / 2, sign);
+            __asm__ volatile("; adjacent pairs");  // keeps the two forms' ends apart: joined, they would put x into memory
+        } else if (p.turned0) {
+            float cv[8], sv[8];
+            four(base + 4 * j, cv, sv);
+            four(base + 4 * lanes + 4 * j, cv + 4, sv + 4);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                const float p = x[2 * k], q = x[2 * k + 1], t = sign * sv[k];
-                x[2 * k] = p * cv[k] - q * t;
-                x[2 * k + 1] = q * cv[k] + p * t;
+                const float u = x[k], v = x[8 + k], t = sign * sv[k];
+                x[k] = u * cv[k] - v * t;
+                x[8 + k] = v * cv[k] + u * t;
             }
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float p = x[k], q = x[8 + k], t = sign * sv[k];
-                x[k] = p * cv[k] - q * t;
-                x[8 + k] = q * cv[k] + p * t;
-            }
+            __asm__ volatile("; halves");
         }
     }
 };
 
-// The row's channels packed in 8 bits, from the raw values.  The lanes of a block: the quad of each chunk where pairs lie
-// half of the turned channels apart (in halves of whole blocks), two neighbours where the lane's channels follow one another;
-// other halves exchange each block's largest over the whole row.
+// The row's channels packed in 8 bits, from the raw values.  The lanes of a block: the quad of each chunk where chunks are
+// spread or halves are whole blocks, two neighbours where the lane's channels follow one another; other halves exchange
+// each block's largest over the whole row.
 template <int D>
 __device__ __forceinline__ void pack_row(const float x[16], const Place& p, int j, int rot, bool interleaved,
                                          uint8_t* codes, uint8_t* scales) {
     constexpr int LANES = D / 16, BLOCKS = D / kCkptBlock;
     int s0, s1;
     bool any0, any1;
-    if (interleaved || rot % 64 == 0) {
-        const bool halves = p.turned && !interleaved;
+    const bool spread = is_spread(D, rot, interleaved);
+    if (spread || rot % 64 == 0) {
+        const bool halves = spread || p.turned0;
         const auto tops = [&](uint32_t a, uint32_t b, uint32_t& t0, uint32_t& t1) {
             const uint32_t both = lanes_max<2>(max(a, b));
             t0 = halves ? lanes_max<4>(a) : both;
@@ -254,8 +306,8 @@ __device__ __forceinline__ void pack_row(const float x[16], const Place& p, int 
         }
     }
     const float i0 = ckpt_inverse(s0), i1 = ckpt_inverse(s1);
-    *reinterpret_cast<uint2*>(codes + p.first) = make_uint2(ckpt_code4(x, i0, any0), ckpt_code4(x + 4, i0, any0));
-    *reinterpret_cast<uint2*>(codes + p.second) = make_uint2(ckpt_code4(x + 8, i1, any1), ckpt_code4(x + 12, i1, any1));
+    *reinterpret_cast<u32x2*>(codes + p.first) = u32x2{ckpt_code4(x, i0, any0), ckpt_code4(x + 4, i0, any0)};
+    *reinterpret_cast<u32x2*>(codes + p.second) = u32x2{ckpt_code4(x + 8, i1, any1), ckpt_code4(x + 12, i1, any1)};
     // a block's first channels are the start of some lane's chunk
     if (p.first % kCkptBlock == 0) scales[p.first / kCkptBlock] = (uint8_t)s0;
     if (p.second % kCkptBlock == 0) scales[p.second / kCkptBlock] = (uint8_t)s1;
@@ -263,14 +315,16 @@ __device__ __forceinline__ void pack_row(const float x[16], const Place& p, int 
 
 // `per` tokens to a workgroup, their rows (queries, then keys, of a token) by passes of 256 / LANES; PASSES passes are
 // loaded before the first of them is used.
-template <int D, bool F32, bool PACKED>
-__global__ __launch_bounds__(kThreads) void qknorm_fwd_kernel(QkArgs a, int per) {
+template <int D, bool F32, bool PACKED, bool STREAM>
+__global__ __launch_bounds__(kThreads, 4) void qknorm_fwd_kernel(QkArgs a, int per) {
     constexpr int LANES = D / 16, ROWS = kThreads / LANES, PASSES = F32 ? 2 : 4;
     __shared__ __align__(16) Tables<D> tab;
     const int H = a.Hq + a.Hk, j = threadIdx.x % LANES;
-    const Place p = place_of(j, a.rot, a.interleaved);
+    const Place p = place_of<D>(j, a.rot, a.interleaved);
     const int64_t t0 = (int64_t)blockIdx.x * per;
     const int tokens = a.tokens - t0 < per ? (int)(a.tokens - t0) : per, rows = tokens * H;
+    const bool weighted = a.wq || a.wk;
+    const typename Tables<D>::Source source = Tables<D>::first_of(a, t0, tokens, weighted);
     for (int base = 0; base < rows; base += PASSES * ROWS) {
         Chunks<F32, PACKED> c[PASSES];
         int tok[PASSES], head[PASSES];
@@ -282,12 +336,12 @@ __global__ __launch_bounds__(kThreads) void qknorm_fwd_kernel(QkArgs a, int per)
             head[i] = r - tok[i] * H;
             const bool key = head[i] >= a.Hq;
             const int64_t t = t0 + tok[i];
-            if (key) load_chunks(a.k, a.ks, t * a.k_stride + (head[i] - a.Hq) * D, p, c[i]);
-            else load_chunks(a.q, a.qs, t * a.q_stride + head[i] * D, p, c[i]);
+            if (key) load_chunks<STREAM>(a.k, a.ks, t * a.k_stride + (head[i] - a.Hq) * D, p, c[i]);
+            else load_chunks<STREAM>(a.q, a.qs, t * a.q_stride + head[i] * D, p, c[i]);
         }
         if (base == 0) {
-            if (a.wq || a.wk) tab.weights(a);
-            tab.angles(a, t0, tokens);
+            if (weighted) tab.fill_weights(source.w);
+            tab.fill_angles(a, t0, tokens, source);
             __syncthreads();
         }
 #pragma unroll
@@ -305,34 +359,34 @@ __global__ __launch_bounds__(kThreads) void qknorm_fwd_kernel(QkArgs a, int per)
             const float r = row_rsqrt<LANES>(x, a.rms ? 1.f / D : 1.f, a.eps);
 #pragma unroll
             for (int k = 0; k < 16; ++k) x[k] *= r;
-            if (a.wq || a.wk) {
+            if (weighted) {
                 float w[16];
                 tab.weight(key, j, w);
 #pragma unroll
                 for (int k = 0; k < 16; ++k) x[k] *= w[k];
             }
-            if (p.turned) tab.turn(x, tok[i], j, a.rot / 16, a.interleaved, 1.f);
-            store_chunks<F32>(key ? a.k_out : a.q_out, out, p, x);
+            tab.turn(x, tok[i], j, p, a.rot, a.interleaved, 1.f);
+            store_chunks<STREAM, F32>(key ? a.k_out : a.q_out, out, p, x);
         }
     }
 }
 
 // Gradients of the rows, queries and keys in turn.  With weights, a workgroup goes on over the tokens with its lanes' sums
 // in registers and writes them, added up in LDS, to its line of the workspace.
-template <int D, bool F32, bool PACKED, bool GF32>
-__global__ __launch_bounds__(kThreads) void qknorm_bwd_kernel(QkArgs a, int per, int64_t tiles) {
+template <int D, bool F32, bool PACKED, bool GF32, bool STREAM>
+__global__ __launch_bounds__(kThreads, 3) void qknorm_bwd_kernel(QkArgs a, int per, int64_t tiles) {
     constexpr int LANES = D / 16, ROWS = kThreads / LANES, PASSES = 2;
     __shared__ __align__(16) Tables<D> tab;
     __shared__ __align__(16) float part[ROWS][D];
     const int j = threadIdx.x % LANES;
-    const Place p = place_of(j, a.rot, a.interleaved);
+    const Place p = place_of<D>(j, a.rot, a.interleaved);
     const float sc = a.rms ? 1.f / D : 1.f;
     const bool weighted = a.wq || a.wk || a.dwq;
-    if (weighted) tab.weights(a);
     float dw[2][16] = {};
     for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         const int64_t t0 = tile * per;
         const int tokens = a.tokens - t0 < per ? (int)(a.tokens - t0) : per;
+        const typename Tables<D>::Source source = Tables<D>::first_of(a, t0, tokens, weighted);
 #pragma unroll
         for (int side = 0; side < 2; ++side) {
             const int Hs = side ? a.Hk : a.Hq, rows = tokens * Hs;
@@ -350,12 +404,13 @@ __global__ __launch_bounds__(kThreads) void qknorm_bwd_kernel(QkArgs a, int per,
                     r = r < rows ? r : rows - 1;
                     tok[i] = (uint32_t)r / (uint32_t)Hs;
                     out[i] = (t0 * Hs + r) * D;
-                    load_chunks(src, scales, (t0 + tok[i]) * stride + (r - tok[i] * Hs) * D, p, c[i]);
-                    load_chunks(side ? a.d_k : a.d_q, nullptr, out[i], p, g[i]);
+                    load_chunks<STREAM>(src, scales, (t0 + tok[i]) * stride + (r - tok[i] * Hs) * D, p, c[i]);
+                    load_chunks<STREAM>(side ? a.d_k : a.d_q, nullptr, out[i], p, g[i]);
                 }
                 if (side == 0 && base == 0) {
                     __syncthreads();  // the tables of the tile before are done with
-                    tab.angles(a, t0, tokens);
+                    if (weighted) tab.fill_weights(source.w);
+                    tab.fill_angles(a, t0, tokens, source);
                     __syncthreads();
                 }
 #pragma unroll
@@ -365,7 +420,7 @@ __global__ __launch_bounds__(kThreads) void qknorm_bwd_kernel(QkArgs a, int per,
                     values_of(c[i], x);
                     values_of(g[i], d);
                     const float r = row_rsqrt<LANES>(x, sc, a.eps);
-                    if (p.turned) tab.turn(d, tok[i], j, a.rot / 16, a.interleaved, -1.f);
+                    tab.turn(d, tok[i], j, p, a.rot, a.interleaved, -1.f);
 #pragma unroll
                     for (int k = 0; k < 16; ++k) x[k] *= r;
                     if (weighted) {
@@ -383,7 +438,7 @@ __global__ __launch_bounds__(kThreads) void qknorm_bwd_kernel(QkArgs a, int per,
                     dot = row_sum<LANES>(dot) * sc;
 #pragma unroll
                     for (int k = 0; k < 16; ++k) x[k] = r * fmaf(-dot, x[k], d[k]);
-                    store_chunks<F32>(side ? a.dk : a.dq, out[i], p, x);
+                    store_chunks<STREAM, F32>(side ? a.dk : a.dq, out[i], p, x);
                 }
             }
         }
@@ -427,71 +482,76 @@ __global__ __launch_bounds__(1024) void qknorm_dw_kernel(const float* __restrict
     }
 }
 
-// Tokens of a workgroup: enough rows of their H heads to fill `passes` passes, as far as their angles fit.
-int tokens_of(int H, int D, int rot, int passes) {
+constexpr int kGroups = 1024;  // four workgroups a CU
+
+// Tokens of a workgroup: enough rows of their H heads to fill `passes` passes, as far as their angles fit and the card is
+// filled (4099 tokens of 12 + 2 fp32 heads, forward: 13 us in 216 workgroups, 8 us in 820).
+int tokens_of(int64_t tokens, int H, int D, int rot, int passes) {
     const int rows = passes * kThreads / (D / 16);
     int per = (rows + H - 1) / H;
     if (rot && per > kAngles / (rot / 2)) per = kAngles / (rot / 2);
-    return per;
-}
-
-constexpr int kBwdGroups = 1024;  // four workgroups a CU
-
-int64_t bwd_tiles(int64_t tokens, int Hq, int Hk, int D, int rot) {
-    const int per = tokens_of(Hq > Hk ? Hq : Hk, D, rot, 2);
-    return (tokens + per - 1) / per;
+    const int64_t share = (tokens + kGroups - 1) / kGroups;
+    return per < share ? per : share < 1 ? 1 : (int)share;
 }
 
 }  // namespace
 
 // At most as many lines as workgroups (rot only cuts the tiles smaller).
 int64_t qknorm_bwd_workspace_bytes(int64_t tokens, int, int, int D) {
-    return (tokens < kBwdGroups ? tokens : kBwdGroups) * 2 * D * 4;
+    return (tokens < kGroups ? tokens : kGroups) * 2 * D * 4;
+}
+
+// Whether a call's rows go past the caches: many bytes, and whole lines at a time (of a line that two instructions share each
+// would fetch it).
+static bool streams(const QkArgs& a, int64_t bytes_per_channel) {
+    return a.tokens * (a.Hq + a.Hk) * a.D * bytes_per_channel > kStreamBytes && is_spread(a.D, a.rot, a.interleaved);
+}
+
+template <int D, bool F32, bool PACKED, bool STREAM>
+static void fwd(const QkArgs& a, hipStream_t st, int64_t tiles, int per) {
+    hipLaunchKernelGGL((qknorm_fwd_kernel<D, F32, PACKED, STREAM>), dim3((unsigned)tiles), dim3(kThreads), 0, st, a, per);
+}
+template <int D, bool F32, bool PACKED, bool STREAM>
+static void bwd(const QkArgs& a, hipStream_t st, int64_t tiles, int per, int groups) {
+    const dim3 grid((unsigned)groups), block(kThreads);
+    if (a.grad_f32)
+        hipLaunchKernelGGL((qknorm_bwd_kernel<D, F32, PACKED, true, STREAM>), grid, block, 0, st, a, per, tiles);
+    else hipLaunchKernelGGL((qknorm_bwd_kernel<D, F32, PACKED, false, STREAM>), grid, block, 0, st, a, per, tiles);
+}
+// `f` with D, the rows' type, whether they are packed and whether they go past the caches.
+template <class F>
+static void by_kind(const QkArgs& a, bool stream, F f) {
+    typedef std::true_type Y;
+    typedef std::false_type N;
+    const auto with = [&](auto d, auto f32, auto packed) { stream ? f(d, f32, packed, Y()) : f(d, f32, packed, N()); };
+    const auto of = [&](auto d) {
+        if (a.f32) a.qs ? with(d, Y(), Y()) : with(d, Y(), N());
+        else a.qs ? with(d, N(), Y()) : with(d, N(), N());
+    };
+    if (a.D == 128) of(std::integral_constant<int, 128>());
+    else of(std::integral_constant<int, 64>());
 }
 
 hipError_t launch_qknorm_fwd(const QkArgs& a, hipStream_t st) {
-    const int per = tokens_of(a.Hq + a.Hk, a.D, a.rot, 4);
+    const int per = tokens_of(a.tokens, a.Hq + a.Hk, a.D, a.rot, 4);
     const int64_t tiles = (a.tokens + per - 1) / per;
     if (tiles > 0x7fffffff) return hipErrorInvalidConfiguration;
-    const dim3 grid((unsigned)tiles), block(kThreads);
-    const bool packed = a.qs != nullptr;
-#define KDA_FWD(DIM)                                                                                             \
-    if (a.f32 && packed) hipLaunchKernelGGL((qknorm_fwd_kernel<DIM, true, true>), grid, block, 0, st, a, per);   \
-    else if (a.f32) hipLaunchKernelGGL((qknorm_fwd_kernel<DIM, true, false>), grid, block, 0, st, a, per);       \
-    else if (packed) hipLaunchKernelGGL((qknorm_fwd_kernel<DIM, false, true>), grid, block, 0, st, a, per);      \
-    else hipLaunchKernelGGL((qknorm_fwd_kernel<DIM, false, false>), grid, block, 0, st, a, per);
-    if (a.D == 128) {
-        KDA_FWD(128)
-    } else {
-        KDA_FWD(64)
-    }
-#undef KDA_FWD
+    by_kind(a, streams(a, a.f32 ? 8 : 4), [&](auto d, auto f32, auto packed, auto stream) {
+        fwd<decltype(d)::value, decltype(f32)::value, decltype(packed)::value, decltype(stream)::value>(a, st, tiles, per);
+    });
     return hipGetLastError();
 }
 
-template <int D, bool GF32>
-static void launch_bwd_types(const QkArgs& a, int groups, int per, int64_t tiles, hipStream_t st) {
-    const dim3 grid((unsigned)groups), block(kThreads);
-    const bool packed = a.qs != nullptr;
-    if (a.f32 && packed) hipLaunchKernelGGL((qknorm_bwd_kernel<D, true, true, GF32>), grid, block, 0, st, a, per, tiles);
-    else if (a.f32) hipLaunchKernelGGL((qknorm_bwd_kernel<D, true, false, GF32>), grid, block, 0, st, a, per, tiles);
-    else if (packed) hipLaunchKernelGGL((qknorm_bwd_kernel<D, false, true, GF32>), grid, block, 0, st, a, per, tiles);
-    else hipLaunchKernelGGL((qknorm_bwd_kernel<D, false, false, GF32>), grid, block, 0, st, a, per, tiles);
-}
-
 hipError_t launch_qknorm_bwd(const QkArgs& a, hipStream_t st) {
-    const int per = tokens_of(a.Hq > a.Hk ? a.Hq : a.Hk, a.D, a.rot, 2);
-    const int64_t tiles = bwd_tiles(a.tokens, a.Hq, a.Hk, a.D, a.rot);
-    const int64_t most = a.dwq ? kBwdGroups : 0x7fffffff;
+    const int per = tokens_of(a.tokens, a.Hq > a.Hk ? a.Hq : a.Hk, a.D, a.rot, 2);
+    const int64_t tiles = (a.tokens + per - 1) / per;
+    const int64_t most = a.dwq ? kGroups : 0x7fffffff;
     const int groups = (int)(tiles < most ? tiles : most);
-    if (groups == 0) {  // no tokens: only the weights' zero gradients are written
-    } else if (a.D == 128) {
-        a.grad_f32 ? launch_bwd_types<128, true>(a, groups, per, tiles, st)
-                   : launch_bwd_types<128, false>(a, groups, per, tiles, st);
-    } else {
-        a.grad_f32 ? launch_bwd_types<64, true>(a, groups, per, tiles, st)
-                   : launch_bwd_types<64, false>(a, groups, per, tiles, st);
-    }
+    if (groups > 0)  // without tokens only the weights' zero gradients are written
+        by_kind(a, streams(a, (a.f32 ? 8 : 4) + (a.grad_f32 ? 4 : 2)), [&](auto d, auto f32, auto packed, auto stream) {
+            bwd<decltype(d)::value, decltype(f32)::value, decltype(packed)::value, decltype(stream)::value>(a, st, tiles, per,
+                                                                                                          groups);
+        });
     if (a.dwq)
         hipLaunchKernelGGL(qknorm_dw_kernel, dim3((unsigned)(2 * a.D / 32)), dim3(1024), 0, st,
                            static_cast<const float*>(a.ws), groups, a.D, a.dwq, a.dwk);

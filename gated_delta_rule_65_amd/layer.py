@@ -7,12 +7,13 @@ allocates outputs and workspaces with torch and passes pointers and torch's curr
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from typing import NamedTuple, Optional, Tuple
 
 import torch
 
-from . import (DTYPE, _check, _dtype_code, _need, _ptr, _stream, chunk_bwd, chunk_fwd, load_library)
+from . import DTYPE, _check, _need, _ptr, _stream, chunk_bwd, chunk_fwd, load_library
 
 NORM = {"l2": 0, "rms": 1}
 
@@ -48,6 +49,23 @@ def declare(L):
     for name, args in {"kda_scan_workspace_bytes": [i64] * 3, "kda_scan_carry_bytes": [i64] * 3,
                        "kda_qknorm_bwd_workspace_bytes": [i64, ci, ci, ci]}.items():
         getattr(L, name).argtypes, getattr(L, name).restype = args, sz
+
+
+def _launch(entry, device, *args):
+    """Call an entry point of the library with torch's current stream on `device` as its last argument."""
+    index = device.index
+    if index == _current_device():
+        status = entry(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(device):
+            status = entry(*args, _raw_stream(index))
+    if status != 0:
+        _check(status)
+
+
+# The host's share of a call of a few microseconds counts: torch's own short ways to these two, where it has them.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda index: _stream(torch.device("cuda", index)))
 
 
 def _same_device(device, **tensors):
@@ -103,10 +121,8 @@ def ckpt8_pack(x: torch.Tensor) -> Packed8:
         raise ValueError("x needs at least one dimension")
     cols = x.shape[-1]
     out = _empty8(x.shape, x.dtype, x.device)
-    with torch.cuda.device(x.device):
-        _check(load_library().kda_ckpt8_pack(_ptr(x), _ptr(out.codes), _ptr(out.scales),
-                                             x.numel() // cols if cols else 0, cols, DTYPE[x.dtype],
-                                             _stream(x.device)))
+    _launch(load_library().kda_ckpt8_pack, x.device, _ptr(x), _ptr(out.codes), _ptr(out.scales), x.numel() // cols if
+            cols else 0, cols, DTYPE[x.dtype])
     return out
 
 
@@ -118,9 +134,8 @@ def ckpt8_unpack(packed: Packed8, dtype: Optional[torch.dtype] = None) -> torch.
         raise TypeError(f"dtype must be float32 or bfloat16 (got {dtype})")
     cols, device = packed.codes.shape[-1], packed.codes.device
     x = torch.empty(packed.codes.shape, dtype=dtype, device=device)
-    with torch.cuda.device(device):
-        _check(load_library().kda_ckpt8_unpack(_ptr(packed.codes), _ptr(packed.scales), _ptr(x),
-                                               x.numel() // cols if cols else 0, cols, DTYPE[dtype], _stream(device)))
+    _launch(load_library().kda_ckpt8_unpack, device, _ptr(packed.codes), _ptr(packed.scales), _ptr(x), x.numel() //
+            cols if cols else 0, cols, DTYPE[dtype])
     return x
 
 
@@ -134,9 +149,14 @@ def scan_carry_bytes(N: int, total: int, D: int) -> int:
     return int(load_library().kda_scan_carry_bytes(N, total, D))
 
 
+@functools.lru_cache(maxsize=None)
 def _form(x_dtype, g_dtype, g_logit, complement):
-    return ctypes.byref(ScanForm(_dtype_code(x_dtype), _dtype_code(g_dtype), int(bool(g_logit)),
-                                 int(bool(complement))))
+    return ctypes.pointer(ScanForm(DTYPE[x_dtype], DTYPE[g_dtype], int(bool(g_logit)), int(bool(complement))))
+
+
+@functools.lru_cache(maxsize=256)
+def _qk_form(norm, eps, rot, interleaved, pos_bytes):
+    return ctypes.pointer(QkNormForm(NORM[norm], eps, rot, int(bool(interleaved)), pos_bytes))
 
 
 def _ws(need: int, workspace: Optional[torch.Tensor], device) -> Tuple[Optional[torch.Tensor], int]:
@@ -182,15 +202,14 @@ def _scan_fwd(x, g, cu, h0, g_logit, complement, output_final_state, save, works
         saved = u = _empty8((total, D), x.dtype, x.device)
     ws, ws_bytes = _ws(scan_workspace_bytes(N, total, D), workspace, x.device)
     u_ptrs = (_ptr(u.codes), _ptr(u.scales)) if u is not None else (None, None)
-    form = _form(x.dtype, g.dtype, g_logit, complement)
+    form = _form(x.dtype, g.dtype, bool(g_logit), bool(complement))
     L = load_library()
-    with torch.cuda.device(x.device):
-        if cu is None:
-            _check(L.kda_scan_fwd(_ptr(x), _ptr(g), _ptr(h0), _ptr(y), _ptr(hf), _ptr(carry), *u_ptrs, x.shape[0],
-                                  x.shape[1], D, form, _ptr(ws), ws_bytes, _stream(x.device)))
-        else:
-            _check(L.kda_scan_varlen_fwd(_ptr(x), _ptr(g), _ptr(cu), N, total, _ptr(h0), _ptr(y), _ptr(hf),
-                                         _ptr(carry), *u_ptrs, D, form, _ptr(ws), ws_bytes, _stream(x.device)))
+    if cu is None:
+        _launch(L.kda_scan_fwd, x.device, _ptr(x), _ptr(g), _ptr(h0), _ptr(y), _ptr(hf), _ptr(carry), *u_ptrs,
+                x.shape[0], x.shape[1], D, form, _ptr(ws), ws_bytes)
+    else:
+        _launch(L.kda_scan_varlen_fwd, x.device, _ptr(x), _ptr(g), _ptr(cu), N, total, _ptr(h0), _ptr(y), _ptr(hf),
+                _ptr(carry), *u_ptrs, D, form, _ptr(ws), ws_bytes)
     return y, hf, saved
 
 
@@ -246,17 +265,16 @@ def _scan_bwd(g, dy, cu, saved, x, h0, dh_final, g_logit, complement, workspace)
     dx, dg = torch.empty_like(dy), torch.empty_like(g)
     dh0 = torch.empty((N, *chans), dtype=torch.float32, device=dy.device)
     ws, ws_bytes = _ws(scan_workspace_bytes(N, total, D), workspace, dy.device)
-    form = _form(dy.dtype, g.dtype, g_logit, complement)
+    form = _form(dy.dtype, g.dtype, bool(g_logit), bool(complement))
     L = load_library()
-    with torch.cuda.device(dy.device):
-        if cu is None:
-            _check(L.kda_scan_bwd(_ptr(x), _ptr(g), _ptr(h0), _ptr(carry), _ptr(codes), _ptr(scales), _ptr(dy),
-                                  _ptr(dh_final), _ptr(dx), _ptr(dg), _ptr(dh0), dy.shape[0], dy.shape[1], D, form,
-                                  _ptr(ws), ws_bytes, _stream(dy.device)))
-        else:
-            _check(L.kda_scan_varlen_bwd(_ptr(x), _ptr(g), _ptr(cu), N, total, _ptr(h0), _ptr(carry), _ptr(codes),
-                                         _ptr(scales), _ptr(dy), _ptr(dh_final), _ptr(dx), _ptr(dg), _ptr(dh0), D,
-                                         form, _ptr(ws), ws_bytes, _stream(dy.device)))
+    if cu is None:
+        _launch(L.kda_scan_bwd, dy.device, _ptr(x), _ptr(g), _ptr(h0), _ptr(carry), _ptr(codes), _ptr(scales),
+                _ptr(dy), _ptr(dh_final), _ptr(dx), _ptr(dg), _ptr(dh0), dy.shape[0], dy.shape[1], D, form, _ptr(ws),
+                ws_bytes)
+    else:
+        _launch(L.kda_scan_varlen_bwd, dy.device, _ptr(x), _ptr(g), _ptr(cu), N, total, _ptr(h0), _ptr(carry),
+                _ptr(codes), _ptr(scales), _ptr(dy), _ptr(dh_final), _ptr(dx), _ptr(dg), _ptr(dh0), D, form, _ptr(ws),
+                ws_bytes)
     return dx, dg, dh0
 
 
@@ -292,10 +310,8 @@ def scan_step(x: torch.Tensor, g: torch.Tensor, state: torch.Tensor, *, inplace:
     _same_device(x.device, g=g, state=state)
     y = torch.empty_like(x)
     out = state if inplace else torch.empty_like(state)
-    with torch.cuda.device(x.device):
-        _check(load_library().kda_scan_step(_ptr(x), _ptr(g), _ptr(state), _ptr(out), _ptr(y), x.shape[0],
-                                            math.prod(x.shape[1:]), _form(x.dtype, g.dtype, g_logit, complement),
-                                            _stream(x.device)))
+    _launch(load_library().kda_scan_step, x.device, _ptr(x), _ptr(g), _ptr(state), _ptr(out), _ptr(y), x.shape[0],
+            math.prod(x.shape[1:]), _form(x.dtype, g.dtype, bool(g_logit), bool(complement)))
     return y, out
 
 
@@ -425,7 +441,7 @@ def _qk_inputs(q, k, weight_q, weight_k, pos, freqs, norm, eps, interleaved):
     if norm not in NORM:
         raise ValueError(f"norm must be one of {sorted(NORM)} (got {norm!r})")
     _same_device(qt.device, q_scales=qs, k=kt, k_scales=ks, weight_q=weight_q, weight_k=weight_k, pos=pos, freqs=freqs)
-    form = QkNormForm(NORM[norm], float(eps), rot, int(bool(interleaved)), pos_bytes)
+    form = _qk_form(norm, float(eps), rot, bool(interleaved), pos_bytes)
     args = (_ptr(qt), _ptr(kt), _ptr(qs), _ptr(ks), q_stride, k_stride, _ptr(weight_q), _ptr(weight_k), _ptr(pos),
             _ptr(freqs))
     return args, math.prod(lead), qt.shape[-2], kt.shape[-2], D, q_dtype, qt.device, form
@@ -454,9 +470,8 @@ def qk_norm_rope_fwd(q, k, *, weight_q: Optional[torch.Tensor] = None, weight_k:
             raise ValueError("q and k are packed already")
         saved = (_empty8(q.shape, dtype, device), _empty8(k.shape, dtype, device))
         ptrs = tuple(_ptr(t) for p in saved for t in p[:2])
-    with torch.cuda.device(device):
-        _check(load_library().kda_qknorm_fwd(*args, _ptr(q_out), _ptr(k_out), *ptrs, tokens, Hq, Hk, D, DTYPE[dtype],
-                                             ctypes.byref(form), _stream(device)))
+    _launch(load_library().kda_qknorm_fwd, device, *args, _ptr(q_out), _ptr(k_out), *ptrs, tokens, Hq, Hk, D,
+            DTYPE[dtype], form)
     return q_out, k_out, saved
 
 
@@ -480,10 +495,8 @@ def qk_norm_rope_bwd(q, k, d_q: torch.Tensor, d_k: torch.Tensor, *, weight_q: Op
     if weight_q is not None or weight_k is not None:
         dwq, dwk = (torch.empty(D, dtype=torch.float32, device=device) for _ in range(2))
         ws, ws_bytes = _ws(qk_norm_rope_workspace_bytes(tokens, Hq, Hk, D), workspace, device)
-    with torch.cuda.device(device):
-        _check(load_library().kda_qknorm_bwd(*args, _ptr(d_q), _ptr(d_k), _ptr(dq), _ptr(dk), _ptr(dwq), _ptr(dwk),
-                                             tokens, Hq, Hk, D, DTYPE[dtype], DTYPE[d_q.dtype], ctypes.byref(form),
-                                             _ptr(ws), ws_bytes, _stream(device)))
+    _launch(load_library().kda_qknorm_bwd, device, *args, _ptr(d_q), _ptr(d_k), _ptr(dq), _ptr(dk), _ptr(dwq),
+            _ptr(dwk), tokens, Hq, Hk, D, DTYPE[dtype], DTYPE[d_q.dtype], form, _ptr(ws), ws_bytes)
     return dq, dk, (dwq if weight_q is not None else None), (dwk if weight_k is not None else None)
 
 
