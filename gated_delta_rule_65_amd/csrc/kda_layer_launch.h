@@ -40,10 +40,12 @@ struct ScanArgs {
     float* dh0;
 };
 
-// Segments of 64 tokens: of each sequence where all are equally long (the last one of each may be
-// shorter), of the packed rows otherwise.
+// Segments of 64 tokens: of the packed rows, or of each sequence where all are equally long (the last one of each may be
+// shorter).  Sequences of less than half a segment are taken as packed rows: a segment each would leave most of a
+// workgroup without rows.
+inline bool scan_flat(const ScanArgs& a) { return a.cu || a.T_fixed < kScanSeg / 2; }
 inline int64_t scan_segments(const ScanArgs& a) {
-    return a.cu ? (a.total + kScanSeg - 1) / kScanSeg : a.N * ((a.T_fixed + kScanSeg - 1) / kScanSeg);
+    return scan_flat(a) ? (a.total + kScanSeg - 1) / kScanSeg : a.N * ((a.T_fixed + kScanSeg - 1) / kScanSeg);
 }
 int64_t scan_places(const ScanArgs& a);  // workgroups of a call
 int64_t scan_workspace_bytes(int64_t N, int64_t total, int64_t D);

@@ -194,17 +194,18 @@ __device__ __forceinline__ uint32_t take_place(uint32_t* counter, uint32_t* shar
     return (uint32_t)__builtin_amdgcn_readfirstlane((int)*shared);
 }
 
-// An offset of packed rows, read through the scalar cache (the kernels do not write them).
-__device__ __forceinline__ int64_t offset_of(const int32_t* cu, int64_t n) {
+// Where sequence n of packed rows begins; offsets are read through the scalar cache (the kernels do not write them).
+__device__ __forceinline__ int64_t offset_of(const ScanArgs& a, int64_t n) {
     typedef const __attribute__((address_space(4))) int32_t* scalar;
-    return ((scalar)cu)[__builtin_amdgcn_readfirstlane((int)n)];
+    return a.cu ? (int64_t)((scalar)a.cu)[__builtin_amdgcn_readfirstlane((int)n)] : n * a.T_fixed;
 }
-// The sequence that holds row r of packed rows: the last n with cu[n] <= r.
-__device__ __forceinline__ int64_t seq_of(const int32_t* cu, int64_t N, int64_t r) {
-    int lo = 0, hi = (int)N - 1;
+// The sequence that holds row r of packed rows: the last n that begins at r or before.
+__device__ __forceinline__ int64_t seq_of(const ScanArgs& a, int64_t r) {
+    if (!a.cu) return r / a.T_fixed;
+    int lo = 0, hi = (int)a.N - 1;
     while (lo < hi) {
         const int mid = lo + (hi - lo + 1) / 2;
-        if (offset_of(cu, mid) <= r) lo = mid;
+        if (offset_of(a, mid) <= r) lo = mid;
         else hi = mid - 1;
     }
     return lo;
@@ -246,43 +247,54 @@ __device__ __forceinline__ Pair await(const u64* at, u64 w) {
     return {__uint_as_float((uint32_t)(w >> 32)), __uint_as_float((uint32_t)w)};
 }
 
-// The pair of the segments of t.at's group before it, for channel c; the group's last segment publishes the group's.
-__device__ __forceinline__ Pair group_before(const ScanArgs& a, const ScanPlan& p, const Tile& t, int64_t c, Pair own) {
-    const int n = (int)(t.at % kGroup);
-    const u64* at = p.pairs + (t.chain * p.per_chain + t.at - n) * a.D + c;
-    u64 w[kGroup - 1];
+// What earlier segments have published for a channel, as far as a thread folds it: the pairs of the segments before t.at in
+// its group, or (OUTER) the pairs of the groups before it in its block and the state before the block.
+constexpr int kPeeked = kGroup - 1;
+static_assert(kBlock / kGroup - 1 == kPeeked, "as many groups in a block as segments in a group");
+struct Peeked {
+    const u64 *at, *state;  // state nullptr: none has a part in it
+    int n;
+    u64 w[kPeeked], ws;
+};
+// Reads what is there so far.  `reach` segments back at most have a part in the state (packed rows: those from the sequence's
+// first on).
+template <bool OUTER>
+__device__ __forceinline__ void peek_before(const ScanArgs& a, const ScanPlan& p, const Tile& t, int64_t c, int64_t reach,
+                                            Peeked& k) {
+    k.state = nullptr;
+    if constexpr (OUTER) {
+        const int64_t groups = (p.per_chain + kGroup - 1) / kGroup, blocks = (p.per_chain + kBlock - 1) / kBlock;
+        k.n = (int)(t.at / kGroup % (kPeeked + 1));
+        k.at = p.groups + (t.chain * groups + t.at / kGroup - k.n) * a.D + c;
+        if (t.at >= kBlock && t.at - reach < t.at / kBlock * kBlock)
+            k.state = p.states + (t.chain * blocks + t.at / kBlock - 1) * a.D + c;
+        k.ws = k.state ? peek(k.state) : 0;
+    } else {
+        k.n = (int)(t.at % kGroup);
+        k.at = p.pairs + (t.chain * p.per_chain + t.at - k.n) * a.D + c;
+    }
 #pragma unroll
-    for (int i = 0; i < kGroup - 1; ++i) w[i] = i < n ? peek(at + i * a.D) : 0;
-    Pair group = {1.f, 0.f};
+    for (int i = 0; i < kPeeked; ++i) k.w[i] = i < k.n ? peek(k.at + i * a.D) : 0;
+}
+__device__ __forceinline__ Pair fold(const ScanArgs& a, const Peeked& k) {
+    Pair all = {1.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < kGroup - 1; ++i)
-        if (i < n) group = then(group, await(at + i * a.D, w[i]));
-    if (n == kGroup - 1) {
+    for (int i = 0; i < kPeeked; ++i)
+        if (i < k.n) all = then(all, await(k.at + i * a.D, k.w[i]));
+    return all;
+}
+// The state before the group; the group's last segment publishes the group's pair.
+__device__ __forceinline__ float state_before_group(const ScanArgs& a, const Peeked& k) {
+    return apply(fold(a, k), k.state ? await(k.state, k.ws).b : 0.f);
+}
+__device__ __forceinline__ Pair group_before(const ScanArgs& a, const ScanPlan& p, const Tile& t, int64_t c, const Peeked& k,
+                                             Pair own) {
+    const Pair group = fold(a, k);
+    if (k.n == kPeeked) {
         const int64_t groups = (p.per_chain + kGroup - 1) / kGroup;
         publish(p.groups + (t.chain * groups + t.at / kGroup) * a.D + c, then(group, own));
     }
     return group;
-}
-
-// The state of channel c before t.at's group, from the groups of its block and the state before the block; `reach` segments
-// back at most have a part in it (packed rows: those from the sequence's first on).
-__device__ __forceinline__ float state_before_group(const ScanArgs& a, const ScanPlan& p, const Tile& t, int64_t c,
-                                                    int64_t reach) {
-    constexpr int most = kBlock / kGroup - 1;
-    const int64_t groups = (p.per_chain + kGroup - 1) / kGroup, blocks = (p.per_chain + kBlock - 1) / kBlock;
-    const int n = (int)(t.at / kGroup % (most + 1));
-    const bool further = t.at >= kBlock && t.at - reach < t.at / kBlock * kBlock;
-    const u64* at = p.groups + (t.chain * groups + t.at / kGroup - n) * a.D + c;
-    const u64* state = p.states + (t.chain * blocks + t.at / kBlock - 1) * a.D + c;
-    u64 w[most], ws = 0;
-    if (further) ws = peek(state);
-#pragma unroll
-    for (int i = 0; i < most; ++i) w[i] = i < n ? peek(at + i * a.D) : 0;
-    Pair before = {1.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < most; ++i)
-        if (i < n) before = then(before, await(at + i * a.D, w[i]));
-    return apply(before, further ? await(state, ws).b : 0.f);
 }
 
 // What the waves of a workgroup tell one another of its channels: their pairs, then the states before them, and
@@ -344,10 +356,16 @@ __device__ __forceinline__ void join_waves(const ScanArgs& a, const ScanPlan& p,
         if (reach < 0) own = {__uint_as_float(kBegins), apply(own, start ? start[c] : 0.f)};
         if (p.counter) {
             publish(p.pairs + (t.chain * p.per_chain + t.at) * a.D + c, own);
-            group = group_before(a, p, t, c, own);
+            Peeked k;
+            peek_before<false>(a, p, t, c, reach, k);
+            group = group_before(a, p, t, c, k, own);
         }
     }
-    if (part == 1 && mine && p.counter) x.before[ch] = state_before_group(a, p, t, c, reach);
+    if (part == 1 && mine && p.counter) {
+        Peeked k;
+        peek_before<true>(a, p, t, c, reach, k);
+        x.before[ch] = state_before_group(a, k);
+    }
     if (p.counter) __syncthreads();
     if (part != 0 || !mine) return;
     float s;
@@ -375,15 +393,15 @@ struct Marks {
 __device__ __forceinline__ Marks marks_of(const ScanArgs& a, int64_t r0, int rows) {
     Marks m{0, 0, {}};
     if (rows <= 0) return m;
-    int64_t n = seq_of(a.cu, a.N, r0);
-    int64_t next = offset_of(a.cu, n + 1);
-    bool begins = offset_of(a.cu, n) == r0;
+    int64_t n = seq_of(a, r0);
+    int64_t next = offset_of(a, n + 1);
+    bool begins = offset_of(a, n) == r0;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
         if (i < rows) {
             while (r0 + i >= next && n + 1 < a.N) {
                 ++n;
-                next = offset_of(a.cu, n + 1);
+                next = offset_of(a, n + 1);
                 begins = true;
             }
             m.n[i] = (int)n;
@@ -399,7 +417,7 @@ __device__ __forceinline__ Marks marks_of(const ScanArgs& a, int64_t r0, int row
 template <bool FLAT>
 __device__ __forceinline__ int64_t rows_used(const ScanArgs& a) {
     if constexpr (!FLAT) return a.total;
-    const int64_t used = offset_of(a.cu, a.N);
+    const int64_t used = offset_of(a, a.N);
     return used < 0 ? 0 : used < a.total ? used : a.total;
 }
 // Of the segment's rows, how many are the wave's.

@@ -57,8 +57,8 @@ int64_t words_of(int64_t chains, int64_t per_chain, int64_t D) {
 ScanPlan scan_plan(const ScanArgs& a, int cpl, const float* from, float* to, hipStream_t st) {
     ScanPlan p{};
     p.cols = (uint32_t)((a.D + 64 * cpl - 1) / (64 * cpl));
-    p.chains = a.cu ? 1 : (uint32_t)a.N;
-    p.per_chain = (uint32_t)(a.cu ? scan_segments(a) : (a.T_fixed + kScanSeg - 1) / kScanSeg);
+    p.chains = scan_flat(a) ? 1 : (uint32_t)a.N;
+    p.per_chain = (uint32_t)(scan_segments(a) / p.chains);
     int64_t words = 0;
     if (p.per_chain > 1) {
         p.counter = static_cast<uint32_t*>(a.ws);

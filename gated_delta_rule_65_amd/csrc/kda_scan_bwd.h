@@ -193,7 +193,7 @@ __global__ __launch_bounds__(kThreads, bwd_waves(XF, GF, PACKED)) void scan_bwd_
         m = marks_of(a, r0, rows);
         reach = 0;
         if (t.rows == kScanSeg) {  // segments on to the one where the sequence of the last row ends
-            const int64_t next = offset_of(a.cu, seq_of(a.cu, a.N, last) + 1), end = next < total ? next : total;
+            const int64_t next = offset_of(a, seq_of(a, last) + 1), end = next < total ? next : total;
             reach = end > last ? (end - 1) / kScanSeg - t.id : 0;
         }
     }
@@ -209,7 +209,7 @@ void bwd(const ScanArgs& a, hipStream_t st) {
     if (a.total == 0) return;
     const dim3 grid(p.cols * p.chains * p.per_chain), block(kThreads);
     const bool stream = a.total * a.D * ((XF ? 8 : 4) + (GF ? 8 : 4)) > kStreamBytes;
-    by_kind<CPL>(a.cu, a.u, stream, [&](auto flat, auto packed, auto s) {
+    by_kind<CPL>(scan_flat(a), a.u, stream, [&](auto flat, auto packed, auto s) {
         hipLaunchKernelGGL((scan_bwd_kernel<XF, GF, CPL, decltype(flat)::value, decltype(packed)::value, decltype(s)::value>),
                            grid, block, 0, st, a, p);
     });

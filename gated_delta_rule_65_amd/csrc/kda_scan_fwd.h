@@ -73,8 +73,8 @@ __device__ __forceinline__ void fwd_body(const ScanArgs& a, const ScanPlan& p, c
                 if constexpr (CPL == 1) {
                     *codes = (uint8_t)ckpt_code_any(u[0], inv);
                 } else {
-#pragma unroll
-                    for (int k = 0; k < CPL; k += 4) *reinterpret_cast<uint32_t*>(codes + k) = ckpt_code4(u + k, inv, any);
+                    static_assert(CPL == 1 || CPL == 4, "a word of codes");
+                    *reinterpret_cast<uint32_t*>(codes) = ckpt_code4(u, inv, any);
                 }
                 if (c % kCkptBlock == 0) a.us_out[r * blocks + c / kCkptBlock] = (uint8_t)s;
             }
@@ -125,7 +125,7 @@ __global__ __launch_bounds__(kThreads, fwd_waves(XF, GF)) void scan_fwd_kernel(S
         // segments back to the one where the sequence of the first row begins
         reach = 0;
         if (t.rows > 0) {
-            const int64_t begin = offset_of(a.cu, seq_of(a.cu, a.N, t.row0));
+            const int64_t begin = offset_of(a, seq_of(a, t.row0));
             reach = begin < t.row0 ? t.at - (begin < 0 ? 0 : begin) / kScanSeg : 0;
         }
     }
@@ -141,7 +141,7 @@ void fwd(const ScanArgs& a, hipStream_t st) {
     if (a.total == 0) return;
     const dim3 grid(p.cols * p.chains * p.per_chain), block(kThreads);
     const bool stream = a.total * a.D * ((XF ? 8 : 4) + (GF ? 4 : 2)) > kStreamBytes;
-    by_kind<CPL>(a.cu, a.u_out, stream, [&](auto flat, auto packed, auto s) {
+    by_kind<CPL>(scan_flat(a), a.u_out, stream, [&](auto flat, auto packed, auto s) {
         hipLaunchKernelGGL((scan_fwd_kernel<XF, GF, CPL, decltype(flat)::value, decltype(packed)::value, decltype(s)::value>),
                            grid, block, 0, st, a, p);
     });

@@ -69,8 +69,9 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda index: _stre
 
 
 def _same_device(device, **tensors):
+    index = device.index
     for name, t in tensors.items():
-        if t is not None and t.device != device:
+        if t is not None and t.get_device() != index:
             raise ValueError(f"{name} must be on {device} (got {t.device})")
 
 
@@ -384,7 +385,7 @@ def _token_stride(t: torch.Tensor, name: str) -> int:
     """Elements from one token to the next of [..., H, D] whose heads are contiguous and whose leading dimensions lie
     behind one another at one stride."""
     H, D = t.shape[-2:]
-    if t.numel() == 0:
+    if t.is_contiguous() or t.numel() == 0:
         return H * D
     if t.stride(-1) != 1 or (H > 1 and t.stride(-2) != D):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
@@ -424,9 +425,10 @@ def _qk_inputs(q, k, weight_q, weight_k, pos, freqs, norm, eps, interleaved):
     lead, D = tuple(qt.shape[:-2]), qt.shape[-1]
     if tuple(kt.shape[:-2]) != lead or kt.shape[-1] != D:
         raise ValueError(f"k has shape {tuple(kt.shape)}, expected {lead} tokens of heads of {D}")
-    for w, name in ((weight_q, "weight_q"), (weight_k, "weight_k")):
-        if w is not None:
-            _need(w, name, torch.float32, (D,))
+    if weight_q is not None:
+        _need(weight_q, "weight_q", torch.float32, (D,))
+    if weight_k is not None:
+        _need(weight_k, "weight_k", torch.float32, (D,))
     if (pos is None) != (freqs is None):
         raise ValueError("pos and freqs must both be given, or neither")
     rot, pos_bytes = 0, 0

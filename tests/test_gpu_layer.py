@@ -162,7 +162,8 @@ def check_scan(where, D, xk, gk, logit, mix, batch=None, cu=None, total=None, h0
 
 
 @pytest.mark.parametrize("D", [1, 36, 200])
-@pytest.mark.parametrize("B,T", [(1, 1), (3, 1), (2, 7), (5, 63), (1, 64), (2, 65), (3, 130), (1, 515), (2, 700)])
+@pytest.mark.parametrize("B,T", [(1, 1), (3, 1), (2, 7), (5, 63), (1, 64), (2, 65), (3, 130), (1, 515), (2, 700), (70, 1),
+                                 (40, 20), (23, 31), (4, 32), (300, 3)])
 def test_scan_batches(B, T, D):
     check_scan([(i * T, (i + 1) * T) for i in range(B)], D, "bf16", "bf16", D == 36, B % 2 == 1, batch=(B, T), h0=T != 7)
 
