@@ -143,6 +143,8 @@ kda_status check_ckpt8(int64_t rows, int64_t cols, kda_dtype dtype) {
     if (rows < 0 || cols < 0) return fail(KDA_ERR_BAD_SHAPE, "rows and cols must be >= 0");
     if (cols > 0 && rows > kMostElements / cols) return fail(KDA_ERR_BAD_SHAPE, "rows*cols exceeds 2^40");
     if (cols > 0x7fffffff) return fail(KDA_ERR_BAD_SHAPE, "cols must be below 2^31");
+    if (cols % 8 == 0 && rows * ((cols + 31) / 32) > kda::kMaxThreads - 256)  // a thread a block of 32 values
+        return fail(KDA_ERR_BAD_SHAPE, "rows*ceil(cols/32) exceeds the grid limit");
     return KDA_OK;
 }
 
@@ -188,7 +190,7 @@ kda_status scan_form(kda::ScanArgs& a, int64_t D, const kda_scan_form* f) {
 }
 
 kda_status scan_ws(kda::ScanArgs& a, void* ws, size_t bytes, const char* what) {
-    if (kda::scan_places(a) > 0x7fffffffLL)
+    if (kda::scan_places(a) > kda::kMaxThreads / kda::kScanThreads)
         return fail(KDA_ERR_BAD_SHAPE, "%s: %lld tokens of %lld channels exceed the grid limit", what,
                     (long long)a.total, (long long)a.D);
     const int64_t need = a.total ? kda::scan_workspace_bytes(a.N, a.total, a.D) : 0;
@@ -618,7 +620,7 @@ kda_status kda_scan_step(const void* x, const void* g, const float* h_in, float*
     kda_status st;
     kda::ScanArgs a{};
     if ((st = scan_batch(a, B, 1)) != KDA_OK || (st = scan_form(a, D, form)) != KDA_OK) return st;
-    if (B * D > (int64_t(1) << 38)) return fail(KDA_ERR_BAD_SHAPE, "B*D exceeds the grid limit");
+    if (B * D / (B * D % 4 ? 1 : 4) > kda::kMaxThreads - 256) return fail(KDA_ERR_BAD_SHAPE, "B*D exceeds the grid limit");
     const bool any = B > 0;
     if ((st = check_ptrs({{x, "x", any}, {g, "g", any}, {h_in, "h_in", any}, {h_out, "h_out", any},
                           {y, "y", any}})) != KDA_OK)

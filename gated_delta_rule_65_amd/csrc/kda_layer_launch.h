@@ -10,6 +10,9 @@ namespace kda {
 // 4099 x 14 x 64 fp32, forward: 13 us through the caches, 20 past them; backward of 32768 x 32 x 128 bf16: 157 and 141).
 constexpr int64_t kStreamBytes = int64_t(128) << 20;
 
+// Threads of a launch: its size is a 32-bit number of them.
+constexpr int64_t kMaxThreads = 0xffffffffLL;
+
 // ---- checkpoints in 8 bits (kda_ckpt8.hip)
 hipError_t launch_ckpt8_pack(const void* x, uint8_t* codes, uint8_t* scales, int64_t rows, int64_t cols, bool f32,
                              hipStream_t st);
@@ -18,6 +21,7 @@ hipError_t launch_ckpt8_unpack(const uint8_t* codes, const uint8_t* scales, void
 
 // ---- gated scan (kda_scan.hip)
 constexpr int kScanSeg = 64;  // tokens of a segment
+constexpr int kScanThreads = 512;
 constexpr int64_t kMaxChannels = 1 << 24;
 
 struct ScanArgs {

@@ -14,6 +14,14 @@
 // are read about 8 times, from the cache behind the L2s.  What waits is a chain of one hop for each 4096 tokens.
 // All sums are in a fixed order, so results do not depend on the timing.
 //
+// Why this size: 64 tokens give 4096 workgroups at B = 4, T = 8192, D = 2048, several to each place on the card, and 64
+// pairs of 8 bytes against 64 rows of 2 or 4 each way; a workgroup that goes on over several segments and asks for the next
+// one's rows early was slower (152 us against 98), since those who wait for its tiles wait for tiles not begun.  256
+// channels a row (CPL = 4: 8 or 16 bytes a lane) and 512 do the same (98.1 and 98.9 us).
+// What bounds it: HBM, at the rate that this pattern of rows reaches (84 us for the 403 MB of that call when rows are
+// moved and nothing else; a plain copy takes 64), then 10 to 15 us in which segments wait for earlier ones (35 in one
+// long sequence), the counter (2 us) and the emptying of the words in front (4 to 8 us).
+//
 // Why every wait ends: a workgroup takes its place in the order of work from a counter when it starts, and only waits for
 // segments whose places were taken earlier, by workgroups that are therefore running or done.  The one
 // with the lowest place among those not done waits for nobody.
@@ -39,8 +47,8 @@ struct ScanPlan {
 
 namespace {
 
-constexpr int kWaves = 8, kRows = 8, kThreads = kWaves * 64;
-static_assert(kWaves * kRows == kScanSeg, "a wave's rows");
+constexpr int kWaves = 8, kRows = 8, kThreads = kScanThreads;
+static_assert(kWaves * kRows == kScanSeg && kWaves * 64 == kThreads, "a wave's rows");
 constexpr int kGroup = 8, kBlock = 64;  // segments of a group and of a block
 
 // ---------------------------------------------------------------------------- rows in registers

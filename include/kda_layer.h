@@ -30,7 +30,7 @@ extern "C" {
  * 1.875 * 2^127 are packed as that, so that they do not unpack to infinity.
  */
 
-/* x [rows, cols] dtype -> codes [rows, cols], scales [rows, ceil(cols / 32)]. */
+/* x [rows, cols] dtype -> codes [rows, cols], scales [rows, ceil(cols / 32)]; cols below 2^31. */
 kda_status kda_ckpt8_pack(const void* x, uint8_t* codes, uint8_t* scales, int64_t rows, int64_t cols,
                           kda_dtype dtype, void* stream);
 
@@ -44,9 +44,9 @@ kda_status kda_ckpt8_unpack(const uint8_t* codes, const uint8_t* scales, void* x
  *     l_t = clamp(g_t, -5, 0), or clamp(-softplus(g_t), -5, 0) with g_logit;   a_t = e^(l_t)
  *     h_t = a_t h_{t-1} + w_t x_t,    w_t = 1, or 1 - a_t with complement;     y_t = h_t
  * x, g, y: [B, T, D] (or [total, D] packed); h0, h_final: [B, D] (or [N, D]) float32.  y has x's
- * type and is rounded once; the state is float32 throughout.  D is any number of channels, heads
- * and their sizes flattened; D % 4 == 0 takes wide loads.  A non-finite x or g makes the rest of its own
- * sequence and channel non-finite and touches nothing else.
+ * type and is rounded once; the state is float32 throughout.  D is any number of channels up
+ * to 2^24, heads and their sizes flattened; D % 4 == 0 takes wide loads.  A non-finite x or g makes the
+ * rest of its own sequence and channel non-finite and touches nothing else.
  */
 typedef struct {
     kda_dtype x_dtype;  /* x, y, dy, dx */

@@ -338,6 +338,30 @@ def test_scan_bits_streams_and_graphs():
         assert torch.equal(out[0], want[0]) == (i % 2 == 0)
 
 
+def test_scans_on_two_streams_at_once():
+    """Workgroups of one call wait only for others of that call: two that share the card end with the bits of each alone."""
+    B, T, D = 2, 8192, 1024
+    data = [scan_data(B * T, D, B, False, seed, "bf16", "bf16")[0] for seed in (31, 32)]
+
+    def step(d):
+        x, g, dy = (d[k].reshape(B, T, D) for k in ("x", "g", "dy"))
+        y, h, s = kda.scan_fwd(x, g, d["h0"], save="carry")
+        return (y, h, *kda.scan_bwd(g, dy, s, x=x, h0=d["h0"], dh_final=d["dh"]))
+
+    want = [step(d) for d in data]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in data]
+    got = [[], []]
+    for _ in range(4):
+        for i, d in enumerate(data):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(step(d))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for out in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(out, want[i]))
+
+
 @pytest.mark.parametrize("ckpt8", [False, True])
 @pytest.mark.parametrize("packed", [False, True])
 def test_scan_autograd(ckpt8, packed):

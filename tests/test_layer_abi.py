@@ -38,6 +38,7 @@ PACK = dict(x=FAKE, codes=FAKE, scales=FAKE, rows=3, cols=40, dtype=1, stream=No
 @pytest.mark.parametrize("kw,status,msg", [
     (dict(x=None), 1, "x"), (dict(codes=None), 1, "codes"), (dict(scales=None), 1, "scales"),
     (dict(rows=-1), 2, "rows"), (dict(cols=-1), 2, "cols"), (dict(rows=1 << 40, cols=2), 2, "2^40"), (dict(rows=1, cols=1 << 31), 2, "2^31"),
+    (dict(rows=1 << 32, cols=8), 2, "grid limit"), (dict(rows=1 << 28, cols=512), 2, "grid limit"),
     (dict(dtype=2), 3, "dtype"), (dict(codes=FAKE + 1), 4, "codes"), (dict(x=FAKE + 8), 4, "x"),
 ])
 def test_ckpt8_validation(name, kw, status, msg):
@@ -101,6 +102,12 @@ def test_scan_validation(name, defaults, kw, status, msg):
     ("kda_scan_step", STEP, dict(form=None), 1, "form"), ("kda_scan_step", STEP, dict(y=None), 1, "y"),
     ("kda_scan_step", STEP, dict(h_in=None), 1, "h_in"), ("kda_scan_step", STEP, dict(h_out=FAKE + 16), 2, "overlap"),
     ("kda_scan_step", STEP, dict(B=-1), 2, "B"), ("kda_scan_step", STEP, dict(D=0), 2, "D"),
+    # launches of 2^32 threads and more: 512 to 64 tokens of 64 channels, or of 256 where D % 4 == 0; a thread to a
+    # value of a step, or to 4
+    ("kda_scan_fwd", FWD, dict(B=1, T=1 << 29, D=1), 2, "grid limit"),
+    ("kda_scan_varlen_bwd", VBWD, dict(total=1 << 29, D=257 * 4), 2, "grid limit"),
+    ("kda_scan_step", STEP, dict(B=(1 << 16) + 1, D=(1 << 16) + 1), 2, "grid limit"),
+    ("kda_scan_step", STEP, dict(B=1 << 18, D=1 << 16), 2, "grid limit"),
 ])
 def test_scan_entry_validation(name, defaults, kw, status, msg):
     expect(name, defaults, kw, status, msg)
