@@ -10,10 +10,10 @@
 // dw = the sum over rows of (d turned back) z^.
 //
 // Measured (q and k of 16 heads of 128 bf16 channels, 32768 tokens): forward, half of the channels turned, columns of one
-// projection, 537 MB in 101 us (5.3 TB/s); forward with the raw rows packed in 8 bits beside, 675 MB in 110 us (6.1
-// TB/s); backward from the packed rows with the weights' gradients, 675 MB in 145 us (4.7 TB/s; its three workgroups a CU
+// projection, 537 MB in 101 us (5.3 TB/s); forward with the raw rows packed in 8 bits beside, 675 MB in 108 us (6.2
+// TB/s); backward from the packed rows with the weights' gradients, 675 MB in 121 us (5.6 TB/s; its three workgroups a CU
 // stop at each tile's tables) and 5 us for the weights' sums.  4099 tokens of 12 + 2 heads of 64 fp32 channels: 9.4 us
-// forward and 19 backward for 59 MB in all; 32 tokens: 4.4 us, one pass of latency.
+// forward and 14 backward for 74 MB in all; 32 tokens: 4.4 us, one pass of latency.
 #include <type_traits>
 
 #include "kda_ckpt8.h"
@@ -30,8 +30,8 @@ constexpr int kAngles = 2048;  // pairs of a workgroup's tokens at most: 16 KiB 
 // one lane: lane j of D/16 holds channels first .. +7 and second .. +7.
 //   Spread (adjacent pairs, no rotation, or halves of the whole head): 8j and D/2 + 8j.  Pairs (2i, 2i + 1) lie in a
 //     chunk, pairs (i, i + D/2) in the two of a lane, and the lanes' chunks are side by side: whole lines at a time.
-//   Else (halves of part of the head, pairs (i, i + rot/2)): 8j and rot/2 + 8j for the lanes j < rot/16, and
-//     sixteen in a row for those behind the turned channels.
+//   Else (halves of part of the head, pairs (i, i + rot/2)): 8j and rot/2 + 8j for the lanes j < rot/16, and the channels
+//     behind in the same way for those after them.
 struct Place {
     int first, second;
     bool turned0, turned1;  // the chunks lie in the turned channels
@@ -40,7 +40,7 @@ __host__ __device__ __forceinline__ bool is_spread(int D, int rot, bool interlea
 template <int D>
 __device__ __forceinline__ Place place_of(int j, int rot, bool interleaved) {
     const bool spread = is_spread(D, rot, interleaved), half = spread || j < rot / 16;
-    const int first = (half ? 8 : 16) * j, apart = spread ? D / 2 : half ? rot / 2 : 8;
+    const int first = 8 * j + (half ? 0 : rot / 2), apart = spread ? D / 2 : half ? rot / 2 : (D - rot) / 2;
     return {first, first + apart, first < rot, first + apart < rot};
 }
 
@@ -279,27 +279,21 @@ struct Tables {
 };
 
 // The row's channels packed in 8 bits, from the raw values.  The lanes of a block: the quad of each chunk where chunks are
-// spread or halves are whole blocks, two neighbours where the lane's channels follow one another; other halves exchange
-// each block's largest over the whole row.
+// spread or halves are whole blocks; other halves exchange each block's largest over the whole row.
 template <int D>
 __device__ __forceinline__ void pack_row(const float x[16], const Place& p, int j, int rot, bool interleaved,
                                          uint8_t* codes, uint8_t* scales) {
     constexpr int LANES = D / 16, BLOCKS = D / kCkptBlock;
     int s0, s1;
     bool any0, any1;
-    const bool spread = is_spread(D, rot, interleaved);
-    if (spread || rot % 64 == 0) {
-        const bool halves = spread || p.turned0;
-        const auto tops = [&](uint32_t a, uint32_t b, uint32_t& t0, uint32_t& t1) {
-            const uint32_t both = lanes_max<2>(max(a, b));
-            t0 = halves ? lanes_max<4>(a) : both;
-            t1 = halves ? lanes_max<4>(b) : both;
-        };
-        uint32_t t0, t1;
-        tops(ckpt_amax<8>(x), ckpt_amax<8>(x + 8), t0, t1);
+    if (is_spread(D, rot, interleaved) || rot % 64 == 0) {
+        uint32_t t0 = lanes_max<4>(ckpt_amax<8>(x)), t1 = lanes_max<4>(ckpt_amax<8>(x + 8));
         any0 = t0 > kCkptTopBits;
         any1 = t1 > kCkptTopBits;
-        if (__any(any0 || any1)) tops(ckpt_amax_finite<8>(x), ckpt_amax_finite<8>(x + 8), t0, t1);
+        if (__any(any0 || any1)) {
+            t0 = lanes_max<4>(ckpt_amax_finite<8>(x));
+            t1 = lanes_max<4>(ckpt_amax_finite<8>(x + 8));
+        }
         s0 = ckpt_scale(t0);
         s1 = ckpt_scale(t1);
     } else {
@@ -380,10 +374,18 @@ __global__ __launch_bounds__(kThreads, 4) void qknorm_fwd_kernel(QkArgs a, int p
     }
 }
 
-// Gradients of the rows, queries and keys in turn.  With weights, a workgroup goes on over the tokens with its lanes' sums
-// in registers and writes them, added up in LDS, to its line of the workspace.
+// The tokens' queries by tiles of per[0] tokens, then their keys by tiles of per[1].
+struct Sides {
+    int per[2];
+    int64_t tiles[2];
+};
+
+// Gradients of the rows.  With weights, a workgroup goes on over the tiles with its lanes' sums in registers and writes them,
+// added up in LDS, to its line of the workspace: queries' when it comes to the keys, keys' at the end.  One side's sums at a
+// time and as many workgroups as fit at once: with both sides' sums the registers spilled, and of 1024 workgroups
+// the last 256 ran alone (145 us against 121 for the call below; tiles of 2, 4, 8 or 16 passes: 124, 121, 122 and 130).
 template <int D, bool F32, bool PACKED, bool GF32, bool STREAM>
-__global__ __launch_bounds__(kThreads, 3) void qknorm_bwd_kernel(QkArgs a, int per, int64_t tiles) {
+__global__ __launch_bounds__(kThreads, 3) void qknorm_bwd_kernel(QkArgs a, Sides sides) {
     constexpr int LANES = D / 16, ROWS = kThreads / LANES, PASSES = 2;
     __shared__ __align__(16) Tables<D> tab;
     __shared__ __align__(16) float part[ROWS][D];
@@ -391,84 +393,89 @@ __global__ __launch_bounds__(kThreads, 3) void qknorm_bwd_kernel(QkArgs a, int p
     const Place p = place_of<D>(j, a.rot, a.interleaved);
     const float sc = a.rms ? 1.f / D : 1.f;
     const bool weighted = a.wq || a.wk || a.dwq;
-    float dw[2][16] = {};
-    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const int64_t t0 = tile * per;
-        const int tokens = a.tokens - t0 < per ? (int)(a.tokens - t0) : per;
+    float* line = static_cast<float*>(a.ws) + (int64_t)blockIdx.x * 2 * D;
+    float dw[16] = {};
+    int at = 0;  // the side whose sums dw holds
+    const auto flush = [&] {
+        if (a.dwq) {
+            __syncthreads();
+            float* mine = part[threadIdx.x / LANES];
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+                *reinterpret_cast<float4*>(mine + (m < 2 ? p.first : p.second) + 4 * (m & 1)) =
+                    make_float4(dw[4 * m], dw[4 * m + 1], dw[4 * m + 2], dw[4 * m + 3]);
+            __syncthreads();
+            if (threadIdx.x < D) {
+                float sum = 0.f;
+                for (int i = 0; i < ROWS; ++i) sum += part[i][threadIdx.x];
+                line[at * D + threadIdx.x] = sum;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) dw[k] = 0.f;
+        ++at;
+    };
+    for (int64_t tile = blockIdx.x; tile < sides.tiles[0] + sides.tiles[1]; tile += gridDim.x) {
+        const int side = tile >= sides.tiles[0];
+        if (side != at) flush();
+        const int per = sides.per[side], Hs = side ? a.Hk : a.Hq;
+        const int64_t t0 = (tile - (side ? sides.tiles[0] : 0)) * per;
+        const int tokens = a.tokens - t0 < per ? (int)(a.tokens - t0) : per, rows = tokens * Hs;
         const typename Tables<D>::Source source = Tables<D>::first_of(a, t0, tokens, weighted);
+        const void *src = side ? a.k : a.q, *grad = side ? a.d_k : a.d_q;
+        const uint8_t* scales = side ? a.ks : a.qs;
+        void* to = side ? a.dk : a.dq;
+        const int64_t stride = side ? a.k_stride : a.q_stride;
+        for (int base = 0; base < rows; base += PASSES * ROWS) {
+            Chunks<F32, PACKED> c[PASSES];
+            Chunks<GF32, false> g[PASSES];
+            int tok[PASSES];
+            int64_t out[PASSES];
 #pragma unroll
-        for (int side = 0; side < 2; ++side) {
-            const int Hs = side ? a.Hk : a.Hq, rows = tokens * Hs;
-            const void* src = side ? a.k : a.q;
-            const uint8_t* scales = side ? a.ks : a.qs;
-            const int64_t stride = side ? a.k_stride : a.q_stride;
-            for (int base = 0; base < rows; base += PASSES * ROWS) {
-                Chunks<F32, PACKED> c[PASSES];
-                Chunks<GF32, false> g[PASSES];
-                int tok[PASSES];
-                int64_t out[PASSES];
+            for (int i = 0; i < PASSES; ++i) {
+                int r = base + i * ROWS + threadIdx.x / LANES;
+                r = r < rows ? r : rows - 1;
+                tok[i] = (uint32_t)r / (uint32_t)Hs;
+                out[i] = (t0 * Hs + r) * D;
+                load_chunks<STREAM>(src, scales, (t0 + tok[i]) * stride + (r - tok[i] * Hs) * D, p, c[i]);
+                load_chunks<STREAM>(grad, nullptr, out[i], p, g[i]);
+            }
+            if (base == 0) {
+                __syncthreads();  // the tables of the tile before are done with
+                if (weighted) tab.fill_weights(source.w);
+                tab.fill_angles(a, t0, tokens, source);
+                __syncthreads();
+            }
 #pragma unroll
-                for (int i = 0; i < PASSES; ++i) {
-                    int r = base + i * ROWS + threadIdx.x / LANES;
-                    r = r < rows ? r : rows - 1;
-                    tok[i] = (uint32_t)r / (uint32_t)Hs;
-                    out[i] = (t0 * Hs + r) * D;
-                    load_chunks<STREAM>(src, scales, (t0 + tok[i]) * stride + (r - tok[i] * Hs) * D, p, c[i]);
-                    load_chunks<STREAM>(side ? a.d_k : a.d_q, nullptr, out[i], p, g[i]);
-                }
-                if (side == 0 && base == 0) {
-                    __syncthreads();  // the tables of the tile before are done with
-                    if (weighted) tab.fill_weights(source.w);
-                    tab.fill_angles(a, t0, tokens, source);
-                    __syncthreads();
-                }
+            for (int i = 0; i < PASSES; ++i) {
+                if (base + i * ROWS + (int)threadIdx.x / LANES >= rows) continue;
+                float x[16], d[16];
+                values_of(c[i], x);
+                values_of(g[i], d);
+                const float r = row_rsqrt<LANES>(x, sc, a.eps);
+                tab.turn(d, tok[i], j, p, a.rot, a.interleaved, -1.f);
 #pragma unroll
-                for (int i = 0; i < PASSES; ++i) {
-                    if (base + i * ROWS + (int)threadIdx.x / LANES >= rows) continue;
-                    float x[16], d[16];
-                    values_of(c[i], x);
-                    values_of(g[i], d);
-                    const float r = row_rsqrt<LANES>(x, sc, a.eps);
-                    tab.turn(d, tok[i], j, p, a.rot, a.interleaved, -1.f);
+                for (int k = 0; k < 16; ++k) x[k] *= r;
+                if (weighted) {
+                    float w[16];
+                    tab.weight(side, j, w);
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) x[k] *= r;
-                    if (weighted) {
-                        float w[16];
-                        tab.weight(side, j, w);
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            dw[side][k] = fmaf(d[k], x[k], dw[side][k]);
-                            d[k] *= w[k];
-                        }
+                    for (int k = 0; k < 16; ++k) {
+                        dw[k] = fmaf(d[k], x[k], dw[k]);
+                        d[k] *= w[k];
                     }
-                    float dot = 0.f;
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) dot = fmaf(d[k], x[k], dot);
-                    dot = row_sum<LANES>(dot) * sc;
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) x[k] = r * fmaf(-dot, x[k], d[k]);
-                    store_chunks<STREAM, F32>(side ? a.dk : a.dq, out[i], p, x);
                 }
+                float dot = 0.f;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) dot = fmaf(d[k], x[k], dot);
+                dot = row_sum<LANES>(dot) * sc;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) x[k] = r * fmaf(-dot, x[k], d[k]);
+                store_chunks<STREAM, F32>(to, out[i], p, x);
             }
         }
     }
-    if (!a.dwq) return;
-    float* line = static_cast<float*>(a.ws) + (int64_t)blockIdx.x * 2 * D;
-#pragma unroll
-    for (int side = 0; side < 2; ++side) {
-        __syncthreads();
-        float* mine = part[threadIdx.x / LANES];
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-            *reinterpret_cast<float4*>(mine + (m < 2 ? p.first : p.second) + 4 * (m & 1)) =
-                make_float4(dw[side][4 * m], dw[side][4 * m + 1], dw[side][4 * m + 2], dw[side][4 * m + 3]);
-        __syncthreads();
-        if (threadIdx.x < D) {
-            float sum = 0.f;
-            for (int i = 0; i < ROWS; ++i) sum += part[i][threadIdx.x];
-            line[side * D + threadIdx.x] = sum;
-        }
-    }
+    while (at < 2) flush();
 }
 
 // The workgroups' lines added up in a fixed order: 32 threads to a column, each every 32nd line, then those in their
@@ -491,24 +498,25 @@ __global__ __launch_bounds__(1024) void qknorm_dw_kernel(const float* __restrict
     }
 }
 
-constexpr int kGroups = 1024;  // four workgroups a CU
+// Workgroups that the card holds at once: four a CU of the forward kernel, three of the backward kernel.
+constexpr int kFwdGroups = 1024, kBwdGroups = 768;
 
-// Tokens of a workgroup: enough rows of their H heads to fill `passes` passes, as far as their angles fit and the card is
-// filled (4099 tokens of 12 + 2 fp32 heads, forward: 15 us in 216 workgroups, 13 us in 820; 9.4 us there since the
-// tables' sources are asked for before the rows).
-int tokens_of(int64_t tokens, int H, int D, int rot, int passes) {
-    const int rows = passes * kThreads / (D / 16);
-    int per = (rows + H - 1) / H;
-    if (rot && per > kAngles / (rot / 2)) per = kAngles / (rot / 2);
-    const int64_t share = (tokens + kGroups - 1) / kGroups;
-    return per < share ? per : share < 1 ? 1 : (int)share;
+// Tokens of a tile of H heads: enough rows to fill `passes` passes, as far as their angles fit and the card is filled, all
+// the tokens' `heads` taken together (4099 tokens of 12 + 2 fp32 heads, forward: 15 us in 216 workgroups, 13 us in 820; 9.4
+// us there since the tables' sources are asked for before the rows).
+int tokens_of(int64_t tokens, int H, int heads, int D, int rot, int passes, int groups) {
+    const int most = passes * kThreads / (D / 16);
+    const int64_t share = (tokens * heads + groups - 1) / groups;
+    const int rows = most < share ? most : (int)share;
+    const int per = (rows + H - 1) / H;
+    return rot && per > kAngles / (rot / 2) ? kAngles / (rot / 2) : per;
 }
 
 }  // namespace
 
-// At most as many lines as workgroups (rot only cuts the tiles smaller).
+// At most as many lines as workgroups, and a tile holds a token or more of a side.
 int64_t qknorm_bwd_workspace_bytes(int64_t tokens, int, int, int D) {
-    return (tokens < kGroups ? tokens : kGroups) * 2 * D * 4;
+    return (2 * tokens < kBwdGroups ? 2 * tokens : kBwdGroups) * 2 * D * 4;
 }
 
 // Whether a call's rows go past the caches: many bytes, and whole lines at a time (of a line that two instructions share each
@@ -522,11 +530,11 @@ static void fwd(const QkArgs& a, hipStream_t st, int64_t tiles, int per) {
     hipLaunchKernelGGL((qknorm_fwd_kernel<D, F32, PACKED, STREAM>), dim3((unsigned)tiles), dim3(kThreads), 0, st, a, per);
 }
 template <int D, bool F32, bool PACKED, bool STREAM>
-static void bwd(const QkArgs& a, hipStream_t st, int64_t tiles, int per, int groups) {
+static void bwd(const QkArgs& a, hipStream_t st, const Sides& sides, int groups) {
     const dim3 grid((unsigned)groups), block(kThreads);
     if (a.grad_f32)
-        hipLaunchKernelGGL((qknorm_bwd_kernel<D, F32, PACKED, true, STREAM>), grid, block, 0, st, a, per, tiles);
-    else hipLaunchKernelGGL((qknorm_bwd_kernel<D, F32, PACKED, false, STREAM>), grid, block, 0, st, a, per, tiles);
+        hipLaunchKernelGGL((qknorm_bwd_kernel<D, F32, PACKED, true, STREAM>), grid, block, 0, st, a, sides);
+    else hipLaunchKernelGGL((qknorm_bwd_kernel<D, F32, PACKED, false, STREAM>), grid, block, 0, st, a, sides);
 }
 // `f` with D, the rows' type, whether they are packed and whether they go past the caches.
 template <class F>
@@ -543,7 +551,7 @@ static void by_kind(const QkArgs& a, bool stream, F f) {
 }
 
 hipError_t launch_qknorm_fwd(const QkArgs& a, hipStream_t st) {
-    const int per = tokens_of(a.tokens, a.Hq + a.Hk, a.D, a.rot, 4);
+    const int per = tokens_of(a.tokens, a.Hq + a.Hk, a.Hq + a.Hk, a.D, a.rot, 4, kFwdGroups);
     const int64_t tiles = (a.tokens + per - 1) / per;
     if (tiles > kMaxThreads / kThreads) return hipErrorInvalidConfiguration;
     by_kind(a, streams(a, a.f32 ? 8 : 4), [&](auto d, auto f32, auto packed, auto stream) {
@@ -553,13 +561,16 @@ hipError_t launch_qknorm_fwd(const QkArgs& a, hipStream_t st) {
 }
 
 hipError_t launch_qknorm_bwd(const QkArgs& a, hipStream_t st) {
-    const int per = tokens_of(a.tokens, a.Hq > a.Hk ? a.Hq : a.Hk, a.D, a.rot, 2);
-    const int64_t tiles = (a.tokens + per - 1) / per;
-    const int64_t most = a.dwq ? kGroups : kMaxThreads / kThreads;
+    Sides sides;
+    for (int i = 0; i < 2; ++i) {
+        sides.per[i] = tokens_of(a.tokens, i ? a.Hk : a.Hq, a.Hq + a.Hk, a.D, a.rot, 4, kBwdGroups);
+        sides.tiles[i] = a.tokens ? (a.tokens + sides.per[i] - 1) / sides.per[i] : 0;
+    }
+    const int64_t tiles = sides.tiles[0] + sides.tiles[1], most = a.dwq ? kBwdGroups : kMaxThreads / kThreads;
     const int groups = (int)(tiles < most ? tiles : most);
     if (groups > 0)  // without tokens only the weights' zero gradients are written
         by_kind(a, streams(a, (a.f32 ? 8 : 4) + (a.grad_f32 ? 4 : 2)), [&](auto d, auto f32, auto packed, auto stream) {
-            bwd<decltype(d)::value, decltype(f32)::value, decltype(packed)::value, decltype(stream)::value>(a, st, tiles, per,
+            bwd<decltype(d)::value, decltype(f32)::value, decltype(packed)::value, decltype(stream)::value>(a, st, sides,
                                                                                                           groups);
         });
     if (a.dwq)
