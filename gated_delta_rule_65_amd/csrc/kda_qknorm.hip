@@ -10,10 +10,11 @@
 // dw = the sum over rows of (d turned back) z^.
 //
 // Measured (q and k of 16 heads of 128 bf16 channels, 32768 tokens): forward, half of the channels turned, columns of one
-// projection, 537 MB in 101 us (5.3 TB/s); forward with the raw rows packed in 8 bits beside, 675 MB in 108 us (6.2
+// projection, 537 MB in 92 us (5.8 TB/s; 101 without the exchange of chunks, since
+// half lines at a time do not go past the caches); forward with the raw rows packed in 8 bits beside, 675 MB in 109 us (6.2
 // TB/s); backward from the packed rows with the weights' gradients, 675 MB in 121 us (5.6 TB/s; its three workgroups a CU
-// stop at each tile's tables) and 5 us for the weights' sums.  4099 tokens of 12 + 2 heads of 64 fp32 channels: 9.4 us
-// forward and 14 backward for 74 MB in all; 32 tokens: 4.4 us, one pass of latency.
+// stop at each tile's tables) and 5 us for the weights' sums.  4099 tokens of 12 + 2 heads of 64 fp32 channels: 10
+// us forward and 14 backward for 74 MB in all; 32 tokens: 4.4 us, one pass of latency.
 #include <type_traits>
 
 #include "kda_ckpt8.h"
@@ -32,16 +33,37 @@ constexpr int kAngles = 2048;  // pairs of a workgroup's tokens at most: 16 KiB 
 //     chunk, pairs (i, i + D/2) in the two of a lane, and the lanes' chunks are side by side: whole lines at a time.
 //   Else (halves of part of the head, pairs (i, i + rot/2)): 8j and rot/2 + 8j for the lanes j < rot/16, and the channels
 //     behind in the same way for those after them.
+//   Halves of half of the head lie in whole lines too once lanes exchange a chunk: lane j of the lower half and lane
+//     LANES - 1 - j load and store as if spread (so that a line takes one instruction) and each keeps what the other
+//     needs: (8j, D/2 + 8j) and (D/4 + 8j, 3D/4 + 8j) in memory, (8j, D/4 + 8j) and (D/2 + 8j, 3D/4 + 8j) in use.
 struct Place {
     int first, second;
     bool turned0, turned1;  // the chunks lie in the turned channels
+    int mem_first, mem_second;
+    bool exchange, low;     // chunks are exchanged; the lane is of the lower half
 };
 __host__ __device__ __forceinline__ bool is_spread(int D, int rot, bool interleaved) { return interleaved || rot == 0 || rot == D; }
+__host__ __device__ __forceinline__ bool is_exchanged(int D, int rot, bool interleaved) { return !interleaved && 2 * rot == D; }
 template <int D>
 __device__ __forceinline__ Place place_of(int j, int rot, bool interleaved) {
     const bool spread = is_spread(D, rot, interleaved), half = spread || j < rot / 16;
     const int first = 8 * j + (half ? 0 : rot / 2), apart = spread ? D / 2 : half ? rot / 2 : (D - rot) / 2;
-    return {first, first + apart, first < rot, first + apart < rot};
+    if (!is_exchanged(D, rot, interleaved)) return {first, first + apart, first < rot, first + apart < rot, first, first + apart, false, half};
+    const int m = half ? j : D / 16 - 1 - j, in_use = 8 * m + (half ? 0 : D / 2), in_memory = 8 * m + (half ? 0 : D / 4);
+    return {in_use, in_use + D / 4, half, half, in_memory, in_memory + D / 2, true, half};
+}
+
+// From chunks a and b as they lie in memory to those in use, and back: the same exchange.
+template <int D, int WORDS>
+__device__ __forceinline__ void exchange(uint32_t* a, uint32_t* b, bool low) {
+#pragma unroll
+    for (int k = 0; k < WORDS; ++k) {
+        const int send = (int)(low ? b[k] : a[k]);
+        const uint32_t got = (uint32_t)(D == 128 ? __builtin_amdgcn_update_dpp(0, send, 0x141, 0xf, 0xf, true)   // 7 - lane
+                                                 : __builtin_amdgcn_update_dpp(0, send, 0x1B, 0xf, 0xf, true));  // 3 - lane
+        a[k] = low ? a[k] : got;
+        b[k] = low ? got : b[k];
+    }
 }
 
 // The sum over the lanes of a row (4 or 8 neighbours), the same bits in each of them.
@@ -88,7 +110,6 @@ __device__ __forceinline__ float row_rsqrt(const float x[16], float s, float eps
 // Sixteen channels of a row as they come from memory: two chunks of eight.
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 template <bool F32, bool PACKED>
 struct Chunks {
     u32x4 a[F32 ? 2 : 1], b[F32 ? 2 : 1];
@@ -113,56 +134,71 @@ __device__ __forceinline__ void load_chunks(const void* p, const uint8_t* scales
                                             Chunks<F32, PACKED>& c) {
     if constexpr (PACKED) {
         const uint8_t* s = static_cast<const uint8_t*>(p) + row;
-        c.a = load_as<u32x2, STREAM>(s + at.first);
-        c.b = load_as<u32x2, STREAM>(s + at.second);
+        c.a = load_as<u32x2, STREAM>(s + at.mem_first);
+        c.b = load_as<u32x2, STREAM>(s + at.mem_second);
         c.sa = scales[(row + at.first) / kCkptBlock];
         c.sb = scales[(row + at.second) / kCkptBlock];
     } else {
         const char* s = static_cast<const char*>(p) + row * (F32 ? 4 : 2);
 #pragma unroll
         for (int i = 0; i < (F32 ? 2 : 1); ++i) {
-            c.a[i] = load_as<u32x4, STREAM>(s + at.first * (F32 ? 4 : 2) + 16 * i);
-            c.b[i] = load_as<u32x4, STREAM>(s + at.second * (F32 ? 4 : 2) + 16 * i);
+            c.a[i] = load_as<u32x4, STREAM>(s + at.mem_first * (F32 ? 4 : 2) + 16 * i);
+            c.b[i] = load_as<u32x4, STREAM>(s + at.mem_second * (F32 ? 4 : 2) + 16 * i);
         }
     }
 }
 template <bool F32>
-__device__ __forceinline__ void chunk_values(const u32x4* c, float x[8]) {
+__device__ __forceinline__ void chunk_values(const uint32_t* c, float x[8]) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-        if constexpr (F32) x[k] = __uint_as_float(c[k / 4][k % 4]);
-        else x[k] = __uint_as_float(k % 2 ? c[0][k / 2] & 0xffff0000u : c[0][k / 2] << 16);
+        if constexpr (F32) x[k] = __uint_as_float(c[k]);
+        else x[k] = __uint_as_float(k % 2 ? c[k / 2] & 0xffff0000u : c[k / 2] << 16);
     }
 }
-template <bool F32, bool PACKED>
-__device__ __forceinline__ void values_of(const Chunks<F32, PACKED>& c, float x[16]) {
+template <int D, bool F32, bool PACKED>
+__device__ __forceinline__ void values_of(const Chunks<F32, PACKED>& c, const Place& at, float x[16]) {
     if constexpr (PACKED) {
+        uint32_t a[2] = {c.a[0], c.a[1]}, b[2] = {c.b[0], c.b[1]};
+        if (at.exchange) exchange<D, 2>(a, b, at.low);
         const float ua = ckpt_unit(c.sa), ub = ckpt_unit(c.sb);
-        ckpt_value4(c.a[0], ua, x);
-        ckpt_value4(c.a[1], ua, x + 4);
-        ckpt_value4(c.b[0], ub, x + 8);
-        ckpt_value4(c.b[1], ub, x + 12);
+        ckpt_value4(a[0], ua, x);
+        ckpt_value4(a[1], ua, x + 4);
+        ckpt_value4(b[0], ub, x + 8);
+        ckpt_value4(b[1], ub, x + 12);
     } else {
-        chunk_values<F32>(c.a, x);
-        chunk_values<F32>(c.b, x + 8);
+        constexpr int N = F32 ? 2 : 1;
+        uint32_t a[4 * N], b[4 * N];
+#pragma unroll
+        for (int k = 0; k < 4 * N; ++k) a[k] = c.a[k / 4][k % 4], b[k] = c.b[k / 4][k % 4];
+        if (at.exchange) exchange<D, 4 * N>(a, b, at.low);
+        chunk_values<F32>(a, x);
+        chunk_values<F32>(b, x + 8);
     }
 }
-template <bool STREAM, bool F32>
+template <int D, bool STREAM, bool F32>
 __device__ __forceinline__ void store_chunks(void* p, int64_t row, const Place& at, const float x[16]) {
     if constexpr (F32) {
+        uint32_t a[8], b[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) a[k] = __float_as_uint(x[k]), b[k] = __float_as_uint(x[8 + k]);
+        if (at.exchange) exchange<D, 8>(a, b, at.low);
         float* d = static_cast<float*>(p) + row;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            store_as<STREAM>(d + (i < 2 ? at.first : at.second) + 4 * (i & 1),
-                             f32x4{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]});
+        for (int i = 0; i < 8; i += 4) {
+            store_as<STREAM>(d + at.mem_first + i, u32x4{a[i], a[i + 1], a[i + 2], a[i + 3]});
+            store_as<STREAM>(d + at.mem_second + i, u32x4{b[i], b[i + 1], b[i + 2], b[i + 3]});
+        }
     } else {
         typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
         bf8 u, v;
 #pragma unroll
         for (int k = 0; k < 8; ++k) u[k] = (__bf16)x[k], v[k] = (__bf16)x[8 + k];
+        const u32x4 pu = __builtin_bit_cast(u32x4, u), pv = __builtin_bit_cast(u32x4, v);
+        uint32_t a[4] = {pu[0], pu[1], pu[2], pu[3]}, b[4] = {pv[0], pv[1], pv[2], pv[3]};
+        if (at.exchange) exchange<D, 4>(a, b, at.low);
         uint16_t* d = static_cast<uint16_t*>(p) + row;
-        store_as<STREAM>(d + at.first, u);
-        store_as<STREAM>(d + at.second, v);
+        store_as<STREAM>(d + at.mem_first, u32x4{a[0], a[1], a[2], a[3]});
+        store_as<STREAM>(d + at.mem_second, u32x4{b[0], b[1], b[2], b[3]});
     }
 }
 
@@ -353,7 +389,7 @@ __global__ __launch_bounds__(kThreads, 4) void qknorm_fwd_kernel(QkArgs a, int p
             const bool key = head[i] >= a.Hq;
             const int64_t out = key ? ((t0 + tok[i]) * a.Hk + head[i] - a.Hq) * D : ((t0 + tok[i]) * a.Hq + head[i]) * D;
             float x[16];
-            values_of(c[i], x);
+            values_of<D>(c[i], p, x);
             if constexpr (!PACKED) {
                 if (a.q8)
                     pack_row<D>(x, p, j, a.rot, a.interleaved, (key ? a.k8 : a.q8) + out,
@@ -369,7 +405,7 @@ __global__ __launch_bounds__(kThreads, 4) void qknorm_fwd_kernel(QkArgs a, int p
                 for (int k = 0; k < 16; ++k) x[k] *= w[k];
             }
             tab.turn(x, tok[i], j, p, a.rot, a.interleaved, 1.f);
-            store_chunks<STREAM, F32>(key ? a.k_out : a.q_out, out, p, x);
+            store_chunks<D, STREAM, F32>(key ? a.k_out : a.q_out, out, p, x);
         }
     }
 }
@@ -450,8 +486,8 @@ __global__ __launch_bounds__(kThreads, 3) void qknorm_bwd_kernel(QkArgs a, Sides
             for (int i = 0; i < PASSES; ++i) {
                 if (base + i * ROWS + (int)threadIdx.x / LANES >= rows) continue;
                 float x[16], d[16];
-                values_of(c[i], x);
-                values_of(g[i], d);
+                values_of<D>(c[i], p, x);
+                values_of<D>(g[i], p, d);
                 const float r = row_rsqrt<LANES>(x, sc, a.eps);
                 tab.turn(d, tok[i], j, p, a.rot, a.interleaved, -1.f);
 #pragma unroll
@@ -471,7 +507,7 @@ __global__ __launch_bounds__(kThreads, 3) void qknorm_bwd_kernel(QkArgs a, Sides
                 dot = row_sum<LANES>(dot) * sc;
 #pragma unroll
                 for (int k = 0; k < 16; ++k) x[k] = r * fmaf(-dot, x[k], d[k]);
-                store_chunks<STREAM, F32>(to, out[i], p, x);
+                store_chunks<D, STREAM, F32>(to, out[i], p, x);
             }
         }
     }
@@ -502,8 +538,8 @@ __global__ __launch_bounds__(1024) void qknorm_dw_kernel(const float* __restrict
 constexpr int kFwdGroups = 1024, kBwdGroups = 768;
 
 // Tokens of a tile of H heads: enough rows to fill `passes` passes, as far as their angles fit and the card is filled, all
-// the tokens' `heads` taken together (4099 tokens of 12 + 2 fp32 heads, forward: 15 us in 216 workgroups, 13 us in 820; 9.4
-// us there since the tables' sources are asked for before the rows).
+// the tokens' `heads` taken together (4099 tokens of 12 + 2 fp32 heads, forward: 15 us in 216 workgroups, 13 us in 820; 10 us
+// there since the tables' sources are asked for before the rows).
 int tokens_of(int64_t tokens, int H, int heads, int D, int rot, int passes, int groups) {
     const int most = passes * kThreads / (D / 16);
     const int64_t share = (tokens * heads + groups - 1) / groups;
@@ -519,10 +555,12 @@ int64_t qknorm_bwd_workspace_bytes(int64_t tokens, int, int, int D) {
     return (2 * tokens < kBwdGroups ? 2 * tokens : kBwdGroups) * 2 * D * 4;
 }
 
-// Whether a call's rows go past the caches: many bytes, and whole lines at a time (of a line that two instructions share each
-// would fetch it).
+// Whether a call's rows go past the caches: many bytes, and whole lines at a time (a line that two instructions share
+// is written in two parts: 108 us past the caches and 101 through them for the call above before its lanes
+// exchanged chunks, 92 and 102 since).
 static bool streams(const QkArgs& a, int64_t bytes_per_channel) {
-    return a.tokens * (a.Hq + a.Hk) * a.D * bytes_per_channel > kStreamBytes && is_spread(a.D, a.rot, a.interleaved);
+    return a.tokens * (a.Hq + a.Hk) * a.D * bytes_per_channel > kStreamBytes &&
+           (is_spread(a.D, a.rot, a.interleaved) || is_exchanged(a.D, a.rot, a.interleaved));
 }
 
 template <int D, bool F32, bool PACKED, bool STREAM>

@@ -459,6 +459,34 @@ def test_qk_types(kind, gk, packed):
     check_qk(41, 5, 3, 64, 32, kind, gk=gk, packed=packed, interleaved=True, norm="l2", weight=False)
 
 
+@pytest.mark.parametrize("D,rot", [(64, 16), (64, 32), (64, 48), (128, 16), (128, 48), (128, 64), (128, 96)])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_qk_halves_of_part_of_the_head(D, rot, kind):
+    check_qk(21, 3, 2, D, rot, kind, packed=True)
+
+
+@pytest.mark.parametrize("D,rot", [(64, 32), (128, 64), (128, 32), (128, 128)])
+@pytest.mark.parametrize("ckpt8", [False, True])
+def test_qk_large_calls_have_the_bits_of_small_ones(D, rot, ckpt8):
+    """Rows of calls of more than 128 MiB go past the caches; a row's result does not depend on that."""
+    tokens, Hq, Hk, n = 36000 * 128 // D, 5, 3, 50
+    d, _ = qk_data(tokens, Hq, Hk, D, rot, "bf16", False, 9)
+    form = {"freqs": d["freqs"], "eps": 1e-6}
+    q8 = kda.qk_norm_rope_fwd(d["q"], d["k"], pos=d["pos"], ckpt8=ckpt8, **form)
+    dq = kda.qk_norm_rope_bwd(*(q8[2] if ckpt8 else (d["q"], d["k"])), d["dq"], d["dk"], pos=d["pos"], **form)
+    for at in (0, tokens // 2, tokens - n):
+        part = {k: d[k][at:at + n] for k in ("q", "k", "dq", "dk", "pos")}
+        s8 = kda.qk_norm_rope_fwd(part["q"], part["k"], pos=part["pos"], ckpt8=ckpt8, **form)
+        raw = s8[2] if ckpt8 else (part["q"], part["k"])
+        ds = kda.qk_norm_rope_bwd(*raw, part["dq"], part["dk"], pos=part["pos"], **form)
+        for big, small in (*zip(q8[:2], s8[:2]), *zip(dq[:2], ds[:2])):
+            assert torch.equal(big[at:at + n], small)
+        if ckpt8:
+            for big, small in zip(q8[2], s8[2]):
+                assert torch.equal(big.codes[at:at + n], small.codes)
+                assert torch.equal(big.scales[at:at + n], small.scales)
+
+
 @pytest.mark.parametrize("pos", [np.arange(11, dtype=np.int64) * 10 ** 8, np.arange(11, dtype=np.int32) - 5,
                                  np.full(11, 2 ** 31 - 1, np.int32), np.full(11, 1048575, np.int64)])
 def test_qk_far_and_negative_positions(pos):
