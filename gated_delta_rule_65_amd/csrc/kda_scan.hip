@@ -24,7 +24,7 @@ __global__ __launch_bounds__(256) void scan_begin_kernel(u64* words, int64_t cou
 }
 
 // One token: an element a value, 4 to a lane.  Bound by the launch: 64 x 2048 channels take 2.8 us of 0.3 us of traffic, and
-// the call 8.7 us from the host.
+// the call 8.1 us from the host.
 template <bool XF, bool GF, int CPL>
 __global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs a, const float* h_in, float* h_out, int64_t count) {
     const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * CPL;

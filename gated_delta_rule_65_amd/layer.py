@@ -410,7 +410,7 @@ def _qk_side(t, name):
     _float(t, name)
     if t.dim() < 2:
         raise ValueError(f"{name} must be [..., H, D]")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU (got {t.device})")
     return t, None, _token_stride(t, name), t.dtype
 
