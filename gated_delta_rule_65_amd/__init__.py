@@ -19,6 +19,7 @@ scales q and k to unit length per token and head inside the kernels.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -439,10 +440,39 @@ def varlen_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tenso
     return dq, dk, dv, dg, dbeta, ds0
 
 
+class _NoGraph(torch.autograd.Function):
+    """Hands a gradient on, and refuses to be differentiated."""
+
+    @staticmethod
+    def forward(ctx, t, mark):
+        return t.detach()
+
+    @staticmethod
+    def backward(ctx, _):
+        raise RuntimeError("the backward kernels give first-order gradients only: no gradient of a gradient")
+
+
+def _first_order(backward):
+    """Marks the results of a backward pass that runs kernels.  They carry no graph; under ``create_graph=True`` a loss of
+    them would be differentiated as if they were constants, silently, so differentiating them raises instead.  (torch's
+    once_differentiable does so only where an incoming gradient carries a graph, which that of a plain sum does not.)"""
+
+    @functools.wraps(backward)
+    def run(ctx, *grads):
+        if not torch.is_grad_enabled():
+            return backward(ctx, *grads)
+        with torch.no_grad():
+            out = backward(ctx, *grads)
+        mark = torch.empty(0, requires_grad=True)
+        return tuple(None if t is None else _NoGraph.apply(t, mark) for t in out)
+
+    return run
+
+
 class ChunkKDA(torch.autograd.Function):
     """Autograd wrapper: ``o, s_final = ChunkKDA.apply(q, k, v, g, beta, s0)`` with the forward and
     backward both in the library's kernels.  Gradients of q, k, v come back in fp32 and are cast
-    to the input type; s0 may be None."""
+    to the input type; s0 may be None.  Gradients of gradients are refused."""
 
     @staticmethod
     def forward(ctx, q, k, v, g, beta, s0=None):
@@ -451,6 +481,7 @@ class ChunkKDA(torch.autograd.Function):
         return o, sf
 
     @staticmethod
+    @_first_order
     def backward(ctx, d_o, d_sf):
         q, k, v, g, beta, s0 = ctx.saved_tensors
         d_o = torch.zeros_like(q[..., :1].float()).expand(*q.shape[:-1], v.shape[-1]).contiguous() \

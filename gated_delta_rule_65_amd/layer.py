@@ -2,7 +2,8 @@
 norm of queries and keys with the position rotation, and activation checkpoints in 8 bits.
 
 As in the package's other calls, everything is computed in the library's HIP kernels; this module checks tensors,
-allocates outputs and workspaces with torch and passes pointers and torch's current stream.
+allocates outputs and workspaces with torch and passes pointers and torch's current stream.  The autograd functions give
+first-order gradients: the gradient of a gradient is refused.
 """
 from __future__ import annotations
 
@@ -13,7 +14,7 @@ from typing import NamedTuple, Optional, Tuple
 
 import torch
 
-from . import DTYPE, _check, _need, _ptr, _stream, chunk_bwd, chunk_fwd, load_library
+from . import DTYPE, _check, _first_order, _need, _ptr, _stream, chunk_bwd, chunk_fwd, load_library
 
 NORM = {"l2": 0, "rms": 1}
 
@@ -328,6 +329,7 @@ class GatedScan(torch.autograd.Function):
         return y, hf
 
     @staticmethod
+    @_first_order
     def backward(ctx, dy, dh_final):
         g, saved, x, h0, form = _kept_scan(ctx)
         dx, dg, dh0 = scan_bwd(g, _grad(dy, g, ctx.x_dtype), saved, x=x, h0=h0,
@@ -347,6 +349,7 @@ class VarlenGatedScan(torch.autograd.Function):
         return y, hf
 
     @staticmethod
+    @_first_order
     def backward(ctx, dy, dh_final):
         g, saved, x, h0, form = _kept_scan(ctx)
         dx, dg, dh0 = scan_varlen_bwd(g, ctx.cu, _grad(dy, g, ctx.x_dtype), saved, x=x, h0=h0,
@@ -526,6 +529,7 @@ class NormChunkKDA(torch.autograd.Function):
         return o, sf
 
     @staticmethod
+    @_first_order
     def backward(ctx, d_o, d_sf):
         g, beta, s0, weight_q, weight_k, pos, freqs, *kept = ctx.saved_tensors
         if ctx.ckpt8:

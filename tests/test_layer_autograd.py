@@ -1,0 +1,105 @@
+"""The autograd functions' own work (what they keep, refuse and hand on), with plain stand-ins on the CPU for the calls that
+run kernels."""
+import pytest
+import torch
+
+import gated_delta_rule_65_amd as kda
+from gated_delta_rule_65_amd import layer
+
+
+def plain_scan(x, g, where, h0):
+    """y and the last states of the scan of log gates, rows x [total, D]."""
+    a, y, last = torch.exp(g.clamp(-5, 0)), [None] * len(x), []
+    for n, (i, j) in enumerate(where):
+        h = torch.zeros_like(x[0]) if h0 is None else h0[n]
+        for t in range(i, j):
+            h = a[t] * h + x[t]
+            y[t] = h
+        last.append(h)
+    return torch.stack([torch.zeros_like(x[0]) if v is None else v for v in y]), torch.stack(last)
+
+
+def spans_of(cu):
+    return list(zip(cu.tolist()[:-1], cu.tolist()[1:]))
+
+
+@pytest.fixture
+def stand_ins(monkeypatch):
+    def varlen_fwd(x, g, cu, h0=None, **kw):
+        with torch.no_grad():
+            return (*plain_scan(x, g, spans_of(cu), h0), torch.zeros(1))
+
+    def varlen_bwd(g, cu, dy, saved, *, x, h0, dh_final, **kw):
+        with torch.enable_grad():
+            leaves = [t.detach().requires_grad_() for t in (x, g, torch.zeros_like(dh_final) if h0 is None else h0)]
+            out = plain_scan(leaves[0], leaves[1], spans_of(cu), leaves[2])
+            return torch.autograd.grad(out, leaves, (dy.detach(), dh_final.detach()), allow_unused=True)
+
+    def offsets(x):
+        return torch.arange(x.shape[0] + 1, dtype=torch.int32) * x.shape[1]
+
+    def fwd(x, g, h0=None, **kw):
+        y, h, saved = varlen_fwd(x.flatten(0, 1), g.flatten(0, 1), offsets(x), h0)
+        return y.view(x.shape), h, saved
+
+    def bwd(g, dy, saved, *, x, h0, dh_final, **kw):
+        dx, dg, dh0 = varlen_bwd(g.flatten(0, 1), offsets(x), dy.flatten(0, 1), saved, x=x.flatten(0, 1), h0=h0,
+                                 dh_final=dh_final)
+        return dx.view(x.shape), dg.view(x.shape), dh0
+
+    def norm_fwd(q, k, **kw):
+        return q.detach() * 2, k.detach() * 2, None
+
+    def norm_bwd(q, k, dq, dk, **kw):
+        return dq.detach().to(q.dtype) * 2, dk.detach().to(k.dtype) * 2, None, None
+
+    def chunk_fwd(q, k, v, g, beta, s0=None):
+        return (q * k * v).detach().float(), torch.zeros(q.shape[0], q.shape[2], q.shape[3], v.shape[3])
+
+    def chunk_bwd(q, k, v, g, beta, d_o, s0=None, d_sfinal=None):
+        if g.dtype != torch.float32 or beta.dtype != torch.float32:
+            raise TypeError("g must be torch.float32")
+        d = d_o.detach()
+        return d * (k * v), d * (q * v), d * (q * k), torch.ones_like(g), torch.ones_like(beta), torch.zeros(1)
+
+    for name, f in (("scan_fwd", fwd), ("scan_bwd", bwd), ("scan_varlen_fwd", varlen_fwd), ("scan_varlen_bwd", varlen_bwd),
+                    ("qk_norm_rope_fwd", norm_fwd), ("qk_norm_rope_bwd", norm_bwd), ("chunk_fwd", chunk_fwd),
+                    ("chunk_bwd", chunk_bwd)):
+        monkeypatch.setattr(layer, name, f)
+    monkeypatch.setattr(kda, "chunk_fwd", chunk_fwd)
+    monkeypatch.setattr(kda, "chunk_bwd", chunk_bwd)
+
+
+def applied(name, x, g):
+    """y of an autograd function at x and g, both [1, T, H, D]."""
+    if name == "GatedScan":
+        return kda.GatedScan.apply(x, g, None)[0]
+    if name == "VarlenGatedScan":
+        cu = torch.tensor([0, 2, x.shape[1]], dtype=torch.int32)
+        return kda.VarlenGatedScan.apply(x.flatten(0, 1), g.flatten(0, 1), cu, None)[0]
+    beta = torch.ones(x.shape[:3])
+    return getattr(kda, name).apply(x, x, x, g, beta)[0]
+
+
+@pytest.mark.parametrize("name", ["GatedScan", "VarlenGatedScan", "ChunkKDA", "NormChunkKDA"])
+@pytest.mark.parametrize("weighted", [False, True])
+def test_second_order_gradients_are_refused(stand_ins, name, weighted):
+    """A penalty on a gradient needs the gradient's gradient, which the backward kernels do not give: an error, also where
+    other terms have theirs and where the gradient that comes in has no graph of its own."""
+    torch.manual_seed(1)
+    x, g = torch.randn(1, 5, 2, 4).requires_grad_(), (-torch.rand(1, 5, 2, 4)).requires_grad_()
+    y = applied(name, x, g)
+    loss = ((y * y).sum() if weighted else y.sum()) + (x ** 3).sum()
+    dx, = torch.autograd.grad(loss, x, create_graph=True)
+    assert torch.isfinite(dx).all()  # the gradient itself is there
+    with pytest.raises(RuntimeError, match="first-order"):
+        (dx ** 2).sum().backward()
+
+
+@pytest.mark.parametrize("name", ["GatedScan", "VarlenGatedScan", "ChunkKDA", "NormChunkKDA"])
+def test_first_order_gradients_are_the_same_with_a_graph(stand_ins, name):
+    torch.manual_seed(2)
+    x, g = torch.randn(1, 5, 2, 4).requires_grad_(), (-torch.rand(1, 5, 2, 4)).requires_grad_()
+    grads = [torch.autograd.grad((applied(name, x, g) ** 2).sum(), (x, g), create_graph=graph) for graph in (False, True)]
+    assert all(torch.equal(a, b) for a, b in zip(*grads))
+    assert not any(t.requires_grad for t in grads[0])
