@@ -331,7 +331,7 @@ class GatedScan(torch.autograd.Function):
     @staticmethod
     @_first_order
     def backward(ctx, dy, dh_final):
-        g, saved, x, h0, form = _kept_scan(ctx)
+        g, saved, x, h0, _, form = _kept_scan(ctx)
         dx, dg, dh0 = scan_bwd(g, _grad(dy, g, ctx.x_dtype), saved, x=x, h0=h0,
                                dh_final=_grad(dh_final, None, torch.float32), **form)
         return dx, dg, (dh0 if ctx.has_h0 else None), None, None, None
@@ -351,8 +351,8 @@ class VarlenGatedScan(torch.autograd.Function):
     @staticmethod
     @_first_order
     def backward(ctx, dy, dh_final):
-        g, saved, x, h0, form = _kept_scan(ctx)
-        dx, dg, dh0 = scan_varlen_bwd(g, ctx.cu, _grad(dy, g, ctx.x_dtype), saved, x=x, h0=h0,
+        g, saved, x, h0, cu, form = _kept_scan(ctx)
+        dx, dg, dh0 = scan_varlen_bwd(g, cu, _grad(dy, g, ctx.x_dtype), saved, x=x, h0=h0,
                                       dh_final=_grad(dh_final, None, torch.float32), **form)
         return dx, dg, None, (dh0 if ctx.has_h0 else None), None, None, None
 
@@ -365,17 +365,17 @@ def _grad(t, like, dtype):
 
 
 def _keep_scan(ctx, x, g, h0, saved, g_logit, complement, ckpt8, cu=None):
-    ctx.x_dtype, ctx.has_h0, ctx.ckpt8, ctx.cu = x.dtype, h0 is not None, ckpt8, cu
+    ctx.x_dtype, ctx.has_h0, ctx.ckpt8 = x.dtype, h0 is not None, ckpt8
     ctx.form = {"g_logit": g_logit, "complement": complement}
-    ctx.save_for_backward(*((g, saved.codes, saved.scales) if ckpt8 else (g, saved, x, h0)))
+    ctx.save_for_backward(cu, g, *((saved.codes, saved.scales) if ckpt8 else (saved, x, h0)))
 
 
 def _kept_scan(ctx):
     if ctx.ckpt8:
-        g, codes, scales = ctx.saved_tensors
-        return g, Packed8(codes, scales, ctx.x_dtype), None, None, ctx.form
-    g, carry, x, h0 = ctx.saved_tensors
-    return g, carry, x, h0, ctx.form
+        cu, g, codes, scales = ctx.saved_tensors
+        return g, Packed8(codes, scales, ctx.x_dtype), None, None, cu, ctx.form
+    cu, g, carry, x, h0 = ctx.saved_tensors
+    return g, carry, x, h0, cu, ctx.form
 
 
 # ----------------------------------------------------------------- head norm with rotation

@@ -103,3 +103,25 @@ def test_first_order_gradients_are_the_same_with_a_graph(stand_ins, name):
     grads = [torch.autograd.grad((applied(name, x, g) ** 2).sum(), (x, g), create_graph=graph) for graph in (False, True)]
     assert all(torch.equal(a, b) for a, b in zip(*grads))
     assert not any(t.requires_grad for t in grads[0])
+
+
+def test_offsets_changed_before_the_backward_pass_are_an_error(stand_ins):
+    """Offsets are kept like the other tensors: rewritten in place in between, they would give another batch's gradients."""
+    x, g = torch.randn(6, 3).requires_grad_(), (-torch.rand(6, 3)).requires_grad_()
+    cu = torch.tensor([0, 2, 6], dtype=torch.int32)
+    y, _ = kda.VarlenGatedScan.apply(x, g, cu, None)
+    cu.copy_(torch.tensor([0, 5, 6]))
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+
+
+@pytest.mark.parametrize("name", ["GatedScan", "VarlenGatedScan", "ChunkKDA", "NormChunkKDA"])
+def test_what_is_kept_passes_the_hooks_of_saved_tensors(stand_ins, name):
+    """Hooks that move saved tensors away see all of them."""
+    x, g = torch.randn(1, 5, 2, 4).requires_grad_(), (-torch.rand(1, 5, 2, 4)).requires_grad_()
+    kinds = []
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: kinds.append(t.dtype) or t.clone(), lambda t: t):
+        y = applied(name, x, g)
+    assert (torch.int32 in kinds) == (name == "VarlenGatedScan")
+    y.sum().backward()
+    assert torch.isfinite(x.grad).all() and torch.isfinite(g.grad).all()
