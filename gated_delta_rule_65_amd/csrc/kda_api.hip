@@ -615,6 +615,25 @@ kda_status kda_scan_varlen_bwd(const void* x, const void* g, const int32_t* cu_s
                     stream, "kda_scan_varlen_bwd");
 }
 
+kda_status kda_scan_zero_behind(const int32_t* cu_seqlens, int64_t N, int64_t total, void* a, int64_t a_row_bytes,
+                                void* b, int64_t b_row_bytes, void* stream) {
+    kda_status st;
+    if (N < 0 || total < 0) return fail(KDA_ERR_BAD_SHAPE, "N and total must be >= 0");
+    if (N > 0x7fffffffLL || total > 0x7fffffffLL)
+        return fail(KDA_ERR_BAD_SHAPE, "N or total exceeds the int32 range of cu_seqlens");
+    if (!b) b_row_bytes = 0;
+    for (const int64_t row : {a_row_bytes, b_row_bytes})
+        if (row < 0 || row % 2 || row > kda::kMaxChannels * 4)
+            return fail(KDA_ERR_BAD_SHAPE, "row bytes must be even and in [0, 4 * 2^24] (got %lld)", (long long)row);
+    const bool any = total > 0 && (a_row_bytes > 0 || b_row_bytes > 0);
+    if (any && !cu_seqlens) return fail(KDA_ERR_NULL_ARG, "cu_seqlens is NULL");
+    if (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u) return fail(KDA_ERR_MISALIGNED, "cu_seqlens is not 4-byte aligned");
+    if ((st = check_ptrs({{a, "a", any}, {b, "b", false}})) != KDA_OK) return st;
+    if (!any) return ok();
+    return launched(kda::launch_scan_zero_behind(cu_seqlens, N, total, a, a_row_bytes, b, b_row_bytes,
+                                                 static_cast<hipStream_t>(stream)), "kda_scan_zero_behind");
+}
+
 kda_status kda_scan_step(const void* x, const void* g, const float* h_in, float* h_out, void* y, int64_t B,
                          int64_t D, const kda_scan_form* form, void* stream) {
     kda_status st;

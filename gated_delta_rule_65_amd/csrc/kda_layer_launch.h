@@ -55,6 +55,9 @@ int64_t scan_places(const ScanArgs& a);  // workgroups of a call
 int64_t scan_workspace_bytes(int64_t N, int64_t total, int64_t D);
 hipError_t launch_scan_fwd(const ScanArgs& a, hipStream_t st);
 hipError_t launch_scan_bwd(const ScanArgs& a, hipStream_t st);
+// rows cu[N] .. total - 1 of both buffers (b may be nullptr) to zero
+hipError_t launch_scan_zero_behind(const int32_t* cu, int64_t N, int64_t total, void* a, int64_t a_row, void* b,
+                                   int64_t b_row, hipStream_t st);
 hipError_t launch_scan_step(const ScanArgs& a, const float* h_in, float* h_out, hipStream_t st);
 
 // ---- head norm with rotation (kda_qknorm.hip)

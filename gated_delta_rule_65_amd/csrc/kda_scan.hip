@@ -23,6 +23,25 @@ __global__ __launch_bounds__(256) void scan_begin_kernel(u64* words, int64_t cou
     }
 }
 
+// Zeros for the rows behind the last sequence; where that is only the device knows.  Whole 16-byte words, and what lies before
+// the first and behind the last of them 2 bytes at a time (rows are of 2- or 4-byte elements, buffers aligned).
+struct Behind {
+    void* p;
+    int64_t row;  // bytes
+};
+__global__ __launch_bounds__(256) void scan_zero_behind_kernel(Behind a, Behind b, const int32_t* cu, int64_t N, int64_t total) {
+    const int64_t used = cu[N] < 0 ? 0 : cu[N];
+    if (used >= total) return;
+    const Behind to = blockIdx.y ? b : a;
+    char* base = static_cast<char*>(to.p);
+    const int64_t from = used * to.row, end = total * to.row, up = (from + 15) / 16 * 16;
+    const int64_t first = up < end ? up : end, last = first > end / 16 * 16 ? first : end / 16 * 16;
+    const int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
+    for (int64_t i = first / 16 + i0; i < last / 16; i += step) reinterpret_cast<uint4*>(base)[i] = make_uint4(0, 0, 0, 0);
+    if (i0 < 8 && from + 2 * i0 < first) *reinterpret_cast<uint16_t*>(base + from + 2 * i0) = 0;
+    if (i0 < 8 && last + 2 * i0 < end) *reinterpret_cast<uint16_t*>(base + last + 2 * i0) = 0;
+}
+
 // One token: an element a value, 4 to a lane.  Bound by the launch: 64 x 2048 channels take 2.8 us of 0.3 us of traffic, and
 // the call 8.1 us from the host.
 template <bool XF, bool GF, int CPL>
@@ -102,6 +121,14 @@ hipError_t launch_scan_fwd(const ScanArgs& a, hipStream_t st) {
 
 hipError_t launch_scan_bwd(const ScanArgs& a, hipStream_t st) {
     a.x_f32 ? scan_bwd_of<true>(a, st) : scan_bwd_of<false>(a, st);
+    return hipGetLastError();
+}
+
+hipError_t launch_scan_zero_behind(const int32_t* cu, int64_t N, int64_t total, void* a, int64_t a_row, void* b,
+                                   int64_t b_row, hipStream_t st) {
+    const int64_t words = total * (a_row > b_row ? a_row : b_row) / 16, groups = words / 1024 + 1;
+    hipLaunchKernelGGL(scan_zero_behind_kernel, dim3((unsigned)(groups < 512 ? groups : 512), b ? 2 : 1), dim3(256), 0, st,
+                       Behind{a, a_row}, Behind{b, b_row}, cu, N, total);
     return hipGetLastError();
 }
 

@@ -42,6 +42,7 @@ def declare(L):
         "kda_scan_varlen_fwd": [vp] * 3 + [i64, i64] + [vp] * 6 + [i64, sf, vp, sz, vp],
         "kda_scan_bwd": [vp] * 11 + [i64, i64, i64, sf, vp, sz, vp],
         "kda_scan_varlen_bwd": [vp] * 3 + [i64, i64] + [vp] * 9 + [i64, sf, vp, sz, vp],
+        "kda_scan_zero_behind": [vp, i64, i64, vp, i64, vp, i64, vp],
         "kda_scan_step": [vp] * 5 + [i64, i64, sf, vp],
         "kda_qknorm_fwd": [vp] * 4 + [i64, i64] + [vp] * 10 + [i64, ci, ci, ci, ci, qf, vp],
         "kda_qknorm_bwd": [vp] * 4 + [i64, i64] + [vp] * 10 + [i64, ci, ci, ci, ci, ci, qf, vp, sz, vp],
@@ -339,12 +340,13 @@ class GatedScan(torch.autograd.Function):
 
 class VarlenGatedScan(torch.autograd.Function):
     """:class:`GatedScan` over packed sequences: ``y, h_final = VarlenGatedScan.apply(x, g, cu_seqlens, h0, g_logit,
-    complement, ckpt8)``.  The sequences must cover x: rows behind the last one have no gradient to give."""
+    complement, ckpt8)``.  Rows behind the last sequence, where x is longer, are zeros in y and have zero gradients."""
 
     @staticmethod
     def forward(ctx, x, g, cu_seqlens, h0=None, g_logit=False, complement=False, ckpt8=False):
         y, hf, saved = scan_varlen_fwd(x, g, cu_seqlens, h0, g_logit=g_logit, complement=complement,
                                        save="ckpt8" if ckpt8 else "carry")
+        _zero_behind(cu_seqlens, y)
         _keep_scan(ctx, x, g, h0, saved, g_logit, complement, ckpt8, cu_seqlens)
         return y, hf
 
@@ -354,7 +356,14 @@ class VarlenGatedScan(torch.autograd.Function):
         g, saved, x, h0, cu, form = _kept_scan(ctx)
         dx, dg, dh0 = scan_varlen_bwd(g, cu, _grad(dy, g, ctx.x_dtype), saved, x=x, h0=h0,
                                       dh_final=_grad(dh_final, None, torch.float32), **form)
+        _zero_behind(cu, dx, dg)
         return dx, dg, None, (dh0 if ctx.has_h0 else None), None, None, None
+
+
+def _zero_behind(cu, a, b=None):
+    """Zeros for the rows of a and b [total, channels...] that the calls over packed sequences leave unwritten."""
+    total, rows = a.shape[0], [0 if t is None else math.prod(t.shape[1:]) * t.element_size() for t in (a, b)]
+    _launch(load_library().kda_scan_zero_behind, a.device, _ptr(cu), cu.numel() - 1, total, _ptr(a), rows[0], _ptr(b), rows[1])
 
 
 def _grad(t, like, dtype):

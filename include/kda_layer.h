@@ -80,7 +80,7 @@ kda_status kda_scan_varlen_fwd(const void* x, const void* g, const int32_t* cu_s
  * Gradients for dL/dy = dy (x's type) and dL/dh_T = dh_final (float32, or NULL for zero):
  *   dx (x's type), dg (g's type; with respect to g before the clamp, which passes on [-5, 0]),
  *   dh0 float32 or NULL.  Either x and carry, or u_codes and u_scales, as the forward pass wrote
- * them; h0 as given to it.
+ * them; h0 as given to it.  Rows of dx and dg behind the last packed sequence are left as they were.
  */
 kda_status kda_scan_bwd(const void* x, const void* g, const float* h0, const float* carry, const uint8_t* u_codes,
                         const uint8_t* u_scales, const void* dy, const float* dh_final, void* dx, void* dg,
@@ -90,6 +90,11 @@ kda_status kda_scan_varlen_bwd(const void* x, const void* g, const int32_t* cu_s
                                const float* h0, const float* carry, const uint8_t* u_codes, const uint8_t* u_scales,
                                const void* dy, const float* dh_final, void* dx, void* dg, float* dh0, int64_t D,
                                const kda_scan_form* form, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Sets rows cu_seqlens[N] .. total - 1 of a and of b (or NULL) to zero: rows of a packed buffer behind its last
+ * sequence, which the calls above leave as they were.  Row sizes in bytes, even. */
+kda_status kda_scan_zero_behind(const int32_t* cu_seqlens, int64_t N, int64_t total, void* a, int64_t a_row_bytes,
+                                void* b, int64_t b_row_bytes, void* stream);
 
 /* One token per sequence: x, g, y [B, D], h_in, h_out [B, D] float32 (h_out == h_in allowed). */
 kda_status kda_scan_step(const void* x, const void* g, const float* h_in, float* h_out, void* y, int64_t B,

@@ -62,7 +62,11 @@ def stand_ins(monkeypatch):
         d = d_o.detach()
         return d * (k * v), d * (q * v), d * (q * k), torch.ones_like(g), torch.ones_like(beta), torch.zeros(1)
 
-    for name, f in (("scan_fwd", fwd), ("scan_bwd", bwd), ("scan_varlen_fwd", varlen_fwd), ("scan_varlen_bwd", varlen_bwd),
+    def zero_behind(cu, *tensors):
+        for t in tensors:
+            t[cu[-1]:] = 0
+
+    for name, f in (("_zero_behind", zero_behind), ("scan_fwd", fwd), ("scan_bwd", bwd), ("scan_varlen_fwd", varlen_fwd), ("scan_varlen_bwd", varlen_bwd),
                     ("qk_norm_rope_fwd", norm_fwd), ("qk_norm_rope_bwd", norm_bwd), ("chunk_fwd", chunk_fwd),
                     ("chunk_bwd", chunk_bwd)):
         monkeypatch.setattr(layer, name, f)
