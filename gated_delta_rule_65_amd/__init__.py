@@ -440,6 +440,13 @@ def varlen_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tenso
     return dq, dk, dv, dg, dbeta, ds0
 
 
+def _aligned_grad(t, dtype):
+    """An incoming gradient as the kernels take it.  Where it comes from torch (the parts of a concatenation, say) it may be
+    a view that begins anywhere, contiguous or not; the kernels read from 16-byte boundaries."""
+    t = t.to(dtype).contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
+
+
 class _NoGraph(torch.autograd.Function):
     """Hands a gradient on, and refuses to be differentiated."""
 
@@ -484,10 +491,8 @@ class ChunkKDA(torch.autograd.Function):
     @_first_order
     def backward(ctx, d_o, d_sf):
         q, k, v, g, beta, s0 = ctx.saved_tensors
-        d_o = torch.zeros_like(q[..., :1].float()).expand(*q.shape[:-1], v.shape[-1]).contiguous() \
-            if d_o is None else d_o.float().contiguous()
-        d_sf = None if d_sf is None else d_sf.float().contiguous()
-        dq, dk, dv, dg, dbeta, ds0 = chunk_bwd(q, k, v, g, beta, d_o, s0, d_sf)
+        dq, dk, dv, dg, dbeta, ds0 = chunk_bwd(q, k, v, g, beta, _aligned_grad(d_o, torch.float32), s0,
+                                               _aligned_grad(d_sf, torch.float32))
         return dq.to(q.dtype), dk.to(k.dtype), dv.to(v.dtype), dg, dbeta, (ds0 if s0 is not None else None)
 
 

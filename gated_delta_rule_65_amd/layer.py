@@ -14,7 +14,7 @@ from typing import NamedTuple, Optional, Tuple
 
 import torch
 
-from . import DTYPE, _check, _first_order, _need, _ptr, _stream, chunk_bwd, chunk_fwd, load_library
+from . import DTYPE, _aligned_grad, _check, _first_order, _need, _ptr, _stream, chunk_bwd, chunk_fwd, load_library
 
 NORM = {"l2": 0, "rms": 1}
 
@@ -333,8 +333,8 @@ class GatedScan(torch.autograd.Function):
     @_first_order
     def backward(ctx, dy, dh_final):
         g, saved, x, h0, _, form = _kept_scan(ctx)
-        dx, dg, dh0 = scan_bwd(g, _grad(dy, g, ctx.x_dtype), saved, x=x, h0=h0,
-                               dh_final=_grad(dh_final, None, torch.float32), **form)
+        dx, dg, dh0 = scan_bwd(g, _aligned_grad(dy, ctx.x_dtype), saved, x=x, h0=h0,
+                               dh_final=_aligned_grad(dh_final, torch.float32), **form)
         return dx, dg, (dh0 if ctx.has_h0 else None), None, None, None
 
 
@@ -354,8 +354,8 @@ class VarlenGatedScan(torch.autograd.Function):
     @_first_order
     def backward(ctx, dy, dh_final):
         g, saved, x, h0, cu, form = _kept_scan(ctx)
-        dx, dg, dh0 = scan_varlen_bwd(g, cu, _grad(dy, g, ctx.x_dtype), saved, x=x, h0=h0,
-                                      dh_final=_grad(dh_final, None, torch.float32), **form)
+        dx, dg, dh0 = scan_varlen_bwd(g, cu, _aligned_grad(dy, ctx.x_dtype), saved, x=x, h0=h0,
+                                      dh_final=_aligned_grad(dh_final, torch.float32), **form)
         _zero_behind(cu, dx, dg)
         return dx, dg, None, (dh0 if ctx.has_h0 else None), None, None, None
 
@@ -364,13 +364,6 @@ def _zero_behind(cu, a, b=None):
     """Zeros for the rows of a and b [total, channels...] that the calls over packed sequences leave unwritten."""
     total, rows = a.shape[0], [0 if t is None else math.prod(t.shape[1:]) * t.element_size() for t in (a, b)]
     _launch(load_library().kda_scan_zero_behind, a.device, _ptr(cu), cu.numel() - 1, total, _ptr(a), rows[0], _ptr(b), rows[1])
-
-
-def _grad(t, like, dtype):
-    """An incoming gradient as the kernels take it; where there is none, zeros of the shape of `like`, or None."""
-    if t is None:
-        return None if like is None else torch.zeros(like.shape, dtype=dtype, device=like.device)
-    return t.to(dtype).contiguous()
 
 
 def _keep_scan(ctx, x, g, h0, saved, g_logit, complement, ckpt8, cu=None):
@@ -548,8 +541,8 @@ class NormChunkKDA(torch.autograd.Function):
             q, k, v = kept
         form = {"weight_q": weight_q, "weight_k": weight_k, "pos": pos, "freqs": freqs, **ctx.form}
         qn, kn, _ = qk_norm_rope_fwd(q, k, **form)
-        dqn, dkn, dv, dg, dbeta, ds0 = chunk_bwd(qn, kn, v, g, beta, _grad(d_o, v, torch.float32), s0,
-                                                 _grad(d_sf, None, torch.float32))
+        dqn, dkn, dv, dg, dbeta, ds0 = chunk_bwd(qn, kn, v, g, beta, _aligned_grad(d_o, torch.float32), s0,
+                                                 _aligned_grad(d_sf, torch.float32))
         dq, dk, dwq, dwk = qk_norm_rope_bwd(q, k, dqn, dkn, **form)
         return (dq, dk, dv.to(ctx.dtype), dg, dbeta, ds0 if s0 is not None else None, dwq, dwk, None, None, None, None,
                 None, None)

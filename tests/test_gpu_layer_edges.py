@@ -44,3 +44,47 @@ def test_scan_autograd_gives_zeros_behind_the_last_sequence(lengths, total, xk, 
     for got, full in ((y, want), (x.grad, dx)):
         torch.testing.assert_close(got[:used].double().cpu(), torch.from_numpy(full[:used]), rtol=2.0 ** -7, atol=1e-4)
     assert torch.isfinite(g.grad).all() and torch.isfinite(h0.grad).all() and torch.isfinite(hf).all()
+
+
+# ----------------------------------------------------------------- views at any offset
+
+@pytest.mark.parametrize("C", [37, 36])
+def test_gradients_that_come_as_views_at_any_offset(C):
+    """A concatenation hands its backward pass contiguous views that begin anywhere."""
+    torch.manual_seed(3)
+    x, g = torch.randn(2, 3, C, device="cuda").bfloat16(), (-torch.rand(2, 3, C, device="cuda")).bfloat16()
+    grads = []
+    for joined in (False, True):
+        a, b = x.clone().requires_grad_(), g.clone().requires_grad_()
+        y = [kda.GatedScan.apply(a[i:i + 1].clone(), b[i:i + 1].clone())[0] for i in range(2)]
+        cu = torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+        z = [kda.VarlenGatedScan.apply(a[i].clone(), b[i].clone(), cu)[0] for i in range(2)]
+        w = torch.arange(12 * C, device="cuda").view(4, 3, C).bfloat16()
+        if joined:
+            torch.cat([*y, *(t[None] for t in z)]).backward(w)
+        else:
+            torch.autograd.backward([*y, *z], [w[0:1].clone(), w[1:2].clone(), w[2].clone(), w[3].clone()])
+        grads.append((a.grad, b.grad))
+    assert all(torch.equal(*pair) for pair in zip(*grads))
+
+
+@pytest.mark.parametrize("norm", [False, True])
+def test_layer_gradients_that_come_as_views_at_any_offset(norm):
+    torch.manual_seed(4)
+    B, T, H, D = 1, 5, 1, 64
+    q, k, v = (torch.randn(B, T, H, D, device="cuda") * 0.2 for _ in range(3))
+    g, beta = -torch.rand(B, T, H, D, device="cuda"), torch.rand(B, T, H, device="cuda")
+    f = kda.NormChunkKDA if norm else kda.ChunkKDA
+    grads = []
+    for joined in (False, True):
+        leaves = [t.clone().requires_grad_() for t in (q, k, v, g, beta)]
+        o, s = f.apply(*leaves)
+        w, ws = torch.randn(1 + o.numel(), generator=torch.Generator().manual_seed(1)).cuda(), torch.ones_like(s)
+        if joined:
+            torch.autograd.backward([torch.cat([torch.ones(1, device="cuda"), o.flatten()]),
+                                     torch.cat([torch.ones(1, device="cuda"), s.flatten()])],
+                                    [w, torch.ones(1 + s.numel(), device="cuda")])
+        else:
+            torch.autograd.backward([o, s], [w[1:].clone().view(o.shape), ws])
+        grads.append([t.grad for t in leaves])
+    assert all(torch.equal(*pair) for pair in zip(*grads))

@@ -129,3 +129,15 @@ def test_what_is_kept_passes_the_hooks_of_saved_tensors(stand_ins, name):
     assert (torch.int32 in kinds) == (name == "VarlenGatedScan")
     y.sum().backward()
     assert torch.isfinite(x.grad).all() and torch.isfinite(g.grad).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_gradients_come_to_the_kernels_whole_and_aligned(dtype):
+    """torch hands a backward pass views that begin anywhere; the kernels read 16 bytes at a time."""
+    whole = torch.arange(33, dtype=torch.float32).to(dtype)
+    for t in (whole[1:], whole[4:], whole[:32].view(4, 8).t(), whole[:1].expand(5), whole[16:]):
+        for to in (torch.float32, torch.bfloat16):
+            got = kda._aligned_grad(t, to)
+            assert got.is_contiguous() and got.data_ptr() % 16 == 0 and got.dtype == to
+            assert torch.equal(got, t.to(to))
+    assert kda._aligned_grad(whole, dtype) is whole  # no copy where none is needed
