@@ -478,8 +478,8 @@ def _first_order(backward):
 
 class ChunkKDA(torch.autograd.Function):
     """Autograd wrapper: ``o, s_final = ChunkKDA.apply(q, k, v, g, beta, s0)`` with the forward and
-    backward both in the library's kernels.  Gradients of q, k, v come back in fp32 and are cast
-    to the input type; s0 may be None.  Gradients of gradients are refused."""
+    backward both in the library's kernels.  Gradients come back in fp32 and are cast to the
+    input's type; s0 may be None.  Gradients of gradients are refused."""
 
     @staticmethod
     def forward(ctx, q, k, v, g, beta, s0=None):
@@ -491,9 +491,11 @@ class ChunkKDA(torch.autograd.Function):
     @_first_order
     def backward(ctx, d_o, d_sf):
         q, k, v, g, beta, s0 = ctx.saved_tensors
-        dq, dk, dv, dg, dbeta, ds0 = chunk_bwd(q, k, v, g, beta, _aligned_grad(d_o, torch.float32), s0,
+        # gates of 16 bits stand for their values: 32 bits hold them
+        dq, dk, dv, dg, dbeta, ds0 = chunk_bwd(q, k, v, g.float(), beta.float(), _aligned_grad(d_o, torch.float32), s0,
                                                _aligned_grad(d_sf, torch.float32))
-        return dq.to(q.dtype), dk.to(k.dtype), dv.to(v.dtype), dg, dbeta, (ds0 if s0 is not None else None)
+        return (dq.to(q.dtype), dk.to(k.dtype), dv.to(v.dtype), dg.to(g.dtype), dbeta.to(beta.dtype),
+                (ds0 if s0 is not None else None))
 
 
 from . import layer  # noqa: E402

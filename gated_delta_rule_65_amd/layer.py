@@ -541,8 +541,9 @@ class NormChunkKDA(torch.autograd.Function):
             q, k, v = kept
         form = {"weight_q": weight_q, "weight_k": weight_k, "pos": pos, "freqs": freqs, **ctx.form}
         qn, kn, _ = qk_norm_rope_fwd(q, k, **form)
-        dqn, dkn, dv, dg, dbeta, ds0 = chunk_bwd(qn, kn, v, g, beta, _aligned_grad(d_o, torch.float32), s0,
-                                                 _aligned_grad(d_sf, torch.float32))
+        # gates of 16 bits stand for their values: 32 bits hold them
+        dqn, dkn, dv, dg, dbeta, ds0 = chunk_bwd(qn, kn, v, g.float(), beta.float(), _aligned_grad(d_o, torch.float32),
+                                                 s0, _aligned_grad(d_sf, torch.float32))
         dq, dk, dwq, dwk = qk_norm_rope_bwd(q, k, dqn, dkn, **form)
-        return (dq, dk, dv.to(ctx.dtype), dg, dbeta, ds0 if s0 is not None else None, dwq, dwk, None, None, None, None,
-                None, None)
+        return (dq, dk, dv.to(ctx.dtype), dg.to(g.dtype), dbeta.to(beta.dtype), ds0 if s0 is not None else None, dwq, dwk,
+                None, None, None, None, None, None)

@@ -88,3 +88,23 @@ def test_layer_gradients_that_come_as_views_at_any_offset(norm):
             torch.autograd.backward([o, s], [w[1:].clone().view(o.shape), ws])
         grads.append([t.grad for t in leaves])
     assert all(torch.equal(*pair) for pair in zip(*grads))
+
+
+# ----------------------------------------------------------------- 16-bit gates in training
+
+@pytest.mark.parametrize("norm", [False, True])
+def test_layer_trains_with_16_bit_gates(norm):
+    """What the forward pass takes the backward pass takes: gradients at the gates' values, in their type."""
+    B, T, H, D = 1, 70, 2, 64
+    rng = np.random.default_rng(5)
+    q, k, v = (dev(0.2 * rng.normal(size=(B, T, H, D)), "bf16") for _ in range(3))
+    g, beta = dev(-rng.random(size=(B, T, H, D)), "bf16"), dev(rng.random(size=(B, T, H)), "bf16")
+    f = kda.NormChunkKDA if norm else kda.ChunkKDA
+    grads = []
+    for wide in (False, True):
+        leaves = [t.clone().requires_grad_() for t in (q, k, v, g.float() if wide else g, beta.float() if wide else beta)]
+        o, _ = f.apply(*leaves)
+        o.backward(torch.ones_like(o))
+        grads.append([t.grad for t in leaves])
+        assert all(t.grad.dtype == t.dtype for t in leaves)
+    assert all(torch.equal(a, b.to(a.dtype)) for a, b in zip(*grads))

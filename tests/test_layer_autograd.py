@@ -141,3 +141,11 @@ def test_gradients_come_to_the_kernels_whole_and_aligned(dtype):
             assert got.is_contiguous() and got.data_ptr() % 16 == 0 and got.dtype == to
             assert torch.equal(got, t.to(to))
     assert kda._aligned_grad(whole, dtype) is whole  # no copy where none is needed
+
+
+@pytest.mark.parametrize("name", ["ChunkKDA", "NormChunkKDA"])
+def test_gates_that_the_forward_pass_takes_in_16_bits_have_gradients(stand_ins, name):
+    q, g, beta = torch.randn(1, 5, 2, 4), -torch.rand(1, 5, 2, 4).bfloat16(), torch.rand(1, 5, 2).bfloat16()
+    leaves = [t.requires_grad_() for t in (q, g, beta)]
+    getattr(kda, name).apply(leaves[0], leaves[0], leaves[0], leaves[1], leaves[2])[0].sum().backward()
+    assert all(t.grad is not None and t.grad.dtype == t.dtype for t in leaves)
