@@ -516,11 +516,13 @@ class NormChunkKDA(torch.autograd.Function):
     q, k, v, g, beta, s0 as for :func:`chunk_fwd` (q and k raw, possibly columns of a projection), the rest as for
     :func:`qk_norm_rope_fwd`.  The normed q and k are not kept: the backward pass makes them again.  With ``ckpt8`` it
     keeps the raw q, k and v in 8 bits (3 bytes per channel instead of 6 in bf16) and the gradients are those at the
-    values these stand for."""
+    values these stand for.  Positions and frequencies are constants."""
 
     @staticmethod
     def forward(ctx, q, k, v, g, beta, s0=None, weight_q=None, weight_k=None, pos=None, freqs=None, norm="l2",
                 eps=0.0, interleaved=False, ckpt8=False):
+        if ctx.needs_input_grad[9]:
+            raise ValueError("freqs have no gradient here: pass them detached")
         ctx.form = {"norm": norm, "eps": eps, "interleaved": interleaved}
         qn, kn, raw = qk_norm_rope_fwd(q, k, weight_q=weight_q, weight_k=weight_k, pos=pos, freqs=freqs, ckpt8=ckpt8,
                                        **ctx.form)

@@ -149,3 +149,14 @@ def test_gates_that_the_forward_pass_takes_in_16_bits_have_gradients(stand_ins, 
     leaves = [t.requires_grad_() for t in (q, g, beta)]
     getattr(kda, name).apply(leaves[0], leaves[0], leaves[0], leaves[1], leaves[2])[0].sum().backward()
     assert all(t.grad is not None and t.grad.dtype == t.dtype for t in leaves)
+
+
+def test_frequencies_that_want_a_gradient_are_refused(stand_ins):
+    """The rotation gives its frequencies none; learned ones would stay as they were, silently."""
+    x, g, beta = torch.randn(1, 5, 2, 4).requires_grad_(), -torch.rand(1, 5, 2, 4), torch.rand(1, 5, 2)
+    pos, freqs = torch.arange(5)[None], torch.ones(2, dtype=torch.float64)
+    args = lambda f: (x, x, x, g, beta, None, None, None, pos, f)
+    with pytest.raises(ValueError, match="freqs"):
+        kda.NormChunkKDA.apply(*args(freqs.clone().requires_grad_()))
+    kda.NormChunkKDA.apply(*args(freqs))[0].sum().backward()
+    assert x.grad is not None
