@@ -521,8 +521,6 @@ class NormChunkKDA(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, g, beta, s0=None, weight_q=None, weight_k=None, pos=None, freqs=None, norm="l2",
                 eps=0.0, interleaved=False, ckpt8=False):
-        if ctx.needs_input_grad[9]:
-            raise ValueError("freqs have no gradient here: pass them detached")
         ctx.form = {"norm": norm, "eps": eps, "interleaved": interleaved}
         qn, kn, raw = qk_norm_rope_fwd(q, k, weight_q=weight_q, weight_k=weight_k, pos=pos, freqs=freqs, ckpt8=ckpt8,
                                        **ctx.form)
@@ -536,6 +534,8 @@ class NormChunkKDA(torch.autograd.Function):
     @_first_order
     def backward(ctx, d_o, d_sf):
         g, beta, s0, weight_q, weight_k, pos, freqs, *kept = ctx.saved_tensors
+        if any(ctx.needs_input_grad[9:10]):
+            raise ValueError("freqs have no gradient here: pass them detached")
         if ctx.ckpt8:
             q, k, v = (Packed8(kept[2 * i], kept[2 * i + 1], ctx.dtype) for i in range(3))
             v = ckpt8_unpack(v)

@@ -156,7 +156,10 @@ def test_frequencies_that_want_a_gradient_are_refused(stand_ins):
     x, g, beta = torch.randn(1, 5, 2, 4).requires_grad_(), -torch.rand(1, 5, 2, 4), torch.rand(1, 5, 2)
     pos, freqs = torch.arange(5)[None], torch.ones(2, dtype=torch.float64)
     args = lambda f: (x, x, x, g, beta, None, None, None, pos, f)
+    learned = freqs.clone().requires_grad_()
     with pytest.raises(ValueError, match="freqs"):
-        kda.NormChunkKDA.apply(*args(freqs.clone().requires_grad_()))
+        kda.NormChunkKDA.apply(*args(learned))[0].sum().backward()
+    with torch.no_grad():
+        kda.NormChunkKDA.apply(*args(learned))  # without gradients they are as good as any
     kda.NormChunkKDA.apply(*args(freqs))[0].sum().backward()
     assert x.grad is not None
