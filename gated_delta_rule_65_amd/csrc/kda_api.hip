@@ -660,7 +660,7 @@ size_t kda_scan_workspace_bytes(int64_t N, int64_t total, int64_t D) {
 
 size_t kda_scan_carry_bytes(int64_t N, int64_t total, int64_t D) {
     if (!scan_sizes(N, total, D) || total == 0) return 0;
-    return (size_t)((total / kda::kScanSeg + N) * D * 4);
+    return (size_t)(kda::scan_most_segments(N, total) * D * 4);
 }
 
 kda_status kda_qknorm_fwd(const void* q, const void* k, const uint8_t* q_scales, const uint8_t* k_scales,

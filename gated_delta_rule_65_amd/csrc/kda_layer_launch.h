@@ -52,6 +52,7 @@ inline int64_t scan_segments(const ScanArgs& a) {
     return scan_flat(a) ? (a.total + kScanSeg - 1) / kScanSeg : a.N * ((a.T_fixed + kScanSeg - 1) / kScanSeg);
 }
 int64_t scan_places(const ScanArgs& a);  // workgroups of a call
+int64_t scan_most_segments(int64_t N, int64_t total);
 int64_t scan_workspace_bytes(int64_t N, int64_t total, int64_t D);
 hipError_t launch_scan_fwd(const ScanArgs& a, hipStream_t st);
 hipError_t launch_scan_bwd(const ScanArgs& a, hipStream_t st);

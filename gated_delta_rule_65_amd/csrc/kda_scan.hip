@@ -106,12 +106,20 @@ int64_t scan_places(const ScanArgs& a) {
     return (a.D + wide - 1) / wide * scan_segments(a);
 }
 
-// For N sequences and total tokens, packed or of equal lengths: at most total/64 + N segments in all, each group and
-// block started anew for each sequence.
+// The most segments that N sequences of total tokens in all make, packed or of equal lengths.  Only equally long sequences of
+// half a segment or more have segments of their own, so there are at most total / 32 of these and each rounds up once;
+// packed rows are one chain.
+static int64_t own_chains(int64_t N, int64_t total) {
+    const int64_t most = total / (kScanSeg / 2) + 1;
+    return N < most ? N : most;
+}
+int64_t scan_most_segments(int64_t N, int64_t total) { return total / kScanSeg + own_chains(N, total); }
+
+// Groups and blocks are started anew for each chain.
 int64_t scan_workspace_bytes(int64_t N, int64_t total, int64_t D) {
     if (total <= kScanSeg) return 0;
-    const int64_t s = total / kScanSeg + N;
-    return 256 + 8 * D * (s + s / kGroup + N + s / kBlock + N);
+    const int64_t s = scan_most_segments(N, total), m = own_chains(N, total);
+    return 256 + 8 * D * (s + s / kGroup + m + s / kBlock + m);
 }
 
 hipError_t launch_scan_fwd(const ScanArgs& a, hipStream_t st) {

@@ -21,3 +21,40 @@ def test_zero_behind_nothing_to_do():
     assert call("kda_scan_zero_behind", BEHIND, total=0, a=None, cu=None) == 0
     assert call("kda_scan_zero_behind", BEHIND, a_row=0, a=None, cu=None) == 0
     assert last_error() == ""
+
+
+def segments(N, T=None, total=None):
+    """Chains and the segments of each: of equally long sequences of T tokens, or of packed rows."""
+    if T is not None and T >= 32:
+        return N, -(-T // 64)
+    return 1, -(-(total if T is None else N * T) // 64)
+
+
+def sizes(N, total, D):
+    return kda.scan_workspace_bytes(N, total, D), kda.scan_carry_bytes(N, total, D)
+
+
+def used(chains, per, D):
+    """Bytes of the words that segments, groups of 8 and blocks of 64 of them publish (none where no chain is longer than a
+    segment), and of the states at the segments."""
+    words = chains * D * (per + -(-per // 8) + -(-per // 64))
+    return 256 + 8 * words if per > 1 else 0, chains * per * D * 4
+
+
+@pytest.mark.parametrize("N", [1, 2, 3, 7, 31, 64, 65, 255, 1000, 16384])
+def test_scan_sizes_hold_what_is_used(N):
+    for T in [*range(1, 70), 95, 96, 127, 128, 129, 511, 512, 513, 4095, 4096, 4097, 4160, 8192]:
+        for layout in (dict(T=T), dict(total=N * T)):
+            got, want = sizes(N, N * T, 5), used(*segments(N, **layout), 5)
+            assert got[0] >= want[0] and got[1] >= want[1], (N, layout)
+    for total in (1, 2, 63, 64, 65, 100, 640, 4097, 100003):  # packed: any number of sequences, most of them empty
+        got, want = sizes(N, total, 3), used(*segments(N, total=total), 3)
+        assert got[0] >= want[0] and got[1] >= want[1], (N, total)
+
+
+@pytest.mark.parametrize("N,total", [(16384, 32768), (1 << 20, 1 << 20), (100000, 7), (4096, 4096 * 16), (1 << 16, 65)])
+def test_scan_sizes_do_not_grow_with_empty_and_short_sequences(N, total):
+    """Only sequences of 32 tokens and more have segments of their own."""
+    D, segs = 8, -(-total // 64)
+    ws, carry = sizes(N, total, D)
+    assert ws <= 256 + 8 * D * (8 * segs + 8) and carry <= 4 * D * (3 * segs + 1)
