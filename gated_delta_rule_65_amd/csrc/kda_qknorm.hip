@@ -202,11 +202,23 @@ __device__ __forceinline__ void store_chunks(void* p, int64_t row, const Place& 
     }
 }
 
-// Cosine and sine of pos * freq radians.  The product is taken in 64 bits and reduced to a fraction of a turn there, so that
-// far positions keep float32's accuracy.
-__device__ __forceinline__ void angle(double pos, double freq, float& c, float& s) {
-    constexpr double inv_2pi = 0.15915494309189533577;
-    const double t = pos * (freq * inv_2pi);
+// Cosine and sine of pos * freq radians.  Only the fraction of a turn counts, and pos * freq / 2 pi may be many turns: freq / 2 pi
+// is taken as a sum hi + lo of two 64-bit numbers and each product with the position as its rounded value and what that
+// leaves, so that of 2^k turns the fraction keeps 2^(k - 106): angles below 2^80 radians are as good as small ones, for
+// any position (64-bit ones go in two parts, each a whole number of at most 40 bits).  Contraction off: the rounded
+// product has to be the same number in both of its uses.
+__device__ __forceinline__ double turn_part(double p, double hi, double lo) {
+#pragma clang fp contract(off)
+    const double t = p * hi, e = fma(p, lo, fma(p, hi, -t));
+    return (t - rint(t)) + (e - rint(e));
+}
+__device__ __forceinline__ void angle(int64_t pos, double freq, bool wide, float& c, float& s) {
+#pragma clang fp contract(off)
+    constexpr double inv_hi = 0x1.45f306dc9c883p-3, inv_lo = -0x1.6b01ec5417056p-57;  // 1 / 2 pi
+    const double hi = freq * inv_hi, lo = fma(freq, inv_lo, fma(freq, inv_hi, -hi));
+    double t;
+    if (wide) t = turn_part((double)(pos >> 24) * 0x1p24, hi, lo) + turn_part((double)(int32_t)(pos & 0xffffff), hi, lo);
+    else t = turn_part((double)(int32_t)pos, hi, lo);
     sincospif(2.f * (float)(t - rint(t)), &s, &c);
 }
 
@@ -226,14 +238,15 @@ struct Tables {
     // What the tables are made from is asked for before the rows, and used while those are on their way: loads come
     // back in order.
     struct Source {
-        double pos, freq;
+        int64_t pos;
+        double freq;
         float w;
     };
-    static __device__ __forceinline__ double position(const QkArgs& a, int64_t t) {
-        return a.pos64 ? (double)static_cast<const int64_t*>(a.pos)[t] : (double)static_cast<const int32_t*>(a.pos)[t];
+    static __device__ __forceinline__ int64_t position(const QkArgs& a, int64_t t) {
+        return a.pos64 ? static_cast<const int64_t*>(a.pos)[t] : static_cast<const int32_t*>(a.pos)[t];
     }
     static __device__ __forceinline__ Source first_of(const QkArgs& a, int64_t t0, int tokens, bool weighted) {
-        Source s{0.0, 0.0, 1.f};
+        Source s{0, 0.0, 1.f};
         const int pairs = a.rot / 2, i = threadIdx.x;
         if (i < tokens * pairs) {
             const int t = (uint32_t)i / (uint32_t)pairs;
@@ -256,7 +269,8 @@ struct Tables {
     }
     __device__ __forceinline__ void fill_angles(const QkArgs& a, int64_t t0, int tokens, const Source& first) {
         const int pairs = a.rot / 2;
-        double pos = first.pos, freq = first.freq;
+        int64_t pos = first.pos;
+        double freq = first.freq;
         for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
             const int t = (uint32_t)i / (uint32_t)pairs, q = i - t * pairs;
             if (i != (int)threadIdx.x) {
@@ -264,7 +278,7 @@ struct Tables {
                 freq = a.freqs[q];
             }
             const int at = slot(t, q, a.rot, a.interleaved);
-            angle(pos, freq, c[at], s[at]);
+            angle(pos, freq, a.pos64, c[at], s[at]);
         }
     }
     __device__ __forceinline__ void weight(int side, int j, float v[16]) const {

@@ -114,8 +114,8 @@ size_t kda_scan_carry_bytes(int64_t N, int64_t total, int64_t D);
  *     z = w * r x   (w per channel of a head, shared by the heads; NULL: ones)
  *     y = z with the pairs of its first `rot` channels turned by pos * freqs[i], i < rot / 2:
  *         pair i is (i, i + rot/2), or (2i, 2i + 1) with interleaved
- * Angles are taken in float64 and reduced before the sine and cosine: positions of any size keep
- * float32's accuracy.
+ * Angles are reduced to a fraction of a turn in twice float64's precision before the sine and cosine:
+ * positions of any size keep float32's accuracy, as long as |pos * freq| is below 2^80 radians.
  */
 enum { KDA_NORM_L2 = 0, KDA_NORM_RMS = 1 };
 

@@ -1,5 +1,7 @@
 """The operators around the recurrence at the edges of what their calls allow: buffers longer than their sequences, views at
 any offset, 16-bit gates in training, positions and rows of any size."""
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -108,3 +110,41 @@ def test_layer_trains_with_16_bit_gates(norm):
         grads.append([t.grad for t in leaves])
         assert all(t.grad.dtype == t.dtype for t in leaves)
     assert all(torch.equal(a, b.to(a.dtype)) for a, b in zip(*grads))
+
+
+# ----------------------------------------------------------------- positions and rows of any size
+
+PI = Fraction("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899862803482534211706798214808651")
+
+
+def angles(pos, freqs):
+    """pos * freq mod a turn, in rational arithmetic up to the last rounding."""
+    out = np.zeros((len(pos), len(freqs)))
+    for i, p in enumerate(pos):
+        for j, f in enumerate(freqs):
+            turns = int(p) * Fraction(float(f)) / (2 * PI)
+            out[i, j] = float((turns - round(turns)) * 2 * PI)
+    return out
+
+
+FAR = [0, 1, -1, 2 ** 28, 2 ** 30 + 1, 2 ** 31 - 1, 2 ** 36 - 5, 2 ** 40, -2 ** 40 - 1, 2 ** 50 + 3, 2 ** 53 + 1, -2 ** 53 - 1,
+       2 ** 62 + 12345, 2 ** 63 - 1, -2 ** 63]
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** 12])
+@pytest.mark.parametrize("kind", [np.int64, np.int32])
+def test_qk_any_position_keeps_its_angle(kind, scale, interleaved):
+    pos = np.array([p for p in FAR if np.iinfo(kind).min <= p <= np.iinfo(kind).max], kind)
+    n, H, D = len(pos), 2, 64
+    rng = np.random.default_rng(8)
+    q, k, dq, dk = (dev(rng.normal(size=(n, H, D))) for _ in range(4))
+    f = scale * 10000.0 ** (-np.arange(0, D, 2) / D)
+    angle = angles(pos, f)
+    form = {"pos": torch.from_numpy(pos).cuda(), "freqs": torch.from_numpy(f).cuda(), "eps": 1e-6, "interleaved": interleaved}
+    out = kda.qk_norm_rope_fwd(q, k, **form)
+    grads = kda.qk_norm_rope_bwd(q, k, dq, dk, **form)
+    for i, (x, d) in enumerate(((q, dq), (k, dk))):
+        y, dx, _ = ref.qk_norm(host(x), None, angle, False, np.float32(1e-6), interleaved, host(d))
+        near(out[i], y, "f32", "y")
+        near(grads[i], dx, "f32", "dx")
