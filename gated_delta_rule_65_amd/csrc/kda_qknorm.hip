@@ -80,9 +80,12 @@ __device__ __forceinline__ float row_sum(float v) {
 }
 
 // (s |x|^2 + eps)^(-1/2) of a row, 0 where that is 0.  Rows whose sum of squares leaves float32's comfortable
-// range are summed again at a power of two of their own size.
+// range are summed again at a power of two of their own size.  A root beyond 2^66 would have a reciprocal near or below the
+// smallest normal float (2^-132 at worst): such a row is scaled down by 2^64 in place, `unit` says by what (else 1), and
+// what is returned is the root's reciprocal for the row as it then is.
 template <int LANES>
-__device__ __forceinline__ float row_rsqrt(const float x[16], float s, float eps) {
+__device__ __forceinline__ float row_rsqrt(float x[16], float s, float eps, float& unit) {
+    unit = 1.f;
     float ss = 0.f;
 #pragma unroll
     for (int k = 0; k < 16; ++k) ss = fmaf(x[k], x[k], ss);
@@ -104,6 +107,12 @@ __device__ __forceinline__ float row_rsqrt(const float x[16], float s, float eps
     }
     sum = row_sum<LANES>(sum);
     const double total = (double)sum * s * ldexp(1.0, 2 * e) + eps;
+    if (total > 0x1p132) {
+        unit = 0x1p-64f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) x[k] *= unit;
+        return (float)(0x1p64 / sqrt(total));
+    }
     return total < 0x1p-252 ? 0.f : (float)(1.0 / sqrt(total));
 }
 
@@ -409,7 +418,8 @@ __global__ __launch_bounds__(kThreads, 4) void qknorm_fwd_kernel(QkArgs a, int p
                     pack_row<D>(x, p, j, a.rot, a.interleaved, (key ? a.k8 : a.q8) + out,
                                 (key ? a.k8s : a.q8s) + out / kCkptBlock);
             }
-            const float r = row_rsqrt<LANES>(x, a.rms ? 1.f / D : 1.f, a.eps);
+            float unit;
+            const float r = row_rsqrt<LANES>(x, a.rms ? 1.f / D : 1.f, a.eps, unit);
 #pragma unroll
             for (int k = 0; k < 16; ++k) x[k] *= r;
             if (weighted) {
@@ -502,7 +512,8 @@ __global__ __launch_bounds__(kThreads, 3) void qknorm_bwd_kernel(QkArgs a, Sides
                 float x[16], d[16];
                 values_of<D>(c[i], p, x);
                 values_of<D>(g[i], p, d);
-                const float r = row_rsqrt<LANES>(x, sc, a.eps);
+                float unit;
+                const float r = row_rsqrt<LANES>(x, sc, a.eps, unit);
                 tab.turn(d, tok[i], j, p, a.rot, a.interleaved, -1.f);
 #pragma unroll
                 for (int k = 0; k < 16; ++k) x[k] *= r;
@@ -521,6 +532,10 @@ __global__ __launch_bounds__(kThreads, 3) void qknorm_bwd_kernel(QkArgs a, Sides
                 dot = row_sum<LANES>(dot) * sc;
 #pragma unroll
                 for (int k = 0; k < 16; ++k) x[k] = r * fmaf(-dot, x[k], d[k]);
+                if (unit != 1.f) {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) x[k] *= unit;
+                }
                 store_chunks<D, STREAM, F32>(to, out[i], p, x);
             }
         }

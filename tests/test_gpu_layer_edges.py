@@ -148,3 +148,24 @@ def test_qk_any_position_keeps_its_angle(kind, scale, interleaved):
         y, dx, _ = ref.qk_norm(host(x), None, angle, False, np.float32(1e-6), interleaved, host(d))
         near(out[i], y, "f32", "y")
         near(grads[i], dx, "f32", "dx")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("norm", ["l2", "rms"])
+def test_qk_rows_of_the_largest_size(D, norm):
+    """Rows whose length is beyond float32 altogether are normed as closely as others, both ways."""
+    rng = np.random.default_rng(9)
+    size = np.linspace(0.9, 1.0, 4001).astype(np.float32) * np.float32(3.4e38)
+    r = 1 / (size.astype(float) * np.sqrt(D if norm == "l2" else 1))
+    size = size[np.argsort(-np.abs(r.astype(np.float32) / r - 1))[:40]]  # whose reciprocal length rounds worst as one float
+    q = dev(size[:, None, None] * rng.choice([-1.0, 1.0], size=(40, 1, D)))
+    k = dev(1e30 * rng.normal(size=(40, 1, D)))
+    dq, dk = (dev(2.0 ** 60 * rng.normal(size=(40, 1, D))) for _ in range(2))
+    w = dev(1 + 0.2 * rng.normal(size=D))
+    out = kda.qk_norm_rope_fwd(q, k, weight_q=w, weight_k=w, norm=norm)
+    grads = kda.qk_norm_rope_bwd(q, k, dq, dk, weight_q=w, weight_k=w, norm=norm)
+    for i, (x, d) in enumerate(((q, dq), (k, dk))):
+        y, dx, dw = ref.qk_norm(host(x), host(w), np.zeros((40, 0)), norm == "rms", 0.0, False, host(d))
+        near(out[i], y, "f32", "y")
+        near(grads[i], dx, "f32", "dx")
+        near(grads[2 + i], dw, "f32", "dw")
