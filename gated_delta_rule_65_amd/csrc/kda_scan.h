@@ -306,15 +306,15 @@ __device__ __forceinline__ Pair group_before(const ScanArgs& a, const ScanPlan& 
 }
 
 // What the waves of a workgroup tell one another of its channels: their pairs, then the states before them, and
-// the state before the segment's group.
+// the state before the segment's group.  put() and take() move 16 bytes at a time.
 template <int CPL>
-struct Exchange {
+struct alignas(16) Exchange {
     float A[kWaves][64 * CPL], b[kWaves][64 * CPL], before[64 * CPL];
 };
 // Half of what a lane keeps of its rows in the backward pass, so that two workgroups' registers fit a CU.
 constexpr int kKept = kRows / 2;
 template <int CPL, bool USED>
-struct Kept {
+struct alignas(16) Kept {
     float rows[USED ? kKept : 1][USED ? kWaves : 1][USED ? 64 * CPL : 1];
 };
 template <int CPL>

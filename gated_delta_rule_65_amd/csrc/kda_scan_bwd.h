@@ -162,8 +162,8 @@ constexpr int bwd_waves(bool xf, bool gf, bool packed) { return packed && !xf &&
 
 template <bool XF, bool GF, int CPL, bool FLAT, bool PACKED, bool STREAM>
 __global__ __launch_bounds__(kThreads, bwd_waves(XF, GF, PACKED)) void scan_bwd_kernel(ScanArgs a, ScanPlan p) {
-    __shared__ __align__(16) Exchange<CPL> x;
-    __shared__ __align__(16) Kept<CPL, !PACKED> kept;
+    __shared__ Exchange<CPL> x;
+    __shared__ Kept<CPL, !PACKED> kept;
     __shared__ uint32_t place;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t pl = take_place(p.counter, &place);

@@ -1,7 +1,10 @@
 """Refusals and sizes of the calls around the operators' edges, before any HIP call."""
+import subprocess
+
 import pytest
 
 import gated_delta_rule_65_amd as kda
+from gated_delta_rule_65_amd import _build
 from tests.test_layer_abi import FAKE, call, expect, last_error
 
 BEHIND = dict(cu=FAKE, N=2, total=9, a=FAKE, a_row=6, b=None, b_row=0, stream=None)
@@ -58,3 +61,17 @@ def test_scan_sizes_do_not_grow_with_empty_and_short_sequences(N, total):
     D, segs = 8, -(-total // 64)
     ws, carry = sizes(N, total, D)
     assert ws <= 256 + 8 * D * (8 * segs + 8) and carry <= 4 * D * (3 * segs + 1)
+
+
+def test_scan_lds_buffers_are_aligned_for_wide_access(tmp_path):
+    """Their rows are read and written 16 bytes at a time, in every kernel that declares one."""
+    probe = tmp_path / "probe.hip"
+    probe.write_text("""#include "kda_scan.h"
+static_assert(alignof(kda::Exchange<1>) >= 16 && alignof(kda::Exchange<4>) >= 16, "exchange");
+static_assert(alignof(kda::Kept<1, true>) >= 16 && alignof(kda::Kept<4, true>) >= 16, "kept");
+static_assert(sizeof(kda::Exchange<4>::A[0]) % 16 == 0 && sizeof(kda::Kept<4, true>::rows[0][0]) % 16 == 0, "rows");
+static_assert(offsetof(kda::Exchange<4>, b) % 16 == 0 && offsetof(kda::Exchange<4>, before) % 16 == 0, "parts");
+""")
+    r = subprocess.run([_build.hipcc(), *_build.HIPCC_FLAGS, "--offload-device-only", "-fsyntax-only", str(probe)],
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
