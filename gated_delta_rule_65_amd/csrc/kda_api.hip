@@ -31,8 +31,6 @@ kda_status ok() {
     return KDA_OK;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 kda_status check_head_dims(int H, int Dk, int Dv) {
     if (H < 1 || H > 65536) return fail(KDA_ERR_BAD_SHAPE, "H must be in [1, 65536] (got %d)", H);
     if (Dk != 64 && Dk != 128) return fail(KDA_ERR_BAD_SHAPE, "Dk must be 64 or 128 (got %d)", Dk);
@@ -49,12 +47,14 @@ struct Ptr {
     const void* p;
     const char* name;
     bool required;
+    int align = 16;
 };
 
 kda_status check_ptrs(std::initializer_list<Ptr> ptrs) {
     for (const Ptr& x : ptrs) {
         if (x.required && !x.p) return fail(KDA_ERR_NULL_ARG, "%s is NULL", x.name);
-        if (x.p && !aligned16(x.p)) return fail(KDA_ERR_MISALIGNED, "%s is not 16-byte aligned", x.name);
+        if (reinterpret_cast<uintptr_t>(x.p) % x.align)
+            return fail(KDA_ERR_MISALIGNED, "%s is not %d-byte aligned", x.name, x.align);
     }
     return KDA_OK;
 }
@@ -148,6 +148,13 @@ kda_status check_ckpt8(int64_t rows, int64_t cols, kda_dtype dtype) {
     return KDA_OK;
 }
 
+// Rows that no wide load divides are read a value at a time and may begin at any.
+kda_status ckpt8_ptrs(const void* x, const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, kda_dtype dtype) {
+    const bool any = rows > 0 && cols > 0;
+    const int value = cols % 8 == 0 ? 16 : dtype == KDA_F32 ? 4 : 2, byte = cols % 8 == 0 ? 16 : 1;
+    return check_ptrs({{x, "x", any, value}, {codes, "codes", any, byte}, {scales, "scales", any, byte}});
+}
+
 bool scan_sizes(int64_t N, int64_t total, int64_t D) {
     return N >= 1 && N <= 0x7fffffff && total >= 0 && D >= 1 && D <= kda::kMaxChannels && total <= kMostElements / D &&
            N <= kMostElements / D;
@@ -203,13 +210,27 @@ kda_status scan_ws(kda::ScanArgs& a, void* ws, size_t bytes, const char* what) {
     return KDA_OK;
 }
 
+// What a scan's rows are aligned to: 16 bytes, or an element where they are read one at a time.
+struct ScanAlign {
+    int x, g, state, code;
+    ScanAlign(const kda::ScanArgs& a, int64_t together) {
+        const bool wide = together % 4 == 0;
+        x = wide ? 16 : a.x_f32 ? 4 : 2;
+        g = wide ? 16 : a.g_f32 ? 4 : 2;
+        state = wide ? 16 : 4;
+        code = wide ? 16 : 1;
+    }
+};
+
 kda_status scan_fwd(kda::ScanArgs& a, const void* x, const void* g, const float* h0, void* y, float* h_final,
                     float* carry, uint8_t* u, uint8_t* us, void* ws, size_t ws_bytes, void* stream, const char* what) {
     kda_status st;
     const bool tokens = a.N > 0 && a.total > 0, save = tokens && (u || us);
-    if ((st = check_ptrs({{x, "x", tokens}, {g, "g", tokens}, {y, "y", tokens}, {h0, "h0", false},
-                          {h_final, "h_final", false}, {carry, "carry", false}, {u, "u_codes", save},
-                          {us, "u_scales", save}, {ws, "workspace", false}})) != KDA_OK)
+    const ScanAlign to(a, a.D);
+    if ((st = check_ptrs({{x, "x", tokens, to.x}, {g, "g", tokens, to.g}, {y, "y", tokens, to.x},
+                          {h0, "h0", false, to.state}, {h_final, "h_final", false, to.state},
+                          {carry, "carry", false, to.state}, {u, "u_codes", save, to.code},
+                          {us, "u_scales", save, to.code}, {ws, "workspace", false}})) != KDA_OK)
         return st;
     if (overlap(h0, h_final, a.N * a.D * 4, a.N * a.D * 4))
         return fail(KDA_ERR_BAD_SHAPE, "%s: h_final must not overlap h0", what);
@@ -234,10 +255,12 @@ kda_status scan_bwd(kda::ScanArgs& a, const void* x, const void* g, const float*
     const bool need_x = tokens && !packed;
     if (need_x && !(x && carry))
         return fail(KDA_ERR_NULL_ARG, "%s: either x and carry or u_codes and u_scales must be given", what);
-    if ((st = check_ptrs({{x, "x", false}, {g, "g", tokens}, {dy, "dy", tokens}, {dx, "dx", tokens},
-                          {dg, "dg", tokens}, {h0, "h0", false}, {carry, "carry", false}, {u, "u_codes", need_u},
-                          {us, "u_scales", need_u}, {dh_final, "dh_final", false}, {dh0, "dh0", false},
-                          {ws, "workspace", false}})) != KDA_OK)
+    const ScanAlign to(a, a.D);
+    if ((st = check_ptrs({{x, "x", false, to.x}, {g, "g", tokens, to.g}, {dy, "dy", tokens, to.x},
+                          {dx, "dx", tokens, to.x}, {dg, "dg", tokens, to.g}, {h0, "h0", false, to.state},
+                          {carry, "carry", false, to.state}, {u, "u_codes", need_u, to.code},
+                          {us, "u_scales", need_u, to.code}, {dh_final, "dh_final", false, to.state},
+                          {dh0, "dh0", false, to.state}, {ws, "workspace", false}})) != KDA_OK)
         return st;
     if (overlap(dh0, dh_final, a.N * a.D * 4, a.N * a.D * 4) || overlap(dh0, h0, a.N * a.D * 4, a.N * a.D * 4))
         return fail(KDA_ERR_BAD_SHAPE, "%s: dh0 must not overlap dh_final or h0", what);
@@ -287,8 +310,8 @@ kda_status qk_inputs(kda::QkArgs& a, const void* q, const void* k, const uint8_t
         return fail(KDA_ERR_BAD_SHAPE, "q and k exceed 2^40 elements");
     const bool any = tokens > 0, packed = any && (qs || ks), turned = any && f->rot > 0;
     if ((st = check_ptrs({{q, "q", any}, {k, "k", any}, {qs, "q_scales", packed}, {ks, "k_scales", packed},
-                          {wq, "wq", false}, {wk, "wk", false}, {pos, "pos", turned},
-                          {freqs, "freqs", turned}})) != KDA_OK)
+                          {wq, "wq", false}, {wk, "wk", false}, {pos, "pos", turned, f->rot ? f->pos_bytes : 1},
+                          {freqs, "freqs", turned, f->rot ? 8 : 1}})) != KDA_OK)
         return st;
     a.q = q;
     a.k = k;
@@ -555,7 +578,7 @@ kda_status kda_ckpt8_pack(const void* x, uint8_t* codes, uint8_t* scales, int64_
     kda_status st;
     if ((st = check_ckpt8(rows, cols, dtype)) != KDA_OK) return st;
     const bool any = rows > 0 && cols > 0;
-    if ((st = check_ptrs({{x, "x", any}, {codes, "codes", any}, {scales, "scales", any}})) != KDA_OK) return st;
+    if ((st = ckpt8_ptrs(x, codes, scales, rows, cols, dtype)) != KDA_OK) return st;
     if (!any) return ok();
     return launched(kda::launch_ckpt8_pack(x, codes, scales, rows, cols, dtype == KDA_F32,
                                            static_cast<hipStream_t>(stream)), "kda_ckpt8_pack");
@@ -566,7 +589,7 @@ kda_status kda_ckpt8_unpack(const uint8_t* codes, const uint8_t* scales, void* x
     kda_status st;
     if ((st = check_ckpt8(rows, cols, dtype)) != KDA_OK) return st;
     const bool any = rows > 0 && cols > 0;
-    if ((st = check_ptrs({{x, "x", any}, {codes, "codes", any}, {scales, "scales", any}})) != KDA_OK) return st;
+    if ((st = ckpt8_ptrs(x, codes, scales, rows, cols, dtype)) != KDA_OK) return st;
     if (!any) return ok();
     return launched(kda::launch_ckpt8_unpack(codes, scales, x, rows, cols, dtype == KDA_F32,
                                              static_cast<hipStream_t>(stream)), "kda_ckpt8_unpack");
@@ -641,8 +664,9 @@ kda_status kda_scan_step(const void* x, const void* g, const float* h_in, float*
     if ((st = scan_batch(a, B, 1)) != KDA_OK || (st = scan_form(a, D, form)) != KDA_OK) return st;
     if (B * D / (B * D % 4 ? 1 : 4) > kda::kMaxThreads - 256) return fail(KDA_ERR_BAD_SHAPE, "B*D exceeds the grid limit");
     const bool any = B > 0;
-    if ((st = check_ptrs({{x, "x", any}, {g, "g", any}, {h_in, "h_in", any}, {h_out, "h_out", any},
-                          {y, "y", any}})) != KDA_OK)
+    const ScanAlign to(a, B * D);
+    if ((st = check_ptrs({{x, "x", any, to.x}, {g, "g", any, to.g}, {h_in, "h_in", any, to.state},
+                          {h_out, "h_out", any, to.state}, {y, "y", any, to.x}})) != KDA_OK)
         return st;
     if (h_in != h_out && overlap(h_in, h_out, B * D * 4, B * D * 4))
         return fail(KDA_ERR_BAD_SHAPE, "h_in and h_out overlap without being the same buffer");

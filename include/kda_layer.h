@@ -3,7 +3,7 @@
  * channels (the recurrence's sibling with a vector state), the head norm of queries and keys with
  * the position rotation, and activation checkpoints in 8 bits.  Same library, conventions, status
  * codes and kda_last_error() as kda.h: DEVICE pointers, row-major and contiguous unless a stride
- * is named, 16-byte aligned; the caller owns every buffer, the library allocates nothing; calls
+ * is named, 16-byte aligned unless said otherwise; the caller owns every buffer, the library allocates nothing; calls
  * are asynchronous on `stream`, validated on the host before any launch, and never abort or
  * throw.  Outputs must not overlap inputs or one another except where an argument says so.
  */
@@ -30,7 +30,8 @@ extern "C" {
  * 1.875 * 2^127 are packed as that, so that they do not unpack to infinity.
  */
 
-/* x [rows, cols] dtype -> codes [rows, cols], scales [rows, ceil(cols / 32)]; cols below 2^31. */
+/* x [rows, cols] dtype -> codes [rows, cols], scales [rows, ceil(cols / 32)]; cols below 2^31.  Where cols
+ * is not a multiple of 8, rows are read a value at a time and the buffers may begin at any value. */
 kda_status kda_ckpt8_pack(const void* x, uint8_t* codes, uint8_t* scales, int64_t rows, int64_t cols,
                           kda_dtype dtype, void* stream);
 
@@ -45,7 +46,8 @@ kda_status kda_ckpt8_unpack(const uint8_t* codes, const uint8_t* scales, void* x
  *     h_t = a_t h_{t-1} + w_t x_t,    w_t = 1, or 1 - a_t with complement;     y_t = h_t
  * x, g, y: [B, T, D] (or [total, D] packed); h0, h_final: [B, D] (or [N, D]) float32.  y has x's
  * type and is rounded once; the state is float32 throughout.  D is any number of channels up
- * to 2^24, heads and their sizes flattened; D % 4 == 0 takes wide loads.  A non-finite x or g makes the
+ * to 2^24, heads and their sizes flattened.  D % 4 == 0 takes wide loads; others are read an element
+ * at a time, and their buffers may begin at any element (not the workspace).  A non-finite x or g makes the
  * rest of its own sequence and channel non-finite and touches nothing else.
  */
 typedef struct {
@@ -96,7 +98,8 @@ kda_status kda_scan_varlen_bwd(const void* x, const void* g, const int32_t* cu_s
 kda_status kda_scan_zero_behind(const int32_t* cu_seqlens, int64_t N, int64_t total, void* a, int64_t a_row_bytes,
                                 void* b, int64_t b_row_bytes, void* stream);
 
-/* One token per sequence: x, g, y [B, D], h_in, h_out [B, D] float32 (h_out == h_in allowed). */
+/* One token per sequence: x, g, y [B, D], h_in, h_out [B, D] float32 (h_out == h_in allowed).  Where B * D is
+ * not a multiple of 4 they may begin at any element. */
 kda_status kda_scan_step(const void* x, const void* g, const float* h_in, float* h_out, void* y, int64_t B,
                          int64_t D, const kda_scan_form* form, void* stream);
 
@@ -133,7 +136,7 @@ typedef struct {
  *     a wider projection.  With q_scales and k_scales given (both or neither), q and k are packed
  *     codes instead, contiguous, and `dtype` is the type of the outputs.
  *   wq, wk [D] float32 or NULL; pos [tokens]; freqs [rot/2] float64, radians per position (both
- *     may be NULL when rot = 0).
+ *     may be NULL when rot = 0; they may begin at any element).
  *   q_out, k_out: contiguous, dtype.
  *   q8, q8_scales, k8, k8_scales: q and k packed in 8 bits as by kda_ckpt8_pack with rows of D, for the
  *     backward pass; NULL (all four) not to, and refused where q and k are packed already.

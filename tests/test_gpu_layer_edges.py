@@ -169,3 +169,47 @@ def test_qk_rows_of_the_largest_size(D, norm):
         near(out[i], y, "f32", "y")
         near(grads[i], dx, "f32", "dx")
         near(grads[2 + i], dw, "f32", "dw")
+
+
+# ----------------------------------------------------------------- rows read an element at a time begin anywhere
+
+@pytest.mark.parametrize("xk,gk", [("bf16", "bf16"), ("f32", "f32"), ("bf16", "f32")])
+def test_scan_of_odd_channels_takes_views_at_any_offset(xk, gk):
+    """Channel counts that are no multiple of 4 are read an element at a time: a row of a larger tensor is taken as it is."""
+    B, T, D = 1, 130, 37
+    d, _ = scan_data(3 * T, D, 3, False, 6, xk, gk)
+    d["x"], d["g"], d["dy"] = (d[n].view(3, T, D) for n in ("x", "g", "dy"))
+    part = {n: t[1:2] for n, t in d.items()}
+    assert any(t.data_ptr() % 16 for t in part.values())
+    whole = {n: t.clone() for n, t in part.items()}
+    results = []
+    for p in (part, whole):
+        for save in ("carry", "ckpt8"):
+            y, h, saved = kda.scan_fwd(p["x"], p["g"], p["h0"], save=save)
+            grads = kda.scan_bwd(p["g"], p["dy"], saved, x=p["x"], h0=p["h0"], dh_final=p["dh"])
+            results.append((y, h, *grads))
+        out, state = kda.scan_step(p["x"][:, 5], p["g"][:, 5], p["h0"])
+        results.append((out, state))
+    for a, b in zip(results[:3], results[3:]):
+        assert all(torch.equal(s, t) for s, t in zip(a, b))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_ckpt8_of_odd_rows_takes_views_at_any_offset(kind):
+    x = torch.randn(5, 37, device="cuda").to(TYPES[kind])
+    p = kda.ckpt8_pack(x)
+    part = kda.ckpt8_pack(x[1:4])
+    assert torch.equal(part.codes, p.codes[1:4]) and torch.equal(part.scales, p.scales[1:4])
+    view = kda.Packed8(p.codes[1:4], p.scales[1:4], p.dtype)
+    assert torch.equal(kda.ckpt8_unpack(view), kda.ckpt8_unpack(p)[1:4])
+
+
+@pytest.mark.parametrize("kind", [torch.int32, torch.int64])
+def test_qk_positions_and_frequencies_begin_anywhere(kind):
+    q = torch.randn(9, 2, 64, device="cuda")
+    pos = torch.arange(20, device="cuda", dtype=kind)
+    f = 10000.0 ** (-torch.arange(0, 66, 2, dtype=torch.float64, device="cuda") / 64)
+    for at in (1, 2, 3):
+        a = kda.qk_norm_rope_fwd(q, q, pos=pos[at:at + 9], freqs=f[1:])
+        b = kda.qk_norm_rope_fwd(q, q, pos=pos[at:at + 9].clone(), freqs=f[1:].clone())
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])

@@ -5,7 +5,7 @@ import pytest
 
 import gated_delta_rule_65_amd as kda
 from gated_delta_rule_65_amd import _build
-from tests.test_layer_abi import FAKE, call, expect, last_error
+from tests.test_layer_abi import BWD, FAKE, FWD, PACK, QKF, STEP, VBWD, VFWD, call, expect, last_error, qk_form
 
 BEHIND = dict(cu=FAKE, N=2, total=9, a=FAKE, a_row=6, b=None, b_row=0, stream=None)
 
@@ -75,3 +75,36 @@ static_assert(offsetof(kda::Exchange<4>, b) % 16 == 0 && offsetof(kda::Exchange<
     r = subprocess.run([_build.hipcc(), *_build.HIPCC_FLAGS, "--offload-device-only", "-fsyntax-only", str(probe)],
                        capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+ODD = {"kda_scan_fwd": dict(FWD, D=37), "kda_scan_varlen_fwd": dict(VFWD, D=37), "kda_scan_bwd": dict(BWD, D=37),
+       "kda_scan_varlen_bwd": dict(VBWD, D=37), "kda_scan_step": dict(STEP, B=1, D=37)}
+
+
+@pytest.mark.parametrize("name", ODD)
+@pytest.mark.parametrize("kw,size", [(dict(x=FAKE + 1), 2), (dict(g=FAKE + 2), 4)])
+def test_rows_read_an_element_at_a_time_begin_at_an_element(name, kw, size):
+    expect(name, ODD[name], kw, 4, f"is not {size}-byte aligned")
+
+
+@pytest.mark.parametrize("name,kw,what", [
+    ("kda_scan_fwd", dict(y=FAKE + 1), "y is not 2"), ("kda_scan_fwd", dict(h0=FAKE + 2), "h0 is not 4"),
+    ("kda_scan_fwd", dict(h_final=FAKE + 2), "h_final is not 4"), ("kda_scan_fwd", dict(carry=FAKE + 2), "carry is not 4"),
+    ("kda_scan_fwd", dict(ws=FAKE + 8), "workspace is not 16"), ("kda_scan_bwd", dict(dy=FAKE + 1), "dy is not 2"),
+    ("kda_scan_bwd", dict(dg=FAKE + 2), "dg is not 4"), ("kda_scan_bwd", dict(dh0=FAKE + 2), "dh0 is not 4"),
+    ("kda_scan_step", dict(h_in=FAKE + 2), "h_in is not 4"), ("kda_scan_step", dict(B=4, x=FAKE + 8), "x is not 16"),
+])
+def test_alignment_is_named(name, kw, what):
+    expect(name, ODD[name], kw, 4, what)
+
+
+@pytest.mark.parametrize("kw,what", [(dict(x=FAKE + 1), "x is not 2"), (dict(x=FAKE + 2, dtype=0), "x is not 4"),
+                                     (dict(x=FAKE + 8, cols=64), "x is not 16"), (dict(codes=FAKE + 8, cols=64), "codes is not 16")])
+def test_ckpt8_alignment_is_named(kw, what):
+    expect("kda_ckpt8_pack", dict(PACK, cols=37), kw, 4, what)
+
+
+@pytest.mark.parametrize("kw,what", [(dict(pos=FAKE + 4), "pos is not 8"), (dict(freqs=FAKE + 4), "freqs is not 8"),
+                                     (dict(pos=FAKE + 2, form=qk_form(pos_bytes=4)), "pos is not 4")])
+def test_qknorm_alignment_is_named(kw, what):
+    expect("kda_qknorm_fwd", QKF, kw, 4, what)
