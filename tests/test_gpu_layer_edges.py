@@ -213,3 +213,111 @@ def test_qk_positions_and_frequencies_begin_anywhere(kind):
         a = kda.qk_norm_rope_fwd(q, q, pos=pos[at:at + 9], freqs=f[1:])
         b = kda.qk_norm_rope_fwd(q, q, pos=pos[at:at + 9].clone(), freqs=f[1:].clone())
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+# ----------------------------------------------------------------- large calls
+
+def scan_both(x, g, dy, cu, h0, dh, save):
+    if cu is None:
+        y, h, saved = kda.scan_fwd(x, g, h0, save=save, g_logit=True, complement=True)
+        grads = kda.scan_bwd(g, dy, saved, x=x, h0=h0, dh_final=dh, g_logit=True, complement=True)
+    else:
+        y, h, saved = kda.scan_varlen_fwd(x, g, cu, h0, save=save, g_logit=True, complement=True)
+        grads = kda.scan_varlen_bwd(g, cu, dy, saved, x=x, h0=h0, dh_final=dh, g_logit=True, complement=True)
+    return (y, *grads[:2]), (h, grads[2]), saved
+
+
+@pytest.mark.parametrize("save", ["carry", "ckpt8"])
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("xk,gk,blocks", [("bf16", "bf16", 22), ("bf16", "f32", 17), ("f32", "bf16", 13), ("f32", "f32", 11)])
+def test_scan_large_calls_have_the_bits_of_small_ones(xk, gk, blocks, packed, save):
+    """Rows of calls of more than 128 MiB go past the caches; a sequence's results do not depend on that.  Packed rows are cut
+    where sequences begin at whole blocks of 64 segments, so that sums are taken in the same order."""
+    D, rows = 256, 4096 * blocks + (0 if packed else 4)  # batches end inside a segment
+    assert rows * D * ((4 if xk == "bf16" else 8) + (2 if gk == "bf16" else 4)) > 1 << 27
+    torch.manual_seed(blocks)
+    x, dy = (torch.randn(rows, D, device="cuda").to(TYPES[xk]) for _ in range(2))
+    g = (torch.randn(rows, D, device="cuda") * 1.5 - 2).to(TYPES[gk])
+    if packed:
+        lengths = [1000, 3096, 5, 0, 4091, *[4096] * (blocks - 6), 9000, 3000, 1, 287, 0, 4096]
+        cuts = np.cumsum([0, *lengths])
+        assert cuts[-1] == rows and cuts[-2] == rows - 4096
+        cu = torch.tensor(cuts, dtype=torch.int32, device="cuda")
+        N = len(lengths)
+        parts = [(0, 2, 0, 4096), (2, 5, 4096, 8192), (N - 6, N - 1, rows - 4 * 4096, rows - 4096),
+                 (N - 1, N, rows - 4096, rows)]  # sequences and rows of each
+    else:
+        N, T = 4, rows // 4
+        cu, parts = None, [(0, 1, 0, T), (3, 4, 3 * T, 4 * T)]
+    h0, dh = torch.randn(N, D, device="cuda"), torch.randn(N, D, device="cuda")
+    shape = (rows, D) if packed else (N, T, D)
+    large = scan_both(x.view(shape), g.view(shape), dy.view(shape), cu, h0, dh, save)
+    for i, j, a, b in parts:
+        part = [t[a:b] if packed else t[a:b][None] for t in (x, g, dy)]
+        small = scan_both(*part, (cu[i:j + 1] - cu[i]).contiguous() if packed else None, h0[i:j], dh[i:j], save)
+        for s, t in zip(large[0], small[0]):
+            assert torch.equal(s.view(rows, D)[a:b], t.view(b - a, D))
+        for s, t in zip(large[1], small[1]):
+            assert torch.equal(s[i:j], t)
+        if save == "ckpt8":
+            assert torch.equal(large[2].codes[a:b], small[2].codes) and torch.equal(large[2].scales[a:b], small[2].scales)
+
+
+@pytest.mark.parametrize("D,rot", [(64, 32), (128, 64), (128, 32), (128, 0)])
+@pytest.mark.parametrize("ckpt8", [False, True])
+def test_qk_large_fp32_calls_have_the_bits_of_small_ones(D, rot, ckpt8):
+    tokens, Hq, Hk, n = 20000 * 128 // D, 5, 3, 50
+    torch.manual_seed(D + rot)
+    q, dq = (torch.randn(tokens, Hq, D, device="cuda") for _ in range(2))
+    k, dk = (torch.randn(tokens, Hk, D, device="cuda") for _ in range(2))
+    assert tokens * (Hq + Hk) * D * 8 > 1 << 27
+    pos = torch.arange(tokens, device="cuda") * 37 if rot else None
+    form = {"freqs": 10000.0 ** (-torch.arange(0, rot, 2, dtype=torch.float64, device="cuda") / rot) if rot else None}
+
+    def both(at, end):
+        p = {**form, "pos": pos[at:end] if rot else None, "norm": "rms", "eps": 1e-6}
+        qo, ko, raw = kda.qk_norm_rope_fwd(q[at:end], k[at:end], ckpt8=ckpt8, **p)
+        grads = kda.qk_norm_rope_bwd(*(raw if ckpt8 else (q[at:end], k[at:end])), dq[at:end], dk[at:end], **p)
+        return [qo, ko, *grads[:2], *([t for r in raw for t in r[:2]] if ckpt8 else [])]
+
+    large = both(0, tokens)
+    for at in (0, tokens // 2, tokens - n):
+        assert all(torch.equal(s[at:at + n], t) for s, t in zip(large, both(at, at + n)))
+
+
+@pytest.mark.parametrize("cols", [32, 33, 40])
+def test_ckpt8_offsets_beyond_32_bits(cols):
+    rows = (1 << 31) // cols + 1001
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda").normal_()
+    p = kda.ckpt8_pack(x)
+    u = kda.ckpt8_unpack(p)
+    for at in (0, rows // 2, rows - 1000):
+        small = kda.ckpt8_pack(x[at:at + 1000].clone())
+        assert torch.equal(p.codes[at:at + 1000], small.codes) and torch.equal(p.scales[at:at + 1000], small.scales)
+        assert torch.equal(u[at:at + 1000], kda.ckpt8_unpack(small))
+
+
+def test_qk_offsets_beyond_32_bits():
+    tokens, Hq, Hk, D, n = (1 << 20) + 77, 16, 1, 128, 100
+    q, dq = (torch.empty(tokens, Hq, D, dtype=torch.bfloat16, device="cuda").normal_() for _ in range(2))
+    k, dk = (torch.empty(tokens, Hk, D, dtype=torch.bfloat16, device="cuda").normal_() for _ in range(2))
+    pos, f = torch.arange(tokens, device="cuda"), 10000.0 ** (-torch.arange(0, D, 2, dtype=torch.float64, device="cuda") / D)
+
+    def both(at, end):
+        p = {"freqs": f, "pos": pos[at:end], "eps": 1e-6}
+        qo, ko, raw = kda.qk_norm_rope_fwd(q[at:end], k[at:end], ckpt8=True, **p)
+        return [qo, ko, *kda.qk_norm_rope_bwd(*raw, dq[at:end], dk[at:end], **p)[:2], *(t for r in raw for t in r[:2])]
+
+    large = both(0, tokens)
+    for at in (0, tokens // 2, tokens - n):
+        assert all(torch.equal(s[at:at + n], t) for s, t in zip(large, both(at, at + n)))
+
+
+@pytest.mark.parametrize("B", [1, 300])
+@pytest.mark.parametrize("save", ["carry", "ckpt8"])
+def test_scan_of_a_batch_without_tokens(B, save):
+    D = 37
+    x, h0, dh = torch.zeros(B, 0, D, device="cuda"), torch.randn(B, D, device="cuda"), torch.randn(B, D, device="cuda")
+    (y, dx, dg), (h, dh0), _ = scan_both(x, x, x, None, h0, dh, save)
+    assert torch.equal(h, h0) and torch.equal(dh0, dh) and y.shape == dx.shape == dg.shape == x.shape
+    assert (scan_both(x, x, x, None, None, dh, save)[1][0] == 0).all()
