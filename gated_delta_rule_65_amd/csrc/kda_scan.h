@@ -207,16 +207,17 @@ __device__ __forceinline__ int64_t offset_of(const ScanArgs& a, int64_t n) {
     typedef const __attribute__((address_space(4))) int32_t* scalar;
     return a.cu ? (int64_t)((scalar)a.cu)[__builtin_amdgcn_readfirstlane((int)n)] : n * a.T_fixed;
 }
-// The sequence that holds row r of packed rows: the last n that begins at r or before.
-__device__ __forceinline__ int64_t seq_of(const ScanArgs& a, int64_t r) {
-    if (!a.cu) return r / a.T_fixed;
-    int lo = 0, hi = (int)a.N - 1;
+// The sequence that holds row r of packed rows: the last n that begins at r or before, of lo .. hi.
+__device__ __forceinline__ int search(const ScanArgs& a, int64_t r, int lo, int hi) {
     while (lo < hi) {
         const int mid = lo + (hi - lo + 1) / 2;
         if (offset_of(a, mid) <= r) lo = mid;
         else hi = mid - 1;
     }
     return lo;
+}
+__device__ __forceinline__ int64_t seq_of(const ScanArgs& a, int64_t r) {
+    return a.cu ? search(a, r, 0, (int)a.N - 1) : r / a.T_fixed;
 }
 
 // ---------------------------------------------------------------------------- published words
@@ -393,32 +394,43 @@ __device__ __forceinline__ void join_waves(const ScanArgs& a, const ScanPlan& p,
     }
 }
 
-// Where sequences begin or end among a wave's rows of packed rows (bit i: row i), and their numbers.
+// Where sequences begin or end among a wave's rows of packed rows (bit i: row i), and their numbers, row i's in lane i (in
+// scalar registers they cost more than they give: the few places that ask are where sequences begin or end).
 struct Marks {
     uint32_t begins, ends;
-    int n[kRows];
+    int n;
+    __device__ __forceinline__ int64_t seq(int i) const { return __builtin_amdgcn_readlane(n, i); }
 };
+// A turn of the loop for each sequence that has rows here.  The next one is most often the one behind; past more empty ones
+// the steps double, and a search between the last two ends them, so that any number of them costs a few loads.
 __device__ __forceinline__ Marks marks_of(const ScanArgs& a, int64_t r0, int rows) {
-    Marks m{0, 0, {}};
+    Marks m{0, 0, 0};
     if (rows <= 0) return m;
-    int64_t n = seq_of(a, r0);
-    int64_t next = offset_of(a, n + 1);
-    bool begins = offset_of(a, n) == r0;
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        if (i < rows) {
-            while (r0 + i >= next && n + 1 < a.N) {
-                ++n;
-                next = offset_of(a, n + 1);
-                begins = true;
+    const int last = (int)a.N - 1, lane = threadIdx.x & 63;
+    int n = (int)seq_of(a, r0);
+    int64_t from = offset_of(a, n), next = offset_of(a, n + 1);
+#pragma unroll 1
+    for (int i = 0;;) {
+        const int64_t left = next - r0;
+        const int end = n == last || left >= rows ? rows : left <= i ? i + 1 : (int)left;
+        if (from == r0 + i) m.begins |= 1u << i;
+        if (left == end) m.ends |= 1u << (end - 1);
+        m.n = lane >= i ? n : m.n;
+        if (end == rows) return m;
+        i = end;  // n < last
+        from = next;
+        next = offset_of(a, ++n + 1);
+        if (next <= r0 + i && n < last) {
+            int step = 1;
+            while (step <= last - n && offset_of(a, n + step) <= r0 + i) {
+                n += step;
+                step *= 2;
             }
-            m.n[i] = (int)n;
-            if (begins) m.begins |= 1u << i;
-            if (r0 + i + 1 == next) m.ends |= 1u << i;
-            begins = false;
+            n = search(a, r0 + i, n, step - 1 < last - n ? n + step - 1 : last);
+            from = offset_of(a, n);
+            next = offset_of(a, n + 1);
         }
     }
-    return m;
 }
 
 // Rows in use: all of them, or those up to the last sequence's end.

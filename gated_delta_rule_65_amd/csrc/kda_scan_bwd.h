@@ -41,7 +41,7 @@ __device__ __forceinline__ void bwd_body(const ScanArgs& a, const ScanPlan& p, c
         for (int i = 0; i < kRows; ++i) {
             if (i >= rows) break;
             if (FLAT && (m.begins >> i & 1)) {
-                state_of<CPL>(a.h0, m.n[i] * a.D + c, in, s);
+                state_of<CPL>(a.h0, m.seq(i) * a.D + c, in, s);
 #pragma unroll
                 for (int k = 0; k < CPL; ++k) A[k] = __uint_as_float(kBegins);
             }
@@ -75,7 +75,7 @@ __device__ __forceinline__ void bwd_body(const ScanArgs& a, const ScanPlan& p, c
         run = again();
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            if (FLAT && (m.begins >> i & 1)) state_of<CPL>(a.h0, m.n[i] * a.D + c, in, s);
+            if (FLAT && (m.begins >> i & 1)) state_of<CPL>(a.h0, m.seq(i) * a.D + c, in, s);
             float f[CPL];
 #pragma unroll
             for (int k = 0; k < CPL; ++k) {
@@ -100,7 +100,7 @@ __device__ __forceinline__ void bwd_body(const ScanArgs& a, const ScanPlan& p, c
     for (int i = kRows - 1; i >= 0; --i) {
         if (i >= rows) continue;
         if (FLAT && (m.ends >> i & 1)) {
-            state_of<CPL>(a.dh_final, m.n[i] * a.D + c, in, s);
+            state_of<CPL>(a.dh_final, m.seq(i) * a.D + c, in, s);
 #pragma unroll
             for (int k = 0; k < CPL; ++k) A[k] = __uint_as_float(kBegins);
         }
@@ -122,7 +122,7 @@ __device__ __forceinline__ void bwd_body(const ScanArgs& a, const ScanPlan& p, c
     for (int i = kRows - 1; i >= 0; --i) {
         if (i >= rows) continue;
         const int64_t r = r0 + i;
-        if (FLAT && (m.ends >> i & 1)) state_of<CPL>(a.dh_final, m.n[i] * a.D + c, in, s);
+        if (FLAT && (m.ends >> i & 1)) state_of<CPL>(a.dh_final, m.seq(i) * a.D + c, in, s);
         float dx[CPL], dg[CPL], f[(CPL + 3) / 4 * 4];
         if constexpr (PACKED) {
             const float unit = ckpt_unit(raw.scale_of(i));
@@ -149,7 +149,7 @@ __device__ __forceinline__ void bwd_body(const ScanArgs& a, const ScanPlan& p, c
             if (a.dh0) {
                 bool begins;
                 int64_t n;
-                if constexpr (FLAT) begins = m.begins >> i & 1, n = m.n[i];
+                if constexpr (FLAT) begins = m.begins >> i & 1, n = m.seq(i);
                 else begins = r == t.chain * a.T_fixed, n = t.chain;
                 if (begins) store_row<true, CPL>(a.dh0, n * a.D + c, s);
             }
@@ -195,7 +195,7 @@ __global__ __launch_bounds__(kThreads, bwd_waves(XF, GF, PACKED)) void scan_bwd_
         for (int i = 0; i < kRows; i += 4)
             raw.scale[i / 4] = scales[i] | scales[i + 1] << 8 | scales[i + 2] << 16 | scales[i + 3] << 24;
     }
-    Marks m{0, 0, {}};
+    Marks m{0, 0, 0};
     int64_t reach = t.at > 0 ? t.at : -1;
     if constexpr (FLAT) {
         m = marks_of(a, r0, rows);

@@ -42,7 +42,7 @@ __device__ __forceinline__ void fwd_body(const ScanArgs& a, const ScanPlan& p, c
     for (int i = 0; i < kRows; ++i) {
         if (i >= rows) break;
         if (FLAT && (m.begins >> i & 1)) {
-            state_of<CPL>(a.h0, m.n[i] * a.D + c, in, h);
+            state_of<CPL>(a.h0, m.seq(i) * a.D + c, in, h);
 #pragma unroll
             for (int k = 0; k < CPL; ++k) A[k] = __uint_as_float(kBegins);
         }
@@ -67,7 +67,7 @@ __device__ __forceinline__ void fwd_body(const ScanArgs& a, const ScanPlan& p, c
     for (int i = 0; i < kRows; ++i) {
         if (i >= rows) break;
         const int64_t r = r0 + i;
-        if (FLAT && (m.begins >> i & 1)) state_of<CPL>(a.h0, m.n[i] * a.D + c, in, h);
+        if (FLAT && (m.begins >> i & 1)) state_of<CPL>(a.h0, m.seq(i) * a.D + c, in, h);
         if constexpr (PACK) {
             float u[CPL];
 #pragma unroll
@@ -96,7 +96,7 @@ __device__ __forceinline__ void fwd_body(const ScanArgs& a, const ScanPlan& p, c
         if (a.h_final && in) {
             bool ends;
             int64_t n;
-            if constexpr (FLAT) ends = m.ends >> i & 1, n = m.n[i];
+            if constexpr (FLAT) ends = m.ends >> i & 1, n = m.seq(i);
             else ends = r + 1 == (t.chain + 1) * a.T_fixed, n = t.chain;
             if (ends) store_row<true, CPL>(a.h_final, n * a.D + c, h);
         }
@@ -125,7 +125,7 @@ __global__ __launch_bounds__(kThreads, fwd_waves(XF, GF)) void scan_fwd_kernel(S
         raw.g[i] = load_raw<GF, CPL, STREAM>(a.g, at);
         raw.x[i] = load_raw<XF, CPL, STREAM>(a.x, at);
     }
-    Marks m{0, 0, {}};
+    Marks m{0, 0, 0};
     int64_t reach = t.at > 0 ? t.at : -1;
     if constexpr (FLAT) {
         m = marks_of(a, r0, rows);

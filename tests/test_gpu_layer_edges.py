@@ -321,3 +321,26 @@ def test_scan_of_a_batch_without_tokens(B, save):
     (y, dx, dg), (h, dh0), _ = scan_both(x, x, x, None, h0, dh, save)
     assert torch.equal(h, h0) and torch.equal(dh0, dh) and y.shape == dx.shape == dg.shape == x.shape
     assert (scan_both(x, x, x, None, None, dh, save)[1][0] == 0).all()
+
+
+def test_scan_passes_empty_sequences_in_a_few_steps():
+    """A million empty sequences between two tokens: the results without them, and not a step for each."""
+    D, E = 4, 10 ** 6
+    x, g, dy = torch.randn(300, D, device="cuda"), -torch.rand(300, D, device="cuda"), torch.randn(300, D, device="cuda")
+    few = torch.tensor([0, 70, 100, 130, 300], dtype=torch.int32, device="cuda")
+    many = torch.cat([few[:3], torch.full((E,), 100, dtype=torch.int32, device="cuda"), few[3:]])
+    real = torch.tensor([0, 1, E + 2, E + 3], device="cuda")  # the sequences that have tokens
+    h0, dh = torch.randn(E + 4, D, device="cuda"), torch.randn(E + 4, D, device="cuda")
+    want = scan_both(x, g, dy, few, h0[real], dh[real], "carry")
+    for _ in range(2):
+        start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        start.record()
+        got = scan_both(x, g, dy, many, h0, dh, "carry")
+        end.record()
+        torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got[0], want[0]))
+    empty = torch.ones(E + 4, dtype=torch.bool, device="cuda")
+    empty[real] = False
+    for a, b, through in zip(got[1], want[1], (h0, dh)):
+        assert torch.equal(a[real], b) and torch.equal(a[empty], through[empty])
+    assert start.elapsed_time(end) < 30  # a step for each takes 170 ms, a search well under 10
