@@ -10,11 +10,11 @@
 // dw = the sum over rows of (d turned back) z^.
 //
 // Measured (q and k of 16 heads of 128 bf16 channels, 32768 tokens): forward, half of the channels turned, columns of one
-// projection, 537 MB in 92 us (5.8 TB/s; 101 without the exchange of chunks, since
-// half lines at a time do not go past the caches); forward with the raw rows packed in 8 bits beside, 675 MB in 109 us (6.2
-// TB/s); backward from the packed rows with the weights' gradients, 675 MB in 121 us (5.6 TB/s; its three workgroups a CU
+// projection, 537 MB in 93 us (5.8 TB/s; 101 without the exchange of chunks, since
+// half lines at a time do not go past the caches); forward with the raw rows packed in 8 bits beside, 675 MB in 110 us (6.1
+// TB/s); backward from the packed rows with the weights' gradients, 675 MB in 123 us (5.5 TB/s; its three workgroups a CU
 // stop at each tile's tables) and 5 us for the weights' sums.  4099 tokens of 12 + 2 heads of 64 fp32 channels: 10
-// us forward and 14 backward for 74 MB in all; 32 tokens: 4.4 us, one pass of latency.
+// us forward and 14 backward for 74 MB in all; 32 tokens: 4.8 us, one pass of latency.
 #include <type_traits>
 
 #include "kda_ckpt8.h"

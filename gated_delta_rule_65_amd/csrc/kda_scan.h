@@ -18,9 +18,11 @@
 // pairs of 8 bytes against 64 rows of 2 or 4 each way; a workgroup that goes on over several segments and asks for the next
 // one's rows early was slower (152 us against 98), since those who wait for its tiles wait for tiles not begun.  256
 // channels a row (CPL = 4: 8 or 16 bytes a lane) and 512 do the same (98.1 and 98.9 us).
-// What bounds it: HBM, at the rate that this pattern of rows reaches (84 us for the 403 MB of that call when rows are
-// moved and nothing else; a plain copy takes 64), then 10 to 15 us in which segments wait for earlier ones (35 in one
-// long sequence), the counter (2 us) and the emptying of the words in front (4 to 8 us).
+// What bounds it: memory and the vector units, each busy most of the time, and the waits between.  Of the 92 us of that call
+// the vector units work 69% (each gate takes an exponential and, from logits, a reciprocal, in both runs); its rows
+// moved by the same workgroups and nothing else take 77 us, of a plain copy's 64.  Its waves spend half of their
+// cycles waiting, for rows and for earlier segments.  fp32 rows leave the vector units idle (20%) and are bound by memory.
+// Before the kernel comes the emptying of the words, 4 to 8 us.
 //
 // Why every wait ends: a workgroup takes its place in the order of work from a counter when it starts, and only waits for
 // segments whose places were taken earlier, by workgroups that are therefore running or done.  The one
@@ -58,8 +60,8 @@ struct Raw {
     static constexpr int WORDS = F32 ? CPL : (CPL + 1) / 2;
     uint32_t w[WORDS];
 };
-// Rows are read once and written once, past the caches where `stream` says so.  (B = 4, T = 8192, D = 2048 in bf16, rows
-// moved in this pattern and nothing else: 90 us through the caches, 84 past them.)
+// Rows are read once and written once, past the caches where `stream` says so.  (One sequence of 131072 tokens of 1024 bf16
+// channels: 240 us through the caches, 228 past them; B = 4, T = 8192, D = 2048: 98.5 and 97.7.)
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));

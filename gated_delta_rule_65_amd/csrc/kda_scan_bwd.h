@@ -3,10 +3,12 @@
 // With e_t = a_t (dy_t + e_{t+1}), the gradient of the state behind token t being dh_t = dy_t + e_{t+1}: dx_t = w_t dh_t,
 // dl_t = e_t u_t with u_t = h_{t-1} (less x_t with complement, where 1 - a_t carries part of the gradient), dh0 = e_1.
 //
-// What bounds it: HBM, as in the forward pass, and the registers of two workgroups a CU (half of the factors u lie in LDS
-// for that; the fp32 forms from the carry still spill 36 to 100 bytes a lane).  Measured: B = 4, T = 8192, D = 2048 in
+// What bounds it: from the carry the vector units, busy 78% of the time (the gates are made four times: for the states' pairs,
+// the states, the reversed pairs and the results); from the 8-bit factor, which needs two, they are busy 49% (log gates) and
+// memory and the waits weigh more.  Then the registers of two workgroups a CU (half of the factors u lie in LDS for that;
+// forms with fp32 rows from the carry still spill 20 to 88 bytes a lane).  Measured: B = 4, T = 8192, D = 2048 in
 // bf16 from the carry, 671 MB, 158 us (4.3 TB/s); 24001 packed tokens of 2048 bf16 channels from the 8-bit factor,
-// 444 MB, 102 us (4.3 TB/s).  Both passes and what goes before them: 256 us and 201 us.
+// 444 MB, 100 us (4.4 TB/s).  Both passes and what goes before them: 256 us and 199 us.
 #pragma once
 #include "kda_scan.h"
 
