@@ -343,4 +343,89 @@ def test_scan_passes_empty_sequences_in_a_few_steps():
     empty[real] = False
     for a, b, through in zip(got[1], want[1], (h0, dh)):
         assert torch.equal(a[real], b) and torch.equal(a[empty], through[empty])
+    print(f"{start.elapsed_time(end):.2f} ms")
     assert start.elapsed_time(end) < 30  # a step for each takes 170 ms, a search well under 10
+
+
+# ----------------------------------------------------------------- together, captured, and on other streams
+
+@pytest.mark.parametrize("name", ["GatedScan", "VarlenGatedScan", "ChunkKDA", "NormChunkKDA"])
+def test_second_order_gradients_are_refused(name):
+    torch.manual_seed(5)
+    x = (0.3 * torch.randn(1, 70, 2, 64, device="cuda")).requires_grad_()
+    g, beta = -torch.rand(1, 70, 2, 64, device="cuda"), torch.rand(1, 70, 2, device="cuda")
+    cu = torch.tensor([0, 30, 70], dtype=torch.int32, device="cuda")
+    y = {"GatedScan": lambda: kda.GatedScan.apply(x, g)[0],
+         "VarlenGatedScan": lambda: kda.VarlenGatedScan.apply(x.flatten(0, 1), g.flatten(0, 1), cu)[0],
+         "ChunkKDA": lambda: kda.ChunkKDA.apply(x, x, x, g, beta)[0],
+         "NormChunkKDA": lambda: kda.NormChunkKDA.apply(x, x, x, g, beta)[0]}[name]
+    first, = torch.autograd.grad(y().sum(), x)
+    dx, = torch.autograd.grad(y().sum() + (x ** 3).sum(), x, create_graph=True)
+    torch.testing.assert_close(dx.detach(), first + 3 * x.detach() ** 2)
+    with pytest.raises(RuntimeError, match="first-order"):
+        (dx ** 2).sum().backward()
+
+
+def test_zero_behind_in_a_graph_and_on_another_stream():
+    """The end of the last sequence is the device's: a replay follows the offsets as they then are."""
+    total, D = 333, 37
+    cu = torch.tensor([0, 100, 200], dtype=torch.int32, device="cuda")
+    a, b = torch.empty(total, D, device="cuda"), torch.empty(total, D, dtype=torch.bfloat16, device="cuda")
+
+    def step():
+        a.fill_(1)
+        b.fill_(2)
+        kda.layer._zero_behind(cu, a, b)
+
+    def check(used):
+        torch.cuda.synchronize()
+        assert (a[:used] == 1).all() and (a[used:] == 0).all() and (b[:used] == 2).all() and (b[used:] == 0).all()
+
+    step()
+    check(200)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    check(200)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for used in (200, 1, 333, 0, 332, 200):
+        cu.copy_(torch.tensor([0, used // 2, used], dtype=torch.int32))
+        graph.replay()
+        check(used)
+        step()
+        check(used)
+
+
+@pytest.mark.parametrize("used", [5, 69990])
+def test_zero_behind_beyond_32_bits(used):
+    total, D = 70000, 65536
+    a = torch.ones(total, D, dtype=torch.bfloat16, device="cuda")
+    kda.layer._zero_behind(torch.tensor([0, used], dtype=torch.int32, device="cuda"), a)
+    assert not a[used:].any() and a[:used].all()
+
+
+def test_packed_layer_with_padding():
+    """A padded buffer of packed prompts through norm, rotation and scan in training: what stands behind the sequences has no
+    part in any gradient."""
+    D, H, total, lengths = 64, 2, 260, [70, 1, 0, 129]
+    used = sum(lengths)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lengths)]), dtype=torch.int32, device="cuda")
+    torch.manual_seed(6)
+    base, gate = torch.randn(total, H * D, device="cuda"), torch.randn(total, H, D, device="cuda")
+    weight = torch.randn(H * D, H * D, device="cuda") / 12
+    grads = []
+    for n, fill in ((used, 0.0), (total, 3.0), (total, 1e30)):
+        x, z, w = base[:n].clone(), gate[:n].clone(), weight.clone().requires_grad_()
+        x[used:], z[used:] = fill, fill
+        z.requires_grad_()
+        v = (x @ w).view(n, H, D)
+        y, h = kda.VarlenGatedScan.apply(v, z, cu, None, True, True)
+        (y ** 2).sum().backward()
+        grads.append((w.grad, z.grad[:used]))
+    for w, z in grads[1:]:
+        # rows of zeros add nothing; another number of rows may be summed in another order
+        torch.testing.assert_close(w, grads[0][0], rtol=1e-4, atol=1e-3)
+        torch.testing.assert_close(z, grads[0][1], rtol=1e-5, atol=1e-5)
