@@ -32,7 +32,9 @@ __all__ = ["chunk_fwd", "chunk_fwd_noalloc", "chunk_fwd_noalloc_raw", "varlen_fw
            "calib_copy_raw", "calib_mfma_raw", "layer", "Packed8", "ckpt8_pack", "ckpt8_unpack", "scan_fwd",
            "scan_varlen_fwd", "scan_bwd", "scan_varlen_bwd", "scan_step", "scan_workspace_bytes", "scan_carry_bytes",
            "GatedScan", "VarlenGatedScan", "qk_norm_rope_fwd", "qk_norm_rope_bwd", "qk_norm_rope_workspace_bytes",
-           "NormChunkKDA"]
+           "NormChunkKDA", "linattn", "linattn_fwd", "linattn_varlen_fwd", "linattn_step", "linattn_bwd", "linattn_varlen_bwd",
+           "linattn_workspace_bytes", "linattn_bwd_workspace_bytes", "LinearAttention", "VarlenLinearAttention", "groupnorm",
+           "group_norm_act_fwd", "group_norm_act_bwd", "group_norm_act_workspace_bytes", "GroupNormAct"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libkda.so")
@@ -106,6 +108,8 @@ def load_library():
     L.kda_calib_mfma.argtypes = [vp, ci, i64, ci, vp]
     L.kda_calib_mfma.restype = ci
     layer.declare(L)
+    linattn.declare(L)
+    groupnorm.declare(L)
     L.kda_last_error.restype = ctypes.c_char_p
     L.kda_version.restype = ctypes.c_char_p
     _lib = L
@@ -502,3 +506,7 @@ from . import layer  # noqa: E402
 from .layer import (GatedScan, NormChunkKDA, Packed8, VarlenGatedScan, ckpt8_pack, ckpt8_unpack,  # noqa: E402
                     qk_norm_rope_bwd, qk_norm_rope_fwd, qk_norm_rope_workspace_bytes, scan_bwd, scan_carry_bytes,
                     scan_fwd, scan_step, scan_varlen_bwd, scan_varlen_fwd, scan_workspace_bytes)
+from . import groupnorm, linattn  # noqa: E402
+from .groupnorm import GroupNormAct, group_norm_act_bwd, group_norm_act_fwd, group_norm_act_workspace_bytes  # noqa: E402
+from .linattn import (LinearAttention, VarlenLinearAttention, linattn_bwd, linattn_bwd_workspace_bytes,  # noqa: E402
+                      linattn_fwd, linattn_step, linattn_varlen_bwd, linattn_varlen_fwd, linattn_workspace_bytes)

@@ -336,6 +336,164 @@ kda_status qk_inputs(kda::QkArgs& a, const void* q, const void* k, const uint8_t
     return KDA_OK;
 }
 
+// ---------------------------------------------------------------------------- linear attention
+kda_status lin_sizes(kda::LinArgs& a, int64_t N, int64_t total, int H, int Dk, int Dv, float scale, kda_dtype dtype) {
+    kda_status st;
+    if ((st = check_dtype(dtype)) != KDA_OK) return st;
+    if ((st = check_head_dims(H, Dk, Dv)) != KDA_OK) return st;
+    const int64_t most = kMostElements / H / 128;
+    if (N > most / 128 || total > most)
+        return fail(KDA_ERR_BAD_SHAPE, "sizes out of range: %lld sequences, %lld tokens, H = %d", (long long)N,
+                    (long long)total, H);
+    a.N = N;
+    a.total = total;
+    a.H = H;
+    a.Dk = Dk;
+    a.Dv = Dv;
+    a.scale = scale;
+    a.f32 = dtype == KDA_F32;
+    return KDA_OK;
+}
+
+kda_status lin_batch(kda::LinArgs& a, int64_t B, int64_t T, int H, int Dk, int Dv, float scale, kda_dtype dtype) {
+    if (B < 0 || T < 0) return fail(KDA_ERR_BAD_SHAPE, "B and T must be >= 0");
+    if (T > 0 && B > kMostElements / T) return fail(KDA_ERR_BAD_SHAPE, "B*T exceeds 2^40");
+    a.T_fixed = T;
+    return lin_sizes(a, B, B * T, H, Dk, Dv, scale, dtype);
+}
+
+kda_status lin_packed(kda::LinArgs& a, const int32_t* cu, int64_t N, int64_t total, int H, int Dk, int Dv, float scale,
+                      kda_dtype dtype) {
+    if (N < 0 || total < 0) return fail(KDA_ERR_BAD_SHAPE, "N and total must be >= 0");
+    if (total > 0x7fffffffLL) return fail(KDA_ERR_BAD_SHAPE, "total exceeds the int32 range of cu_seqlens");
+    if (N > 0 && !cu) return fail(KDA_ERR_NULL_ARG, "cu_seqlens is NULL");
+    if (reinterpret_cast<uintptr_t>(cu) & 3u) return fail(KDA_ERR_MISALIGNED, "cu_seqlens is not 4-byte aligned");
+    a.cu = cu;
+    return lin_sizes(a, N, total, H, Dk, Dv, scale, dtype);
+}
+
+kda_status lin_ws(kda::LinArgs& a, bool backward, void* ws, size_t bytes, const char* what) {
+    if (kda::linattn_groups(a, backward) > kda::kMaxThreads / 256)
+        return fail(KDA_ERR_BAD_SHAPE, "%s: %lld tokens of %lld sequences and %d heads exceed the grid limit", what,
+                    (long long)a.total, (long long)a.N, a.H);
+    const int64_t need = kda::linattn_workspace_bytes(a, backward);
+    if (need > 0 && !ws)
+        return fail(KDA_ERR_NULL_ARG, "%s: workspace is NULL (%lld bytes needed)", what, (long long)need);
+    if ((uint64_t)need > (uint64_t)bytes)
+        return fail(KDA_ERR_BAD_SHAPE, "%s: workspace holds %llu bytes, %lld needed", what, (unsigned long long)bytes,
+                    (long long)need);
+    a.ws = ws;
+    return KDA_OK;
+}
+
+kda_status lin_fwd(kda::LinArgs& a, const void* q, const void* k, const void* v, const float* g, const float* s0, void* o,
+                   float* s_final, void* ws, size_t ws_bytes, void* stream, const char* what) {
+    kda_status st;
+    const bool tokens = a.N > 0 && a.total > 0;
+    const int64_t states = a.N * a.H * a.Dk * a.Dv * 4;
+    if ((st = check_ptrs({{q, "q", tokens}, {k, "k", tokens}, {v, "v", tokens}, {g, "g", tokens, 4}, {o, "o", tokens},
+                          {s0, "s0", false}, {s_final, "s_final", false}, {ws, "workspace", false}})) != KDA_OK)
+        return st;
+    if (overlap(s0, s_final, states, states)) return fail(KDA_ERR_BAD_SHAPE, "%s: s_final must not overlap s0", what);
+    if (a.N == 0 || (!tokens && !s_final)) return ok();
+    if ((st = lin_ws(a, false, ws, ws_bytes, what)) != KDA_OK) return st;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.g = g;
+    a.s0 = s0;
+    a.o = o;
+    a.s_final = s_final;
+    return launched(kda::launch_linattn_fwd(a, static_cast<hipStream_t>(stream)), what);
+}
+
+kda_status lin_bwd(kda::LinArgs& a, const void* q, const void* k, const void* v, const float* g, const float* s0,
+                   const void* d_o, const float* d_sfinal, void* dq, void* dk, void* dv, float* ds0, void* ws,
+                   size_t ws_bytes, void* stream, const char* what) {
+    kda_status st;
+    const bool tokens = a.N > 0 && a.total > 0;
+    const int64_t states = a.N * a.H * a.Dk * a.Dv * 4;
+    if ((st = check_ptrs({{q, "q", tokens}, {k, "k", tokens}, {v, "v", tokens}, {g, "g", tokens, 4},
+                          {d_o, "d_o", tokens}, {dq, "dq", tokens}, {dk, "dk", tokens}, {dv, "dv", tokens},
+                          {s0, "s0", false}, {d_sfinal, "d_sfinal", false}, {ds0, "ds0", false},
+                          {ws, "workspace", false}})) != KDA_OK)
+        return st;
+    if (overlap(d_sfinal, ds0, states, states) || overlap(s0, ds0, states, states))
+        return fail(KDA_ERR_BAD_SHAPE, "%s: ds0 must not overlap s0 or d_sfinal", what);
+    if (a.N == 0 || (!tokens && !ds0)) return ok();
+    if ((st = lin_ws(a, true, ws, ws_bytes, what)) != KDA_OK) return st;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.g = g;
+    a.s0 = s0;
+    a.d_o = d_o;
+    a.d_sfinal = d_sfinal;
+    a.dq = dq;
+    a.dk = dk;
+    a.dv = dv;
+    a.ds0 = ds0;
+    return launched(kda::launch_linattn_bwd(a, static_cast<hipStream_t>(stream)), what);
+}
+
+size_t lin_workspace_bytes(int64_t N, int64_t total, int H, int Dk, int Dv, kda_dtype dtype, bool backward) {
+    kda::LinArgs a{};
+    if (N < 1 || total < 1) return 0;
+    if (H < 1 || H > 65536 || (Dk != 64 && Dk != 128) || (Dv != 64 && Dv != 128)) return 0;
+    if ((dtype != KDA_F32 && dtype != KDA_BF16) || N > kMostElements / H / 128 / 128 || total > kMostElements / H / 128) return 0;
+    a.N = N;
+    a.total = total;
+    a.H = H;
+    a.Dk = Dk;
+    a.Dv = Dv;
+    a.f32 = dtype == KDA_F32;
+    return (size_t)kda::linattn_workspace_bytes(a, backward);
+}
+
+// ---------------------------------------------------------------------------- group norm
+kda_status gn_inputs(kda::GroupNormArgs& a, const void* x, int64_t x_stride, const float* weight, const float* bias,
+                     const void* gate, int64_t gate_stride, int64_t tokens, int64_t groups, int64_t width,
+                     const kda_groupnorm_form* f) {
+    kda_status st;
+    if (!f) return fail(KDA_ERR_NULL_ARG, "form is NULL");
+    if ((f->x_dtype != KDA_F32 && f->x_dtype != KDA_BF16) || (f->y_dtype != KDA_F32 && f->y_dtype != KDA_BF16))
+        return fail(KDA_ERR_BAD_DTYPE, "form x_dtype and y_dtype must be KDA_F32 or KDA_BF16");
+    if (f->act != KDA_ACT_NONE && f->act != KDA_ACT_SILU && f->act != KDA_ACT_SIGMOID)
+        return fail(KDA_ERR_BAD_SHAPE, "form act must be KDA_ACT_NONE, KDA_ACT_SILU or KDA_ACT_SIGMOID (got %d)", f->act);
+    if (!(f->eps >= 0.f)) return fail(KDA_ERR_BAD_SHAPE, "form eps must be >= 0");
+    if (tokens < 0) return fail(KDA_ERR_BAD_SHAPE, "tokens must be >= 0");
+    if (groups < 1 || groups > kda::kMaxChannels) return fail(KDA_ERR_BAD_SHAPE, "groups must be in [1, 2^24]");
+    if (width < 1 || width > kda::kMaxGroupWidth) return fail(KDA_ERR_BAD_SHAPE, "width must be in [1, 2^16]");
+    const int64_t C = groups * width;
+    if (C > kda::kMaxChannels) return fail(KDA_ERR_BAD_SHAPE, "groups*width exceeds 2^24");
+    if (x_stride < C || (gate && gate_stride < C))
+        return fail(KDA_ERR_BAD_SHAPE, "x_stride and gate_stride must be at least groups*width");
+    if (x_stride > kMostElements || (gate && gate_stride > kMostElements) ||
+        (tokens > 0 && tokens > kMostElements / (gate && gate_stride > x_stride ? gate_stride : x_stride)))
+        return fail(KDA_ERR_BAD_SHAPE, "tokens times a stride exceeds 2^40");
+    a.x = x;
+    a.gate = gate;
+    a.x_stride = x_stride;
+    a.gate_stride = gate ? gate_stride : C;
+    a.weight = weight;
+    a.bias = bias;
+    a.tokens = tokens;
+    a.groups = groups;
+    a.width = width;
+    a.x_f32 = f->x_dtype == KDA_F32;
+    a.y_f32 = f->y_dtype == KDA_F32;
+    a.act = f->act;
+    a.eps = f->eps;
+    const bool wide = kda::groupnorm_wide(a);
+    const int xa = wide ? 16 : a.x_f32 ? 4 : 2, ya = wide ? 16 : a.y_f32 ? 4 : 2;
+    if ((st = check_ptrs({{x, "x", tokens > 0, xa}, {gate, "gate", false, ya}, {weight, "weight", false, wide ? 16 : 4},
+                          {bias, "bias", false, wide ? 16 : 4}})) != KDA_OK)
+        return st;
+    if (kda::groupnorm_groups(a) > kda::kMaxThreads / 256)
+        return fail(KDA_ERR_BAD_SHAPE, "%lld tokens of %lld groups exceed the grid limit", (long long)tokens, (long long)groups);
+    return KDA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -749,6 +907,127 @@ kda_status kda_qknorm_bwd(const void* q, const void* k, const uint8_t* q_scales,
 size_t kda_qknorm_bwd_workspace_bytes(int64_t tokens, int Hq, int Hk, int D) {
     if (tokens <= 0 || Hq < 1 || Hk < 1 || Hq > 65536 || Hk > 65536 || (D != 64 && D != 128)) return 0;
     return (size_t)kda::qknorm_bwd_workspace_bytes(tokens, Hq, Hk, D);
+}
+
+kda_status kda_linattn_fwd(const void* q, const void* k, const void* v, const float* g, const float* s0, void* o,
+                           float* s_final, int64_t B, int64_t T, int H, int Dk, int Dv, float scale, kda_dtype dtype,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+    kda_status st;
+    kda::LinArgs a{};
+    if ((st = lin_batch(a, B, T, H, Dk, Dv, scale, dtype)) != KDA_OK) return st;
+    return lin_fwd(a, q, k, v, g, s0, o, s_final, workspace, workspace_bytes, stream, "kda_linattn_fwd");
+}
+
+kda_status kda_linattn_varlen_fwd(const void* q, const void* k, const void* v, const float* g, const int32_t* cu_seqlens,
+                                  int64_t N, int64_t total, const float* s0, void* o, float* s_final, int H, int Dk,
+                                  int Dv, float scale, kda_dtype dtype, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+    kda_status st;
+    kda::LinArgs a{};
+    if ((st = lin_packed(a, cu_seqlens, N, total, H, Dk, Dv, scale, dtype)) != KDA_OK) return st;
+    return lin_fwd(a, q, k, v, g, s0, o, s_final, workspace, workspace_bytes, stream, "kda_linattn_varlen_fwd");
+}
+
+kda_status kda_linattn_bwd(const void* q, const void* k, const void* v, const float* g, const float* s0, const void* d_o,
+                           const float* d_sfinal, void* dq, void* dk, void* dv, float* ds0, int64_t B, int64_t T, int H,
+                           int Dk, int Dv, float scale, kda_dtype dtype, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+    kda_status st;
+    kda::LinArgs a{};
+    if ((st = lin_batch(a, B, T, H, Dk, Dv, scale, dtype)) != KDA_OK) return st;
+    return lin_bwd(a, q, k, v, g, s0, d_o, d_sfinal, dq, dk, dv, ds0, workspace, workspace_bytes, stream,
+                   "kda_linattn_bwd");
+}
+
+kda_status kda_linattn_varlen_bwd(const void* q, const void* k, const void* v, const float* g, const int32_t* cu_seqlens,
+                                  int64_t N, int64_t total, const float* s0, const void* d_o, const float* d_sfinal,
+                                  void* dq, void* dk, void* dv, float* ds0, int H, int Dk, int Dv, float scale,
+                                  kda_dtype dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    kda_status st;
+    kda::LinArgs a{};
+    if ((st = lin_packed(a, cu_seqlens, N, total, H, Dk, Dv, scale, dtype)) != KDA_OK) return st;
+    return lin_bwd(a, q, k, v, g, s0, d_o, d_sfinal, dq, dk, dv, ds0, workspace, workspace_bytes, stream,
+                   "kda_linattn_varlen_bwd");
+}
+
+kda_status kda_linattn_step(const void* q, const void* k, const void* v, const float* g, const float* s_in, float* s_out,
+                            void* o, int64_t B, int H, int Dk, int Dv, float scale, kda_dtype dtype, void* stream) {
+    kda_status st;
+    kda::LinArgs a{};
+    if ((st = lin_batch(a, B, 1, H, Dk, Dv, scale, dtype)) != KDA_OK) return st;
+    if (B * H > kda::kMaxThreads / 256)
+        return fail(KDA_ERR_BAD_SHAPE, "%lld sequence-heads exceed the grid limit", (long long)(B * H));
+    const bool any = B > 0;
+    if ((st = check_ptrs({{q, "q", any}, {k, "k", any}, {v, "v", any}, {g, "g", any, 4}, {s_in, "s_in", any},
+                          {s_out, "s_out", any}, {o, "o", any}})) != KDA_OK)
+        return st;
+    const int64_t states = B * H * Dk * Dv * 4;
+    if (s_in != s_out && overlap(s_in, s_out, states, states))
+        return fail(KDA_ERR_BAD_SHAPE, "s_in and s_out overlap without being the same buffer");
+    if (!any) return ok();
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.g = g;
+    a.o = o;
+    return launched(kda::launch_linattn_step(a, s_in, s_out, static_cast<hipStream_t>(stream)), "kda_linattn_step");
+}
+
+size_t kda_linattn_workspace_bytes(int64_t N, int64_t total, int H, int Dk, int Dv, kda_dtype dtype) {
+    return lin_workspace_bytes(N, total, H, Dk, Dv, dtype, false);
+}
+
+size_t kda_linattn_bwd_workspace_bytes(int64_t N, int64_t total, int H, int Dk, int Dv, kda_dtype dtype) {
+    return lin_workspace_bytes(N, total, H, Dk, Dv, dtype, true);
+}
+
+kda_status kda_groupnorm_fwd(const void* x, int64_t x_stride, const float* weight, const float* bias, const void* gate,
+                             int64_t gate_stride, void* y, int64_t tokens, int64_t groups, int64_t width,
+                             const kda_groupnorm_form* form, void* stream) {
+    kda_status st;
+    kda::GroupNormArgs a{};
+    if ((st = gn_inputs(a, x, x_stride, weight, bias, gate, gate_stride, tokens, groups, width, form)) != KDA_OK) return st;
+    const int ya = kda::groupnorm_wide(a) ? 16 : a.y_f32 ? 4 : 2;
+    if ((st = check_ptrs({{y, "y", tokens > 0, ya}})) != KDA_OK) return st;
+    if (tokens == 0) return ok();
+    a.y = y;
+    return launched(kda::launch_groupnorm_fwd(a, static_cast<hipStream_t>(stream)), "kda_groupnorm_fwd");
+}
+
+kda_status kda_groupnorm_bwd(const void* x, int64_t x_stride, const float* weight, const float* bias, const void* gate,
+                             int64_t gate_stride, const void* dy, void* dx, void* dgate, float* dweight, float* dbias,
+                             int64_t tokens, int64_t groups, int64_t width, const kda_groupnorm_form* form,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+    kda_status st;
+    kda::GroupNormArgs a{};
+    if ((st = gn_inputs(a, x, x_stride, weight, bias, gate, gate_stride, tokens, groups, width, form)) != KDA_OK) return st;
+    const bool any = tokens > 0, wide = kda::groupnorm_wide(a), sums = dweight || dbias;
+    const int xa = wide ? 16 : a.x_f32 ? 4 : 2, ya = wide ? 16 : a.y_f32 ? 4 : 2;
+    if ((st = check_ptrs({{dy, "dy", any, ya}, {dx, "dx", any, xa}, {dgate, "dgate", any && gate, ya},
+                          {dweight, "dweight", sums}, {dbias, "dbias", sums}, {workspace, "workspace", false}})) != KDA_OK)
+        return st;
+    if (dgate && !gate) return fail(KDA_ERR_BAD_SHAPE, "dgate without a gate");
+    if (!any && !sums) return ok();
+    const int64_t need = sums ? kda::groupnorm_bwd_workspace_bytes(tokens, groups, width) : 0;
+    if (need > 0 && !workspace)
+        return fail(KDA_ERR_NULL_ARG, "kda_groupnorm_bwd: workspace is NULL (%lld bytes needed)", (long long)need);
+    if ((uint64_t)need > (uint64_t)workspace_bytes)
+        return fail(KDA_ERR_BAD_SHAPE, "kda_groupnorm_bwd: workspace holds %llu bytes, %lld needed",
+                    (unsigned long long)workspace_bytes, (long long)need);
+    a.dy = dy;
+    a.dx = dx;
+    a.dgate = dgate;
+    a.dweight = dweight;
+    a.dbias = dbias;
+    a.ws = workspace;
+    return launched(kda::launch_groupnorm_bwd(a, static_cast<hipStream_t>(stream)), "kda_groupnorm_bwd");
+}
+
+size_t kda_groupnorm_bwd_workspace_bytes(int64_t tokens, int64_t groups, int64_t width) {
+    if (tokens < 1 || groups < 1 || groups > kda::kMaxChannels || width < 1 || width > kda::kMaxGroupWidth ||
+        groups * width > kda::kMaxChannels)
+        return 0;
+    return (size_t)kda::groupnorm_bwd_workspace_bytes(tokens, groups, width);
 }
 
 const char* kda_last_error(void) { return g_last_error.c_str(); }

@@ -87,4 +87,54 @@ int64_t qknorm_bwd_workspace_bytes(int64_t tokens, int Hq, int Hk, int D);
 hipError_t launch_qknorm_fwd(const QkArgs& a, hipStream_t st);
 hipError_t launch_qknorm_bwd(const QkArgs& a, hipStream_t st);
 
+// ---- linear attention with a decay for each head (kda_linattn.hip)
+struct LinArgs {
+    const void *q, *k, *v;
+    const float *g, *s0;
+    int64_t T_fixed, N, total;  // cu == nullptr: N sequences of T_fixed tokens
+    const int32_t* cu;
+    int H, Dk, Dv;
+    float scale;
+    bool f32;
+    void* ws;
+    // forward
+    void* o;
+    float* s_final;
+    // backward
+    const void* d_o;
+    const float* d_sfinal;
+    void *dq, *dk, *dv;
+    float* ds0;
+};
+int64_t linattn_workspace_bytes(const LinArgs& a, bool backward);
+int64_t linattn_groups(const LinArgs& a, bool backward);  // workgroups of a call's largest launch
+hipError_t launch_linattn_fwd(const LinArgs& a, hipStream_t st);
+hipError_t launch_linattn_bwd(const LinArgs& a, hipStream_t st);
+hipError_t launch_linattn_step(const LinArgs& a, const float* s_in, float* s_out, hipStream_t st);
+
+// ---- group norm with an activation (kda_groupnorm.hip)
+constexpr int64_t kMaxGroupWidth = 1 << 16;
+
+struct GroupNormArgs {
+    const void *x, *gate;
+    int64_t x_stride, gate_stride;
+    const float *weight, *bias;
+    int64_t tokens, groups, width;
+    bool x_f32, y_f32;
+    int act;
+    float eps;
+    // forward
+    void* y;
+    // backward
+    const void* dy;
+    void *dx, *dgate;
+    float *dweight, *dbias;
+    void* ws;
+};
+bool groupnorm_wide(const GroupNormArgs& a);  // rows are read 16 bytes at a time
+int64_t groupnorm_groups(const GroupNormArgs& a);  // workgroups of a call's largest launch
+int64_t groupnorm_bwd_workspace_bytes(int64_t tokens, int64_t groups, int64_t width);
+hipError_t launch_groupnorm_fwd(const GroupNormArgs& a, hipStream_t st);
+hipError_t launch_groupnorm_bwd(const GroupNormArgs& a, hipStream_t st);
+
 }  // namespace kda

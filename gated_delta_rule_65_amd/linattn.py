@@ -1,0 +1,208 @@
+"""Linear attention with a decay for each head (C ABI in ``include/kda_layer.h``): prompts in equal lengths or packed, single
+tokens, and the backward pass.
+
+As in the package's other calls, everything is computed in the library's HIP kernels; this module checks tensors,
+allocates outputs and workspaces with torch and passes pointers and torch's current stream.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional, Tuple
+
+import torch
+
+from . import DTYPE, _aligned_grad, _first_order, _need, _ptr, layer, load_library
+from .layer import _launch, _same_device, _seqs, _ws
+
+
+def declare(L):
+    """Argument types of the entry points."""
+    vp, i64, ci, sz, f = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
+    dims = [ci, ci, ci, f, ci]
+    for name, args in {
+        "kda_linattn_fwd": [vp] * 7 + [i64, i64] + dims + [vp, sz, vp],
+        "kda_linattn_varlen_fwd": [vp] * 5 + [i64, i64] + [vp] * 3 + dims + [vp, sz, vp],
+        "kda_linattn_bwd": [vp] * 11 + [i64, i64] + dims + [vp, sz, vp],
+        "kda_linattn_varlen_bwd": [vp] * 5 + [i64, i64] + [vp] * 7 + dims + [vp, sz, vp],
+        "kda_linattn_step": [vp] * 7 + [i64] + dims + [vp],
+    }.items():
+        getattr(L, name).argtypes, getattr(L, name).restype = args, ci
+    for name in ("kda_linattn_workspace_bytes", "kda_linattn_bwd_workspace_bytes"):
+        getattr(L, name).argtypes, getattr(L, name).restype = [i64, i64, ci, ci, ci, ci], sz
+
+
+def linattn_workspace_bytes(N: int, total: int, H: int, Dk: int, Dv: int, dtype: torch.dtype) -> int:
+    return int(load_library().kda_linattn_workspace_bytes(N, total, H, Dk, Dv, DTYPE[dtype]))
+
+
+def linattn_bwd_workspace_bytes(N: int, total: int, H: int, Dk: int, Dv: int, dtype: torch.dtype) -> int:
+    return int(load_library().kda_linattn_bwd_workspace_bytes(N, total, H, Dk, Dv, DTYPE[dtype]))
+
+
+def _inputs(q, k, v, g, states, lead):
+    """Checks q, k, v, g and the named states; returns the leading sizes, H, Dk, Dv."""
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+    if q.dim() != lead + 2:
+        raise ValueError(f"q must be [{'B, T, ' if lead == 2 else ''}H, Dk]")
+    if q.dtype not in DTYPE:
+        raise TypeError(f"q, k and v must be float32 or bfloat16 (got {q.dtype})")
+    *front, H, Dk = q.shape
+    if v.dim() != q.dim():
+        raise ValueError(f"v has shape {tuple(v.shape)}, expected {(*front, H)} and its own head size")
+    Dv = v.shape[-1]
+    _need(q, "q", q.dtype)
+    _need(k, "k", q.dtype, (*front, H, Dk))
+    _need(v, "v", q.dtype, (*front, H, Dv))
+    _need(g, "g", torch.float32, (H,))
+    _same_device(q.device, k=k, v=v, g=g, **states)
+    return front, H, Dk, Dv
+
+
+def _state_like(t, name, shape):
+    if t is not None:
+        _need(t, name, torch.float32, shape)
+
+
+def _fwd(q, k, v, g, cu, s0, scale, output_final_state, workspace):
+    packed = cu is not None
+    front, H, Dk, Dv = _inputs(q, k, v, g, {"s0": s0, "cu_seqlens": cu}, 1 if packed else 2)
+    N, total = (_seqs(cu), front[0]) if packed else (front[0], front[0] * front[1])
+    _state_like(s0, "s0", (N, H, Dk, Dv))
+    o = torch.empty(v.shape, dtype=q.dtype, device=q.device)
+    sf = torch.empty((N, H, Dk, Dv), dtype=torch.float32, device=q.device) if output_final_state else None
+    ws, ws_bytes = _ws(linattn_workspace_bytes(N, total, H, Dk, Dv, q.dtype), workspace, q.device)
+    tail = (H, Dk, Dv, scale, DTYPE[q.dtype], _ptr(ws), ws_bytes)
+    L = load_library()
+    if packed:
+        _launch(L.kda_linattn_varlen_fwd, q.device, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(cu), N, total, _ptr(s0),
+                _ptr(o), _ptr(sf), *tail)
+    else:
+        _launch(L.kda_linattn_fwd, q.device, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(s0), _ptr(o), _ptr(sf), *front,
+                *tail)
+    return o, sf
+
+
+def linattn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, s0: Optional[torch.Tensor] = None, *,
+                scale: float = 1.0, output_final_state: bool = True, workspace: Optional[torch.Tensor] = None):
+    """Linear attention with a decay for each head: S_t = a S_{t-1} + k_t v_t^T, o_t = scale * S_t^T q_t with
+    a = exp(min(g, 0)) of the head.
+
+    q, k: [B, T, H, Dk], v: [B, T, H, Dv] (bf16 or fp32, Dk and Dv 64 or 128); g (fp32): [H], the log of the decay, a
+    constant of the layer; s0 (fp32): [B, H, Dk, Dv] or None.  Returns o (v's shape, q's type) and the final state (fp32, or
+    None)."""
+    return _fwd(q, k, v, g, None, s0, scale, output_final_state, workspace)
+
+
+def linattn_varlen_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, cu_seqlens: torch.Tensor,
+                       s0: Optional[torch.Tensor] = None, *, scale: float = 1.0, output_final_state: bool = True,
+                       workspace: Optional[torch.Tensor] = None):
+    """:func:`linattn_fwd` over packed sequences: q, k [total, H, Dk], v [total, H, Dv], cu_seqlens int32 [N+1] on the GPU,
+    s0 [N, H, Dk, Dv] or None.  Rows behind the last sequence are left unwritten in o."""
+    if cu_seqlens is None:
+        raise ValueError("cu_seqlens is needed")
+    return _fwd(q, k, v, g, cu_seqlens, s0, scale, output_final_state, workspace)
+
+
+def _bwd(q, k, v, g, cu, d_o, s0, d_sfinal, scale, workspace):
+    packed = cu is not None
+    front, H, Dk, Dv = _inputs(q, k, v, g, {"d_o": d_o, "s0": s0, "d_sfinal": d_sfinal, "cu_seqlens": cu},
+                               1 if packed else 2)
+    N, total = (_seqs(cu), front[0]) if packed else (front[0], front[0] * front[1])
+    _need(d_o, "d_o", q.dtype, v.shape)
+    _state_like(s0, "s0", (N, H, Dk, Dv))
+    _state_like(d_sfinal, "d_sfinal", (N, H, Dk, Dv))
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    ds0 = torch.empty((N, H, Dk, Dv), dtype=torch.float32, device=q.device)
+    ws, ws_bytes = _ws(linattn_bwd_workspace_bytes(N, total, H, Dk, Dv, q.dtype), workspace, q.device)
+    tail = (H, Dk, Dv, scale, DTYPE[q.dtype], _ptr(ws), ws_bytes)
+    outs = (_ptr(d_o), _ptr(d_sfinal), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ds0))
+    L = load_library()
+    if packed:
+        _launch(L.kda_linattn_varlen_bwd, q.device, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(cu), N, total, _ptr(s0),
+                *outs, *tail)
+    else:
+        _launch(L.kda_linattn_bwd, q.device, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(s0), *outs, *front, *tail)
+    return dq, dk, dv, ds0
+
+
+def linattn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, d_o: torch.Tensor,
+                s0: Optional[torch.Tensor] = None, d_sfinal: Optional[torch.Tensor] = None, *, scale: float = 1.0,
+                workspace: Optional[torch.Tensor] = None):
+    """Gradients of :func:`linattn_fwd` for dL/do = d_o (q's type) and dL/dS_T = d_sfinal (fp32, None = 0).  Returns dq, dk,
+    dv (q's type) and ds0 (fp32)."""
+    return _bwd(q, k, v, g, None, d_o, s0, d_sfinal, scale, workspace)
+
+
+def linattn_varlen_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, cu_seqlens: torch.Tensor,
+                       d_o: torch.Tensor, s0: Optional[torch.Tensor] = None, d_sfinal: Optional[torch.Tensor] = None, *,
+                       scale: float = 1.0, workspace: Optional[torch.Tensor] = None):
+    """Gradients of :func:`linattn_varlen_fwd`; arguments and results as for :func:`linattn_bwd`.  Rows behind the last
+    sequence are left unwritten."""
+    if cu_seqlens is None:
+        raise ValueError("cu_seqlens is needed")
+    return _bwd(q, k, v, g, cu_seqlens, d_o, s0, d_sfinal, scale, workspace)
+
+
+def linattn_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, state: torch.Tensor, *,
+                 scale: float = 1.0, inplace: bool = False) -> Tuple[torch.Tensor, torch.Tensor]:
+    """One token per sequence: q, k [B, H, Dk], v [B, H, Dv], state (fp32) [B, H, Dk, Dv].  Returns o [B, H, Dv] (q's type)
+    and the new state (``state`` itself when ``inplace``)."""
+    (B,), H, Dk, Dv = _inputs(q, k, v, g, {"state": state}, 1)
+    _need(state, "state", torch.float32, (B, H, Dk, Dv))
+    o = torch.empty_like(v)
+    out = state if inplace else torch.empty_like(state)
+    _launch(load_library().kda_linattn_step, q.device, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state), _ptr(out), _ptr(o),
+            B, H, Dk, Dv, scale, DTYPE[q.dtype])
+    return o, out
+
+
+def _constant(ctx, index):
+    if ctx.needs_input_grad[index]:
+        raise ValueError("g has no gradient here, the decays are constants: pass it detached")
+
+
+class LinearAttention(torch.autograd.Function):
+    """Autograd wrapper: ``o, s_final = LinearAttention.apply(q, k, v, g, s0, scale)``; s0 may be None.  The decays are
+    constants; gradients of gradients are refused."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, g, s0=None, scale=1.0):
+        o, sf = linattn_fwd(q, k, v, g, s0, scale=scale)
+        ctx.scale = scale
+        ctx.save_for_backward(q, k, v, g, s0)
+        return o, sf
+
+    @staticmethod
+    @_first_order
+    def backward(ctx, d_o, d_sf):
+        _constant(ctx, 3)
+        q, k, v, g, s0 = ctx.saved_tensors
+        dq, dk, dv, ds0 = linattn_bwd(q, k, v, g, _aligned_grad(d_o, q.dtype), s0, _aligned_grad(d_sf, torch.float32),
+                                      scale=ctx.scale)
+        return dq, dk, dv, None, (ds0 if s0 is not None else None), None
+
+
+class VarlenLinearAttention(torch.autograd.Function):
+    """:class:`LinearAttention` over packed sequences: ``o, s_final = VarlenLinearAttention.apply(q, k, v, g, cu_seqlens, s0,
+    scale)``.  Rows behind the last sequence, where q is longer, are zeros in o and have zero gradients."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, g, cu_seqlens, s0=None, scale=1.0):
+        o, sf = linattn_varlen_fwd(q, k, v, g, cu_seqlens, s0, scale=scale)
+        layer._zero_behind(cu_seqlens, o)
+        ctx.scale = scale
+        ctx.save_for_backward(q, k, v, g, cu_seqlens, s0)
+        return o, sf
+
+    @staticmethod
+    @_first_order
+    def backward(ctx, d_o, d_sf):
+        _constant(ctx, 3)
+        q, k, v, g, cu, s0 = ctx.saved_tensors
+        dq, dk, dv, ds0 = linattn_varlen_bwd(q, k, v, g, cu, _aligned_grad(d_o, q.dtype), s0,
+                                             _aligned_grad(d_sf, torch.float32), scale=ctx.scale)
+        layer._zero_behind(cu, dq, dk)
+        layer._zero_behind(cu, dv)
+        return dq, dk, dv, None, None, (ds0 if s0 is not None else None), None

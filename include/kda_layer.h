@@ -1,7 +1,9 @@
 /*
  * kda_layer.h -- the operators around the gated delta rule in a layer: the gated scan over
  * channels (the recurrence's sibling with a vector state), the head norm of queries and keys with
- * the position rotation, and activation checkpoints in 8 bits.  Same library, conventions, status
+ * the position rotation, activation checkpoints in 8 bits, linear attention with a decay for each head
+ * (the recurrence's sibling without the delta rule) and the group norm with an activation that the heads'
+ * outputs pass.  Same library, conventions, status
  * codes and kda_last_error() as kda.h: DEVICE pointers, row-major and contiguous unless a stride
  * is named, 16-byte aligned unless said otherwise; the caller owns every buffer, the library allocates nothing; calls
  * are asynchronous on `stream`, validated on the host before any launch, and never abort or
@@ -162,6 +164,89 @@ kda_status kda_qknorm_bwd(const void* q, const void* k, const uint8_t* q_scales,
                           const kda_qknorm_form* form, void* workspace, size_t workspace_bytes, void* stream);
 
 size_t kda_qknorm_bwd_workspace_bytes(int64_t tokens, int Hq, int Hk, int D);
+
+/* ------------------------------------------------------------------ linear attention with a decay for each head
+ *
+ * Per sequence and head h, with a state S (Dk x Dv, float32) and one decay a = e^(min(g_h, 0)) for all tokens:
+ *     S_t = a S_(t-1) + k_t v_t^T,    o_t = scale * S_t^T q_t
+ * q, k: [B, T, H, Dk], v, o: [B, T, H, Dv] (or [total, H, D] packed), all of `dtype`; g [H] float32, the log of the decay
+ * (any value; -infinity keeps nothing; may begin at any element); s0, s_final [B, H, Dk, Dv] (or [N, ...]) float32.
+ * Dk, Dv in {64, 128}.  The state and all sums are float32, o is rounded once.  What is not finite in q reaches its own row
+ * of o; what is not finite in k or v makes that sequence's rows of that head non-finite from that token on, and touches no
+ * row before it nor another head or sequence.  s_final may be NULL, s0 NULL is zero.
+ */
+kda_status kda_linattn_fwd(const void* q, const void* k, const void* v, const float* g, const float* s0, void* o,
+                           float* s_final, int64_t B, int64_t T, int H, int Dk, int Dv, float scale, kda_dtype dtype,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* Packed sequences; cu_seqlens as for kda_varlen_fwd (sequences may be empty: their s_final is s0).  Tokens from
+ * cu_seqlens[N] on, if total is larger, are neither read into any sequence nor written. */
+kda_status kda_linattn_varlen_fwd(const void* q, const void* k, const void* v, const float* g, const int32_t* cu_seqlens,
+                                  int64_t N, int64_t total, const float* s0, void* o, float* s_final, int H, int Dk,
+                                  int Dv, float scale, kda_dtype dtype, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/*
+ * Gradients for dL/do = d_o (dtype) and dL/dS_T = d_sfinal (float32, or NULL for zero): dq, dk, dv (dtype) and ds0
+ * (float32, or NULL):
+ *     dS_t = scale q_t d_o_t^T + a dS_(t+1)  (from dS_T = scale q_T d_o_T^T + d_sfinal),   ds0 = a dS_1
+ *     dq_t = scale S_t d_o_t,  dk_t = dS_t v_t,  dv_t = dS_t^T k_t
+ * The decays are constants.  Rows of dq, dk, dv behind the last packed sequence are left as they were.
+ */
+kda_status kda_linattn_bwd(const void* q, const void* k, const void* v, const float* g, const float* s0, const void* d_o,
+                           const float* d_sfinal, void* dq, void* dk, void* dv, float* ds0, int64_t B, int64_t T, int H,
+                           int Dk, int Dv, float scale, kda_dtype dtype, void* workspace, size_t workspace_bytes,
+                           void* stream);
+kda_status kda_linattn_varlen_bwd(const void* q, const void* k, const void* v, const float* g, const int32_t* cu_seqlens,
+                                  int64_t N, int64_t total, const float* s0, const void* d_o, const float* d_sfinal,
+                                  void* dq, void* dk, void* dv, float* ds0, int H, int Dk, int Dv, float scale,
+                                  kda_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token per sequence: q, k [B, H, Dk], v, o [B, H, Dv], s_in, s_out [B, H, Dk, Dv] (s_out == s_in allowed). */
+kda_status kda_linattn_step(const void* q, const void* k, const void* v, const float* g, const float* s_in, float* s_out,
+                            void* o, int64_t B, int H, int Dk, int Dv, float scale, kda_dtype dtype, void* stream);
+
+/* Bytes of the workspace of the forward calls and of the backward calls for N sequences of total tokens in all, equally
+ * long or packed (no initial contents needed; not to be shared by calls that may run at once).  0: none needed, or
+ * unsupported sizes. */
+size_t kda_linattn_workspace_bytes(int64_t N, int64_t total, int H, int Dk, int Dv, kda_dtype dtype);
+size_t kda_linattn_bwd_workspace_bytes(int64_t N, int64_t total, int H, int Dk, int Dv, kda_dtype dtype);
+
+/* ------------------------------------------------------------------ group norm with an activation, channels last
+ *
+ * Per token and group of `width` adjacent channels (a head's outputs, say):
+ *     n = (x - mean x) / sqrt(mean (x - mean x)^2 + eps),    z = n * weight + bias
+ *     y = act(z),  or with a gate  y = z * act(gate)
+ * act: the value itself, x / (1 + e^-x) or 1 / (1 + e^-x).  x [tokens, groups * width] x_dtype, gate and y as many of
+ * y_dtype; x_stride, gate_stride: elements from one token to the next (at least groups * width), so that they may be columns
+ * of wider rows; y is contiguous.  weight, bias [groups * width] float32, each may be NULL (ones, zeros).  All of it is
+ * computed in float32 and rounded once.  Where width and the strides are multiples of 8, rows are read 16 bytes at a time
+ * and x, gate and y have to be 16-byte aligned; else an element at a time, and they may begin at any (weight and bias too).
+ * width up to 2^16.
+ */
+enum { KDA_ACT_NONE = 0, KDA_ACT_SILU = 1, KDA_ACT_SIGMOID = 2 };
+
+typedef struct {
+    kda_dtype x_dtype;  /* x, dx */
+    kda_dtype y_dtype;  /* y, gate, dy, dgate */
+    int act;
+    float eps;          /* >= 0 */
+} kda_groupnorm_form;
+
+kda_status kda_groupnorm_fwd(const void* x, int64_t x_stride, const float* weight, const float* bias, const void* gate,
+                             int64_t gate_stride, void* y, int64_t tokens, int64_t groups, int64_t width,
+                             const kda_groupnorm_form* form, void* stream);
+
+/* Gradients for dL/dy = dy (contiguous, y_dtype): dx (contiguous, x_dtype), dgate (contiguous, y_dtype; NULL exactly where
+ * gate is), dweight and dbias [groups * width] float32 (both or neither: NULL where no sums are wanted; a NULL weight's is
+ * that of ones).  The sums over tokens are in a fixed order: the same call gives the same bits.  The workspace
+ * (kda_groupnorm_bwd_workspace_bytes, no initial contents needed) is read only if dweight and dbias are given. */
+kda_status kda_groupnorm_bwd(const void* x, int64_t x_stride, const float* weight, const float* bias, const void* gate,
+                             int64_t gate_stride, const void* dy, void* dx, void* dgate, float* dweight, float* dbias,
+                             int64_t tokens, int64_t groups, int64_t width, const kda_groupnorm_form* form,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+size_t kda_groupnorm_bwd_workspace_bytes(int64_t tokens, int64_t groups, int64_t width);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,284 @@
+"""The group norm with an activation on the GPU, against the formula in 64 bits."""
+import math
+
+import pytest
+import torch
+
+import gated_delta_rule_65_amd as kda
+from tests import linattn_ref as ref
+
+pytestmark = pytest.mark.gpu
+TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+E = 2.0 ** -24
+
+
+def make(seed, tokens, groups, width, xt, yt, gate=True, affine=True, offset=0.3):
+    gen = torch.Generator().manual_seed(seed)
+
+    def normal(*shape):
+        return torch.randn(shape, generator=gen)
+
+    C = groups * width
+    x = (normal(tokens, C) + offset * normal(tokens, 1)).to(TYPES[xt])
+    w, b = (1 + 0.3 * normal(C), 0.3 * normal(C)) if affine else (None, None)
+    return x, w, b, normal(tokens, C).to(TYPES[yt]) if gate else None, normal(tokens, C).to(TYPES[yt])
+
+
+def near(got, want, allowed, what):
+    got = got.detach().cpu().double()
+    bad = ~((got - want).abs() <= allowed)
+    assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.numel()} off, worst {float(((got - want).abs() / allowed).max()):.2f}x"
+
+
+def slack(x, groups, width, p):
+    """How far n may be off: the mean's and the variance's sums are of `width` terms, one rounding each at most, relative to
+    the largest |x| of the group against its deviation, and a few roundings of n itself."""
+    X = x.double().unflatten(-1, (groups, -1))
+    rel = (X.abs().amax(-1, keepdim=True) * p["r"])  # |x| / sigma
+    steps = width / 8 + 16  # sums go over lanes and chunks of 8: log2 and width / 64, taken generously
+    return steps * E * (rel + p["n"].abs())
+
+
+def check_fwd(y, x, groups, w, b, gate, act, eps, what="y"):
+    p = ref.group_norm(x, groups, w, b, gate, act, eps)
+    dn = slack(x, groups, x.shape[-1] // groups, p)
+    dz = dn * p["W"].abs() + 4 * E * p["z"].abs() + 4 * E * (p["n"] * p["W"]).abs()
+    # act' is below 1.1 in size; with a gate z's error is scaled by act(gate)
+    err = (1.1 * dz if gate is None else dz * p["f"].abs()) + 16 * E * p["y"].unflatten(-1, (groups, -1)).abs()
+    half = ref.HALF[y.dtype]
+    near(y, p["y"], half * p["y"].abs() + (1 + half) * err.flatten(-2) + 1e-36, what)
+
+
+def check_bwd(got, x, groups, dy, w, b, gate, act, eps):
+    want = ref.group_norm_grads(x, groups, dy, w, b, gate, act, eps)
+    p, D, dz, dn = want["parts"]
+    width = x.shape[-1] // groups
+    en = slack(x, groups, width, p)
+    ez = en * p["W"].abs() + 8 * E * (p["z"].abs() + (p["n"] * p["W"]).abs())
+    # act'' is below 1 in size: the slope moves by the argument's error
+    edz = D.abs() * ((ez if gate is None else 0.0) + 32 * E) + 8 * E * dz.abs()
+    edn = edz * p["W"].abs()
+    steps = width / 8 + 16
+    mean = lambda t: t.mean(-1, keepdim=True)  # noqa: E731
+    rms = mean(dn.abs()) + p["n"].abs() * mean((dn * p["n"]).abs()) + dn.abs()
+    edx = p["r"] * (edn + mean(edn) + p["n"].abs() * mean(edn * p["n"].abs() + dn.abs() * en) + en * mean((dn * p["n"]).abs()) +
+                    steps * E * rms) + (4 * E + en.amax(-1, keepdim=True)) * (p["r"] * rms)
+    half = ref.HALF[got[0].dtype]
+    near(got[0], want["dx"], half * want["dx"].abs() + (1 + half) * edx.flatten(-2) + 1e-36, "dx")
+    if gate is not None:
+        half = ref.HALF[got[3].dtype]
+        eg = (D.abs() * (ez * p["slope"].abs() + 32 * E * p["z"].abs())).flatten(-2)
+        near(got[3], want["dgate"], half * want["dgate"].abs() + (1 + half) * eg + 1e-36, "dgate")
+    lead = tuple(range(x.dim() - 1))
+    rows = x.shape[:-1].numel()
+    if w is not None:
+        near(got[1], want["dw"], (edz * p["n"].abs() + dz.abs() * en).sum(lead).flatten() +
+             (rows / 16 + 64) * E * (dz * p["n"]).abs().sum(lead).flatten() + 1e-36, "dweight")
+    if b is not None:
+        near(got[2], want["db"], edz.sum(lead).flatten() + (rows / 16 + 64) * E * dz.abs().sum(lead).flatten() + 1e-36, "dbias")
+
+
+def run(x, groups, w, b, gate, dy, act, eps):
+    c = lambda t: None if t is None else t.cuda()  # noqa: E731
+    y = kda.group_norm_act_fwd(c(x), groups, weight=c(w), bias=c(b), gate=c(gate), act=act, eps=eps, dtype=dy.dtype)
+    check_fwd(y, x, groups, w, b, gate, act, eps)
+    got = kda.group_norm_act_bwd(c(x), groups, c(dy), weight=c(w), bias=c(b), gate=c(gate), act=act, eps=eps)
+    check_bwd(got, x, groups, dy, w, b, gate, act, eps)
+
+
+SIZES = [(1, 1, 16), (1, 3, 128), (5, 16, 64), (70, 3, 90), (33, 2, 100), (17, 1, 1000), (4, 5, 33), (300, 4, 256),
+         (9, 2, 2048), (3, 1, 5000), (1027, 2, 64), (2, 1, 9000)]
+
+
+@pytest.mark.parametrize("xt,yt", [("bf16", "bf16"), ("f32", "bf16"), ("f32", "f32"), ("bf16", "f32")])
+@pytest.mark.parametrize("tokens,groups,width", SIZES)
+def test_sizes(tokens, groups, width, xt, yt):
+    act = ["silu", "sigmoid", "none"][(tokens + width) % 3]
+    x, w, b, gate, dy = make(tokens + width, tokens, groups, width, xt, yt)
+    run(x, groups, w, b, gate, dy, act, 1e-5)
+    run(x, groups, w, b, None, dy, act, 1e-5)
+
+
+@pytest.mark.parametrize("act", ["none", "silu", "sigmoid"])
+@pytest.mark.parametrize("affine", [(0, 0), (1, 0), (0, 1), (1, 1)])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("width", [64, 50])
+def test_forms(act, affine, gated, width):
+    x, w, b, gate, dy = make(7, 40, 3, width, "bf16", "bf16")
+    run(x, 3, w if affine[0] else None, b if affine[1] else None, gate if gated else None, dy, act, 1e-6)
+
+
+@pytest.mark.parametrize("width", [64, 36])
+def test_strides(width):
+    """Columns of wider rows, aligned or not: the same bits as contiguous ones."""
+    x, w, b, gate, dy = make(8, 50, 4, width, "bf16", "bf16")
+    C = 4 * width
+    for extra in (8, 3):
+        wide = torch.randn(50, 2 * C + 2 * extra).bfloat16().cuda()
+        xs, gs = wide[:, extra:extra + C], wide[:, extra + C:extra + 2 * C]
+        xs.copy_(x)
+        gs.copy_(gate)
+        kw = {"weight": w.cuda(), "bias": b.cuda()}
+        y = kda.group_norm_act_fwd(xs, 4, gate=gs, **kw)
+        check_fwd(y, x, 4, w, b, gate, "silu", 1e-5)
+        got = kda.group_norm_act_bwd(xs, 4, dy.cuda(), gate=gs, **kw)
+        check_bwd(got, x, 4, dy, w, b, gate, "silu", 1e-5)
+
+
+def test_leading_dimensions_and_starts():
+    """[B, T, C], and vectors that begin at any element."""
+    x, w, b, gate, dy = make(9, 24, 2, 50, "f32", "f32")
+    off = lambda t: torch.cat([t.new_zeros(1), t.flatten()]).cuda()[1:].view(t.shape)  # noqa: E731
+    X, W, Bi, G, DY = (off(t) for t in (x, w, b, gate, dy))
+    y = kda.group_norm_act_fwd(X.view(4, 6, 100), 2, weight=W, bias=Bi, gate=G.view(4, 6, 100))
+    check_fwd(y.view(24, 100), x, 2, w, b, gate, "silu", 1e-5)
+    got = kda.group_norm_act_bwd(X, 2, DY, weight=W, bias=Bi, gate=G)
+    check_bwd(got, x, 2, dy, w, b, gate, "silu", 1e-5)
+
+
+def test_far_means():
+    """A mean far from zero against the deviation: the variance is of the centred values."""
+    x, w, b, gate, dy = make(10, 60, 2, 128, "f32", "f32")
+    x = x + 1000.0
+    run(x, 2, w, b, gate, dy, "silu", 1e-5)
+
+
+def test_constant_rows_and_large_values():
+    """Groups without deviation give the bias; values near the type's largest do not overflow on the way."""
+    x, w, b, gate, dy = make(11, 8, 2, 64, "f32", "f32")
+    x[0] = 2.5
+    x[1] = 0.0
+    y = kda.group_norm_act_fwd(x.cuda(), 2, weight=w.cuda(), bias=b.cuda(), act="none")
+    assert torch.equal(y[:2].cpu(), b.expand(2, -1))
+    z = kda.group_norm_act_fwd((x * 2.0 ** 60).cuda(), 2, weight=w.cuda(), bias=b.cuda(), act="none", eps=0.0)
+    check_fwd(z[2:], x[2:], 2, w, b, None, "none", 0.0)
+    for act in ("silu", "sigmoid"):
+        big = torch.tensor([-3e38, -200.0, -90.0, 90.0, 3e38]).repeat(8, 26)[:, :128].contiguous()
+        y = kda.group_norm_act_fwd(x.cuda(), 2, gate=big.cuda(), act=act)
+        got = kda.group_norm_act_bwd(x.cuda(), 2, dy.cuda(), gate=big.cuda(), act=act)
+        assert bool(torch.isfinite(got[0]).all() if act == "sigmoid" else True) and not bool(torch.isnan(y).any())
+        assert not bool(torch.isnan(got[3]).any())
+
+
+@pytest.mark.parametrize("width", [64, 50])
+def test_not_finite(width):
+    """What is not finite reaches its own group of its own token."""
+    x, w, b, gate, dy = make(12, 10, 4, width, "bf16", "bf16")
+    clean = kda.group_norm_act_fwd(x.cuda(), 4, weight=w.cuda(), gate=gate.cuda()).cpu()
+    for bad in (math.nan, math.inf, -math.inf):
+        z = x.clone()
+        z[3, width + 5] = bad
+        y = kda.group_norm_act_fwd(z.cuda(), 4, weight=w.cuda(), gate=gate.cuda()).cpu()
+        hit = torch.zeros(y.shape, dtype=torch.bool)
+        hit[3, width:2 * width] = True
+        assert torch.equal(torch.isnan(y), hit) and torch.equal(y[~hit], clean[~hit])
+
+
+def test_same_bits():
+    x, w, b, gate, dy = (t.cuda() for t in make(13, 5000, 4, 64, "bf16", "bf16"))
+    one, two = (kda.group_norm_act_bwd(x, 4, dy, weight=w, bias=b, gate=gate) for _ in range(2))
+    assert all(torch.equal(a, b) for a, b in zip(one, two))
+
+
+@pytest.mark.parametrize("act", ["silu", "sigmoid", "none"])
+@pytest.mark.parametrize("gated", [False, True])
+def test_differences(act, gated):
+    x, w, b, gate, dy = make(14, 30, 2, 48, "f32", "f32")
+    leaves = [t for t in (x, w, b) + ((gate,) if gated else ())]
+    c = [t.cuda() for t in leaves]
+
+    def loss(*ins):
+        y = kda.group_norm_act_fwd(ins[0], 2, weight=ins[1], bias=ins[2], gate=ins[3] if gated else None, act=act)
+        return float((y.double() * dy.cuda().double()).sum())
+
+    got = kda.group_norm_act_bwd(c[0], 2, dy.cuda(), weight=c[1], bias=c[2], gate=c[3] if gated else None, act=act)
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    h = 2.0 ** -7  # third derivatives are of size one: the difference is off by h^2 / 6 of them, the loss by 2^-24 / h
+    for i, grad in enumerate(got[:len(c)]):
+        d = torch.randn(c[i].shape, generator=gen, device="cuda")
+        up, down = list(c), list(c)
+        up[i], down[i] = c[i] + h * d, c[i] - h * d
+        diff, slope = (loss(*up) - loss(*down)) / (2 * h), float((grad.double() * d.double()).sum())
+        size = float((grad.double() * d.double()).norm()) * 4 + float(dy.double().norm())
+        assert abs(diff - slope) <= (4 * h * h + 2 ** -20 / h) * size * 4, (i, diff, slope, size)
+
+
+def test_autograd():
+    x, w, b, gate, dy = (t.cuda() for t in make(15, 30, 2, 64, "f32", "bf16"))
+    leaves = [t.clone().requires_grad_() for t in (x, w, b, gate)]
+    y = kda.GroupNormAct.apply(leaves[0], 2, *leaves[1:], "sigmoid", 1e-6)
+    assert y.dtype == torch.bfloat16
+    y.backward(dy)
+    dx, dw, db, dgate = kda.group_norm_act_bwd(x, 2, dy, weight=w, bias=b, gate=gate, act="sigmoid", eps=1e-6)
+    for t, want in zip(leaves, (dx, dw, db, dgate)):
+        assert torch.equal(t.grad, want)
+    out = kda.GroupNormAct.apply(leaves[0], 2)
+    grad, = torch.autograd.grad(out.sum(), leaves[0], create_graph=True)
+    with pytest.raises(RuntimeError, match="first-order"):
+        grad.sum().backward()
+
+
+def test_graph():
+    x, w, b, gate, dy = (t.cuda() for t in make(16, 3000, 4, 64, "bf16", "bf16"))
+    other = [t.cuda() for t in make(17, 3000, 4, 64, "bf16", "bf16")]
+    values = [x.clone(), w.clone(), b.clone(), gate.clone(), dy.clone()]
+
+    def calls(x, w, b, gate, dy):
+        return (kda.group_norm_act_fwd(x, 4, weight=w, bias=b, gate=gate),
+                *kda.group_norm_act_bwd(x, 4, dy, weight=w, bias=b, gate=gate))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        calls(x, w, b, gate, dy)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = calls(x, w, b, gate, dy)
+    for new in (values, other, values):
+        for to, t in zip((x, w, b, gate, dy), new):
+            to.copy_(t)
+        graph.replay()
+        want = calls(*new)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_nothing_to_do():
+    x = torch.empty((0, 64), device="cuda")
+    w = torch.ones(64, device="cuda")
+    assert kda.group_norm_act_fwd(x, 2, weight=w).shape == (0, 64)
+    dx, dw, db, dgate = kda.group_norm_act_bwd(x, 2, x, weight=w)
+    assert dx.shape == (0, 64) and not bool(dw.any()) and db is None and dgate is None
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_behind_the_recurrences(dtype):
+    """A layer's way: linear attention, or the gated delta rule with its fp32 outputs, then the gated norm of each head, and
+    the gradients of both together."""
+    B, T, H, D = 2, 100, 2, 64
+    q, k, v, d_o, g, s0, _ = ref.inputs(61, (B, T), H, D, D, TYPES[dtype], B)
+    _, w, b, gate, dy = make(62, B * T, H, D, "f32", dtype)
+    leaves = [t.cuda().requires_grad_() for t in (q, k, v, w, b, gate)]
+    o, _ = kda.LinearAttention.apply(*leaves[:3], g.cuda(), None, D ** -0.5)
+    y = kda.GroupNormAct.apply(o.flatten(2).flatten(0, 1), H, *leaves[3:], "silu", 1e-5)
+    y.backward(dy.cuda())
+    want_o, _ = ref.attend(q, k, v, g, None, None, D ** -0.5)
+    seen = o.detach().cpu()  # the norm's input as it is rounded
+    # a term passes at most T + 2 D additions of 32 bits on its way, each of half a step
+    size, _ = ref.magnitude(ref.attend, q, k, v, g, scale=D ** -0.5)
+    near(seen, want_o, ref.bound(TYPES[dtype], want_o, size, T + 2 * D), "o")
+    rows = seen.flatten(2).flatten(0, 1)
+    check_fwd(y, rows, H, w, b, gate, "silu", 1e-5)
+    p = ref.group_norm_grads(rows, H, dy, w, b, gate, "silu", 1e-5)
+    grads = ref.attend_grads(q, k, v, g, p["dx"].view(B, T, H, D), None, None, None, D ** -0.5)
+    # in norm: a rounding of the norm's gradient and one of each result, and the products'
+    half = 4 * ref.HALF[TYPES[dtype]] + 1e-4
+    for leaf, want in zip(leaves, (*grads[:3], p["dw"], p["db"], p["dgate"])):
+        assert float((leaf.grad.cpu().double() - want).norm()) <= half * float(want.norm())
+    beta = torch.rand(B, T, H, device="cuda")
+    o, _ = kda.chunk_fwd(leaves[0].detach(), torch.nn.functional.normalize(leaves[1].detach().float(), dim=-1).to(TYPES[dtype]),
+                         leaves[2].detach(), -torch.rand(B, T, H, D, device="cuda"), beta)
+    assert o.dtype == torch.float32
+    y = kda.group_norm_act_fwd(o.flatten(2), H, weight=w.cuda(), bias=b.cuda(), gate=gate.cuda().view(B, T, -1), act="sigmoid")
+    check_fwd(y.flatten(0, 1), o.cpu().flatten(2).flatten(0, 1), H, w, b, gate, "sigmoid", 1e-5)
