@@ -59,6 +59,8 @@ def test_common_validation(name, defaults, kw, status, msg):
     ("kda_linattn_fwd", FWD, dict(B=1 << 30, T=1 << 30), 2, "2^40"), ("kda_linattn_fwd", FWD, dict(B=1 << 30, T=1), 2, "out of range"),
     ("kda_linattn_fwd", FWD, dict(T=1 << 34), 2, "out of range"), ("kda_linattn_fwd", FWD, dict(o=None), 1, "o"),
     ("kda_linattn_fwd", FWD, dict(s0=FAKE + 4), 4, "s0"), ("kda_linattn_fwd", FWD, dict(s_final=FAKE), 2, "overlap"),
+    ("kda_linattn_fwd", FWD, dict(T=100000, workspace=None), 1, "workspace"),
+    ("kda_linattn_fwd", FWD, dict(T=100000, workspace_bytes=64), 2, "workspace"),
     ("kda_linattn_varlen_fwd", VARLEN, dict(N=-1), 2, "N"), ("kda_linattn_varlen_fwd", VARLEN, dict(total=-1), 2, "total"),
     ("kda_linattn_varlen_fwd", VARLEN, dict(total=1 << 31), 2, "int32"),
     ("kda_linattn_varlen_fwd", VARLEN, dict(cu_seqlens=None), 1, "cu_seqlens"),
@@ -66,6 +68,8 @@ def test_common_validation(name, defaults, kw, status, msg):
     ("kda_linattn_bwd", BWD, dict(d_o=None), 1, "d_o"), ("kda_linattn_bwd", BWD, dict(dq=None), 1, "dq"),
     ("kda_linattn_bwd", BWD, dict(dk=None), 1, "dk"), ("kda_linattn_bwd", BWD, dict(dv=FAKE + 2), 4, "dv"),
     ("kda_linattn_bwd", BWD, dict(ds0=FAKE), 2, "overlap"),
+    ("kda_linattn_bwd", BWD, dict(T=100000, workspace=None), 1, "workspace"),
+    ("kda_linattn_varlen_bwd", VARLEN_BWD, dict(total=100000, workspace_bytes=64), 2, "workspace"),
     ("kda_linattn_step", STEP, dict(B=-1), 2, "B"), ("kda_linattn_step", STEP, dict(s_in=None), 1, "s_in"),
     ("kda_linattn_step", STEP, dict(s_out=None), 1, "s_out"), ("kda_linattn_step", STEP, dict(s_out=FAKE + 16), 2, "overlap"),
 ])
@@ -89,6 +93,7 @@ def test_linattn_workspace_sizes():
         for dtype in (torch.bfloat16, torch.float32):
             assert size(0, 5, 2, 64, 64, dtype) == size(1, 0, 2, 64, 64, dtype) == size(1, 5, 0, 64, 64, dtype) == 0
             assert size(1, 5, 2, 32, 64, dtype) == size(1 << 30, 1 << 30, 65536, 64, 64, dtype) == 0
+            assert size(1, 1 << 20, 8, 128, 128, dtype) > 0
 
 
 GN = dict(x=FAKE, x_stride=128, weight=FAKE, bias=FAKE, gate=FAKE, gate_stride=128, y=FAKE, tokens=3, groups=2, width=64,
