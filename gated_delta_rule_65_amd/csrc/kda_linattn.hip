@@ -123,76 +123,128 @@ __device__ __forceinline__ f32x4_t mma(const LFrag<true>& a, const LFrag<true>& 
     return c;
 }
 
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+
+// Two values as bf16, the nearest ones; and what they stand for.
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
+}
+__device__ __forceinline__ float low_of(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float high_of(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+
 // x as a sum of PLANES bf16 values, each the nearest to what the ones before leave; in fp32 x itself.
-template <int PLANES, bool F32>
-__device__ __forceinline__ void split(const float x[8], LFrag<F32> f[PLANES]) {
-    if constexpr (F32) {
+template <int PLANES>
+__device__ __forceinline__ void split(const float x[8], LFrag<false> f[PLANES]) {
+    uint4 u[PLANES];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[0].v[j] = x[j];
-    } else {
-        float r[8];
+    for (int j = 0; j < 4; ++j) {
+        float a = x[2 * j], b = x[2 * j + 1];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) r[j] = x[j];
-#pragma unroll
-        for (int p = 0; p < PLANES; ++p)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const __bf16 h = (__bf16)r[j];
-                f[p].v[j] = h;
-                r[j] -= (float)h;
+        for (int p = 0; p < PLANES; ++p) {
+            const uint32_t h = pack2(a, b);
+            (&u[p].x)[j] = h;
+            if (p + 1 < PLANES) {
+                a -= low_of(h);
+                b -= high_of(h);
             }
+        }
     }
+#pragma unroll
+    for (int p = 0; p < PLANES; ++p) f[p].v = __builtin_bit_cast(bf16x8_t, u[p]);
+}
+template <int PLANES>
+__device__ __forceinline__ void split(const float x[8], LFrag<true> f[PLANES]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[0].v[j] = x[j];
+}
+
+__device__ __forceinline__ void values(const LFrag<false>& f, float x[8]) {
+    const uint4 u = __builtin_bit_cast(uint4, f.v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        x[2 * j] = low_of((&u.x)[j]);
+        x[2 * j + 1] = high_of((&u.x)[j]);
+    }
+}
+__device__ __forceinline__ void values(const LFrag<true>& f, float x[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = f.v[j];
+}
+
+// Whether one of a lane's values is not finite: the largest of their bits without sign.
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+template <int COUNT>
+__device__ __forceinline__ bool any_not_finite(const LFrag<false>* f) {
+    u16x2_t most = {0, 0};
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) {
+        const uint4 u = __builtin_bit_cast(uint4, f[i].v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2_t, (&u.x)[j] & 0x7fff7fffu));
+    }
+    return most[0] >= 0x7f80 || most[1] >= 0x7f80;
+}
+template <int COUNT>
+__device__ __forceinline__ bool any_not_finite(const LFrag<true>* f) {
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) most = max(most, __float_as_uint(f[i].v[j]) & 0x7fffffffu);
+    return most >= 0x7f800000u;
 }
 
 // Rows of UNITS 16-byte units in LDS.  A unit's place is turned by its row so that neither 16 rows' same unit nor, transposed,
 // two units of eight rows meet in a bank.
 template <int UNITS, bool F32>
-struct Tile {
-    static constexpr int BYTES = UNITS * 16;
-    static __device__ __forceinline__ int place(int row, int unit) {
-        int f;
-        if constexpr (UNITS == 8) f = (row & 6) | (row >> 3 & 1);
-        else if constexpr (F32) f = row & 15;
-        else f = (row & 7) << 1 | (row >> 3 & 1);
-        return row * BYTES + (unit ^ f) * 16;
-    }
-};
+__device__ __forceinline__ int turn(int row) {
+    if constexpr (UNITS == 4) return row >> 2 & 3;
+    else if constexpr (UNITS == 8) return (row & 6) | (row >> 3 & 1);
+    else if constexpr (F32) return row & 15;
+    else return (row & 7) << 1 | (row >> 3 & 1);
+}
+template <int UNITS, bool F32>
+__device__ __forceinline__ int place(int row, int unit) {
+    return (row * UNITS + (unit ^ turn<UNITS, F32>(row))) * 16;
+}
 
 // Four values of one column of a bf16 tile: lane i of 16 gives the place of four values of row i/4, and gets column i.
 __device__ __forceinline__ bf16x4_t read_turned(const char* p) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4bf16((__attribute__((address_space(3))) bf16x4_t*)const_cast<char*>(p));
 }
 
-template <int DA, int DC, bool F32, bool ROWS>
+// 16 bytes for each lane of a wave from memory to LDS, where they lie one after another from `to` on.
+__device__ __forceinline__ void load_to_lds(const void* from, char* to) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)(uintptr_t)from,
+                                     (__attribute__((address_space(3))) uint32_t*)to, 16, 0, 0);
+}
+
+template <int DA, int DC, bool F32>
 struct LinTile {
     static constexpr int C = F32 ? 32 : 64;      // tokens of a chunk
     static constexpr int ES = F32 ? 4 : 2;
     static constexpr int UA = DA * ES / 16, UC = DC * ES / 16;  // units of a row
-    static constexpr int NA = C * UA / kThreads, NC = C * UC / kThreads;  // units a thread moves
+    static constexpr int KB = C * UA * 16, VB = C * UC * 16;
     static constexpr int ND = DC / 64;           // 16-column tiles of a wave
     static constexpr int KS = C / 32, RB = C / 16, AS = DA / 32, CT = DA / 16;
     static constexpr int PL = F32 ? 1 : 2;       // planes of scores and of the state
     static constexpr int VL = F32 ? 1 : 3;       // planes of the weighted values
-    static constexpr int PU = C * ES / 16;       // units of a row of scores
-    static constexpr int KB = C * UA * 16, VB = C * UC * 16, PB = C * PU * 16;
-    static constexpr int TAB = (C + 4) * 4;
-    static constexpr int LDS = KB + VB + TAB + (ROWS ? KB + PL * PB : 0);
+    static constexpr int PB = F32 ? 32 * 128 : 32 * 64 + 32 * 128;  // a plane of scores: rows up to their diagonal's 32 tokens
 };
 
+// A workgroup's way through its segment, four waves with a quarter of the columns each and all rows of the state for them.
 template <int DA, int DC, bool F32, bool ROWS>
 __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinOp op0, LinOp op1, LinOp op2, int ops, Segs segs,
                                                                     const float* g) {
-    using G = LinTile<DA, DC, F32, ROWS>;
-    using TA = Tile<G::UA, F32>;
-    using TC = Tile<G::UC, F32>;
-    using TP = Tile<G::PU, F32>;
-    constexpr int C = G::C, ND = G::ND;
-    __shared__ __align__(16) char lds[G::LDS];
-    char* const ldsK = lds;
-    char* const ldsV = lds + G::KB;
-    float* const tab = reinterpret_cast<float*>(lds + G::KB + G::VB);  // a^0 .. a^C, and what a^C is rounded off by
-    char* const ldsQ = lds + G::KB + G::VB + G::TAB;
-    char* const ldsP = ldsQ + G::KB;
+    using G = LinTile<DA, DC, F32>;
+    constexpr int C = G::C, ND = G::ND, UA = G::UA, UC = G::UC;
+    __shared__ __align__(16) char ldsK0[G::KB], ldsK1[G::KB];
+    __shared__ __align__(16) char ldsV0[G::VB], ldsV1[ROWS ? 16 : G::VB];
+    __shared__ __align__(16) char ldsQ[ROWS ? G::KB : 16], ldsP[ROWS ? G::PL * G::PB : 16];
+    __shared__ __align__(16) float weights[2][C];  // what a token's product keeps at the end of a whole chunk, and of the last one
+    __shared__ float powers[C + 1];             // of the decay
 
     // the operations of a segment and head in workgroups of one XCD, next to one another
     const int64_t id = (int64_t)(blockIdx.x / (8 * ops)) * 8 + blockIdx.x % 8;
@@ -201,7 +253,7 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinOp op0, L
     const int H = segs.H, h = id % H;
     const Where w = where_of(segs, id / H);
     if (w.count < 0) return;
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, m = lane & 15, grp = lane >> 4;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, m = lane & 15, grp = lane >> 4;
     const bool first = op.back ? w.j == w.count - 1 : w.j == 0, last = op.back ? w.j == 0 : w.j + 1 >= w.count;
     if (w.count == 0) {
         if (ROWS && op.fin) {
@@ -212,12 +264,49 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinOp op0, L
     }
     if (!ROWS && last) return;
 
-    // a column of a wave's 16-column tile d: eight columns of a lane side by side in rows
+    // a wave's columns: those of a lane's rows of a product, of both tiles, are side by side
     auto col = [&](int i, int d) { return ND == 2 ? 32 * wave + 8 * (i >> 2) + 4 * d + (i & 3) : 16 * wave + i; };
 
+    const int tokens = (int)(w.end - w.begin), chunks = (tokens + C - 1) / C;
+    // Rows of a chunk, in the order of the recurrence, to LDS: 64 units a wave at a time.  A whole chunk's places are one offset
+    // a lane from an address that the wave shares; the last one's rows behind its end repeat its last row, and weigh nothing.
+    const int64_t row0 = op.back ? w.end - 1 : w.begin;
+    auto offset_of = [&](auto units) {
+        constexpr int U = decltype(units)::value;
+        const int u = wave * 64 + lane, row = u / U, unit = u % U ^ turn<U, F32>(row);
+        return (uint32_t)((op.back ? C - 1 - row : row) * H * U + unit) * 16u;
+    };
+    auto fetch = [&](const void* from, char* to, int c, auto units, uint32_t offset) {
+        constexpr int U = decltype(units)::value, N = C * U / kThreads, ROWS_AT_ONCE = kThreads / U;
+        static_assert(ROWS_AT_ONCE % 16 == 0 || (F32 && ROWS_AT_ONCE == 8), "what a row's turn is, 16 rows behind or eight");
+        const int64_t pitch = (int64_t)H * U * 16;
+        if (tokens - c * C >= C) {
+            const char* base = static_cast<const char*>(from) + (op.back ? row0 - c * C - (C - 1) : row0 + c * C) * pitch + (int64_t)h * U * 16;
+#pragma unroll
+            for (int x = 0; x < N; ++x)
+                load_to_lds(base + (op.back ? -x : x) * ROWS_AT_ONCE * pitch + (ROWS_AT_ONCE == 8 && x % 2 ? offset ^ 128 : offset),
+                            to + (x * 4 + wave) * 1024);
+        } else {
+#pragma unroll 1
+            for (int x = 0; x < N; ++x) {
+                const int u = (x * 4 + wave) * 64 + lane, row = u / U, unit = u % U ^ turn<U, F32>(row);
+                const int r = c * C + row, t = r < tokens ? r : tokens - 1;
+                load_to_lds(static_cast<const char*>(from) + (row0 + (op.back ? -t : t)) * pitch + ((int64_t)h * U + unit) * 16,
+                            to + (x * 4 + wave) * 1024);
+            }
+        }
+    };
+    using UnitsA = std::integral_constant<int, UA>;
+    using UnitsC = std::integral_constant<int, UC>;
+    const uint32_t offset_a = offset_of(UnitsA()), offset_c = offset_of(UnitsC());
+    fetch(op.b, ldsK0, 0, UnitsA(), offset_a);
+    fetch(op.c, ldsV0, 0, UnitsC(), offset_c);
+    if constexpr (ROWS) fetch(op.a, ldsQ, 0, UnitsA(), offset_a);
+
     const double lg = log_decay(g[h]);
-    for (int i = tid; i <= C; i += kThreads) tab[i] = (float)exp(lg * i);
-    if (tid == 0) tab[C + 1] = (float)(exp(lg * C) - (double)(float)exp(lg * C));
+    if (tid <= C) powers[tid] = (float)exp(lg * tid);
+    const double whole = exp(lg * C);
+    const float whole32 = (float)whole, rest = whole > 0 ? (float)((whole - (double)whole32) / whole) : 0.f;
 
     f32x4_t S[G::CT][ND];
 #pragma unroll
@@ -241,186 +330,158 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinOp op0, L
         }
     }
 
-    const int64_t tokens = w.end - w.begin, chunks = (tokens + C - 1) / C;
-    // row r of chunk c, in the order of the recurrence
-    auto token = [&](int64_t c, int r) { return op.back ? w.end - 1 - (c * C + r) : w.begin + c * C + r; };
+    // Scores of row 16r + m against token 16i + 4 grp + j, r > i: a^(16(r-i)-4 grp-j) a^m.
+    __syncthreads();
+    const float sp = op.su * op.so;
+    float into[G::RB], near[4], far[4], row_part = 0.f, step16 = 0.f;
+    if constexpr (ROWS) {
+        row_part = sp * powers[m];
+        step16 = powers[16];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int apart = m - 4 * grp - j;
+            near[j] = apart >= 0 ? sp * powers[apart >= 0 ? apart : 0] : 0.f;
+            far[j] = powers[16 - 4 * grp - j];
+        }
+#pragma unroll
+        for (int r = 0; r < G::RB; ++r) into[r] = op.so * powers[16 * r + m + (op.back ? 0 : 1)];
+    }
+    float owed = 0.f;
+    if (tid < 2 * C) {
+        const int i = tid % C, n = tid < C ? C : tokens - (chunks - 1) * C;
+        weights[tid / C][i] = i < n ? op.su * powers[n - 1 - i + (op.back ? 1 : 0)] : 0.f;
+    }
 
-    uint4 ra[ROWS ? G::NA : 1], rb[G::NA], rc[G::NC];
-    auto fetch = [&](int64_t c) {
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        const int n = tokens - c * C < C ? (int)(tokens - c * C) : C;
-#pragma unroll
-        for (int x = 0; x < G::NA; ++x) {
-            const int u = tid + x * kThreads, row = u / G::UA;
-            const int64_t at = ((token(c, row < n ? row : 0) * H + h) * DA) * G::ES / 16 + u % G::UA;
-            if constexpr (ROWS) {
-                ra[x] = static_cast<const uint4*>(op.a)[at];
-                if (row >= n) ra[x] = zero;
-            }
-            rb[x] = static_cast<const uint4*>(op.b)[at];
-            if (row >= n) rb[x] = zero;
-        }
-#pragma unroll
-        for (int x = 0; x < G::NC; ++x) {
-            const int u = tid + x * kThreads, row = u / G::UC;
-            rc[x] = static_cast<const uint4*>(op.c)[((token(c, row < n ? row : 0) * H + h) * DC) * G::ES / 16 + u % G::UC];
-            if (row >= n) rc[x] = zero;
-        }
-    };
-    // Contracted channels are taken in the order in which two 16-row tiles of a product lie in a lane: group g holds 4g .. +3
-    // and 16 + 4g .. +3 of each 32.  Rows of `a` are stored in that order.
-    auto stage = [&]() {
-#pragma unroll
-        for (int x = 0; x < G::NA; ++x) {
-            const int u = tid + x * kThreads, row = u / G::UA, v = u % G::UA;
-            *reinterpret_cast<uint4*>(ldsK + TA::place(row, v)) = rb[x];
-            if constexpr (ROWS && F32) {
-                *reinterpret_cast<uint4*>(ldsQ + TA::place(row, (v & ~7) + 2 * (v & 3) + (v >> 2 & 1))) = ra[x];
-            } else if constexpr (ROWS) {
-                const int to = (v & ~3) + 2 * (v & 1), half = (v >> 1 & 1) * 8;
-                *reinterpret_cast<uint2*>(ldsQ + TA::place(row, to) + half) = make_uint2(ra[x].x, ra[x].y);
-                *reinterpret_cast<uint2*>(ldsQ + TA::place(row, to + 1) + half) = make_uint2(ra[x].z, ra[x].w);
-            }
-        }
-#pragma unroll
-        for (int x = 0; x < G::NC; ++x) {
-            const int u = tid + x * kThreads;
-            *reinterpret_cast<uint4*>(ldsV + TC::place(u / G::UC, u % G::UC)) = rc[x];
-        }
-    };
-
-    // fragments: eight contracted values of row (or column) m
-    auto frag_a = [&](int row, int s) {
+    // Fragments: eight contracted values of row (or column) m, in the order in which two 16-row tiles of a product lie in a
+    // lane: group g holds 4g .. +3 and 16 + 4g .. +3 of each 32.  A lane's first place in a tile; the others are it with some
+    // bits of the unit turned over, or whole rows behind it.
+    constexpr int RA = UA * 16, RC = UC * 16;
+    int at_row, at_turned, at_col;
+    if constexpr (F32) {
+        at_row = place<UA, true>(m, grp);
+        at_turned = place<UA, true>(4 * grp, m >> 2) + 4 * (m & 3);
+        at_col = place<UC, true>(4 * grp, ND == 2 ? 8 * wave + 2 * (m >> 2) : 4 * wave + (m >> 2)) + 4 * (m & 3);
+    } else {
+        at_row = place<UA, false>(m, grp >> 1) + 8 * (grp & 1);
+        at_turned = place<UA, false>(4 * grp + (m >> 2), m >> 1 & 1) + 8 * (m & 1);
+        at_col = ND == 2 ? place<UC, false>(4 * grp + (m >> 2), 4 * wave + (m & 3))
+                         : place<UC, false>(4 * grp + (m >> 2), 2 * wave + (m >> 1 & 1)) + 8 * (m & 1);
+    }
+    // scores, read by row: 32 rows of 32 tokens, and behind them 32 of 64; in fp32 one tile of 32
+    int at_score = F32 ? place<8, true>(m, 2 * grp) : place<4, false>(m, grp);
+    int at_score2 = F32 ? 0 : 2048 + place<8, false>(m, grp);
+    auto frag = [&](const char* tile, int r, int s) {
         LFrag<F32> f;
         if constexpr (F32) {
-            const f32x4_t x = *reinterpret_cast<const f32x4_t*>(ldsQ + TA::place(row, 8 * s + 2 * grp));
-            const f32x4_t y = *reinterpret_cast<const f32x4_t*>(ldsQ + TA::place(row, 8 * s + 2 * grp + 1));
+            const f32x4_t x = *reinterpret_cast<const f32x4_t*>(tile + (at_row ^ (128 * s)) + 16 * RA * r);
+            const f32x4_t y = *reinterpret_cast<const f32x4_t*>(tile + (at_row ^ (128 * s + 64)) + 16 * RA * r);
 #pragma unroll
             for (int j = 0; j < 4; ++j) f.v[j] = x[j], f.v[4 + j] = y[j];
         } else {
-            f.v = *reinterpret_cast<const bf16x8_t*>(ldsQ + TA::place(row, 4 * s + grp));
-        }
-        return f;
-    };
-    auto frag_b = [&](int row, int s) {
-        LFrag<F32> f;
-        if constexpr (F32) {
-            const f32x4_t x = *reinterpret_cast<const f32x4_t*>(ldsK + TA::place(row, 8 * s + grp));
-            const f32x4_t y = *reinterpret_cast<const f32x4_t*>(ldsK + TA::place(row, 8 * s + 4 + grp));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) f.v[j] = x[j], f.v[4 + j] = y[j];
-        } else {
-            const bf16x4_t x = *reinterpret_cast<const bf16x4_t*>(ldsK + TA::place(row, 4 * s + (grp >> 1)) + 8 * (grp & 1));
-            const bf16x4_t y = *reinterpret_cast<const bf16x4_t*>(ldsK + TA::place(row, 4 * s + 2 + (grp >> 1)) + 8 * (grp & 1));
+            const bf16x4_t x = *reinterpret_cast<const bf16x4_t*>(tile + (at_row ^ (64 * s)) + 16 * RA * r);
+            const bf16x4_t y = *reinterpret_cast<const bf16x4_t*>(tile + (at_row ^ (64 * s + 32)) + 16 * RA * r);
             f.v = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
         }
         return f;
     };
     // columns of a tile over 32 tokens, in the same order
-    auto frag_bt = [&](int ct, int ks) {
+    auto frag_bt = [&](const char* tile, int ct, int ks) {
         LFrag<F32> f;
+        if constexpr (F32) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int row = 32 * ks + 16 * half + 4 * grp;
-            if constexpr (F32) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    f.v[4 * half + j] = *reinterpret_cast<const float*>(ldsK + TA::place(row + j, 4 * ct + (m >> 2)) + 4 * (m & 3));
-            } else {
-                const bf16x4_t x = read_turned(ldsK + TA::place(row + (m >> 2), 2 * ct + (m >> 1 & 1)) + 8 * (m & 1));
-#pragma unroll
-                for (int j = 0; j < 4; ++j) f.v[4 * half + j] = x[j];
-            }
+            for (int j = 0; j < 8; ++j)
+                f.v[j] = *reinterpret_cast<const float*>(tile + (at_turned ^ (64 * ct + 16 * (j & 3))) + (32 * ks + 16 * (j >> 2) + (j & 3)) * RA);
+        } else {
+            const char* p = tile + (at_turned ^ (32 * ct)) + 32 * ks * RA;
+            f.v = __builtin_shufflevector(read_turned(p), read_turned(p + 16 * RA), 0, 1, 2, 3, 4, 5, 6, 7);
         }
         return f;
     };
-    auto frag_ct = [&](int d, int ks) {
+    auto frag_ct = [&](const char* tile, int d, int ks) {
         LFrag<F32> f;
+        if constexpr (F32) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int row = 32 * ks + 16 * half + 4 * grp;
-            if constexpr (F32) {
-                const int c = col(m, d);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    f.v[4 * half + j] = *reinterpret_cast<const float*>(ldsV + TC::place(row + j, c >> 2) + 4 * (c & 3));
-            } else {
-                const int c = ND == 2 ? 32 * wave + 8 * (m & 3) + 4 * d : 16 * wave + 4 * (m & 3);
-                const bf16x4_t x = read_turned(ldsV + TC::place(row + (m >> 2), c >> 3) + (c & 4) * 2);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) f.v[4 * half + j] = x[j];
-            }
+            for (int j = 0; j < 8; ++j)
+                f.v[j] = *reinterpret_cast<const float*>(tile + (at_col ^ (16 * (d ^ (j & 3)))) + (32 * ks + 16 * (j >> 2) + (j & 3)) * RC);
+        } else {
+            const char* p = tile + at_col + 8 * d + 32 * ks * RC;
+            f.v = __builtin_shufflevector(read_turned(p), read_turned(p + 16 * RC), 0, 1, 2, 3, 4, 5, 6, 7);
         }
         return f;
     };
 
-    fetch(0);
-    __syncthreads();
-    float into[G::RB];  // what a row takes of the state
+    // One chunk with its keys in K; those of the next one go to Kn.
+    auto chunk = [&](int c, char* K, char* Kn, char* V, char* Vn) {
+        const int n = tokens - c * C < C ? tokens - c * C : C;
+        const bool more = c + 1 < chunks;
+        // the places of a chunk's fragments are made again from these few: kept, they would take most of the registers
+        __asm__ volatile("" : "+v"(at_row), "+v"(at_turned), "+v"(at_col), "+v"(at_score), "+v"(at_score2));
+        __asm__ volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (more) {
+            fetch(op.b, Kn, c + 1, UnitsA(), offset_a);
+            if constexpr (!ROWS) fetch(op.c, Vn, c + 1, UnitsC(), offset_c);
+        }
+        LFrag<F32> vf[G::KS * ND];
 #pragma unroll
-    for (int r = 0; r < G::RB; ++r) into[r] = op.so * tab[16 * r + m + (op.back ? 0 : 1)];
-    const float sp = op.su * op.so;
+        for (int ks = 0; ks < G::KS; ++ks)
+#pragma unroll
+            for (int d = 0; d < ND; ++d) vf[ks * ND + d] = frag_ct(V, d, ks);
 
-    for (int64_t c = 0; c < chunks; ++c) {
-        const int n = tokens - c * C < C ? (int)(tokens - c * C) : C;
-        stage();
-        lds_barrier();
-        if (c + 1 < chunks) fetch(c + 1);
-
-        f32x4_t O[G::RB][ND];
         if constexpr (ROWS) {
-            f32x4_t P[G::RB];
+            f32x4_t O[G::RB][ND], P[G::RB];
 #pragma unroll
             for (int r = 0; r < G::RB; ++r) {
                 P[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int d = 0; d < ND; ++d) O[r][d] = f32x4_t{0.f, 0.f, 0.f, 0.f};
             }
+            const int kr = wave < G::RB ? wave : 0;
 #pragma unroll
             for (int s = 0; s < G::AS; ++s) {
-                LFrag<F32> st[ND][G::PL];
+                LFrag<F32> qf[G::RB];
+#pragma unroll
+                for (int r = 0; r < G::RB; ++r) qf[r] = frag(ldsQ, r, s);
+                const LFrag<F32> kf = frag(K, kr, s);
 #pragma unroll
                 for (int d = 0; d < ND; ++d) {
+                    LFrag<F32> st[G::PL];
                     float x[8];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) x[j] = S[2 * s][d][j], x[4 + j] = S[2 * s + 1][d][j];
-                    split<G::PL, F32>(x, st[d]);
+                    split<G::PL>(x, st);
+#pragma unroll
+                    for (int p = 0; p < G::PL; ++p)
+#pragma unroll
+                        for (int r = 0; r < G::RB; ++r) O[r][d] = mma(st[p], qf[r], O[r][d]);
                 }
-                LFrag<F32> kf;
-                if (wave < G::RB) kf = frag_b(16 * wave + m, s);
 #pragma unroll
-                for (int r = 0; r < G::RB; ++r) {
-                    const LFrag<F32> qf = frag_a(16 * r + m, s);
-                    if (wave <= r) P[r] = mma(kf, qf, P[r]);
-#pragma unroll
-                    for (int d = 0; d < ND; ++d)
-#pragma unroll
-                        for (int p = 0; p < G::PL; ++p) O[r][d] = mma(st[d][p], qf, O[r][d]);
-                }
+                for (int r = 0; r < G::RB; ++r) P[r] = mma(kf, qf[r], P[r]);
             }
-            // scores of rows 16r + m against tokens 16 wave + 4 grp + j
+            // scores of rows 16r + m against tokens 16 wave + 4 grp + j; rows of the products' 32 tokens above the diagonal: zeros
+            float part = row_part;
 #pragma unroll
             for (int r = 0; r < G::RB; ++r) {
-                if (wave <= r) {
+                if (wave <= (r | 1)) {
                     float x[4];
+                    if (wave == r) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int apart = 16 * (r - wave) + m - 4 * grp - j;
-                        x[j] = apart >= 0 ? P[r][j] * (sp * tab[apart >= 0 ? apart : 0]) : 0.f;
-                    }
-                    const int unit8 = 4 * (wave >> 1) + grp, half = wave & 1;  // of eight values
-                    if constexpr (F32) {
-                        *reinterpret_cast<f32x4_t*>(ldsP + TP::place(16 * r + m, 2 * unit8 + half)) = f32x4_t{x[0], x[1], x[2], x[3]};
+                        for (int j = 0; j < 4; ++j) x[j] = m >= 4 * grp + j ? P[r][j] * near[j] : 0.f;
+                    } else if (wave < r) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) x[j] = P[r][j] * (far[j] * part);
+                        part *= step16;
                     } else {
-                        bf16x4_t hi, lo;
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            hi[j] = (__bf16)x[j];
-                            lo[j] = (__bf16)(x[j] - (float)hi[j]);
-                        }
-                        char* to = ldsP + TP::place(16 * r + m, unit8) + 8 * half;
-                        *reinterpret_cast<bf16x4_t*>(to) = hi;
-                        *reinterpret_cast<bf16x4_t*>(to + G::PB) = lo;
+                        for (int j = 0; j < 4; ++j) x[j] = 0.f;
+                    }
+                    if constexpr (F32) {
+                        *reinterpret_cast<f32x4_t*>(ldsP + (at_score ^ (16 * wave)) + 2048 * r) = f32x4_t{x[0], x[1], x[2], x[3]};
+                    } else {
+                        const uint32_t h0 = pack2(x[0], x[1]), h1 = pack2(x[2], x[3]);
+                        char* to = ldsP + (r < 2 ? at_score + 1024 * r : (at_score2 ^ (64 * (wave >> 1))) + 2048 * (r - 2)) + 8 * (wave & 1);
+                        *reinterpret_cast<uint2*>(to) = make_uint2(h0, h1);
+                        *reinterpret_cast<uint2*>(to + G::PB) = make_uint2(pack2(x[0] - low_of(h0), x[1] - high_of(h0)),
+                                                                           pack2(x[2] - low_of(h1), x[3] - high_of(h1)));
                     }
                 }
 #pragma unroll
@@ -428,143 +489,132 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinOp op0, L
 #pragma unroll
                     for (int j = 0; j < 4; ++j) O[r][d][j] *= into[r];
             }
-            // the tiles above the diagonal that the products reach
-            if (wave & 1) {
-                const int r = wave - 1;
-                if (r < G::RB) {
-                    const int unit8 = 4 * (wave >> 1) + grp;
-                    if constexpr (F32) {
-                        *reinterpret_cast<f32x4_t*>(ldsP + TP::place(16 * r + m, 2 * unit8 + 1)) = f32x4_t{0.f, 0.f, 0.f, 0.f};
-                    } else {
-                        char* to = ldsP + TP::place(16 * r + m, unit8) + 8;
-                        *reinterpret_cast<uint2*>(to) = make_uint2(0, 0);
-                        *reinterpret_cast<uint2*>(to + G::PB) = make_uint2(0, 0);
-                    }
-                }
-            }
             lds_barrier();
-        }
-
-        LFrag<F32> vf[G::KS][ND];
-#pragma unroll
-        for (int ks = 0; ks < G::KS; ++ks)
-#pragma unroll
-            for (int d = 0; d < ND; ++d) vf[ks][d] = frag_ct(d, ks);
-
-        if constexpr (ROWS) {
-            // A value that is not finite must not meet the zeros of earlier rows: such values are left out of the product, and
-            // its column is made NaN from that token on.
-            int bad[ND];
-            bool any = false;
-#pragma unroll
-            for (int d = 0; d < ND; ++d) {
-                bad[d] = C;
-#pragma unroll
-                for (int ks = G::KS - 1; ks >= 0; --ks)
-#pragma unroll
-                    for (int j = 7; j >= 0; --j)
-                        if (!(fabsf((float)vf[ks][d].v[j]) < __builtin_inff())) bad[d] = 32 * ks + 16 * (j >> 2) + 4 * grp + (j & 3);
-                any |= bad[d] < C;
+            if (more) {
+                fetch(op.a, ldsQ, c + 1, UnitsA(), offset_a);
+                fetch(op.c, Vn, c + 1, UnitsC(), offset_c);
             }
-            const bool marked = __ballot(any) != 0;
-            LFrag<F32> clean[G::KS][ND];
+
+            // A value that is not finite must not meet the zeros of earlier rows: such values are left out of the product, and
+            // their column is made NaN from their token on.
+            int bad[ND];
+            LFrag<F32> clean[G::KS * ND];
 #pragma unroll
-            for (int ks = 0; ks < G::KS; ++ks)
-#pragma unroll
-                for (int d = 0; d < ND; ++d) clean[ks][d] = vf[ks][d];
+            for (int i = 0; i < G::KS * ND; ++i) clean[i] = vf[i];
+            const bool marked = __ballot(any_not_finite<G::KS * ND>(vf)) != 0;
             if (marked) {
 #pragma unroll
                 for (int d = 0; d < ND; ++d) {
+                    bad[d] = C;
+#pragma unroll
+                    for (int ks = G::KS - 1; ks >= 0; --ks)
+#pragma unroll
+                        for (int j = 7; j >= 0; --j)
+                            if (!(fabsf((float)vf[ks * ND + d].v[j]) < __builtin_inff())) {
+                                bad[d] = 32 * ks + 16 * (j >> 2) + 4 * grp + (j & 3);
+                                clean[ks * ND + d].v[j] = 0.f;
+                            }
                     bad[d] = min(bad[d], __shfl_xor(bad[d], 16));
                     bad[d] = min(bad[d], __shfl_xor(bad[d], 32));
-#pragma unroll
-                    for (int ks = 0; ks < G::KS; ++ks)
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            if (!(fabsf((float)clean[ks][d].v[j]) < __builtin_inff())) clean[ks][d].v[j] = 0.f;
                 }
             }
 #pragma unroll
-            for (int r = 0; r < G::RB; ++r) {
+            for (int r = 0; r < G::RB; ++r)
 #pragma unroll
                 for (int ks = 0; ks <= r / 2; ++ks)
 #pragma unroll
                     for (int p = 0; p < G::PL; ++p) {
                         LFrag<F32> pf;
                         if constexpr (F32) {
-                            const f32x4_t x = *reinterpret_cast<const f32x4_t*>(ldsP + TP::place(16 * r + m, 8 * ks + 2 * grp));
-                            const f32x4_t y = *reinterpret_cast<const f32x4_t*>(ldsP + TP::place(16 * r + m, 8 * ks + 2 * grp + 1));
+                            const f32x4_t x = *reinterpret_cast<const f32x4_t*>(ldsP + at_score + 2048 * r);
+                            const f32x4_t y = *reinterpret_cast<const f32x4_t*>(ldsP + (at_score ^ 16) + 2048 * r);
 #pragma unroll
                             for (int j = 0; j < 4; ++j) pf.v[j] = x[j], pf.v[4 + j] = y[j];
                         } else {
-                            pf.v = *reinterpret_cast<const bf16x8_t*>(ldsP + p * G::PB + TP::place(16 * r + m, 4 * ks + grp));
+                            pf.v = *reinterpret_cast<const bf16x8_t*>(
+                                ldsP + p * G::PB + (r < 2 ? at_score + 1024 * r : (at_score2 ^ (64 * ks)) + 2048 * (r - 2)));
                         }
 #pragma unroll
-                        for (int d = 0; d < ND; ++d) O[r][d] = mma(clean[ks][d], pf, O[r][d]);
+                        for (int d = 0; d < ND; ++d) O[r][d] = mma(clean[ks * ND + d], pf, O[r][d]);
                     }
-                if (marked) {
+            if (marked) {
 #pragma unroll
-                    for (int d = 0; d < ND; ++d)
+                for (int d = 0; d < ND; ++d)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (16 * r + m >= __shfl(bad[d], 4 * grp + j)) O[r][d][j] = __builtin_nanf("");
-                }
-                const int row = 16 * r + m;
-                if (row < n) {
-                    const int64_t at = (token(c, row) * H + h) * DC + col(4 * grp, 0);
+                    for (int j = 0; j < 4; ++j) {
+                        const int from = __shfl(bad[d], 4 * grp + j);
+#pragma unroll
+                        for (int r = 0; r < G::RB; ++r)
+                            if (16 * r + m >= from) O[r][d][j] = __builtin_nanf("");
+                    }
+            }
+            // a lane's first row of the chunk; the others are 16 rows apart
+            char* to = static_cast<char*>(op.out) + ((row0 + (op.back ? -c * C : c * C)) * H + h) * (int64_t)(DC * G::ES);
+            const int pitch = (op.back ? -H : H) * DC * G::ES, mine = m * pitch + col(4 * grp, 0) * G::ES;
+#pragma unroll
+            for (int r = 0; r < G::RB; ++r) {
+                if (16 * r + m < n) {
+                    char* p = to + (int64_t)(16 * r * pitch) + mine;
                     if constexpr (F32) {
 #pragma unroll
-                        for (int d = 0; d < ND; ++d)
-                            *reinterpret_cast<f32x4_t*>(static_cast<float*>(op.out) + at + 4 * d) = O[r][d];
+                        for (int d = 0; d < ND; ++d) *reinterpret_cast<f32x4_t*>(p + 16 * d) = O[r][d];
                     } else if constexpr (ND == 2) {
-                        bf16x8_t x;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) x[j] = (__bf16)O[r][0][j], x[4 + j] = (__bf16)O[r][1][j];
-                        *reinterpret_cast<bf16x8_t*>(static_cast<__bf16*>(op.out) + at) = x;
+                        *reinterpret_cast<uint4*>(p) = make_uint4(pack2(O[r][0][0], O[r][0][1]), pack2(O[r][0][2], O[r][0][3]),
+                                                                  pack2(O[r][1][0], O[r][1][1]), pack2(O[r][1][2], O[r][1][3]));
                     } else {
-                        bf16x4_t x;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) x[j] = (__bf16)O[r][0][j];
-                        *reinterpret_cast<bf16x4_t*>(static_cast<__bf16*>(op.out) + at) = x;
+                        *reinterpret_cast<uint2*>(p) = make_uint2(pack2(O[r][0][0], O[r][0][1]), pack2(O[r][0][2], O[r][0][3]));
                     }
                 }
             }
         }
 
-        // the state: decayed in 32 bits and what the power is rounded off by, so that thousands of chunks do not add up to more
-        // than a rounding each; the weighted values as sums of three bf16 values, which hold all of their 24 bits
-        {
-            const float dec = tab[n], rest = n == C ? tab[C + 1] : 0.f;
-#pragma unroll
-            for (int ct = 0; ct < G::CT; ++ct)
-#pragma unroll
-                for (int d = 0; d < ND; ++d)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) S[ct][d][j] = fmaf(S[ct][d][j], rest, S[ct][d][j] * dec);
+        // The state, decayed in 32 bits: what a power's rounding owes is paid in the next ones, so that thousands of chunks do
+        // not add up.  The weighted values are sums of three bf16 values, which hold all of their 24 bits.
+        float dec;
+        if (n == C) {
+            dec = fmaf(whole32, owed, whole32);
+            owed += rest - (whole32 > 0.f ? (dec - whole32) / whole32 : 0.f);
+        } else {
+            dec = powers[n];
         }
 #pragma unroll
+        for (int ct = 0; ct < G::CT; ++ct)
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) S[ct][d][j] *= dec;
+#pragma unroll
         for (int ks = 0; ks < G::KS; ++ks) {
+            const f32x4_t w0 = *reinterpret_cast<const f32x4_t*>(weights[n < C] + 32 * ks + 4 * grp);
+            const f32x4_t w1 = *reinterpret_cast<const f32x4_t*>(weights[n < C] + 32 * ks + 16 + 4 * grp);
             LFrag<F32> vb[ND][G::VL];
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
                 float x[8];
+                values(vf[ks * ND + d], x);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int left = n - 1 - (32 * ks + 16 * (j >> 2) + 4 * grp + (j & 3));
-                    x[j] = (float)vf[ks][d].v[j] * (op.su * tab[(left > 0 ? left : 0) + (op.back ? 1 : 0)]);
-                }
-                split<G::VL, F32>(x, vb[d]);
+                for (int j = 0; j < 4; ++j) x[j] *= w0[j], x[4 + j] *= w1[j];
+                split<G::VL>(x, vb[d]);
             }
 #pragma unroll
             for (int ct = 0; ct < G::CT; ++ct) {
-                const LFrag<F32> kt = frag_bt(ct, ks);
+                const LFrag<F32> kt = frag_bt(K, ct, ks);
 #pragma unroll
                 for (int d = 0; d < ND; ++d)
 #pragma unroll
                     for (int p = 0; p < G::VL; ++p) S[ct][d] = mma(kt, vb[d][p], S[ct][d]);
             }
         }
-        lds_barrier();
+    };
+
+    for (int c = 0; c < chunks; c += 2) {
+        if constexpr (ROWS) {
+            chunk(c, ldsK0, ldsK1, ldsV0, ldsV0);
+            if (c + 1 < chunks) chunk(c + 1, ldsK1, ldsK0, ldsV0, ldsV0);
+        } else {
+            chunk(c, ldsK0, ldsK1, ldsV0, ldsV1);
+            if (c + 1 < chunks) chunk(c + 1, ldsK1, ldsK0, ldsV1, ldsV0);
+        }
     }
 
     float* to = nullptr;
