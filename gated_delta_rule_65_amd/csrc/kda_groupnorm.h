@@ -1,0 +1,321 @@
+// Group norm with an activation over channels-last rows (mathematics and layouts: include/kda_layer.h): the kernel of both
+// passes, for rows that a few lanes hold.
+//
+// A group of a token goes to P lanes of ITER pieces of CPL channels each, held in registers between the mean, the sum of
+// squares around it and the outputs, so that memory is read and written once.  A thread keeps its channels over the tokens
+// of its workgroup: weights are read once, and the weights' gradients are sums in registers until the workgroup's end.
+#pragma once
+#include <type_traits>
+
+#include "kda_device.h"
+#include "kda_layer_launch.h"
+
+namespace kda {
+namespace {
+
+constexpr int kGnThreads = 256;
+
+// How a call's tokens and groups lie over workgroups: `groups` groups and `tokens` tokens of each at a time, `block` tokens
+// in all, `blocks` of those.
+struct GnPlan {
+    int groups, tokens;
+    int64_t block, blocks;
+};
+
+template <int N, bool F32>
+struct GnRaw {
+    using Word = std::conditional_t<N * (F32 ? 4 : 2) >= 16, uint4, std::conditional_t<F32, uint32_t, uint16_t>>;
+    Word w[N * (F32 ? 4 : 2) >= 16 ? N * (F32 ? 4 : 2) / 16 : N];
+};
+template <int N, bool F32>
+__device__ __forceinline__ GnRaw<N, F32> gn_load(const void* p, int64_t at) {
+    using R = GnRaw<N, F32>;
+    R r;
+    const typename R::Word* q = reinterpret_cast<const typename R::Word*>(static_cast<const char*>(p) + at * (F32 ? 4 : 2));
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(r.w) / sizeof(r.w[0])); ++i) r.w[i] = q[i];
+    return r;
+}
+template <int N, bool F32>
+__device__ __forceinline__ void gn_values(const GnRaw<N, F32>& r, float x[N]) {
+    if constexpr (N == 1) {
+        x[0] = F32 ? __uint_as_float(r.w[0]) : __uint_as_float((uint32_t)r.w[0] << 16);
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const uint32_t* u = &r.w[0].x;
+            x[j] = F32 ? __uint_as_float(u[j]) : __uint_as_float(j % 2 ? u[j / 2] & 0xffff0000u : u[j / 2] << 16);
+        }
+    }
+}
+typedef __bf16 gn_bf16x2 __attribute__((ext_vector_type(2)));
+typedef float gn_f32x2 __attribute__((ext_vector_type(2)));
+template <int N, bool F32>
+__device__ __forceinline__ void gn_store(void* p, int64_t at, const float x[N]) {
+    char* q = static_cast<char*>(p) + at * (F32 ? 4 : 2);
+    if constexpr (N == 1) {
+        if constexpr (F32) *reinterpret_cast<float*>(q) = x[0];
+        else *reinterpret_cast<__bf16*>(q) = (__bf16)x[0];
+    } else if constexpr (F32) {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) reinterpret_cast<f32x4_t*>(q)[i] = f32x4_t{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]};
+    } else {
+#pragma unroll
+        for (int i = 0; i < N / 8; ++i) {
+            uint32_t u[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                u[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(gn_f32x2{x[8 * i + 2 * j], x[8 * i + 2 * j + 1]}, gn_bf16x2));
+            reinterpret_cast<uint4*>(q)[i] = make_uint4(u[0], u[1], u[2], u[3]);
+        }
+    }
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_take(float x) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, true));
+}
+// The sum over each P adjacent lanes, in every one of them.
+template <int P>
+__device__ __forceinline__ float lanes_sum(float x) {
+    x += dpp_take<0xb1>(x);              // the neighbour
+    x += dpp_take<0x4e>(x);              // the other pair of four
+    if constexpr (P >= 8) x += dpp_take<0x141>(x);   // the other four of eight
+    if constexpr (P >= 16) x += dpp_take<0x140>(x);  // the other eight of sixteen
+    if constexpr (P >= 32) x += __shfl_xor(x, 16);
+    if constexpr (P >= 64) x += __shfl_xor(x, 32);
+    return x;
+}
+
+// 1 / (1 + e^-u): e^-u from the product's two halves, so that it keeps its accuracy far from zero (the product alone is off by
+// |u| 2^-24); beyond +-100 it is 0 or infinite in 32 bits anyway.
+__device__ __forceinline__ float gn_sigmoid(float u) {
+    constexpr float l2e = 1.44269502162933349609375f, l2e_rest = 1.925963033500011e-8f, ln2 = 0.693147182464599609375f;
+    const float t = __builtin_amdgcn_fmed3f(-u, -100.f, 100.f);
+    const float hi = t * l2e, lo = fmaf(t, l2e_rest, fmaf(t, l2e, -hi));
+    const float e = __builtin_amdgcn_exp2f(hi);
+    const float s = __builtin_amdgcn_rcpf(1.f + fmaf(e, lo * ln2, e));
+    return u == u ? s : u;
+}
+
+// act(u) and its slope.
+template <bool SLOPE>
+__device__ __forceinline__ void gn_act(float u, int act, float& f, float& slope) {
+    if (act == 0) {
+        f = u;
+        slope = 1.f;
+        return;
+    }
+    const float s = gn_sigmoid(u);
+    f = act == 2 ? s : u * s;
+    if constexpr (SLOPE) slope = act == 2 ? s * (1.f - s) : fmaf(u * s, 1.f - s, s);
+}
+
+template <bool XF, bool YF, int CPL, int P, int ITER, bool BWD>
+__global__ __launch_bounds__(kGnThreads) void groupnorm_kernel(GroupNormArgs a, GnPlan plan) {
+    constexpr int N = CPL * ITER;
+    const int tid = threadIdx.x, p = tid % P, W = (int)a.width;
+    const int gi = tid / P % plan.groups, ti = tid / (P * plan.groups);
+    const int64_t group = (int64_t)blockIdx.x * plan.groups + gi, c0 = group * W, C = a.groups * W;
+    const bool mine = group < a.groups && ti < plan.tokens;
+    const float mean_of = 1.f / W;
+    bool in[ITER];
+    int at[ITER];
+    float w[N], b[N], dw[N], db[N];
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) {
+        at[i] = (i * P + p) * CPL;
+        in[i] = mine && at[i] < W;
+        if (!in[i]) at[i] = 0;
+#pragma unroll
+        for (int j = 0; j < CPL; ++j) {
+            w[i * CPL + j] = 1.f;
+            b[i * CPL + j] = dw[i * CPL + j] = db[i * CPL + j] = 0.f;
+        }
+        if (in[i] && a.weight) gn_values<CPL, true>(gn_load<CPL, true>(a.weight, c0 + at[i]), w + i * CPL);
+        if (in[i] && a.bias) gn_values<CPL, true>(gn_load<CPL, true>(a.bias, c0 + at[i]), b + i * CPL);
+    }
+    const int64_t first = (int64_t)blockIdx.y * plan.block;
+    const int64_t end = first + plan.block < a.tokens ? first + plan.block : a.tokens;
+
+    GnRaw<CPL, XF> rx[ITER];
+    GnRaw<CPL, YF> rg[ITER], rd[ITER];
+    auto fetch = [&](int64_t t) {
+#pragma unroll
+        for (int i = 0; i < ITER; ++i) {
+            if (!in[i]) continue;
+            rx[i] = gn_load<CPL, XF>(a.x, t * a.x_stride + c0 + at[i]);
+            if (a.gate) rg[i] = gn_load<CPL, YF>(a.gate, t * a.gate_stride + c0 + at[i]);
+            if constexpr (BWD) rd[i] = gn_load<CPL, YF>(a.dy, t * C + c0 + at[i]);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) rx[i] = {}, rg[i] = {}, rd[i] = {};
+    int64_t t = first + ti;
+    if (mine && t < end) fetch(t);
+    // the loop's count is the workgroup's: every lane takes part in its groups' sums
+    for (int64_t t0 = first; t0 < end; t0 += plan.tokens, t += plan.tokens) {
+        float x[N], u[N], dy[N];
+#pragma unroll
+        for (int i = 0; i < ITER; ++i) {
+            gn_values<CPL, XF>(rx[i], x + i * CPL);
+            gn_values<CPL, YF>(rg[i], u + i * CPL);
+            if constexpr (BWD) gn_values<CPL, YF>(rd[i], dy + i * CPL);
+        }
+        const bool here = mine && t < end;
+        if (mine && t + plan.tokens < end) fetch(t + plan.tokens);
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < ITER; ++i)
+#pragma unroll
+            for (int j = 0; j < CPL; ++j) sum += in[i] ? x[i * CPL + j] : 0.f;
+        const float mean = lanes_sum<P>(sum) * mean_of;
+        float squares = 0.f;
+#pragma unroll
+        for (int i = 0; i < ITER; ++i)
+#pragma unroll
+            for (int j = 0; j < CPL; ++j) {
+                float& v = x[i * CPL + j];
+                v = in[i] ? v - mean : 0.f;
+                squares = fmaf(v, v, squares);
+            }
+        // the square root and the division to the last bit: one each for a row
+        const float rstd = 1.f / sqrtf(fmaf(lanes_sum<P>(squares), mean_of, a.eps));
+        if constexpr (!BWD) {
+#pragma unroll
+            for (int i = 0; i < ITER; ++i) {
+                float y[CPL];
+#pragma unroll
+                for (int j = 0; j < CPL; ++j) {
+                    const int k = i * CPL + j;
+                    const float z = fmaf(x[k] * rstd, w[k], b[k]);
+                    float f, slope;
+                    gn_act<false>(a.gate ? u[k] : z, a.act, f, slope);
+                    y[j] = a.gate ? z * f : f;
+                }
+                if (here && in[i]) gn_store<CPL, YF>(a.y, t * C + c0 + at[i], y);
+            }
+        } else {
+            float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+            for (int i = 0; i < ITER; ++i) {
+#pragma unroll
+                for (int j = 0; j < CPL; ++j) {
+                    const int k = i * CPL + j;
+                    x[k] *= rstd;
+                    const float z = fmaf(x[k], w[k], b[k]);
+                    float f, slope;
+                    gn_act<true>(a.gate ? u[k] : z, a.act, f, slope);
+                    u[k] = dy[k] * z * slope;                   // the gate's gradient
+                    const float dz = dy[k] * (a.gate ? f : slope);
+                    dw[k] = fmaf(here ? dz : 0.f, x[k], dw[k]);
+                    db[k] += here ? dz : 0.f;
+                    dy[k] = dz * w[k];
+                    s1 += in[i] ? dy[k] : 0.f;
+                    s2 = fmaf(in[i] ? dy[k] : 0.f, x[k], s2);
+                }
+                if (a.gate && here && in[i]) gn_store<CPL, YF>(a.dgate, t * C + c0 + at[i], u + i * CPL);
+            }
+            s1 = lanes_sum<P>(s1) * mean_of;
+            s2 = lanes_sum<P>(s2) * mean_of;
+#pragma unroll
+            for (int i = 0; i < ITER; ++i) {
+                float dx[CPL];
+#pragma unroll
+                for (int j = 0; j < CPL; ++j) {
+                    const int k = i * CPL + j;
+                    dx[j] = rstd * (dy[k] - fmaf(x[k], s2, s1));
+                }
+                if (here && in[i]) gn_store<CPL, XF>(a.dx, t * C + c0 + at[i], dx);
+            }
+        }
+    }
+    if constexpr (BWD) {
+        if (!a.dweight) return;
+        // the workgroup's tokens' sums, in the order of its rows
+        __shared__ float part[2][kGnThreads * CPL];
+        float* out = static_cast<float*>(a.ws) + (int64_t)blockIdx.y * 2 * C;
+#pragma unroll
+        for (int i = 0; i < ITER; ++i) {
+            if (plan.tokens > 1) {
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < CPL; ++j) {
+                    part[0][j * kGnThreads + tid] = dw[i * CPL + j];
+                    part[1][j * kGnThreads + tid] = db[i * CPL + j];
+                }
+                __syncthreads();
+            }
+            if (ti || !in[i]) continue;
+#pragma unroll
+            for (int j = 0; j < CPL; ++j) {
+                float sw = dw[i * CPL + j], sb = db[i * CPL + j];
+                for (int r = 1; r < plan.tokens; ++r) {
+                    sw += part[0][j * kGnThreads + tid + r * P * plan.groups];
+                    sb += part[1][j * kGnThreads + tid + r * P * plan.groups];
+                }
+                out[c0 + at[i] + j] = sw;
+                out[C + c0 + at[i] + j] = sb;
+            }
+        }
+    }
+}
+
+// Lanes and pieces of a row: the fewest lanes that hold it.
+template <typename F>
+void gn_shape(bool wide, int64_t width, F&& f) {
+    auto run = [&](auto cpl, auto p, auto iter) { f(cpl, p, iter); };
+    auto i = [](auto v) { return v; };
+#define KDA_GN(CPL, P, ITER) \
+    run(i(std::integral_constant<int, CPL>()), i(std::integral_constant<int, P>()), i(std::integral_constant<int, ITER>()))
+    if (wide) {
+        if (width <= 64) KDA_GN(8, 8, 1);
+        else if (width <= 128) KDA_GN(8, 16, 1);
+        else if (width <= 256) KDA_GN(8, 32, 1);
+        else if (width <= 512) KDA_GN(8, 64, 1);
+        else if (width <= 1024) KDA_GN(8, 64, 2);
+        else KDA_GN(8, 64, 4);
+    } else {
+        if (width <= 16) KDA_GN(1, 16, 1);
+        else if (width <= 32) KDA_GN(1, 32, 1);
+        else if (width <= 64) KDA_GN(1, 32, 2);
+        else if (width <= 96) KDA_GN(1, 32, 3);
+        else if (width <= 128) KDA_GN(1, 32, 4);
+        else if (width <= 256) KDA_GN(1, 64, 4);
+        else if (width <= 512) KDA_GN(1, 64, 8);
+        else KDA_GN(1, 64, 16);
+    }
+#undef KDA_GN
+}
+
+// Workgroups of all groups' columns; tokens in blocks, as many workgroups in all as `places`, none of fewer than `least` tokens.
+inline GnPlan gn_plan(const GroupNormArgs& a, int lanes, int64_t places, int64_t least, int64_t& columns) {
+    GnPlan p;
+    const int64_t fit = kGnThreads / lanes;
+    p.groups = (int)(a.groups < fit ? a.groups : fit);
+    p.tokens = (int)(fit / p.groups);
+    columns = (a.groups + p.groups - 1) / p.groups;
+    int64_t blocks = (places + columns - 1) / columns;
+    const int64_t most = (a.tokens + least - 1) / least;
+    if (blocks > most) blocks = most;
+    if (blocks < 1) blocks = 1;
+    p.block = (a.tokens + blocks - 1) / blocks;
+    p.block = (p.block + p.tokens - 1) / p.tokens * p.tokens;
+    p.blocks = (a.tokens + p.block - 1) / p.block;
+    return p;
+}
+
+}  // namespace
+
+// Rows up to this wide are held in registers.
+inline bool gn_in_registers(const GroupNormArgs& a) { return a.width <= (groupnorm_wide(a) ? 2048 : 1024); }
+// Blocks of tokens in whose sums the weights' gradients are added up: of 16 tokens at least, so that they are small beside the
+// rows, and at most so many that the workspace stays small.
+constexpr int64_t kGnBlocks = 1024, kGnBlockTokens = 16;
+
+template <bool XF, bool YF>
+void groupnorm_fwd_of(const GroupNormArgs& a, hipStream_t st);
+template <bool XF, bool YF>
+void groupnorm_bwd_of(const GroupNormArgs& a, hipStream_t st);
+
+}  // namespace kda

@@ -1,142 +1,156 @@
-// Group norm with an activation over channels-last rows (mathematics and layouts: include/kda_layer.h): a plain form, a
-// wave for each group of a token, for every size and type.
-#include "kda_device.h"
-#include "kda_layer_launch.h"
+// Group norm with an activation over channels-last rows (mathematics and layouts: include/kda_layer.h): rows that are too wide
+// for registers, and which kernel a call takes.
+#include "kda_groupnorm.h"
 
 namespace kda {
 
+void groupnorm_sums(const GroupNormArgs& a, int64_t blocks, hipStream_t st);
+
 namespace {
 
-template <bool F32>
-__device__ __forceinline__ float load1(const void* p, int64_t i) {
-    if constexpr (F32) return static_cast<const float*>(p)[i];
-    else return bf16_bits_to_float(static_cast<const uint16_t*>(p)[i]);
-}
-template <bool F32>
-__device__ __forceinline__ void store1(void* p, int64_t i, float x) {
-    if constexpr (F32) static_cast<float*>(p)[i] = x;
-    else static_cast<__bf16*>(p)[i] = (__bf16)x;
-}
-__device__ __forceinline__ float wave_sum(float x) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) x += __shfl_xor(x, off);
-    return x;
+__device__ __forceinline__ float block_sum(float x, float* lds) {
+    x = lanes_sum<64>(x);
+    __syncthreads();
+    if (threadIdx.x % 64 == 0) lds[threadIdx.x / 64] = x;
+    __syncthreads();
+    return lds[0] + lds[1] + lds[2] + lds[3];
 }
 
-// act(u) and its slope.
-struct Act {
-    float f, slope;
-};
-__device__ __forceinline__ Act act_of(float u, int act) {
-    if (act == 0) return {u, 1.f};
-    const float s = 1.f / (1.f + expf(-u));
-    return act == 2 ? Act{s, s * (1.f - s)} : Act{u * s, s * (1.f + u * (1.f - s))};
-}
-
-struct Row {
-    float mean, rstd;
-};
 template <bool XF>
-__device__ __forceinline__ Row row_of(const GroupNormArgs& a, int64_t x0, int lane) {
-    float sum = 0.f, sq = 0.f;
-    for (int64_t c = lane; c < a.width; c += 64) sum += load1<XF>(a.x, x0 + c);
-    const float mean = wave_sum(sum) / a.width;
-    for (int64_t c = lane; c < a.width; c += 64) {
-        const float d = load1<XF>(a.x, x0 + c) - mean;
-        sq = fmaf(d, d, sq);
-    }
-    return {mean, 1.f / sqrtf(wave_sum(sq) / a.width + a.eps)};
+__device__ __forceinline__ float load1(const void* p, int64_t i) {
+    float x[1];
+    gn_values<1, XF>(gn_load<1, XF>(p, i), x);
+    return x[0];
 }
 
+// A workgroup for a group of a token, an element a thread at a time; the passes after the first find the row in the caches.
+// stats: mean and 1/deviation of every row, for the weights' sums.
 template <bool XF, bool YF>
-__global__ __launch_bounds__(256) void groupnorm_plain_kernel(GroupNormArgs a) {
-    const int64_t row = (int64_t)blockIdx.x * 4 + threadIdx.x / 64, t = row / a.groups, c0 = row % a.groups * a.width;
-    const int lane = threadIdx.x % 64;
-    if (t >= a.tokens) return;
-    const int64_t x0 = t * a.x_stride + c0, g0 = t * a.gate_stride + c0, y0 = t * a.groups * a.width + c0;
-    const Row r = row_of<XF>(a, x0, lane);
+__global__ __launch_bounds__(kGnThreads) void groupnorm_rows_kernel(GroupNormArgs a, float* stats) {
+    __shared__ float lds[4];
+    const int64_t row = blockIdx.x, t = row / a.groups, c0 = row % a.groups * a.width, C = a.groups * a.width;
+    const int64_t x0 = t * a.x_stride + c0, g0 = t * a.gate_stride + c0, y0 = t * C + c0;
+    const float mean_of = 1.f / a.width;
+    float sum = 0.f, squares = 0.f;
+    for (int64_t c = threadIdx.x; c < a.width; c += kGnThreads) sum += load1<XF>(a.x, x0 + c);
+    const float mean = block_sum(sum, lds) * mean_of;
+    for (int64_t c = threadIdx.x; c < a.width; c += kGnThreads) {
+        const float d = load1<XF>(a.x, x0 + c) - mean;
+        squares = fmaf(d, d, squares);
+    }
+    const float rstd = 1.f / sqrtf(fmaf(block_sum(squares, lds), mean_of, a.eps));
+    if (stats && threadIdx.x == 0) {
+        stats[2 * row] = mean;
+        stats[2 * row + 1] = rstd;
+    }
+    auto terms = [&](int64_t c, float& n, float& z, float& w, float& f, float& slope) {
+        n = (load1<XF>(a.x, x0 + c) - mean) * rstd;
+        w = a.weight ? a.weight[c0 + c] : 1.f;
+        z = fmaf(n, w, a.bias ? a.bias[c0 + c] : 0.f);
+        gn_act<true>(a.gate ? load1<YF>(a.gate, g0 + c) : z, a.act, f, slope);
+    };
+    float n, z, w, f, slope;
     if (!a.dy) {
-        for (int64_t c = lane; c < a.width; c += 64) {
-            const float n = (load1<XF>(a.x, x0 + c) - r.mean) * r.rstd;
-            const float z = fmaf(n, a.weight ? a.weight[c0 + c] : 1.f, a.bias ? a.bias[c0 + c] : 0.f);
-            store1<YF>(a.y, y0 + c, a.gate ? z * act_of(load1<YF>(a.gate, g0 + c), a.act).f : act_of(z, a.act).f);
+        for (int64_t c = threadIdx.x; c < a.width; c += kGnThreads) {
+            terms(c, n, z, w, f, slope);
+            const float y = a.gate ? z * f : f;
+            gn_store<1, YF>(a.y, y0 + c, &y);
         }
         return;
     }
     float s1 = 0.f, s2 = 0.f;
-    auto grads = [&](int64_t c, float& n, float& dgate) {
-        n = (load1<XF>(a.x, x0 + c) - r.mean) * r.rstd;
-        const float w = a.weight ? a.weight[c0 + c] : 1.f, z = fmaf(n, w, a.bias ? a.bias[c0 + c] : 0.f);
-        const float dy = load1<YF>(a.dy, y0 + c);
-        const Act f = act_of(a.gate ? load1<YF>(a.gate, g0 + c) : z, a.act);
-        dgate = dy * z * f.slope;
-        return dy * (a.gate ? f.f : f.slope) * w;
-    };
-    float n, dgate;
-    for (int64_t c = lane; c < a.width; c += 64) {
-        const float dn = grads(c, n, dgate);
+    for (int64_t c = threadIdx.x; c < a.width; c += kGnThreads) {
+        terms(c, n, z, w, f, slope);
+        const float dn = load1<YF>(a.dy, y0 + c) * (a.gate ? f : slope) * w;
         s1 += dn;
         s2 = fmaf(dn, n, s2);
     }
-    s1 = wave_sum(s1) / a.width;
-    s2 = wave_sum(s2) / a.width;
-    for (int64_t c = lane; c < a.width; c += 64) {
-        const float dn = grads(c, n, dgate);
-        if (a.gate) store1<YF>(a.dgate, y0 + c, dgate);
-        store1<XF>(a.dx, y0 + c, r.rstd * (dn - s1 - n * s2));
+    s1 = block_sum(s1, lds) * mean_of;
+    s2 = block_sum(s2, lds) * mean_of;
+    for (int64_t c = threadIdx.x; c < a.width; c += kGnThreads) {
+        terms(c, n, z, w, f, slope);
+        const float dy = load1<YF>(a.dy, y0 + c), dx = rstd * (dy * (a.gate ? f : slope) * w - fmaf(n, s2, s1));
+        const float dgate = dy * z * slope;
+        if (a.gate) gn_store<1, YF>(a.dgate, y0 + c, &dgate);
+        gn_store<1, XF>(a.dx, y0 + c, &dx);
     }
 }
 
-// The weights' sums: a wave for each channel's group of a column of tokens, one workgroup for the group.
+// The weights' sums over blocks of tokens, a thread a channel.
 template <bool XF, bool YF>
-__global__ __launch_bounds__(64) void groupnorm_plain_sums_kernel(GroupNormArgs a) {
-    const int64_t c0 = blockIdx.x * a.width;
-    const int lane = threadIdx.x;
-    for (int64_t first = 0; first < a.width; first += 64) {
-        const int64_t c = first + lane;
-        float dw = 0.f, db = 0.f;
-        for (int64_t t = 0; t < a.tokens; ++t) {
-            const Row r = row_of<XF>(a, t * a.x_stride + c0, lane);
-            if (c >= a.width) continue;
-            const float n = (load1<XF>(a.x, t * a.x_stride + c0 + c) - r.mean) * r.rstd;
-            const float z = fmaf(n, a.weight ? a.weight[c0 + c] : 1.f, a.bias ? a.bias[c0 + c] : 0.f);
-            const Act f = act_of(a.gate ? load1<YF>(a.gate, t * a.gate_stride + c0 + c) : z, a.act);
-            const float dz = load1<YF>(a.dy, t * a.groups * a.width + c0 + c) * (a.gate ? f.f : f.slope);
-            dw = fmaf(dz, n, dw);
-            db += dz;
-        }
-        if (c < a.width) {
-            a.dweight[c0 + c] = dw;
-            a.dbias[c0 + c] = db;
-        }
+__global__ __launch_bounds__(kGnThreads) void groupnorm_columns_kernel(GroupNormArgs a, const float* stats, int64_t block) {
+    const int64_t c = (int64_t)blockIdx.x * kGnThreads + threadIdx.x, C = a.groups * a.width;
+    if (c >= C) return;
+    const float w = a.weight ? a.weight[c] : 1.f, b = a.bias ? a.bias[c] : 0.f;
+    const int64_t first = blockIdx.y * block, end = first + block < a.tokens ? first + block : a.tokens;
+    float dw = 0.f, db = 0.f;
+    for (int64_t t = first; t < end; ++t) {
+        const float* s = stats + 2 * (t * a.groups + c / a.width);
+        const float n = (load1<XF>(a.x, t * a.x_stride + c) - s[0]) * s[1], z = fmaf(n, w, b);
+        float f, slope;
+        gn_act<true>(a.gate ? load1<YF>(a.gate, t * a.gate_stride + c) : z, a.act, f, slope);
+        const float dz = load1<YF>(a.dy, t * C + c) * (a.gate ? f : slope);
+        dw = fmaf(dz, n, dw);
+        db += dz;
     }
+    float* out = static_cast<float*>(a.ws) + blockIdx.y * 2 * C;
+    out[c] = dw;
+    out[C + c] = db;
+}
+
+int64_t token_blocks(int64_t tokens) {
+    const int64_t most = (tokens + kGnBlockTokens - 1) / kGnBlockTokens;
+    return most < kGnBlocks ? most : kGnBlocks;
 }
 
 template <bool XF, bool YF>
-void launch(const GroupNormArgs& a, hipStream_t st) {
-    if (a.tokens)
-        hipLaunchKernelGGL((groupnorm_plain_kernel<XF, YF>), dim3((unsigned)groupnorm_groups(a)), dim3(256), 0, st, a);
-    if (a.dweight) hipLaunchKernelGGL((groupnorm_plain_sums_kernel<XF, YF>), dim3((unsigned)a.groups), dim3(64), 0, st, a);
+void wide_rows(const GroupNormArgs& a, hipStream_t st) {
+    const int64_t C = a.groups * a.width, blocks = token_blocks(a.tokens);
+    float* stats = a.dweight ? static_cast<float*>(a.ws) + blocks * 2 * C : nullptr;
+    hipLaunchKernelGGL((groupnorm_rows_kernel<XF, YF>), dim3((unsigned)(a.tokens * a.groups)), dim3(kGnThreads), 0, st, a, stats);
+    if (!a.dweight) return;
+    hipLaunchKernelGGL((groupnorm_columns_kernel<XF, YF>), dim3((unsigned)((C + kGnThreads - 1) / kGnThreads), (unsigned)blocks),
+                       dim3(kGnThreads), 0, st, a, stats, (a.tokens + blocks - 1) / blocks);
+    groupnorm_sums(a, blocks, st);
 }
 
-void by_type(const GroupNormArgs& a, hipStream_t st) {
-    if (a.x_f32) a.y_f32 ? launch<true, true>(a, st) : launch<true, false>(a, st);
-    else a.y_f32 ? launch<false, true>(a, st) : launch<false, false>(a, st);
+template <typename F>
+void by_type(const GroupNormArgs& a, F&& f) {
+    if (a.x_f32) a.y_f32 ? f(std::true_type(), std::true_type()) : f(std::true_type(), std::false_type());
+    else a.y_f32 ? f(std::false_type(), std::true_type()) : f(std::false_type(), std::false_type());
 }
 
 }  // namespace
 
-bool groupnorm_wide(const GroupNormArgs&) { return false; }
-int64_t groupnorm_groups(const GroupNormArgs& a) { return (a.tokens * a.groups + 3) / 4; }
-int64_t groupnorm_bwd_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
+bool groupnorm_wide(const GroupNormArgs& a) { return a.width % 8 == 0 && a.x_stride % 8 == 0 && a.gate_stride % 8 == 0; }
+
+int64_t groupnorm_groups(const GroupNormArgs& a) {
+    if (!gn_in_registers(a)) return a.tokens * a.groups;
+    return 4096 + a.groups;
+}
+
+int64_t groupnorm_bwd_workspace_bytes(int64_t tokens, int64_t groups, int64_t width) {
+    const int64_t stats = width > 1024 ? 2 * tokens * groups : 0;
+    return 4 * (token_blocks(tokens) * 2 * groups * width + stats);
+}
 
 hipError_t launch_groupnorm_fwd(const GroupNormArgs& a, hipStream_t st) {
-    by_type(a, st);
+    by_type(a, [&](auto xf, auto yf) {
+        constexpr bool XF = decltype(xf)::value, YF = decltype(yf)::value;
+        gn_in_registers(a) ? groupnorm_fwd_of<XF, YF>(a, st) : wide_rows<XF, YF>(a, st);
+    });
     return hipGetLastError();
 }
 
 hipError_t launch_groupnorm_bwd(const GroupNormArgs& a, hipStream_t st) {
-    by_type(a, st);
+    if (a.tokens == 0) {  // sums of nothing
+        groupnorm_sums(a, 0, st);
+        return hipGetLastError();
+    }
+    by_type(a, [&](auto xf, auto yf) {
+        constexpr bool XF = decltype(xf)::value, YF = decltype(yf)::value;
+        gn_in_registers(a) ? groupnorm_bwd_of<XF, YF>(a, st) : wide_rows<XF, YF>(a, st);
+    });
     return hipGetLastError();
 }
 
