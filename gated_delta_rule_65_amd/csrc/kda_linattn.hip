@@ -133,9 +133,22 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 __device__ __forceinline__ float low_of(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float high_of(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 
+// x less the low, the high half of u: one dot product of two pairs, with -1 and 0, instead of taking the half out and
+// subtracting.  It is exact: the difference of a value and its nearest bf16 has few enough bits.  The pair of ones has to be
+// in registers: the instruction takes a literal otherwise than it says.
+struct Ones {
+    uint32_t low = 0x0000bf80u, high = 0xbf800000u;
+};
+__device__ __forceinline__ float less_low(float x, uint32_t u, const Ones& k) {
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, u), __builtin_bit_cast(bf16x2_t, k.low), x, false);
+}
+__device__ __forceinline__ float less_high(float x, uint32_t u, const Ones& k) {
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, u), __builtin_bit_cast(bf16x2_t, k.high), x, false);
+}
+
 // x as a sum of PLANES bf16 values, each the nearest to what the ones before leave; in fp32 x itself.
 template <int PLANES>
-__device__ __forceinline__ void split(const float x[8], LFrag<false> f[PLANES]) {
+__device__ __forceinline__ void split(const float x[8], LFrag<false> f[PLANES], const Ones& k) {
     uint4 u[PLANES];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -145,8 +158,8 @@ __device__ __forceinline__ void split(const float x[8], LFrag<false> f[PLANES]) 
             const uint32_t h = pack2(a, b);
             (&u[p].x)[j] = h;
             if (p + 1 < PLANES) {
-                a -= low_of(h);
-                b -= high_of(h);
+                a = less_low(a, h, k);
+                b = less_high(b, h, k);
             }
         }
     }
@@ -154,7 +167,7 @@ __device__ __forceinline__ void split(const float x[8], LFrag<false> f[PLANES]) 
     for (int p = 0; p < PLANES; ++p) f[p].v = __builtin_bit_cast(bf16x8_t, u[p]);
 }
 template <int PLANES>
-__device__ __forceinline__ void split(const float x[8], LFrag<true> f[PLANES]) {
+__device__ __forceinline__ void split(const float x[8], LFrag<true> f[PLANES], const Ones&) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[0].v[j] = x[j];
 }
@@ -347,6 +360,7 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinOp op0, L
         for (int r = 0; r < G::RB; ++r) into[r] = op.so * powers[16 * r + m + (op.back ? 0 : 1)];
     }
     float owed = 0.f;
+    Ones ones;
     if (tid < 2 * C) {
         const int i = tid % C, n = tid < C ? C : tokens - (chunks - 1) * C;
         weights[tid / C][i] = i < n ? op.su * powers[n - 1 - i + (op.back ? 1 : 0)] : 0.f;
@@ -415,7 +429,7 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinOp op0, L
         const int n = tokens - c * C < C ? tokens - c * C : C;
         const bool more = c + 1 < chunks;
         // the places of a chunk's fragments are made again from these few: kept, they would take most of the registers
-        __asm__ volatile("" : "+v"(at_row), "+v"(at_turned), "+v"(at_col), "+v"(at_score), "+v"(at_score2));
+        __asm__ volatile("" : "+v"(ones.low), "+v"(ones.high), "+v"(at_row), "+v"(at_turned), "+v"(at_col), "+v"(at_score), "+v"(at_score2));
         __asm__ volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
         if (more) {
             fetch(op.b, Kn, c + 1, UnitsA(), offset_a);
@@ -427,6 +441,15 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinOp op0, L
 #pragma unroll
             for (int d = 0; d < ND; ++d) vf[ks * ND + d] = frag_ct(V, d, ks);
 
+        // The state's decay, in 32 bits: what a power's rounding owes is paid in the next ones, so that thousands of chunks do
+        // not add up.
+        float dec = powers[n];
+        if (n == C) {
+            dec = fmaf(whole32, owed, whole32);
+            owed += rest - (whole32 > 0.f ? (dec - whole32) / whole32 : 0.f);
+        }
+        int bad[ND];  // a column's first token whose value is not finite
+        bool marked = false;
         if constexpr (ROWS) {
             f32x4_t O[G::RB][ND], P[G::RB];
 #pragma unroll
@@ -447,8 +470,13 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinOp op0, L
                     LFrag<F32> st[G::PL];
                     float x[8];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) x[j] = S[2 * s][d][j], x[4 + j] = S[2 * s + 1][d][j];
-                    split<G::PL>(x, st);
+                    for (int j = 0; j < 4; ++j) {
+                        x[j] = S[2 * s][d][j];
+                        x[4 + j] = S[2 * s + 1][d][j];
+                        S[2 * s][d][j] *= dec;
+                        S[2 * s + 1][d][j] *= dec;
+                    }
+                    split<G::PL>(x, st, ones);
 #pragma unroll
                     for (int p = 0; p < G::PL; ++p)
 #pragma unroll
@@ -480,8 +508,9 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinOp op0, L
                         const uint32_t h0 = pack2(x[0], x[1]), h1 = pack2(x[2], x[3]);
                         char* to = ldsP + (r < 2 ? at_score + 1024 * r : (at_score2 ^ (64 * (wave >> 1))) + 2048 * (r - 2)) + 8 * (wave & 1);
                         *reinterpret_cast<uint2*>(to) = make_uint2(h0, h1);
-                        *reinterpret_cast<uint2*>(to + G::PB) = make_uint2(pack2(x[0] - low_of(h0), x[1] - high_of(h0)),
-                                                                           pack2(x[2] - low_of(h1), x[3] - high_of(h1)));
+                        *reinterpret_cast<uint2*>(to + G::PB) =
+                            make_uint2(pack2(less_low(x[0], h0, ones), less_high(x[1], h0, ones)),
+                                       pack2(less_low(x[2], h1, ones), less_high(x[3], h1, ones)));
                     }
                 }
 #pragma unroll
@@ -495,13 +524,9 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinOp op0, L
                 fetch(op.c, Vn, c + 1, UnitsC(), offset_c);
             }
 
-            // A value that is not finite must not meet the zeros of earlier rows: such values are left out of the product, and
-            // their column is made NaN from their token on.
-            int bad[ND];
-            LFrag<F32> clean[G::KS * ND];
-#pragma unroll
-            for (int i = 0; i < G::KS * ND; ++i) clean[i] = vf[i];
-            const bool marked = __ballot(any_not_finite<G::KS * ND>(vf)) != 0;
+            // A value that is not finite must not meet the zeros of earlier rows: such values are left out of the products, and
+            // their column is made NaN from their token on, here and in the state.
+            marked = __ballot(any_not_finite<G::KS * ND>(vf)) != 0;
             if (marked) {
 #pragma unroll
                 for (int d = 0; d < ND; ++d) {
@@ -512,7 +537,7 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinOp op0, L
                         for (int j = 7; j >= 0; --j)
                             if (!(fabsf((float)vf[ks * ND + d].v[j]) < __builtin_inff())) {
                                 bad[d] = 32 * ks + 16 * (j >> 2) + 4 * grp + (j & 3);
-                                clean[ks * ND + d].v[j] = 0.f;
+                                vf[ks * ND + d].v[j] = 0.f;
                             }
                     bad[d] = min(bad[d], __shfl_xor(bad[d], 16));
                     bad[d] = min(bad[d], __shfl_xor(bad[d], 32));
@@ -535,7 +560,7 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinOp op0, L
                                 ldsP + p * G::PB + (r < 2 ? at_score + 1024 * r : (at_score2 ^ (64 * ks)) + 2048 * (r - 2)));
                         }
 #pragma unroll
-                        for (int d = 0; d < ND; ++d) O[r][d] = mma(clean[ks * ND + d], pf, O[r][d]);
+                        for (int d = 0; d < ND; ++d) O[r][d] = mma(vf[ks * ND + d], pf, O[r][d]);
                     }
             if (marked) {
 #pragma unroll
@@ -568,21 +593,14 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinOp op0, L
             }
         }
 
-        // The state, decayed in 32 bits: what a power's rounding owes is paid in the next ones, so that thousands of chunks do
-        // not add up.  The weighted values are sums of three bf16 values, which hold all of their 24 bits.
-        float dec;
-        if (n == C) {
-            dec = fmaf(whole32, owed, whole32);
-            owed += rest - (whole32 > 0.f ? (dec - whole32) / whole32 : 0.f);
-        } else {
-            dec = powers[n];
-        }
+        if constexpr (!ROWS)
 #pragma unroll
-        for (int ct = 0; ct < G::CT; ++ct)
+            for (int ct = 0; ct < G::CT; ++ct)
 #pragma unroll
-            for (int d = 0; d < ND; ++d)
+                for (int d = 0; d < ND; ++d)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) S[ct][d][j] *= dec;
+                    for (int j = 0; j < 4; ++j) S[ct][d][j] *= dec;
+        // the weighted values as sums of three bf16 values, which hold all of their 24 bits
 #pragma unroll
         for (int ks = 0; ks < G::KS; ++ks) {
             const f32x4_t w0 = *reinterpret_cast<const f32x4_t*>(weights[n < C] + 32 * ks + 4 * grp);
@@ -594,7 +612,7 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinOp op0, L
                 values(vf[ks * ND + d], x);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) x[j] *= w0[j], x[4 + j] *= w1[j];
-                split<G::VL>(x, vb[d]);
+                split<G::VL>(x, vb[d], ones);
             }
 #pragma unroll
             for (int ct = 0; ct < G::CT; ++ct) {
@@ -604,6 +622,15 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinOp op0, L
 #pragma unroll
                     for (int p = 0; p < G::VL; ++p) S[ct][d] = mma(kt, vb[d][p], S[ct][d]);
             }
+        }
+        if (ROWS && marked) {
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+                if (bad[d] < n)
+#pragma unroll
+                    for (int ct = 0; ct < G::CT; ++ct)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) S[ct][d][j] = __builtin_nanf("");
         }
     };
 
