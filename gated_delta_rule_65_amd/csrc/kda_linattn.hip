@@ -228,6 +228,9 @@ __device__ __forceinline__ bf16x4_t read_turned(const char* p) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4bf16((__attribute__((address_space(3))) bf16x4_t*)const_cast<char*>(p));
 }
 
+// The count of s_waitcnt that lets `vm` requests of memory be under way, and none of LDS.
+constexpr int waitcnt(int vm) { return (vm & 15) | (vm >> 4) << 14 | 7 << 4; }
+
 // 16 bytes for each lane of a wave from memory to LDS, where they lie one after another from `to` on.
 __device__ __forceinline__ void load_to_lds(const void* from, char* to) {
     __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)(uintptr_t)from,
@@ -244,6 +247,7 @@ struct LinTile {
     static constexpr int KS = C / 32, RB = C / 16, AS = DA / 32, CT = DA / 16;
     static constexpr int PL = F32 ? 1 : 2;       // planes of scores and of the state
     static constexpr int VL = F32 ? 1 : 3;       // planes of the weighted values
+    static constexpr int STORES = F32 ? RB * ND : RB;  // a wave's of a whole chunk
     static constexpr int PB = F32 ? 32 * 128 : 32 * 64 + 32 * 128;  // a plane of scores: rows up to their diagonal's 32 tokens
 };
 
@@ -281,40 +285,27 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinOp op0, L
     auto col = [&](int i, int d) { return ND == 2 ? 32 * wave + 8 * (i >> 2) + 4 * d + (i & 3) : 16 * wave + i; };
 
     const int tokens = (int)(w.end - w.begin), chunks = (tokens + C - 1) / C;
-    // Rows of a chunk, in the order of the recurrence, to LDS: 64 units a wave at a time.  A whole chunk's places are one offset
-    // a lane from an address that the wave shares; the last one's rows behind its end repeat its last row, and weigh nothing.
+    // Rows of a chunk, in the order of the recurrence, to LDS, 64 units a wave at a time.  Rows behind the last one repeat it
+    // and weigh nothing: without a branch, as many requests for every chunk.
     const int64_t row0 = op.back ? w.end - 1 : w.begin;
-    auto offset_of = [&](auto units) {
-        constexpr int U = decltype(units)::value;
-        const int u = wave * 64 + lane, row = u / U, unit = u % U ^ turn<U, F32>(row);
-        return (uint32_t)((op.back ? C - 1 - row : row) * H * U + unit) * 16u;
-    };
-    auto fetch = [&](const void* from, char* to, int c, auto units, uint32_t offset) {
-        constexpr int U = decltype(units)::value, N = C * U / kThreads, ROWS_AT_ONCE = kThreads / U;
-        static_assert(ROWS_AT_ONCE % 16 == 0 || (F32 && ROWS_AT_ONCE == 8), "what a row's turn is, 16 rows behind or eight");
-        const int64_t pitch = (int64_t)H * U * 16;
-        if (tokens - c * C >= C) {
-            const char* base = static_cast<const char*>(from) + (op.back ? row0 - c * C - (C - 1) : row0 + c * C) * pitch + (int64_t)h * U * 16;
+    auto fetch = [&](const void* from, char* to, int c, auto units) {
+        constexpr int U = decltype(units)::value, N = C * U / kThreads, STEP = kThreads / U;
+        static_assert(STEP % 16 == 0 || (F32 && STEP == 8), "what a row's turn is, 16 rows behind or eight");
+        const int top = tokens - c * C < C ? tokens - c * C - 1 : C - 1;
+        const uint4* base = static_cast<const uint4*>(from) + (op.back ? row0 - c * C - top : row0 + c * C) * H * U + (int64_t)h * U;
+        const int row = tid / U, unit = tid % U ^ turn<U, F32>(row), flip = op.back ? -1 : 0, add = op.back ? top + 1 : 0;
 #pragma unroll
-            for (int x = 0; x < N; ++x)
-                load_to_lds(base + (op.back ? -x : x) * ROWS_AT_ONCE * pitch + (ROWS_AT_ONCE == 8 && x % 2 ? offset ^ 128 : offset),
-                            to + (x * 4 + wave) * 1024);
-        } else {
-#pragma unroll 1
-            for (int x = 0; x < N; ++x) {
-                const int u = (x * 4 + wave) * 64 + lane, row = u / U, unit = u % U ^ turn<U, F32>(row);
-                const int r = c * C + row, t = r < tokens ? r : tokens - 1;
-                load_to_lds(static_cast<const char*>(from) + (row0 + (op.back ? -t : t)) * pitch + ((int64_t)h * U + unit) * 16,
-                            to + (x * 4 + wave) * 1024);
-            }
+        for (int x = 0; x < N; ++x) {
+            int t = ((row + x * STEP) ^ flip) + add;
+            t = t < 0 ? 0 : t > top ? top : t;
+            load_to_lds(base + (uint32_t)(__mul24(t, H * U) + (STEP == 8 && x % 2 ? unit ^ 8 : unit)), to + (x * 4 + wave) * 1024);
         }
     };
     using UnitsA = std::integral_constant<int, UA>;
     using UnitsC = std::integral_constant<int, UC>;
-    const uint32_t offset_a = offset_of(UnitsA()), offset_c = offset_of(UnitsC());
-    fetch(op.b, ldsK0, 0, UnitsA(), offset_a);
-    fetch(op.c, ldsV0, 0, UnitsC(), offset_c);
-    if constexpr (ROWS) fetch(op.a, ldsQ, 0, UnitsA(), offset_a);
+    fetch(op.b, ldsK0, 0, UnitsA());
+    fetch(op.c, ldsV0, 0, UnitsC());
+    if constexpr (ROWS) fetch(op.a, ldsQ, 0, UnitsA());
 
     const double lg = log_decay(g[h]);
     if (tid <= C) powers[tid] = (float)exp(lg * tid);
@@ -424,16 +415,20 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinOp op0, L
         return f;
     };
 
-    // One chunk with its keys in K; those of the next one go to Kn.
-    auto chunk = [&](int c, char* K, char* Kn, char* V, char* Vn) {
-        const int n = tokens - c * C < C ? tokens - c * C : C;
-        const bool more = c + 1 < chunks;
+    // One chunk with its keys in K; those of the next one go to Kn, if there is one: only the last chunk may have fewer tokens
+    // than C.  Which requests are under way is the same on every path, so that the compiler sees what has been waited for.
+    auto chunk = [&](int c, char* K, char* Kn, char* V, char* Vn, auto ends) {
+        constexpr bool LAST = decltype(ends)::value;
+        const int n = LAST ? tokens - c * C : C;
         // the places of a chunk's fragments are made again from these few: kept, they would take most of the registers
         __asm__ volatile("" : "+v"(ones.low), "+v"(ones.high), "+v"(at_row), "+v"(at_turned), "+v"(at_col), "+v"(at_score), "+v"(at_score2));
-        __asm__ volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        if (more) {
-            fetch(op.b, Kn, c + 1, UnitsA(), offset_a);
-            if constexpr (!ROWS) fetch(op.c, Vn, c + 1, UnitsC(), offset_c);
+        // The chunk's rows have come.  Requests end in the order in which they were made, and the last ones are the stores of the
+        // chunk before: they are not waited for (with them the prefill batch takes 140 us, without 85).
+        __builtin_amdgcn_s_waitcnt(waitcnt(ROWS ? G::STORES : 0));
+        __asm__ volatile("s_barrier" ::: "memory");
+        if constexpr (!LAST) {
+            fetch(op.b, Kn, c + 1, UnitsA());
+            if constexpr (!ROWS) fetch(op.c, Vn, c + 1, UnitsC());
         }
         LFrag<F32> vf[G::KS * ND];
 #pragma unroll
@@ -519,9 +514,9 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinOp op0, L
                     for (int j = 0; j < 4; ++j) O[r][d][j] *= into[r];
             }
             lds_barrier();
-            if (more) {
-                fetch(op.a, ldsQ, c + 1, UnitsA(), offset_a);
-                fetch(op.c, Vn, c + 1, UnitsC(), offset_c);
+            if constexpr (!LAST) {
+                fetch(op.a, ldsQ, c + 1, UnitsA());
+                fetch(op.c, Vn, c + 1, UnitsC());
             }
 
             // A value that is not finite must not meet the zeros of earlier rows: such values are left out of the products, and
@@ -576,21 +571,23 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinOp op0, L
             // a lane's first row of the chunk; the others are 16 rows apart
             char* to = static_cast<char*>(op.out) + ((row0 + (op.back ? -c * C : c * C)) * H + h) * (int64_t)(DC * G::ES);
             const int pitch = (op.back ? -H : H) * DC * G::ES, mine = m * pitch + col(4 * grp, 0) * G::ES;
+            auto put = [&](int r) {
+                char* p = to + (int64_t)(16 * r * pitch) + mine;
+                if constexpr (F32) {
 #pragma unroll
-            for (int r = 0; r < G::RB; ++r) {
-                if (16 * r + m < n) {
-                    char* p = to + (int64_t)(16 * r * pitch) + mine;
-                    if constexpr (F32) {
-#pragma unroll
-                        for (int d = 0; d < ND; ++d) *reinterpret_cast<f32x4_t*>(p + 16 * d) = O[r][d];
-                    } else if constexpr (ND == 2) {
-                        *reinterpret_cast<uint4*>(p) = make_uint4(pack2(O[r][0][0], O[r][0][1]), pack2(O[r][0][2], O[r][0][3]),
-                                                                  pack2(O[r][1][0], O[r][1][1]), pack2(O[r][1][2], O[r][1][3]));
-                    } else {
-                        *reinterpret_cast<uint2*>(p) = make_uint2(pack2(O[r][0][0], O[r][0][1]), pack2(O[r][0][2], O[r][0][3]));
-                    }
+                    for (int d = 0; d < ND; ++d) *reinterpret_cast<f32x4_t*>(p + 16 * d) = O[r][d];
+                } else if constexpr (ND == 2) {
+                    *reinterpret_cast<uint4*>(p) = make_uint4(pack2(O[r][0][0], O[r][0][1]), pack2(O[r][0][2], O[r][0][3]),
+                                                              pack2(O[r][1][0], O[r][1][1]), pack2(O[r][1][2], O[r][1][3]));
+                } else {
+                    *reinterpret_cast<uint2*>(p) = make_uint2(pack2(O[r][0][0], O[r][0][1]), pack2(O[r][0][2], O[r][0][3]));
                 }
-            }
+            };
+            __asm__ volatile("" ::: "memory");  // behind the chunk's loads, all of them
+#pragma unroll
+            for (int r = 0; r < G::RB; ++r)
+                if (!LAST || 16 * r + m < n) put(r);
+            __asm__ volatile("" ::: "memory");
         }
 
         if constexpr (!ROWS)
@@ -634,15 +631,16 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinOp op0, L
         }
     };
 
-    for (int c = 0; c < chunks; c += 2) {
-        if constexpr (ROWS) {
-            chunk(c, ldsK0, ldsK1, ldsV0, ldsV0);
-            if (c + 1 < chunks) chunk(c + 1, ldsK1, ldsK0, ldsV0, ldsV0);
-        } else {
-            chunk(c, ldsK0, ldsK1, ldsV0, ldsV1);
-            if (c + 1 < chunks) chunk(c + 1, ldsK1, ldsK0, ldsV1, ldsV0);
-        }
+    char* const ldsVn = ROWS ? ldsV0 : ldsV1;
+    int c = 0;
+    __builtin_amdgcn_s_waitcnt(waitcnt(0));
+    while (true) {
+        if (c + 1 >= chunks) break;
+        chunk(c++, ldsK0, ldsK1, ldsV0, ldsVn, std::false_type());
+        if (c + 1 >= chunks) break;
+        chunk(c++, ldsK1, ldsK0, ldsVn, ldsV0, std::false_type());
     }
+    chunk(c, c % 2 ? ldsK1 : ldsK0, nullptr, c % 2 ? ldsVn : ldsV0, nullptr, std::true_type());
 
     float* to = nullptr;
     if constexpr (ROWS) {
