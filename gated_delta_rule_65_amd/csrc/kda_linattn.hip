@@ -47,6 +47,7 @@ struct Where {
     int64_t n, begin, end;  // sequence, and the segment's tokens
     int64_t slot;           // its place among the states
     int64_t j, count;       // segment j of count; count 0: a sequence without tokens
+    int64_t tail;           // tokens of the sequence's last segment
 };
 
 __device__ __forceinline__ int64_t seq_begin(const Segs& s, int64_t n) {
@@ -85,6 +86,7 @@ __device__ __forceinline__ Where where_of(const Segs& s, int64_t slot) {
         w.count = -1;
         return w;
     }
+    w.tail = w.end - w.begin - (w.count - 1) * s.L;
     w.begin += w.j * s.L;
     if (w.end > w.begin + s.L) w.end = w.begin + s.L;
     return w;
@@ -239,29 +241,43 @@ __device__ __forceinline__ void load_to_lds(const void* from, char* to) {
 
 template <int DA, int DC, bool F32>
 struct LinTile {
+    static constexpr int WAVES = DC / 16, THREADS = 64 * WAVES;  // a wave for 16 columns; two workgroups on a CU
     static constexpr int C = F32 ? 32 : 64;      // tokens of a chunk
     static constexpr int ES = F32 ? 4 : 2;
     static constexpr int UA = DA * ES / 16, UC = DC * ES / 16;  // units of a row
     static constexpr int KB = C * UA * 16, VB = C * UC * 16;
-    static constexpr int ND = DC / 64;           // 16-column tiles of a wave
     static constexpr int KS = C / 32, RB = C / 16, AS = DA / 32, CT = DA / 16;
     static constexpr int PL = F32 ? 1 : 2;       // planes of scores and of the state
     static constexpr int VL = F32 ? 1 : 3;       // planes of the weighted values
-    static constexpr int STORES = F32 ? RB * ND : RB;  // a wave's of a whole chunk
     static constexpr int PB = F32 ? 32 * 128 : 32 * 64 + 32 * 128;  // a plane of scores: rows up to their diagonal's 32 tokens
 };
 
-// A workgroup's way through its segment, four waves with a quarter of the columns each and all rows of the state for them.
+// The state's rows are dealt over tiles of 16 so that a lane's rows of two tiles' products are eight side by side: what the next
+// product contracts lies in a row of `a` as it is.  Row i of tile ct:
+__host__ __device__ constexpr int state_row(int ct, int i) { return 32 * (ct >> 1) + 8 * (i >> 2) + 4 * (ct & 1) + (i & 3); }
+// Segments' states lie as the lanes hold them: the place of four rows from `row` on (a multiple of 4) in column c of a state of
+// DA rows.
+template <int DA>
+__device__ __forceinline__ int state_at(int row, int c) {
+    const int ct = 2 * (row >> 5) + (row >> 2 & 1), grp = row >> 3 & 3;
+    return (((c >> 4) * (DA / 16) + ct) * 64 + grp * 16 + (c & 15)) * 4;
+}
+
+// Sequences of up to so many segments: a segment's workgroup folds those before it by itself, which the last one's seven states
+// of 64 KB make dearer than a kernel for it beyond.
+constexpr int kOwnFold = 8;
+
+// A workgroup's way through its segment: a wave for 16 columns, with all rows of the state for them.
 template <int DA, int DC, bool F32, bool ROWS>
-__global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinOp op0, LinOp op1, LinOp op2, int ops, Segs segs,
-                                                                    const float* g) {
+__global__ __launch_bounds__(4 * DC, DC / 32) void linattn_chunk_kernel(
+    LinOp op0, LinOp op1, LinOp op2, int ops, Segs segs, const float* g) {
     using G = LinTile<DA, DC, F32>;
-    constexpr int C = G::C, ND = G::ND, UA = G::UA, UC = G::UC;
+    constexpr int C = G::C, UA = G::UA, UC = G::UC, THREADS = G::THREADS;
     __shared__ __align__(16) char ldsK0[G::KB], ldsK1[G::KB];
     __shared__ __align__(16) char ldsV0[G::VB], ldsV1[ROWS ? 16 : G::VB];
     __shared__ __align__(16) char ldsQ[ROWS ? G::KB : 16], ldsP[ROWS ? G::PL * G::PB : 16];
     __shared__ __align__(16) float weights[2][C];  // what a token's product keeps at the end of a whole chunk, and of the last one
-    __shared__ float powers[C + 1];             // of the decay
+    __shared__ float powers[C + 1];                // of the decay
 
     // the operations of a segment and head in workgroups of one XCD, next to one another
     const int64_t id = (int64_t)(blockIdx.x / (8 * ops)) * 8 + blockIdx.x % 8;
@@ -271,85 +287,104 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinOp op0, L
     const Where w = where_of(segs, id / H);
     if (w.count < 0) return;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, m = lane & 15, grp = lane >> 4;
-    const bool first = op.back ? w.j == w.count - 1 : w.j == 0, last = op.back ? w.j == 0 : w.j + 1 >= w.count;
+    const bool last = op.back ? w.j == 0 : w.j + 1 >= w.count;
     if (w.count == 0) {
         if (ROWS && op.fin) {
             const int64_t at = (w.n * H + h) * (int64_t)DA * DC;
-            for (int i = tid; i < DA * DC; i += kThreads) op.fin[at + i] = op.x0 ? op.x0[at + i] : 0.f;
+            for (int i = tid; i < DA * DC; i += THREADS) op.fin[at + i] = op.x0 ? op.x0[at + i] : 0.f;
         }
         return;
     }
     if (!ROWS && last) return;
 
-    // a wave's columns: those of a lane's rows of a product, of both tiles, are side by side
-    auto col = [&](int i, int d) { return ND == 2 ? 32 * wave + 8 * (i >> 2) + 4 * d + (i & 3) : 16 * wave + i; };
-
     const int tokens = (int)(w.end - w.begin), chunks = (tokens + C - 1) / C;
-    // Rows of a chunk, in the order of the recurrence, to LDS, 64 units a wave at a time.  Rows behind the last one repeat it
-    // and weigh nothing: without a branch, as many requests for every chunk.
+    // Rows of a chunk, in the order of the recurrence, to LDS, 64 units a wave at a time: for a whole chunk, a lane's offset from
+    // an address that the wave shares.  Rows behind the last one repeat it and weigh nothing: as many requests for every chunk.
     const int64_t row0 = op.back ? w.end - 1 : w.begin;
-    auto fetch = [&](const void* from, char* to, int c, auto units) {
-        constexpr int U = decltype(units)::value, N = C * U / kThreads, STEP = kThreads / U;
-        static_assert(STEP % 16 == 0 || (F32 && STEP == 8), "what a row's turn is, 16 rows behind or eight");
-        const int top = tokens - c * C < C ? tokens - c * C - 1 : C - 1;
-        const uint4* base = static_cast<const uint4*>(from) + (op.back ? row0 - c * C - top : row0 + c * C) * H * U + (int64_t)h * U;
-        const int row = tid / U, unit = tid % U ^ turn<U, F32>(row), flip = op.back ? -1 : 0, add = op.back ? top + 1 : 0;
+    auto offset_of = [&](auto units) {
+        constexpr int U = decltype(units)::value;
+        const int r = tid / U;
+        return (uint32_t)((op.back ? C - 1 - r : r) * H * U + (tid % U ^ turn<U, F32>(r))) * 16u;
+    };
+    auto fetch = [&](const void* from, char* to, int c, auto units, uint32_t offset) {
+        constexpr int U = decltype(units)::value, N = C * U / THREADS, STEP = THREADS / U;
+        static_assert(N * THREADS == C * U && (STEP % 16 == 0 || (F32 && STEP == 8)), "a row's turn is that of 16 rows before");
+        constexpr int other = STEP == 8 ? 8 : 0;
+        if (tokens - c * C >= C) {
+            const char* base = static_cast<const char*>(from) +
+                               ((op.back ? row0 - c * C - (C - 1) : row0 + c * C) * H * U + (int64_t)h * U) * 16;
+            const int64_t step = (int64_t)(op.back ? -STEP : STEP) * H * U * 16;
 #pragma unroll
-        for (int x = 0; x < N; ++x) {
-            int t = ((row + x * STEP) ^ flip) + add;
-            t = t < 0 ? 0 : t > top ? top : t;
-            load_to_lds(base + (uint32_t)(__mul24(t, H * U) + (STEP == 8 && x % 2 ? unit ^ 8 : unit)), to + (x * 4 + wave) * 1024);
+            for (int x = 0; x < N; ++x)
+                load_to_lds(base + x * step + (x % 2 ? offset ^ (other * 16) : offset), to + (x * G::WAVES + wave) * 1024);
+        } else {
+            const int top = tokens - c * C - 1;
+            const uint4* base = static_cast<const uint4*>(from) + (op.back ? row0 - c * C - top : row0 + c * C) * H * U + (int64_t)h * U;
+            int mine = tid / U;
+            __asm__ volatile("" : "+v"(mine));  // made here, for the last chunk alone
+#pragma unroll
+            for (int x = 0; x < N; ++x) {
+                const int r = mine + x * STEP, t = r > top ? top : r;
+                load_to_lds(base + (uint32_t)(__mul24(op.back ? top - t : t, H * U) + (tid % U ^ turn<U, F32>(r))),
+                            to + (x * G::WAVES + wave) * 1024);
+            }
         }
     };
     using UnitsA = std::integral_constant<int, UA>;
     using UnitsC = std::integral_constant<int, UC>;
-    fetch(op.b, ldsK0, 0, UnitsA());
-    fetch(op.c, ldsV0, 0, UnitsC());
-    if constexpr (ROWS) fetch(op.a, ldsQ, 0, UnitsA());
+    const uint32_t offset_a = offset_of(UnitsA()), offset_c = offset_of(UnitsC());
+    fetch(op.b, ldsK0, 0, UnitsA(), offset_a);
+    fetch(op.c, ldsV0, 0, UnitsC(), offset_c);
+    if constexpr (ROWS) fetch(op.a, ldsQ, 0, UnitsA(), offset_a);
 
     const double lg = log_decay(g[h]);
     if (tid <= C) powers[tid] = (float)exp(lg * tid);
     const double whole = exp(lg * C);
     const float whole32 = (float)whole, rest = whole > 0 ? (float)((whole - (double)whole32) / whole) : 0.f;
 
-    f32x4_t S[G::CT][ND];
+    // The state before the segment, column 16 wave + m: what there is before the sequence, and the segments' before this one, or
+    // these folded already.
+    f32x4_t S[G::CT];
 #pragma unroll
-    for (int ct = 0; ct < G::CT; ++ct)
-#pragma unroll
-        for (int d = 0; d < ND; ++d) S[ct][d] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int ct = 0; ct < G::CT; ++ct) S[ct] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     if constexpr (ROWS) {
-        const float* x = first ? op.x0 : op.states;
-        if (x) {
-            x += ((first ? w.n : op.back ? w.slot + 1 : w.slot - 1) * H + h) * (int64_t)DA * DC;
+        const int c = 16 * wave + m;
+        const int64_t before = op.back ? w.count - 1 - w.j : w.j;
+        const bool folded = before > 0 && w.count > kOwnFold;
+        if (op.x0 && !folded) {
+            const float* x = op.x0 + (w.n * H + h) * (int64_t)DA * DC;
 #pragma unroll
-            for (int ct = 0; ct < G::CT; ++ct)
+            for (int ct = 0; ct < G::CT; ++ct) {
+                const int r = state_row(ct, 4 * grp);
+                if (op.turned) S[ct] = *reinterpret_cast<const f32x4_t*>(x + (int64_t)c * DA + r);
+                else
 #pragma unroll
-                for (int d = 0; d < ND; ++d) {
-                    const int c = col(m, d), r = 16 * ct + 4 * grp;
-                    if (op.turned) S[ct][d] = *reinterpret_cast<const f32x4_t*>(x + (int64_t)c * DA + r);
-                    else
+                    for (int j = 0; j < 4; ++j) S[ct][j] = x[(r + j) * DC + c];
+            }
+        }
+        const float f = before > 0 ? (float)exp(lg * segs.L) : 0.f;
+        for (int64_t i = folded ? before - 1 : 0; i < before; ++i) {
+            // segments in the order of the recurrence; the first one of it may be the sequence's last, with fewer tokens
+            const float* x = op.states + ((w.slot + (op.back ? before - i : i - before)) * H + h) * (int64_t)DA * DC;
+            const float fi = folded ? 0.f : op.back && i == 0 ? (float)exp(lg * w.tail) : f;
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) S[ct][d][j] = x[(r + j) * DC + c];
+            for (int ct = 0; ct < G::CT; ++ct) {
+                f32x4_t u;
+                if (op.turned) {
+                    const float* from = x + state_at<DC>(c & ~3, state_row(ct, 4 * grp)) + (c & 3);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) u[j] = from[4 * j];
+                } else {
+                    u = *reinterpret_cast<const f32x4_t*>(x + ((wave * G::CT + ct) * 64 + lane) * 4);
                 }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) S[ct][j] = folded ? u[j] : fmaf(fi, S[ct][j], u[j]);
+            }
         }
     }
 
-    // Scores of row 16r + m against token 16i + 4 grp + j, r > i: a^(16(r-i)-4 grp-j) a^m.
     __syncthreads();
     const float sp = op.su * op.so;
-    float into[G::RB], near[4], far[4], row_part = 0.f, step16 = 0.f;
-    if constexpr (ROWS) {
-        row_part = sp * powers[m];
-        step16 = powers[16];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int apart = m - 4 * grp - j;
-            near[j] = apart >= 0 ? sp * powers[apart >= 0 ? apart : 0] : 0.f;
-            far[j] = powers[16 - 4 * grp - j];
-        }
-#pragma unroll
-        for (int r = 0; r < G::RB; ++r) into[r] = op.so * powers[16 * r + m + (op.back ? 0 : 1)];
-    }
     float owed = 0.f;
     Ones ones;
     if (tid < 2 * C) {
@@ -357,59 +392,57 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinOp op0, L
         weights[tid / C][i] = i < n ? op.su * powers[n - 1 - i + (op.back ? 1 : 0)] : 0.f;
     }
 
-    // Fragments: eight contracted values of row (or column) m, in the order in which two 16-row tiles of a product lie in a
-    // lane: group g holds 4g .. +3 and 16 + 4g .. +3 of each 32.  A lane's first place in a tile; the others are it with some
-    // bits of the unit turned over, or whole rows behind it.
+    // Fragments: eight contracted values of row (or column) m.  A lane's first place in a tile; the others are it with some bits
+    // of the unit turned over, or whole rows behind it.
     constexpr int RA = UA * 16, RC = UC * 16;
     int at_row, at_turned, at_col;
     if constexpr (F32) {
-        at_row = place<UA, true>(m, grp);
-        at_turned = place<UA, true>(4 * grp, m >> 2) + 4 * (m & 3);
-        at_col = place<UC, true>(4 * grp, ND == 2 ? 8 * wave + 2 * (m >> 2) : 4 * wave + (m >> 2)) + 4 * (m & 3);
+        at_row = place<UA, true>(m, 2 * grp);
+        at_turned = place<UA, true>(4 * grp, 2 * (m >> 2)) + 4 * (m & 3);
+        at_col = place<UC, true>(4 * grp, 4 * wave + (m >> 2)) + 4 * (m & 3);
     } else {
-        at_row = place<UA, false>(m, grp >> 1) + 8 * (grp & 1);
-        at_turned = place<UA, false>(4 * grp + (m >> 2), m >> 1 & 1) + 8 * (m & 1);
-        at_col = ND == 2 ? place<UC, false>(4 * grp + (m >> 2), 4 * wave + (m & 3))
-                         : place<UC, false>(4 * grp + (m >> 2), 2 * wave + (m >> 1 & 1)) + 8 * (m & 1);
+        at_row = place<UA, false>(m, grp);
+        at_turned = place<UA, false>(4 * grp + (m >> 2), m & 3);
+        at_col = place<UC, false>(4 * grp + (m >> 2), 2 * wave + (m >> 1 & 1)) + 8 * (m & 1);
     }
     // scores, read by row: 32 rows of 32 tokens, and behind them 32 of 64; in fp32 one tile of 32
     int at_score = F32 ? place<8, true>(m, 2 * grp) : place<4, false>(m, grp);
     int at_score2 = F32 ? 0 : 2048 + place<8, false>(m, grp);
+    int at_power = m, at_far = 16 - 4 * grp;  // of the decay's powers
     auto frag = [&](const char* tile, int r, int s) {
         LFrag<F32> f;
         if constexpr (F32) {
             const f32x4_t x = *reinterpret_cast<const f32x4_t*>(tile + (at_row ^ (128 * s)) + 16 * RA * r);
-            const f32x4_t y = *reinterpret_cast<const f32x4_t*>(tile + (at_row ^ (128 * s + 64)) + 16 * RA * r);
+            const f32x4_t y = *reinterpret_cast<const f32x4_t*>(tile + (at_row ^ (128 * s + 16)) + 16 * RA * r);
 #pragma unroll
             for (int j = 0; j < 4; ++j) f.v[j] = x[j], f.v[4 + j] = y[j];
         } else {
-            const bf16x4_t x = *reinterpret_cast<const bf16x4_t*>(tile + (at_row ^ (64 * s)) + 16 * RA * r);
-            const bf16x4_t y = *reinterpret_cast<const bf16x4_t*>(tile + (at_row ^ (64 * s + 32)) + 16 * RA * r);
-            f.v = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+            f.v = *reinterpret_cast<const bf16x8_t*>(tile + (at_row ^ (64 * s)) + 16 * RA * r);
         }
         return f;
     };
-    // columns of a tile over 32 tokens, in the same order
+    // the channels of a tile of the state over 32 tokens: group g holds tokens 4g .. +3 and 16 + 4g .. +3
     auto frag_bt = [&](const char* tile, int ct, int ks) {
         LFrag<F32> f;
         if constexpr (F32) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                f.v[j] = *reinterpret_cast<const float*>(tile + (at_turned ^ (64 * ct + 16 * (j & 3))) + (32 * ks + 16 * (j >> 2) + (j & 3)) * RA);
+                f.v[j] = *reinterpret_cast<const float*>(tile + (at_turned ^ (128 * (ct >> 1) + 16 * ((ct & 1) ^ (j & 3)))) +
+                                                         (32 * ks + 16 * (j >> 2) + (j & 3)) * RA);
         } else {
-            const char* p = tile + (at_turned ^ (32 * ct)) + 32 * ks * RA;
+            const char* p = tile + (at_turned ^ (64 * (ct >> 1))) + 8 * (ct & 1) + 32 * ks * RA;
             f.v = __builtin_shufflevector(read_turned(p), read_turned(p + 16 * RA), 0, 1, 2, 3, 4, 5, 6, 7);
         }
         return f;
     };
-    auto frag_ct = [&](const char* tile, int d, int ks) {
+    auto frag_ct = [&](const char* tile, int ks) {
         LFrag<F32> f;
         if constexpr (F32) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                f.v[j] = *reinterpret_cast<const float*>(tile + (at_col ^ (16 * (d ^ (j & 3)))) + (32 * ks + 16 * (j >> 2) + (j & 3)) * RC);
+                f.v[j] = *reinterpret_cast<const float*>(tile + (at_col ^ (16 * (j & 3))) + (32 * ks + 16 * (j >> 2) + (j & 3)) * RC);
         } else {
-            const char* p = tile + at_col + 8 * d + 32 * ks * RC;
+            const char* p = tile + at_col + 32 * ks * RC;
             f.v = __builtin_shufflevector(read_turned(p), read_turned(p + 16 * RC), 0, 1, 2, 3, 4, 5, 6, 7);
         }
         return f;
@@ -421,21 +454,16 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinOp op0, L
         constexpr bool LAST = decltype(ends)::value;
         const int n = LAST ? tokens - c * C : C;
         // the places of a chunk's fragments are made again from these few: kept, they would take most of the registers
-        __asm__ volatile("" : "+v"(ones.low), "+v"(ones.high), "+v"(at_row), "+v"(at_turned), "+v"(at_col), "+v"(at_score), "+v"(at_score2));
+        __asm__ volatile("" : "+v"(ones.low), "+v"(ones.high), "+v"(at_row), "+v"(at_turned), "+v"(at_col), "+v"(at_score), "+v"(at_score2),
+                         "+v"(at_power), "+v"(at_far));
         // The chunk's rows have come.  Requests end in the order in which they were made, and the last ones are the stores of the
-        // chunk before: they are not waited for (with them the prefill batch takes 140 us, without 85).
-        __builtin_amdgcn_s_waitcnt(waitcnt(ROWS ? G::STORES : 0));
+        // chunk before: they are not waited for.
+        __builtin_amdgcn_s_waitcnt(waitcnt(ROWS ? G::RB : 0));
         __asm__ volatile("s_barrier" ::: "memory");
         if constexpr (!LAST) {
-            fetch(op.b, Kn, c + 1, UnitsA());
-            if constexpr (!ROWS) fetch(op.c, Vn, c + 1, UnitsC());
+            fetch(op.b, Kn, c + 1, UnitsA(), offset_a);
+            if constexpr (!ROWS) fetch(op.c, Vn, c + 1, UnitsC(), offset_c);
         }
-        LFrag<F32> vf[G::KS * ND];
-#pragma unroll
-        for (int ks = 0; ks < G::KS; ++ks)
-#pragma unroll
-            for (int d = 0; d < ND; ++d) vf[ks * ND + d] = frag_ct(V, d, ks);
-
         // The state's decay, in 32 bits: what a power's rounding owes is paid in the next ones, so that thousands of chunks do
         // not add up.
         float dec = powers[n];
@@ -443,55 +471,39 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinOp op0, L
             dec = fmaf(whole32, owed, whole32);
             owed += rest - (whole32 > 0.f ? (dec - whole32) / whole32 : 0.f);
         }
-        int bad[ND];  // a column's first token whose value is not finite
+
+        LFrag<F32> vf[G::KS];
+        int bad = C;  // the column's first token whose value is not finite
         bool marked = false;
         if constexpr (ROWS) {
-            f32x4_t O[G::RB][ND], P[G::RB];
+            // the scores, by the first waves: every SIMD has one of them
+            if (wave < G::RB) {
+                f32x4_t P[G::RB];
 #pragma unroll
-            for (int r = 0; r < G::RB; ++r) {
-                P[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+                for (int r = 0; r < G::RB; ++r) P[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int d = 0; d < ND; ++d) O[r][d] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-            }
-            const int kr = wave < G::RB ? wave : 0;
+                for (int s = 0; s < G::AS; ++s) {
+                    const LFrag<F32> kf = frag(K, wave, s);
 #pragma unroll
-            for (int s = 0; s < G::AS; ++s) {
-                LFrag<F32> qf[G::RB];
-#pragma unroll
-                for (int r = 0; r < G::RB; ++r) qf[r] = frag(ldsQ, r, s);
-                const LFrag<F32> kf = frag(K, kr, s);
-#pragma unroll
-                for (int d = 0; d < ND; ++d) {
-                    LFrag<F32> st[G::PL];
-                    float x[8];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        x[j] = S[2 * s][d][j];
-                        x[4 + j] = S[2 * s + 1][d][j];
-                        S[2 * s][d][j] *= dec;
-                        S[2 * s + 1][d][j] *= dec;
-                    }
-                    split<G::PL>(x, st, ones);
-#pragma unroll
-                    for (int p = 0; p < G::PL; ++p)
-#pragma unroll
-                        for (int r = 0; r < G::RB; ++r) O[r][d] = mma(st[p], qf[r], O[r][d]);
+                    for (int r = 0; r < G::RB; ++r) P[r] = mma(kf, frag(ldsQ, r, s), P[r]);
                 }
+                // Of row 16r + m against token 16i + 4 grp + j with i = wave: a^(16(r-i)-4 grp-j) a^m above the diagonal's tile; in
+                // it a^(m-4 grp-j) and nothing above the diagonal; rows of the products' 32 tokens behind it: zeros.
+                float part = sp * powers[at_power];
+                const float step16 = powers[16];
 #pragma unroll
-                for (int r = 0; r < G::RB; ++r) P[r] = mma(kf, qf[r], P[r]);
-            }
-            // scores of rows 16r + m against tokens 16 wave + 4 grp + j; rows of the products' 32 tokens above the diagonal: zeros
-            float part = row_part;
-#pragma unroll
-            for (int r = 0; r < G::RB; ++r) {
-                if (wave <= (r | 1)) {
+                for (int r = 0; r < G::RB; ++r) {
+                    if (wave > (r | 1)) continue;
                     float x[4];
                     if (wave == r) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) x[j] = m >= 4 * grp + j ? P[r][j] * near[j] : 0.f;
+                        for (int j = 0; j < 4; ++j) {
+                            const int apart = at_power - 16 + at_far - j;
+                            x[j] = apart >= 0 ? P[r][j] * (sp * powers[apart >= 0 ? apart : 0]) : 0.f;
+                        }
                     } else if (wave < r) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) x[j] = P[r][j] * (far[j] * part);
+                        for (int j = 0; j < 4; ++j) x[j] = P[r][j] * (powers[at_far - j] * part);
                         part *= step16;
                     } else {
 #pragma unroll
@@ -508,127 +520,136 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinOp op0, L
                                        pack2(less_low(x[2], h1, ones), less_high(x[3], h1, ones)));
                     }
                 }
-#pragma unroll
-                for (int d = 0; d < ND; ++d)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) O[r][d][j] *= into[r];
             }
+            __builtin_amdgcn_sched_barrier(0);
+            f32x4_t O[G::RB];
+#pragma unroll
+            for (int r = 0; r < G::RB; ++r) O[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < G::AS; ++s) {
+                LFrag<F32> qf[G::RB], st[G::PL];
+#pragma unroll
+                for (int r = 0; r < G::RB; ++r) qf[r] = frag(ldsQ, r, s);
+                float x[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[j] = S[2 * s][j];
+                    x[4 + j] = S[2 * s + 1][j];
+                    S[2 * s][j] *= dec;
+                    S[2 * s + 1][j] *= dec;
+                }
+                split<G::PL>(x, st, ones);
+#pragma unroll
+                for (int p = 0; p < G::PL; ++p)
+#pragma unroll
+                    for (int r = 0; r < G::RB; ++r) O[r] = mma(st[p], qf[r], O[r]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int ks = 0; ks < G::KS; ++ks) vf[ks] = frag_ct(V, ks);
+#pragma unroll
+            for (int r = 0; r < G::RB; ++r)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) O[r][j] *= op.so * powers[16 * r + at_power + (op.back ? 0 : 1)];
             lds_barrier();
             if constexpr (!LAST) {
-                fetch(op.a, ldsQ, c + 1, UnitsA());
-                fetch(op.c, Vn, c + 1, UnitsC());
+                fetch(op.a, ldsQ, c + 1, UnitsA(), offset_a);
+                fetch(op.c, Vn, c + 1, UnitsC(), offset_c);
             }
 
             // A value that is not finite must not meet the zeros of earlier rows: such values are left out of the products, and
             // their column is made NaN from their token on, here and in the state.
-            marked = __ballot(any_not_finite<G::KS * ND>(vf)) != 0;
+            marked = __ballot(any_not_finite<G::KS>(vf)) != 0;
             if (marked) {
 #pragma unroll
-                for (int d = 0; d < ND; ++d) {
-                    bad[d] = C;
+                for (int ks = G::KS - 1; ks >= 0; --ks)
 #pragma unroll
-                    for (int ks = G::KS - 1; ks >= 0; --ks)
-#pragma unroll
-                        for (int j = 7; j >= 0; --j)
-                            if (!(fabsf((float)vf[ks * ND + d].v[j]) < __builtin_inff())) {
-                                bad[d] = 32 * ks + 16 * (j >> 2) + 4 * grp + (j & 3);
-                                vf[ks * ND + d].v[j] = 0.f;
-                            }
-                    bad[d] = min(bad[d], __shfl_xor(bad[d], 16));
-                    bad[d] = min(bad[d], __shfl_xor(bad[d], 32));
-                }
+                    for (int j = 7; j >= 0; --j)
+                        if (!(fabsf((float)vf[ks].v[j]) < __builtin_inff())) {
+                            bad = 32 * ks + 16 * (j >> 2) + 4 * grp + (j & 3);
+                            vf[ks].v[j] = 0.f;
+                        }
+                bad = min(bad, __shfl_xor(bad, 16));
+                bad = min(bad, __shfl_xor(bad, 32));
             }
 #pragma unroll
-            for (int r = 0; r < G::RB; ++r)
+            for (int ks = 0; ks < G::KS; ++ks)
 #pragma unroll
-                for (int ks = 0; ks <= r / 2; ++ks)
+                for (int p = 0; p < G::PL; ++p)
 #pragma unroll
-                    for (int p = 0; p < G::PL; ++p) {
-                        LFrag<F32> pf;
+                    for (int r = 2 * ks; r < G::RB; ++r) {
+                        LFrag<F32> f;
                         if constexpr (F32) {
                             const f32x4_t x = *reinterpret_cast<const f32x4_t*>(ldsP + at_score + 2048 * r);
                             const f32x4_t y = *reinterpret_cast<const f32x4_t*>(ldsP + (at_score ^ 16) + 2048 * r);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) pf.v[j] = x[j], pf.v[4 + j] = y[j];
+                            for (int j = 0; j < 4; ++j) f.v[j] = x[j], f.v[4 + j] = y[j];
                         } else {
-                            pf.v = *reinterpret_cast<const bf16x8_t*>(
+                            f.v = *reinterpret_cast<const bf16x8_t*>(
                                 ldsP + p * G::PB + (r < 2 ? at_score + 1024 * r : (at_score2 ^ (64 * ks)) + 2048 * (r - 2)));
                         }
-#pragma unroll
-                        for (int d = 0; d < ND; ++d) O[r][d] = mma(vf[ks * ND + d], pf, O[r][d]);
+                        O[r] = mma(vf[ks], f, O[r]);
                     }
             if (marked) {
 #pragma unroll
-                for (int d = 0; d < ND; ++d)
+                for (int j = 0; j < 4; ++j) {
+                    const int from = __shfl(bad, 4 * grp + j);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int from = __shfl(bad[d], 4 * grp + j);
-#pragma unroll
-                        for (int r = 0; r < G::RB; ++r)
-                            if (16 * r + m >= from) O[r][d][j] = __builtin_nanf("");
-                    }
+                    for (int r = 0; r < G::RB; ++r)
+                        if (16 * r + m >= from) O[r][j] = __builtin_nanf("");
+                }
             }
             // a lane's first row of the chunk; the others are 16 rows apart
             char* to = static_cast<char*>(op.out) + ((row0 + (op.back ? -c * C : c * C)) * H + h) * (int64_t)(DC * G::ES);
-            const int pitch = (op.back ? -H : H) * DC * G::ES, mine = m * pitch + col(4 * grp, 0) * G::ES;
-            auto put = [&](int r) {
-                char* p = to + (int64_t)(16 * r * pitch) + mine;
-                if constexpr (F32) {
-#pragma unroll
-                    for (int d = 0; d < ND; ++d) *reinterpret_cast<f32x4_t*>(p + 16 * d) = O[r][d];
-                } else if constexpr (ND == 2) {
-                    *reinterpret_cast<uint4*>(p) = make_uint4(pack2(O[r][0][0], O[r][0][1]), pack2(O[r][0][2], O[r][0][3]),
-                                                              pack2(O[r][1][0], O[r][1][1]), pack2(O[r][1][2], O[r][1][3]));
-                } else {
-                    *reinterpret_cast<uint2*>(p) = make_uint2(pack2(O[r][0][0], O[r][0][1]), pack2(O[r][0][2], O[r][0][3]));
-                }
-            };
+            const int pitch = (op.back ? -H : H) * DC * G::ES, mine = m * pitch + (16 * wave + 4 * grp) * G::ES;
             __asm__ volatile("" ::: "memory");  // behind the chunk's loads, all of them
 #pragma unroll
             for (int r = 0; r < G::RB; ++r)
-                if (!LAST || 16 * r + m < n) put(r);
+                if (!LAST || 16 * r + m < n) {
+                    char* p = to + (int64_t)(16 * r * pitch) + mine;
+                    if constexpr (F32) *reinterpret_cast<f32x4_t*>(p) = O[r];
+                    else *reinterpret_cast<uint2*>(p) = make_uint2(pack2(O[r][0], O[r][1]), pack2(O[r][2], O[r][3]));
+                }
             __asm__ volatile("" ::: "memory");
-        }
-
-        if constexpr (!ROWS)
+        } else {
+#pragma unroll
+            for (int ks = 0; ks < G::KS; ++ks) vf[ks] = frag_ct(V, ks);
 #pragma unroll
             for (int ct = 0; ct < G::CT; ++ct)
 #pragma unroll
-                for (int d = 0; d < ND; ++d)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) S[ct][d][j] *= dec;
+                for (int j = 0; j < 4; ++j) S[ct][j] *= dec;
+        }
+
         // the weighted values as sums of three bf16 values, which hold all of their 24 bits
 #pragma unroll
         for (int ks = 0; ks < G::KS; ++ks) {
-            const f32x4_t w0 = *reinterpret_cast<const f32x4_t*>(weights[n < C] + 32 * ks + 4 * grp);
-            const f32x4_t w1 = *reinterpret_cast<const f32x4_t*>(weights[n < C] + 32 * ks + 16 + 4 * grp);
-            LFrag<F32> vb[ND][G::VL];
+            __builtin_amdgcn_sched_barrier(0);  // what is read ahead stays within the registers
+            const f32x4_t w0 = *reinterpret_cast<const f32x4_t*>(weights[LAST] + 32 * ks + 4 * grp);
+            const f32x4_t w1 = *reinterpret_cast<const f32x4_t*>(weights[LAST] + 32 * ks + 16 + 4 * grp);
+            LFrag<F32> vb[G::VL], kt[4];
 #pragma unroll
-            for (int d = 0; d < ND; ++d) {
-                float x[8];
-                values(vf[ks * ND + d], x);
+            for (int ct = 0; ct < 4; ++ct) kt[ct] = frag_bt(K, ct, ks);
+            float x[8];
+            values(vf[ks], x);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) x[j] *= w0[j], x[4 + j] *= w1[j];
-                split<G::VL>(x, vb[d], ones);
-            }
+            for (int j = 0; j < 4; ++j) x[j] *= w0[j], x[4 + j] *= w1[j];
+            split<G::VL>(x, vb, ones);
 #pragma unroll
-            for (int ct = 0; ct < G::CT; ++ct) {
-                const LFrag<F32> kt = frag_bt(K, ct, ks);
+            for (int four = 0; four < G::CT; four += 4) {
+                if (four > 0)
 #pragma unroll
-                for (int d = 0; d < ND; ++d)
+                    for (int ct = 0; ct < 4; ++ct) kt[ct] = frag_bt(K, four + ct, ks);
 #pragma unroll
-                    for (int p = 0; p < G::VL; ++p) S[ct][d] = mma(kt, vb[d][p], S[ct][d]);
+                for (int p = 0; p < G::VL; ++p)
+#pragma unroll
+                    for (int ct = 0; ct < 4; ++ct) S[four + ct] = mma(kt[ct], vb[p], S[four + ct]);
             }
         }
-        if (ROWS && marked) {
+        if (ROWS && marked && bad < n)
 #pragma unroll
-            for (int d = 0; d < ND; ++d)
-                if (bad[d] < n)
+            for (int ct = 0; ct < G::CT; ++ct)
 #pragma unroll
-                    for (int ct = 0; ct < G::CT; ++ct)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) S[ct][d][j] = __builtin_nanf("");
-        }
+                for (int j = 0; j < 4; ++j) S[ct][j] = __builtin_nanf("");
     };
 
     char* const ldsVn = ROWS ? ldsV0 : ldsV1;
@@ -642,42 +663,45 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinOp op0, L
     }
     chunk(c, c % 2 ? ldsK1 : ldsK0, nullptr, c % 2 ? ldsVn : ldsV0, nullptr, std::true_type());
 
-    float* to = nullptr;
     if constexpr (ROWS) {
-        if (last && op.fin) to = op.fin + (w.n * H + h) * (int64_t)DA * DC;
+        if (last && op.fin) {
+            float* to = op.fin + (w.n * H + h) * (int64_t)DA * DC;
+#pragma unroll
+            for (int ct = 0; ct < G::CT; ++ct)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) to[state_row(ct, 4 * grp + j) * DC + 16 * wave + m] = S[ct][j];
+        }
     } else {
-        to = static_cast<float*>(op.out) + (w.slot * H + h) * (int64_t)DA * DC;
-    }
-    if (to) {
+        float* to = static_cast<float*>(op.out) + (w.slot * H + h) * (int64_t)DA * DC;
 #pragma unroll
-        for (int ct = 0; ct < G::CT; ++ct)
-#pragma unroll
-            for (int d = 0; d < ND; ++d)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) to[(16 * ct + 4 * grp + j) * DC + col(m, d)] = S[ct][d][j];
+        for (int ct = 0; ct < G::CT; ++ct) *reinterpret_cast<f32x4_t*>(to + ((wave * G::CT + ct) * 64 + lane) * 4) = S[ct];
     }
 }
 
-// The states behind (with `back` before) each segment from the segments' own ones, in place: X_j = a^length X_(j-1) + U_j.
-// A thread holds four values of a head's state through all segments.
+// The states behind (with `back` before) each segment from the segments' own ones, in place, for sequences of many segments:
+// X_j = a^length X_(j-1) + U_j.  A thread holds four values of a head's state through all segments.
 struct FoldOp {
     float* states;
     const float* x0;
     bool back;
 };
-__global__ __launch_bounds__(kThreads) void linattn_fold_kernel(FoldOp op0, FoldOp op1, Segs segs, const float* g, int size) {
+template <int DA>
+__global__ __launch_bounds__(kThreads) void linattn_fold_kernel(FoldOp op0, FoldOp op1, Segs segs, const float* g, int DC) {
     const FoldOp op = blockIdx.y ? op1 : op0;
-    const int per = size / (4 * kThreads);
+    const int size = DA * DC, per = size / (4 * kThreads);
     const int64_t nh = blockIdx.x / per, n = nh / segs.H;
-    const int h = nh % segs.H, at = (blockIdx.x % per) * 4 * kThreads + 4 * threadIdx.x;
+    const int h = nh % segs.H, at = (int)(blockIdx.x % per) * 4 * kThreads + 4 * threadIdx.x;
     const int64_t slot0 = segs.cu ? seq_begin(segs, n) / segs.L + n : n * segs.per_seq;
     const Where w = where_of(segs, slot0);
-    if (w.n != n || w.count < 2) return;
-    const int64_t length = segs.cu ? seq_begin(segs, n + 1) - seq_begin(segs, n) : segs.T_fixed;
+    if (w.n != n || w.count <= kOwnFold) return;
     const double lg = log_decay(g[h]);
-    const float whole = (float)exp(lg * segs.L), tail = (float)exp(lg * (length - (w.count - 1) * segs.L));
+    const float whole = (float)exp(lg * segs.L), tail = (float)exp(lg * w.tail);
     f32x4_t x = {0.f, 0.f, 0.f, 0.f};
-    if (op.x0) x = *reinterpret_cast<const f32x4_t*>(op.x0 + nh * size + at);
+    if (op.x0) {
+        const int lane = at / 4 % 64, ct = at / 256 % (DA / 16), c = at / (256 * (DA / 16)) * 16 + lane % 16;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = op.x0[nh * size + state_row(ct, lane / 16 * 4 + j) * DC + c];
+    }
     const int64_t step = (int64_t)segs.H * size;
     f32x4_t* p = reinterpret_cast<f32x4_t*>(op.states + (slot0 * segs.H + h) * (int64_t)size + at);
     constexpr int AHEAD = 8;
@@ -748,11 +772,12 @@ __global__ __launch_bounds__(256) void linattn_step_kernel(const void* q, const 
 
 // ------------------------------------------------------------------------------------------------ launches
 
-// Tokens of a segment.  Two workgroups fit on a CU: with 512 segments every place has one.  A segment's state is written,
-// folded and read, four times its size, which 256 tokens outweigh.
+// Tokens of a segment.  Two workgroups fit on a CU: with 512 segments every place has one.  A segment's state is written and
+// read, several times its size, which 256 tokens outweigh; fewer only where every CU has no segment otherwise.
 int64_t segment_tokens(int64_t total, int H) {
-    const int64_t even = (total * H + 511) / 512, up = (even + 63) / 64 * 64;
-    return up < 256 ? 256 : up;
+    auto whole = [](int64_t x) { return (x + 63) / 64 * 64; };
+    const int64_t two = whole((total * H + 511) / 512), one = whole((total * H + 255) / 256);
+    return two > 256 ? two : one < 64 ? 64 : one < 256 ? one : 256;
 }
 
 Segs segs_of(const LinArgs& a) {
@@ -776,7 +801,7 @@ void chunks(const LinArgs& a, const Segs& s, std::initializer_list<LinOp> ops, i
     for (const LinOp& o : ops) op[count++] = o;
     const int64_t each = (slots_of(s) * a.H + 7) / 8 * 8;  // workgroups behind the last segment find none
     auto run = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, dim3((unsigned)(each * count)), dim3(kThreads), 0, st, op[0], op[1], op[2], count, s, a.g);
+        hipLaunchKernelGGL(kernel, dim3((unsigned)(each * count)), dim3(4 * DC), 0, st, op[0], op[1], op[2], count, s, a.g);
     };
     auto types = [&](auto da, auto dc) {
         constexpr int A = decltype(da)::value, B = decltype(dc)::value;
@@ -787,9 +812,10 @@ void chunks(const LinArgs& a, const Segs& s, std::initializer_list<LinOp> ops, i
 }
 
 void fold(const LinArgs& a, const Segs& s, FoldOp one, const FoldOp* two, hipStream_t st) {
-    const int size = a.Dk * a.Dv;
-    hipLaunchKernelGGL(linattn_fold_kernel, dim3((unsigned)(a.N * a.H * (size / (4 * kThreads))), two ? 2 : 1), dim3(kThreads), 0,
-                       st, one, two ? *two : one, s, a.g, size);
+    if ((s.cu ? (s.total + s.L - 1) / s.L : s.per_seq) <= kOwnFold) return;
+    const dim3 grid((unsigned)(a.N * a.H * (a.Dk * a.Dv / (4 * kThreads))), two ? 2 : 1);
+    auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, st, one, two ? *two : one, s, a.g, a.Dv); };
+    a.Dk == 64 ? run(linattn_fold_kernel<64>) : run(linattn_fold_kernel<128>);
 }
 
 }  // namespace
