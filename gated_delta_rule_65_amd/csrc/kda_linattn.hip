@@ -241,7 +241,9 @@ __device__ __forceinline__ void load_to_lds(const void* from, char* to) {
 
 template <int DA, int DC, bool F32>
 struct LinTile {
-    static constexpr int WAVES = DC / 16, THREADS = 64 * WAVES;  // a wave for 16 columns; two workgroups on a CU
+    // A wave for 32 columns in 16 bits: what all waves read of `a` and `b` is read half as often as with 16 (prefill batch 137
+    // against 147 us).  In fp32 products take most of the time, and 16 columns give twice the waves.
+    static constexpr int ND = !F32 && DC == 128 ? 2 : 1, WAVES = DC / 16 / ND, THREADS = 64 * WAVES;
     static constexpr int C = F32 ? 32 : 64;      // tokens of a chunk
     static constexpr int ES = F32 ? 4 : 2;
     static constexpr int UA = DA * ES / 16, UC = DC * ES / 16;  // units of a row
@@ -255,8 +257,13 @@ struct LinTile {
 // The state's rows are dealt over tiles of 16 so that a lane's rows of two tiles' products are eight side by side: what the next
 // product contracts lies in a row of `a` as it is.  Row i of tile ct:
 __host__ __device__ constexpr int state_row(int ct, int i) { return 32 * (ct >> 1) + 8 * (i >> 2) + 4 * (ct & 1) + (i & 3); }
-// Segments' states lie as the lanes hold them: the place of four rows from `row` on (a multiple of 4) in column c of a state of
-// DA rows.
+// A wave's columns likewise, for what is stored in a row of the outputs: column i of its tile d.
+template <int ND>
+__host__ __device__ constexpr int state_col(int wave, int i, int d) {
+    return ND == 2 ? 32 * wave + 8 * (i >> 2) + 4 * d + (i & 3) : 16 * wave + i;
+}
+// Segments' states lie as tiles of 16 rows and 16 columns, in a tile as lanes hold a product: 64 times four rows.  The place of
+// four rows from `row` on (a multiple of 4) in column c of a state of DA rows; column tiles go by columns / 16.
 template <int DA>
 __device__ __forceinline__ int state_at(int row, int c) {
     const int ct = 2 * (row >> 5) + (row >> 2 & 1), grp = row >> 3 & 3;
@@ -267,12 +274,16 @@ __device__ __forceinline__ int state_at(int row, int c) {
 // of 64 KB make dearer than a kernel for it beyond.
 constexpr int kOwnFold = 8;
 
-// A workgroup's way through its segment: a wave for 16 columns, with all rows of the state for them.
+template <int DC, bool F32>
+constexpr int kLinThreads = !F32 && DC == 128 ? 256 : 4 * DC;
+
+// A workgroup's way through its segment: a wave has all rows of the state for its columns.  Two workgroups on a CU.
 template <int DA, int DC, bool F32, bool ROWS>
-__global__ __launch_bounds__(4 * DC, DC / 32) void linattn_chunk_kernel(
+__global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128)) void linattn_chunk_kernel(
     LinOp op0, LinOp op1, LinOp op2, int ops, Segs segs, const float* g) {
     using G = LinTile<DA, DC, F32>;
-    constexpr int C = G::C, UA = G::UA, UC = G::UC, THREADS = G::THREADS;
+    constexpr int C = G::C, ND = G::ND, UA = G::UA, UC = G::UC, THREADS = G::THREADS;
+    static_assert(THREADS == kLinThreads<DC, F32>, "the launch's");
     __shared__ __align__(16) char ldsK0[G::KB], ldsK1[G::KB];
     __shared__ __align__(16) char ldsV0[G::VB], ldsV1[ROWS ? 16 : G::VB];
     __shared__ __align__(16) char ldsQ[ROWS ? G::KB : 16], ldsP[ROWS ? G::PL * G::PB : 16];
@@ -342,25 +353,27 @@ __global__ __launch_bounds__(4 * DC, DC / 32) void linattn_chunk_kernel(
     const double whole = exp(lg * C);
     const float whole32 = (float)whole, rest = whole > 0 ? (float)((whole - (double)whole32) / whole) : 0.f;
 
-    // The state before the segment, column 16 wave + m: what there is before the sequence, and the segments' before this one, or
-    // these folded already.
-    f32x4_t S[G::CT];
+    // The state before the segment: what there is before the sequence, and the segments' before this one, or these folded already.
+    f32x4_t S[G::CT][ND];
 #pragma unroll
-    for (int ct = 0; ct < G::CT; ++ct) S[ct] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int ct = 0; ct < G::CT; ++ct)
+#pragma unroll
+        for (int d = 0; d < ND; ++d) S[ct][d] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     if constexpr (ROWS) {
-        const int c = 16 * wave + m;
         const int64_t before = op.back ? w.count - 1 - w.j : w.j;
         const bool folded = before > 0 && w.count > kOwnFold;
         if (op.x0 && !folded) {
             const float* x = op.x0 + (w.n * H + h) * (int64_t)DA * DC;
 #pragma unroll
-            for (int ct = 0; ct < G::CT; ++ct) {
-                const int r = state_row(ct, 4 * grp);
-                if (op.turned) S[ct] = *reinterpret_cast<const f32x4_t*>(x + (int64_t)c * DA + r);
-                else
+            for (int ct = 0; ct < G::CT; ++ct)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) S[ct][j] = x[(r + j) * DC + c];
-            }
+                for (int d = 0; d < ND; ++d) {
+                    const int r = state_row(ct, 4 * grp), c = state_col<ND>(wave, m, d);
+                    if (op.turned) S[ct][d] = *reinterpret_cast<const f32x4_t*>(x + (int64_t)c * DA + r);
+                    else
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) S[ct][d][j] = x[(r + j) * DC + c];
+                }
         }
         const float f = before > 0 ? (float)exp(lg * segs.L) : 0.f;
         for (int64_t i = folded ? before - 1 : 0; i < before; ++i) {
@@ -368,18 +381,21 @@ __global__ __launch_bounds__(4 * DC, DC / 32) void linattn_chunk_kernel(
             const float* x = op.states + ((w.slot + (op.back ? before - i : i - before)) * H + h) * (int64_t)DA * DC;
             const float fi = folded ? 0.f : op.back && i == 0 ? (float)exp(lg * w.tail) : f;
 #pragma unroll
-            for (int ct = 0; ct < G::CT; ++ct) {
-                f32x4_t u;
-                if (op.turned) {
-                    const float* from = x + state_at<DC>(c & ~3, state_row(ct, 4 * grp)) + (c & 3);
+            for (int ct = 0; ct < G::CT; ++ct)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) u[j] = from[4 * j];
-                } else {
-                    u = *reinterpret_cast<const f32x4_t*>(x + ((wave * G::CT + ct) * 64 + lane) * 4);
+                for (int d = 0; d < ND; ++d) {
+                    const int r = state_row(ct, 4 * grp), c = state_col<ND>(wave, m, d);
+                    f32x4_t u;
+                    if (op.turned) {
+                        const float* from = x + state_at<DC>(c & ~3, r) + (c & 3);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) u[j] = from[4 * j];
+                    } else {
+                        u = *reinterpret_cast<const f32x4_t*>(x + state_at<DA>(r, c));
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) S[ct][d][j] = folded ? u[j] : fmaf(fi, S[ct][d][j], u[j]);
                 }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) S[ct][j] = folded ? u[j] : fmaf(fi, S[ct][j], u[j]);
-            }
         }
     }
 
@@ -400,10 +416,12 @@ __global__ __launch_bounds__(4 * DC, DC / 32) void linattn_chunk_kernel(
         at_row = place<UA, true>(m, 2 * grp);
         at_turned = place<UA, true>(4 * grp, 2 * (m >> 2)) + 4 * (m & 3);
         at_col = place<UC, true>(4 * grp, 4 * wave + (m >> 2)) + 4 * (m & 3);
+        static_assert(!F32 || ND == 1, "a lane's column");
     } else {
         at_row = place<UA, false>(m, grp);
         at_turned = place<UA, false>(4 * grp + (m >> 2), m & 3);
-        at_col = place<UC, false>(4 * grp + (m >> 2), 2 * wave + (m >> 1 & 1)) + 8 * (m & 1);
+        at_col = ND == 2 ? place<UC, false>(4 * grp + (m >> 2), 4 * wave + (m & 3))
+                         : place<UC, false>(4 * grp + (m >> 2), 2 * wave + (m >> 1 & 1)) + 8 * (m & 1);
     }
     // scores, read by row: 32 rows of 32 tokens, and behind them 32 of 64; in fp32 one tile of 32
     int at_score = F32 ? place<8, true>(m, 2 * grp) : place<4, false>(m, grp);
@@ -435,14 +453,14 @@ __global__ __launch_bounds__(4 * DC, DC / 32) void linattn_chunk_kernel(
         }
         return f;
     };
-    auto frag_ct = [&](const char* tile, int ks) {
+    auto frag_ct = [&](const char* tile, int d, int ks) {
         LFrag<F32> f;
         if constexpr (F32) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 f.v[j] = *reinterpret_cast<const float*>(tile + (at_col ^ (16 * (j & 3))) + (32 * ks + 16 * (j >> 2) + (j & 3)) * RC);
         } else {
-            const char* p = tile + at_col + 32 * ks * RC;
+            const char* p = tile + at_col + 8 * d + 32 * ks * RC;
             f.v = __builtin_shufflevector(read_turned(p), read_turned(p + 16 * RC), 0, 1, 2, 3, 4, 5, 6, 7);
         }
         return f;
@@ -472,21 +490,20 @@ __global__ __launch_bounds__(4 * DC, DC / 32) void linattn_chunk_kernel(
             owed += rest - (whole32 > 0.f ? (dec - whole32) / whole32 : 0.f);
         }
 
-        LFrag<F32> vf[G::KS];
-        int bad = C;  // the column's first token whose value is not finite
+        LFrag<F32> vf[G::KS * ND];
+        auto read_values = [&]() {
+#pragma unroll
+            for (int ks = 0; ks < G::KS; ++ks)
+#pragma unroll
+                for (int d = 0; d < ND; ++d) vf[ks * ND + d] = frag_ct(V, d, ks);
+        };
+        int bad[ND];  // a column's first token whose value is not finite
         bool marked = false;
         if constexpr (ROWS) {
-            // the scores, by the first waves: every SIMD has one of them
-            if (wave < G::RB) {
-                f32x4_t P[G::RB];
-#pragma unroll
-                for (int r = 0; r < G::RB; ++r) P[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int s = 0; s < G::AS; ++s) {
-                    const LFrag<F32> kf = frag(K, wave, s);
-#pragma unroll
-                    for (int r = 0; r < G::RB; ++r) P[r] = mma(kf, frag(ldsQ, r, s), P[r]);
-                }
+            // The scores are the first waves' (every SIMD has one of them), with the products of the state where all waves are.
+            constexpr bool TOGETHER = G::WAVES == G::RB;
+            f32x4_t O[G::RB][ND], P[G::RB];
+            auto scores = [&]() {
                 // Of row 16r + m against token 16i + 4 grp + j with i = wave: a^(16(r-i)-4 grp-j) a^m above the diagonal's tile; in
                 // it a^(m-4 grp-j) and nothing above the diagonal; rows of the products' 32 tokens behind it: zeros.
                 float part = sp * powers[at_power];
@@ -520,65 +537,73 @@ __global__ __launch_bounds__(4 * DC, DC / 32) void linattn_chunk_kernel(
                                        pack2(less_low(x[2], h1, ones), less_high(x[3], h1, ones)));
                     }
                 }
-            }
-            __builtin_amdgcn_sched_barrier(0);
-            f32x4_t O[G::RB];
+            };
 #pragma unroll
-            for (int r = 0; r < G::RB; ++r) O[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            for (int r = 0; r < G::RB; ++r) {
+                P[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int d = 0; d < ND; ++d) O[r][d] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            }
+            if (!TOGETHER && wave < G::RB) {
+#pragma unroll
+                for (int s = 0; s < G::AS; ++s) {
+                    const LFrag<F32> kf = frag(K, wave, s);
+#pragma unroll
+                    for (int r = 0; r < G::RB; ++r) P[r] = mma(kf, frag(ldsQ, r, s), P[r]);
+                }
+                scores();
+            }
 #pragma unroll
             for (int s = 0; s < G::AS; ++s) {
-                LFrag<F32> qf[G::RB], st[G::PL];
+                LFrag<F32> qf[G::RB], kf;
 #pragma unroll
                 for (int r = 0; r < G::RB; ++r) qf[r] = frag(ldsQ, r, s);
-                float x[8];
+                if constexpr (TOGETHER) kf = frag(K, wave, s);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    x[j] = S[2 * s][j];
-                    x[4 + j] = S[2 * s + 1][j];
-                    S[2 * s][j] *= dec;
-                    S[2 * s + 1][j] *= dec;
+                for (int d = 0; d < ND; ++d) {
+                    LFrag<F32> st[G::PL];
+                    float x[8];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        x[j] = S[2 * s][d][j];
+                        x[4 + j] = S[2 * s + 1][d][j];
+                        S[2 * s][d][j] *= dec;
+                        S[2 * s + 1][d][j] *= dec;
+                    }
+                    split<G::PL>(x, st, ones);
+#pragma unroll
+                    for (int p = 0; p < G::PL; ++p)
+#pragma unroll
+                        for (int r = 0; r < G::RB; ++r) O[r][d] = mma(st[p], qf[r], O[r][d]);
                 }
-                split<G::PL>(x, st, ones);
+                if constexpr (TOGETHER)
 #pragma unroll
-                for (int p = 0; p < G::PL; ++p)
-#pragma unroll
-                    for (int r = 0; r < G::RB; ++r) O[r] = mma(st[p], qf[r], O[r]);
-                __builtin_amdgcn_sched_barrier(0);
+                    for (int r = 0; r < G::RB; ++r) P[r] = mma(kf, qf[r], P[r]);
             }
+            read_values();
+            if constexpr (TOGETHER) scores();
 #pragma unroll
-            for (int ks = 0; ks < G::KS; ++ks) vf[ks] = frag_ct(V, ks);
+            for (int r = 0; r < G::RB; ++r) {
+                const float into = op.so * powers[16 * r + at_power + (op.back ? 0 : 1)];
 #pragma unroll
-            for (int r = 0; r < G::RB; ++r)
+                for (int d = 0; d < ND; ++d)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) O[r][j] *= op.so * powers[16 * r + at_power + (op.back ? 0 : 1)];
+                    for (int j = 0; j < 4; ++j) O[r][d][j] *= into;
+            }
             lds_barrier();
             if constexpr (!LAST) {
                 fetch(op.a, ldsQ, c + 1, UnitsA(), offset_a);
                 fetch(op.c, Vn, c + 1, UnitsC(), offset_c);
             }
 
-            // A value that is not finite must not meet the zeros of earlier rows: such values are left out of the products, and
-            // their column is made NaN from their token on, here and in the state.
-            marked = __ballot(any_not_finite<G::KS>(vf)) != 0;
-            if (marked) {
-#pragma unroll
-                for (int ks = G::KS - 1; ks >= 0; --ks)
-#pragma unroll
-                    for (int j = 7; j >= 0; --j)
-                        if (!(fabsf((float)vf[ks].v[j]) < __builtin_inff())) {
-                            bad = 32 * ks + 16 * (j >> 2) + 4 * grp + (j & 3);
-                            vf[ks].v[j] = 0.f;
-                        }
-                bad = min(bad, __shfl_xor(bad, 16));
-                bad = min(bad, __shfl_xor(bad, 32));
-            }
+            LFrag<F32> pf[G::KS][G::PL][G::RB];
 #pragma unroll
             for (int ks = 0; ks < G::KS; ++ks)
 #pragma unroll
                 for (int p = 0; p < G::PL; ++p)
 #pragma unroll
                     for (int r = 2 * ks; r < G::RB; ++r) {
-                        LFrag<F32> f;
+                        LFrag<F32>& f = pf[ks][p][r];
                         if constexpr (F32) {
                             const f32x4_t x = *reinterpret_cast<const f32x4_t*>(ldsP + at_score + 2048 * r);
                             const f32x4_t y = *reinterpret_cast<const f32x4_t*>(ldsP + (at_score ^ 16) + 2048 * r);
@@ -588,52 +613,86 @@ __global__ __launch_bounds__(4 * DC, DC / 32) void linattn_chunk_kernel(
                             f.v = *reinterpret_cast<const bf16x8_t*>(
                                 ldsP + p * G::PB + (r < 2 ? at_score + 1024 * r : (at_score2 ^ (64 * ks)) + 2048 * (r - 2)));
                         }
-                        O[r] = mma(vf[ks], f, O[r]);
                     }
+            // A value that is not finite must not meet the zeros of earlier rows: such values are left out of the products, and
+            // their column is made NaN from their token on, here and in the state.
+            marked = __ballot(any_not_finite<G::KS * ND>(vf)) != 0;
             if (marked) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int from = __shfl(bad, 4 * grp + j);
+                for (int d = 0; d < ND; ++d) {
+                    bad[d] = C;
 #pragma unroll
-                    for (int r = 0; r < G::RB; ++r)
-                        if (16 * r + m >= from) O[r][j] = __builtin_nanf("");
+                    for (int ks = G::KS - 1; ks >= 0; --ks)
+#pragma unroll
+                        for (int j = 7; j >= 0; --j)
+                            if (!(fabsf((float)vf[ks * ND + d].v[j]) < __builtin_inff())) {
+                                bad[d] = 32 * ks + 16 * (j >> 2) + 4 * grp + (j & 3);
+                                vf[ks * ND + d].v[j] = 0.f;
+                            }
+                    bad[d] = min(bad[d], __shfl_xor(bad[d], 16));
+                    bad[d] = min(bad[d], __shfl_xor(bad[d], 32));
                 }
+            }
+#pragma unroll
+            for (int ks = 0; ks < G::KS; ++ks)
+#pragma unroll
+                for (int p = 0; p < G::PL; ++p)
+#pragma unroll
+                    for (int d = 0; d < ND; ++d)
+#pragma unroll
+                        for (int r = 2 * ks; r < G::RB; ++r) O[r][d] = mma(vf[ks * ND + d], pf[ks][p][r], O[r][d]);
+            if (marked) {
+#pragma unroll
+                for (int d = 0; d < ND; ++d)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int from = __shfl(bad[d], 4 * grp + j);
+#pragma unroll
+                        for (int r = 0; r < G::RB; ++r)
+                            if (16 * r + m >= from) O[r][d][j] = __builtin_nanf("");
+                    }
             }
             // a lane's first row of the chunk; the others are 16 rows apart
             char* to = static_cast<char*>(op.out) + ((row0 + (op.back ? -c * C : c * C)) * H + h) * (int64_t)(DC * G::ES);
-            const int pitch = (op.back ? -H : H) * DC * G::ES, mine = m * pitch + (16 * wave + 4 * grp) * G::ES;
+            const int pitch = (op.back ? -H : H) * DC * G::ES, mine = m * pitch + state_col<ND>(wave, 4 * grp, 0) * G::ES;
             __asm__ volatile("" ::: "memory");  // behind the chunk's loads, all of them
 #pragma unroll
             for (int r = 0; r < G::RB; ++r)
                 if (!LAST || 16 * r + m < n) {
                     char* p = to + (int64_t)(16 * r * pitch) + mine;
-                    if constexpr (F32) *reinterpret_cast<f32x4_t*>(p) = O[r];
-                    else *reinterpret_cast<uint2*>(p) = make_uint2(pack2(O[r][0], O[r][1]), pack2(O[r][2], O[r][3]));
+                    if constexpr (F32) *reinterpret_cast<f32x4_t*>(p) = O[r][0];
+                    else if constexpr (ND == 2)
+                        *reinterpret_cast<uint4*>(p) = make_uint4(pack2(O[r][0][0], O[r][0][1]), pack2(O[r][0][2], O[r][0][3]),
+                                                                  pack2(O[r][1][0], O[r][1][1]), pack2(O[r][1][2], O[r][1][3]));
+                    else *reinterpret_cast<uint2*>(p) = make_uint2(pack2(O[r][0][0], O[r][0][1]), pack2(O[r][0][2], O[r][0][3]));
                 }
             __asm__ volatile("" ::: "memory");
         } else {
-#pragma unroll
-            for (int ks = 0; ks < G::KS; ++ks) vf[ks] = frag_ct(V, ks);
+            read_values();
 #pragma unroll
             for (int ct = 0; ct < G::CT; ++ct)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) S[ct][j] *= dec;
+                for (int d = 0; d < ND; ++d)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) S[ct][d][j] *= dec;
         }
 
         // the weighted values as sums of three bf16 values, which hold all of their 24 bits
 #pragma unroll
         for (int ks = 0; ks < G::KS; ++ks) {
-            __builtin_amdgcn_sched_barrier(0);  // what is read ahead stays within the registers
             const f32x4_t w0 = *reinterpret_cast<const f32x4_t*>(weights[LAST] + 32 * ks + 4 * grp);
             const f32x4_t w1 = *reinterpret_cast<const f32x4_t*>(weights[LAST] + 32 * ks + 16 + 4 * grp);
-            LFrag<F32> vb[G::VL], kt[4];
+            LFrag<F32> vb[ND][G::VL], kt[4];
 #pragma unroll
             for (int ct = 0; ct < 4; ++ct) kt[ct] = frag_bt(K, ct, ks);
-            float x[8];
-            values(vf[ks], x);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] *= w0[j], x[4 + j] *= w1[j];
-            split<G::VL>(x, vb, ones);
+            for (int d = 0; d < ND; ++d) {
+                float x[8];
+                values(vf[ks * ND + d], x);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] *= w0[j], x[4 + j] *= w1[j];
+                split<G::VL>(x, vb[d], ones);
+            }
 #pragma unroll
             for (int four = 0; four < G::CT; four += 4) {
                 if (four > 0)
@@ -642,14 +701,20 @@ __global__ __launch_bounds__(4 * DC, DC / 32) void linattn_chunk_kernel(
 #pragma unroll
                 for (int p = 0; p < G::VL; ++p)
 #pragma unroll
-                    for (int ct = 0; ct < 4; ++ct) S[four + ct] = mma(kt[ct], vb[p], S[four + ct]);
+                    for (int ct = 0; ct < 4; ++ct)
+#pragma unroll
+                        for (int d = 0; d < ND; ++d) S[four + ct][d] = mma(kt[ct], vb[d][p], S[four + ct][d]);
             }
         }
-        if (ROWS && marked && bad < n)
+        if (ROWS && marked) {
 #pragma unroll
-            for (int ct = 0; ct < G::CT; ++ct)
+            for (int d = 0; d < ND; ++d)
+                if (bad[d] < n)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) S[ct][j] = __builtin_nanf("");
+                    for (int ct = 0; ct < G::CT; ++ct)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) S[ct][d][j] = __builtin_nanf("");
+        }
     };
 
     char* const ldsVn = ROWS ? ldsV0 : ldsV1;
@@ -669,12 +734,17 @@ __global__ __launch_bounds__(4 * DC, DC / 32) void linattn_chunk_kernel(
 #pragma unroll
             for (int ct = 0; ct < G::CT; ++ct)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) to[state_row(ct, 4 * grp + j) * DC + 16 * wave + m] = S[ct][j];
+                for (int d = 0; d < ND; ++d)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) to[state_row(ct, 4 * grp + j) * DC + state_col<ND>(wave, m, d)] = S[ct][d][j];
         }
     } else {
         float* to = static_cast<float*>(op.out) + (w.slot * H + h) * (int64_t)DA * DC;
 #pragma unroll
-        for (int ct = 0; ct < G::CT; ++ct) *reinterpret_cast<f32x4_t*>(to + ((wave * G::CT + ct) * 64 + lane) * 4) = S[ct];
+        for (int ct = 0; ct < G::CT; ++ct)
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+                *reinterpret_cast<f32x4_t*>(to + state_at<DA>(state_row(ct, 4 * grp), state_col<ND>(wave, m, d))) = S[ct][d];
     }
 }
 
@@ -801,7 +871,7 @@ void chunks(const LinArgs& a, const Segs& s, std::initializer_list<LinOp> ops, i
     for (const LinOp& o : ops) op[count++] = o;
     const int64_t each = (slots_of(s) * a.H + 7) / 8 * 8;  // workgroups behind the last segment find none
     auto run = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, dim3((unsigned)(each * count)), dim3(4 * DC), 0, st, op[0], op[1], op[2], count, s, a.g);
+        hipLaunchKernelGGL(kernel, dim3((unsigned)(each * count)), dim3(a.f32 || DC == 64 ? 4 * DC : 256), 0, st, op[0], op[1], op[2], count, s, a.g);
     };
     auto types = [&](auto da, auto dc) {
         constexpr int A = decltype(da)::value, B = decltype(dc)::value;
