@@ -289,6 +289,7 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
     __shared__ __align__(16) char ldsQ[ROWS ? G::KB : 16], ldsP[ROWS ? G::PL * G::PB : 16];
     __shared__ __align__(16) float weights[2][C];  // what a token's product keeps at the end of a whole chunk, and of the last one
     __shared__ float powers[C + 1];                // of the decay
+    __shared__ float lefts[ROWS ? 1 : THREADS];    // of it over the last chunk and so many before it
 
     // the operations of a segment and head in workgroups of one XCD, next to one another
     const int64_t id = (int64_t)(blockIdx.x / (8 * ops)) * 8 + blockIdx.x % 8;
@@ -350,6 +351,7 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
 
     const double lg = log_decay(g[h]);
     if (tid <= C) powers[tid] = (float)exp(lg * tid);
+    if constexpr (!ROWS) lefts[tid] = (float)exp(lg * (tokens - (chunks - 1) * C + tid * C));
     const double whole = exp(lg * C);
     const float whole32 = (float)whole, rest = whole > 0 ? (float)((whole - (double)whole32) / whole) : 0.f;
 
@@ -483,9 +485,12 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
             if constexpr (!ROWS) fetch(op.c, Vn, c + 1, UnitsC(), offset_c);
         }
         // The state's decay, in 32 bits: what a power's rounding owes is paid in the next ones, so that thousands of chunks do
-        // not add up.
-        float dec = powers[n];
-        if (n == C) {
+        // not add up.  A segment's own state needs none on the way: its tokens are weighed by what is left at the segment's end.
+        float dec = powers[n], left = 1.f;
+        if constexpr (!ROWS) {
+            const int behind = chunks - 2 - c;
+            if (!LAST) left = behind < THREADS ? lefts[behind] : (float)exp(lg * (tokens - (c + 1) * C));
+        } else if (n == C) {
             dec = fmaf(whole32, owed, whole32);
             owed += rest - (whole32 > 0.f ? (dec - whole32) / whole32 : 0.f);
         }
@@ -669,19 +674,16 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
             __asm__ volatile("" ::: "memory");
         } else {
             read_values();
-#pragma unroll
-            for (int ct = 0; ct < G::CT; ++ct)
-#pragma unroll
-                for (int d = 0; d < ND; ++d)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) S[ct][d][j] *= dec;
         }
 
         // the weighted values as sums of three bf16 values, which hold all of their 24 bits
 #pragma unroll
         for (int ks = 0; ks < G::KS; ++ks) {
-            const f32x4_t w0 = *reinterpret_cast<const f32x4_t*>(weights[LAST] + 32 * ks + 4 * grp);
-            const f32x4_t w1 = *reinterpret_cast<const f32x4_t*>(weights[LAST] + 32 * ks + 16 + 4 * grp);
+            f32x4_t w0 = *reinterpret_cast<const f32x4_t*>(weights[LAST] + 32 * ks + 4 * grp);
+            f32x4_t w1 = *reinterpret_cast<const f32x4_t*>(weights[LAST] + 32 * ks + 16 + 4 * grp);
+            if constexpr (!ROWS)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w0[j] *= left, w1[j] *= left;
             LFrag<F32> vb[ND][G::VL], kt[4];
 #pragma unroll
             for (int ct = 0; ct < 4; ++ct) kt[ct] = frag_bt(K, ct, ks);
@@ -842,16 +844,18 @@ __global__ __launch_bounds__(256) void linattn_step_kernel(const void* q, const 
 
 // ------------------------------------------------------------------------------------------------ launches
 
-// Tokens of a segment.  Two workgroups fit on a CU: with 512 segments every place has one.  A segment's state is written and
-// read, several times its size, which 256 tokens outweigh; fewer only where every CU has no segment otherwise.
-int64_t segment_tokens(int64_t total, int H) {
+// Tokens of a segment.  Two workgroups fit on a CU: with 512 segments every place has one.  Packed sequences end anywhere, so
+// that half of the segments are shorter: with 768 of them the places even out (40011 tokens of 16 heads in 32 sequences 214 ->
+// 196 us, 206 -> 240 for equal lengths).  A segment's state is written and read, several times its size, which 256 tokens
+// outweigh; fewer only where every CU has no segment otherwise.
+int64_t segment_tokens(int64_t total, int H, bool packed) {
     auto whole = [](int64_t x) { return (x + 63) / 64 * 64; };
-    const int64_t two = whole((total * H + 511) / 512), one = whole((total * H + 255) / 256);
-    return two > 256 ? two : one < 64 ? 64 : one < 256 ? one : 256;
+    const int64_t places = packed ? 768 : 512, many = whole((total * H + places - 1) / places), one = whole((total * H + 255) / 256);
+    return many > 256 ? many : one < 64 ? 64 : one < 256 ? one : 256;
 }
 
 Segs segs_of(const LinArgs& a) {
-    Segs s{a.cu, a.T_fixed, a.N, a.total, segment_tokens(a.total, a.H), 1, a.H};
+    Segs s{a.cu, a.T_fixed, a.N, a.total, segment_tokens(a.total, a.H, a.cu), 1, a.H};
     if (!a.cu && a.T_fixed > s.L) s.per_seq = (a.T_fixed + s.L - 1) / s.L;
     return s;
 }
@@ -890,8 +894,9 @@ void fold(const LinArgs& a, const Segs& s, FoldOp one, const FoldOp* two, hipStr
 
 }  // namespace
 
+// For either way of giving the sequences: packed ones have the shorter segments.
 int64_t linattn_workspace_bytes(const LinArgs& a, bool backward) {
-    const int64_t L = segment_tokens(a.total, a.H);
+    const int64_t L = segment_tokens(a.total, a.H, true);
     if (a.total <= L) return 0;
     return (a.total / L + a.N) * a.H * a.Dk * (int64_t)a.Dv * 4 * (backward ? 2 : 1);
 }
