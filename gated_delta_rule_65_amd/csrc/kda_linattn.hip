@@ -104,6 +104,7 @@ struct LinOp {
     bool turned;            // states and x0 are taken transposed
     bool back;
     float su, so;           // scales of the state's products, and of the outputs
+    bool stream;            // rows go past the caches
 };
 
 template <bool F32>
@@ -230,6 +231,14 @@ __device__ __forceinline__ bf16x4_t read_turned(const char* p) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4bf16((__attribute__((address_space(3))) bf16x4_t*)const_cast<char*>(p));
 }
 
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+template <typename V>
+__device__ __forceinline__ void put(char* p, V v, bool stream) {
+    if (stream) __builtin_nontemporal_store(v, reinterpret_cast<V*>(p));
+    else *reinterpret_cast<V*>(p) = v;
+}
+
 // The count of s_waitcnt that lets `vm` requests of memory be under way, and none of LDS.
 constexpr int waitcnt(int vm) { return (vm & 15) | (vm >> 4) << 14 | 7 << 4; }
 
@@ -287,9 +296,9 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
     __shared__ __align__(16) char ldsK0[G::KB], ldsK1[G::KB];
     __shared__ __align__(16) char ldsV0[G::VB], ldsV1[ROWS ? 16 : G::VB];
     __shared__ __align__(16) char ldsQ[ROWS ? G::KB : 16], ldsP[ROWS ? G::PL * G::PB : 16];
-    __shared__ __align__(16) float weights[2][C];  // what a token's product keeps at the end of a whole chunk, and of the last one
+    __shared__ __align__(16) float weights[2][C];  // what a token's product keeps at the chunk's end, whole or the last one
     __shared__ float powers[C + 1];                // of the decay
-    __shared__ float lefts[ROWS ? 1 : THREADS];    // of it over the last chunk and so many before it
+    __shared__ float lefts[ROWS ? 1 : THREADS];    // of it over so many chunks
 
     // the operations of a segment and head in workgroups of one XCD, next to one another
     const int64_t id = (int64_t)(blockIdx.x / (8 * ops)) * 8 + blockIdx.x % 8;
@@ -312,11 +321,14 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
     const int tokens = (int)(w.end - w.begin), chunks = (tokens + C - 1) / C;
     // Rows of a chunk, in the order of the recurrence, to LDS, 64 units a wave at a time: for a whole chunk, a lane's offset from
     // an address that the wave shares.  Rows behind the last one repeat it and weigh nothing: as many requests for every chunk.
-    const int64_t row0 = op.back ? w.end - 1 : w.begin;
+    // A segment's own state may be summed in any order: from where the outputs' pass ends to where it begins, which leaves in the
+    // caches what that pass reads first.
+    const bool back = op.back == ROWS;
+    const int64_t row0 = back ? w.end - 1 : w.begin;
     auto offset_of = [&](auto units) {
         constexpr int U = decltype(units)::value;
         const int r = tid / U;
-        return (uint32_t)((op.back ? C - 1 - r : r) * H * U + (tid % U ^ turn<U, F32>(r))) * 16u;
+        return (uint32_t)((back ? C - 1 - r : r) * H * U + (tid % U ^ turn<U, F32>(r))) * 16u;
     };
     auto fetch = [&](const void* from, char* to, int c, auto units, uint32_t offset) {
         constexpr int U = decltype(units)::value, N = C * U / THREADS, STEP = THREADS / U;
@@ -324,20 +336,20 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
         constexpr int other = STEP == 8 ? 8 : 0;
         if (tokens - c * C >= C) {
             const char* base = static_cast<const char*>(from) +
-                               ((op.back ? row0 - c * C - (C - 1) : row0 + c * C) * H * U + (int64_t)h * U) * 16;
-            const int64_t step = (int64_t)(op.back ? -STEP : STEP) * H * U * 16;
+                               ((back ? row0 - c * C - (C - 1) : row0 + c * C) * H * U + (int64_t)h * U) * 16;
+            const int64_t step = (int64_t)(back ? -STEP : STEP) * H * U * 16;
 #pragma unroll
             for (int x = 0; x < N; ++x)
                 load_to_lds(base + x * step + (x % 2 ? offset ^ (other * 16) : offset), to + (x * G::WAVES + wave) * 1024);
         } else {
             const int top = tokens - c * C - 1;
-            const uint4* base = static_cast<const uint4*>(from) + (op.back ? row0 - c * C - top : row0 + c * C) * H * U + (int64_t)h * U;
+            const uint4* base = static_cast<const uint4*>(from) + (back ? row0 - c * C - top : row0 + c * C) * H * U + (int64_t)h * U;
             int mine = tid / U;
             __asm__ volatile("" : "+v"(mine));  // made here, for the last chunk alone
 #pragma unroll
             for (int x = 0; x < N; ++x) {
                 const int r = mine + x * STEP, t = r > top ? top : r;
-                load_to_lds(base + (uint32_t)(__mul24(op.back ? top - t : t, H * U) + (tid % U ^ turn<U, F32>(r))),
+                load_to_lds(base + (uint32_t)(__mul24(back ? top - t : t, H * U) + (tid % U ^ turn<U, F32>(r))),
                             to + (x * G::WAVES + wave) * 1024);
             }
         }
@@ -351,7 +363,7 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
 
     const double lg = log_decay(g[h]);
     if (tid <= C) powers[tid] = (float)exp(lg * tid);
-    if constexpr (!ROWS) lefts[tid] = (float)exp(lg * (tokens - (chunks - 1) * C + tid * C));
+    if constexpr (!ROWS) lefts[tid] = (float)exp(lg * C * tid);
     const double whole = exp(lg * C);
     const float whole32 = (float)whole, rest = whole > 0 ? (float)((whole - (double)whole32) / whole) : 0.f;
 
@@ -407,7 +419,7 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
     Ones ones;
     if (tid < 2 * C) {
         const int i = tid % C, n = tid < C ? C : tokens - (chunks - 1) * C;
-        weights[tid / C][i] = i < n ? op.su * powers[n - 1 - i + (op.back ? 1 : 0)] : 0.f;
+        weights[tid / C][i] = i < n ? op.su * powers[(ROWS ? n - 1 - i : i) + (op.back ? 1 : 0)] : 0.f;
     }
 
     // Fragments: eight contracted values of row (or column) m.  A lane's first place in a tile; the others are it with some bits
@@ -476,6 +488,9 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
         // the places of a chunk's fragments are made again from these few: kept, they would take most of the registers
         __asm__ volatile("" : "+v"(ones.low), "+v"(ones.high), "+v"(at_row), "+v"(at_turned), "+v"(at_col), "+v"(at_score), "+v"(at_score2),
                          "+v"(at_power), "+v"(at_far));
+        // Of two workgroups on a CU one goes first in these products and the other in the state's, else the elder in all of them
+        // (packed 40011 tokens 138 -> 129 us, prefill batch 142 -> 139).
+        __builtin_amdgcn_s_setprio(1);
         // The chunk's rows have come.  Requests end in the order in which they were made, and the last ones are the stores of the
         // chunk before: they are not waited for.
         __builtin_amdgcn_s_waitcnt(waitcnt(ROWS ? G::RB : 0));
@@ -488,8 +503,7 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
         // not add up.  A segment's own state needs none on the way: its tokens are weighed by what is left at the segment's end.
         float dec = powers[n], left = 1.f;
         if constexpr (!ROWS) {
-            const int behind = chunks - 2 - c;
-            if (!LAST) left = behind < THREADS ? lefts[behind] : (float)exp(lg * (tokens - (c + 1) * C));
+            left = c < THREADS ? lefts[c] : (float)exp(lg * c * C);
         } else if (n == C) {
             dec = fmaf(whole32, owed, whole32);
             owed += rest - (whole32 > 0.f ? (dec - whole32) / whole32 : 0.f);
@@ -665,17 +679,18 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
             for (int r = 0; r < G::RB; ++r)
                 if (!LAST || 16 * r + m < n) {
                     char* p = to + (int64_t)(16 * r * pitch) + mine;
-                    if constexpr (F32) *reinterpret_cast<f32x4_t*>(p) = O[r][0];
+                    if constexpr (F32) put(p, O[r][0], op.stream);
                     else if constexpr (ND == 2)
-                        *reinterpret_cast<uint4*>(p) = make_uint4(pack2(O[r][0][0], O[r][0][1]), pack2(O[r][0][2], O[r][0][3]),
-                                                                  pack2(O[r][1][0], O[r][1][1]), pack2(O[r][1][2], O[r][1][3]));
-                    else *reinterpret_cast<uint2*>(p) = make_uint2(pack2(O[r][0][0], O[r][0][1]), pack2(O[r][0][2], O[r][0][3]));
+                        put(p, u32x4_t{pack2(O[r][0][0], O[r][0][1]), pack2(O[r][0][2], O[r][0][3]),
+                                       pack2(O[r][1][0], O[r][1][1]), pack2(O[r][1][2], O[r][1][3])}, op.stream);
+                    else put(p, u32x2_t{pack2(O[r][0][0], O[r][0][1]), pack2(O[r][0][2], O[r][0][3])}, op.stream);
                 }
             __asm__ volatile("" ::: "memory");
         } else {
             read_values();
         }
 
+        __builtin_amdgcn_s_setprio(0);
         // the weighted values as sums of three bf16 values, which hold all of their 24 bits
 #pragma unroll
         for (int ks = 0; ks < G::KS; ++ks) {
@@ -684,9 +699,10 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
             if constexpr (!ROWS)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) w0[j] *= left, w1[j] *= left;
-            LFrag<F32> vb[ND][G::VL], kt[4];
+            constexpr int TOGETHER = F32 ? 2 : 4;  // tiles of the state: as many as the registers hold
+            LFrag<F32> vb[ND][G::VL], kt[TOGETHER];
 #pragma unroll
-            for (int ct = 0; ct < 4; ++ct) kt[ct] = frag_bt(K, ct, ks);
+            for (int ct = 0; ct < TOGETHER; ++ct) kt[ct] = frag_bt(K, ct, ks);
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
                 float x[8];
@@ -696,16 +712,16 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
                 split<G::VL>(x, vb[d], ones);
             }
 #pragma unroll
-            for (int four = 0; four < G::CT; four += 4) {
-                if (four > 0)
+            for (int first = 0; first < G::CT; first += TOGETHER) {
+                if (first > 0)
 #pragma unroll
-                    for (int ct = 0; ct < 4; ++ct) kt[ct] = frag_bt(K, four + ct, ks);
+                    for (int ct = 0; ct < TOGETHER; ++ct) kt[ct] = frag_bt(K, first + ct, ks);
 #pragma unroll
                 for (int p = 0; p < G::VL; ++p)
 #pragma unroll
-                    for (int ct = 0; ct < 4; ++ct)
+                    for (int ct = 0; ct < TOGETHER; ++ct)
 #pragma unroll
-                        for (int d = 0; d < ND; ++d) S[four + ct][d] = mma(kt[ct], vb[d][p], S[four + ct][d]);
+                        for (int d = 0; d < ND; ++d) S[first + ct][d] = mma(kt[ct], vb[d][p], S[first + ct][d]);
             }
         }
         if (ROWS && marked) {
@@ -868,6 +884,10 @@ bool is_split(const Segs& s) { return s.cu ? s.total > s.L : s.per_seq > 1; }
 using I64 = std::integral_constant<int, 64>;
 using I128 = std::integral_constant<int, 128>;
 
+// Outputs past the caches where they and the inputs do not fit there anyway: they then keep what the two passes share (1M tokens
+// of a head in all 406 -> 390 us).
+bool streams(const LinArgs& a) { return a.total * a.H * (a.Dk + a.Dv) * (a.f32 ? 8 : 4) >= 2 * kStreamBytes; }
+
 template <bool ROWS>
 void chunks(const LinArgs& a, const Segs& s, std::initializer_list<LinOp> ops, int DA, int DC, hipStream_t st) {
     LinOp op[3] = {};
@@ -911,10 +931,10 @@ hipError_t launch_linattn_fwd(const LinArgs& a, hipStream_t st) {
     const Segs s = segs_of(a);
     float* states = static_cast<float*>(a.ws);
     if (is_split(s)) {
-        chunks<false>(a, s, {LinOp{nullptr, a.k, a.v, states, nullptr, nullptr, nullptr, false, false, 1.f, 1.f}}, a.Dk, a.Dv, st);
+        chunks<false>(a, s, {LinOp{nullptr, a.k, a.v, states, nullptr, nullptr, nullptr, false, false, 1.f, 1.f, false}}, a.Dk, a.Dv, st);
         fold(a, s, FoldOp{states, a.s0, false}, nullptr, st);
     }
-    chunks<true>(a, s, {LinOp{a.q, a.k, a.v, a.o, a.s0, states, a.s_final, false, false, 1.f, a.scale}}, a.Dk, a.Dv, st);
+    chunks<true>(a, s, {LinOp{a.q, a.k, a.v, a.o, a.s0, states, a.s_final, false, false, 1.f, a.scale, streams(a)}}, a.Dk, a.Dv, st);
     return hipGetLastError();
 }
 
@@ -923,15 +943,15 @@ hipError_t launch_linattn_bwd(const LinArgs& a, hipStream_t st) {
     float* states = static_cast<float*>(a.ws);
     float* grads = states + slots_of(s) * a.H * a.Dk * a.Dv;
     if (is_split(s)) {
-        chunks<false>(a, s, {LinOp{nullptr, a.k, a.v, states, nullptr, nullptr, nullptr, false, false, 1.f, 1.f},
-                             LinOp{nullptr, a.q, a.d_o, grads, nullptr, nullptr, nullptr, false, true, a.scale, 1.f}},
+        chunks<false>(a, s, {LinOp{nullptr, a.k, a.v, states, nullptr, nullptr, nullptr, false, false, 1.f, 1.f, false},
+                             LinOp{nullptr, a.q, a.d_o, grads, nullptr, nullptr, nullptr, false, true, a.scale, 1.f, false}},
                       a.Dk, a.Dv, st);
         const FoldOp two{grads, a.d_sfinal, true};
         fold(a, s, FoldOp{states, a.s0, false}, &two, st);
     }
-    const LinOp dq{a.d_o, a.v, a.k, a.dq, a.s0, states, nullptr, true, false, 1.f, a.scale};
-    const LinOp dk{a.v, a.d_o, a.q, a.dk, a.d_sfinal, grads, nullptr, true, true, a.scale, 1.f};
-    const LinOp dv{a.k, a.q, a.d_o, a.dv, a.d_sfinal, grads, a.ds0, false, true, a.scale, 1.f};
+    const LinOp dq{a.d_o, a.v, a.k, a.dq, a.s0, states, nullptr, true, false, 1.f, a.scale, streams(a)};
+    const LinOp dk{a.v, a.d_o, a.q, a.dk, a.d_sfinal, grads, nullptr, true, true, a.scale, 1.f, streams(a)};
+    const LinOp dv{a.k, a.q, a.d_o, a.dv, a.d_sfinal, grads, a.ds0, false, true, a.scale, 1.f, streams(a)};
     if (a.Dk == a.Dv) {
         chunks<true>(a, s, {dq, dk, dv}, a.Dk, a.Dv, st);
     } else {
