@@ -11,6 +11,13 @@
 #include "kda_layer_launch.h"
 
 namespace kda {
+
+// Blocks of tokens in whose sums the weights' gradients are added up: of 16 tokens at least, so that they are small beside the
+// rows, and at most so many that the workspace stays small.
+constexpr int64_t kGnBlocks = 1024, kGnBlockTokens = 16;
+// the sums of the workspace's blocks
+void groupnorm_sums(const GroupNormArgs& a, int64_t blocks, hipStream_t st);
+
 namespace {
 
 constexpr int kGnThreads = 256;
@@ -87,37 +94,33 @@ __device__ __forceinline__ float lanes_sum(float x) {
     return x;
 }
 
-// 1 / (1 + e^-u): e^-u from the product's two halves, so that it keeps its accuracy far from zero (the product alone is off by
-// |u| 2^-24); beyond +-100 it is 0 or infinite in 32 bits anyway.
+// 1 / (1 + e^-u).  CLOSE: e^-u from the product's two halves, so that it keeps 32 bits' accuracy far from zero (the product alone is
+// off by |u| 2^-24, which 16-bit results do not show).  Beyond +-100 e^-u is 0 or infinite in 32 bits anyway.  Of a NaN, some
+// number.
+template <bool CLOSE>
 __device__ __forceinline__ float gn_sigmoid(float u) {
     constexpr float l2e = 1.44269502162933349609375f, l2e_rest = 1.925963033500011e-8f, ln2 = 0.693147182464599609375f;
-    const float t = __builtin_amdgcn_fmed3f(-u, -100.f, 100.f);
-    const float hi = t * l2e, lo = fmaf(t, l2e_rest, fmaf(t, l2e, -hi));
-    const float e = __builtin_amdgcn_exp2f(hi);
-    const float s = __builtin_amdgcn_rcpf(1.f + fmaf(e, lo * ln2, e));
-    return u == u ? s : u;
+    const float t = __builtin_amdgcn_fmed3f(-u, -100.f, 100.f), hi = t * l2e, e = __builtin_amdgcn_exp2f(hi);
+    if constexpr (!CLOSE) return __builtin_amdgcn_rcpf(1.f + e);
+    const float lo = fmaf(t, l2e_rest, fmaf(t, l2e, -hi));
+    return __builtin_amdgcn_rcpf(1.f + fmaf(e, lo * ln2, e));
 }
 
-// act(u) and its slope.
-template <bool SLOPE>
-__device__ __forceinline__ void gn_act(float u, int act, float& f, float& slope) {
-    if (act == 0) {
-        f = u;
-        slope = 1.f;
-        return;
-    }
-    const float s = gn_sigmoid(u);
-    f = act == 2 ? s : u * s;
-    if constexpr (SLOPE) slope = act == 2 ? s * (1.f - s) : fmaf(u * s, 1.f - s, s);
+// act(u) and its slope; u times the sigmoid, or the sigmoid alone, by selection and not by branches between the values.
+template <bool CLOSE, bool SLOPE>
+__device__ __forceinline__ void gn_act(float u, bool alone, float& f, float& slope) {
+    const float s = gn_sigmoid<CLOSE>(u);
+    f = (alone ? (u == u ? 1.f : u) : u) * s;
+    if constexpr (SLOPE) slope = fmaf(f, 1.f - s, alone ? 0.f : s);
 }
 
-template <bool XF, bool YF, int CPL, int P, int ITER, bool BWD>
+template <bool XF, bool YF, int CPL, int P, int ITER, bool BWD, bool GATE>
 __global__ __launch_bounds__(kGnThreads) void groupnorm_kernel(GroupNormArgs a, GnPlan plan) {
     constexpr int N = CPL * ITER;
     const int tid = threadIdx.x, p = tid % P, W = (int)a.width;
     const int gi = tid / P % plan.groups, ti = tid / (P * plan.groups);
     const int64_t group = (int64_t)blockIdx.x * plan.groups + gi, c0 = group * W, C = a.groups * W;
-    const bool mine = group < a.groups && ti < plan.tokens;
+    const bool mine = group < a.groups && ti < plan.tokens, alone = a.act == 2;
     const float mean_of = 1.f / W;
     bool in[ITER];
     int at[ITER];
@@ -138,95 +141,87 @@ __global__ __launch_bounds__(kGnThreads) void groupnorm_kernel(GroupNormArgs a, 
     const int64_t first = (int64_t)blockIdx.y * plan.block;
     const int64_t end = first + plan.block < a.tokens ? first + plan.block : a.tokens;
 
+    // Lanes without a channel, and rows behind the last one, hold zeros: they add nothing to any sum.
     GnRaw<CPL, XF> rx[ITER];
     GnRaw<CPL, YF> rg[ITER], rd[ITER];
     auto fetch = [&](int64_t t) {
 #pragma unroll
         for (int i = 0; i < ITER; ++i) {
-            if (!in[i]) continue;
+            rx[i] = {}, rg[i] = {}, rd[i] = {};
+            if (!in[i] || t >= end) continue;
             rx[i] = gn_load<CPL, XF>(a.x, t * a.x_stride + c0 + at[i]);
-            if (a.gate) rg[i] = gn_load<CPL, YF>(a.gate, t * a.gate_stride + c0 + at[i]);
+            if constexpr (GATE) rg[i] = gn_load<CPL, YF>(a.gate, t * a.gate_stride + c0 + at[i]);
             if constexpr (BWD) rd[i] = gn_load<CPL, YF>(a.dy, t * C + c0 + at[i]);
         }
     };
-#pragma unroll
-    for (int i = 0; i < ITER; ++i) rx[i] = {}, rg[i] = {}, rd[i] = {};
     int64_t t = first + ti;
-    if (mine && t < end) fetch(t);
+    fetch(t);
     // the loop's count is the workgroup's: every lane takes part in its groups' sums
     for (int64_t t0 = first; t0 < end; t0 += plan.tokens, t += plan.tokens) {
         float x[N], u[N], dy[N];
 #pragma unroll
         for (int i = 0; i < ITER; ++i) {
             gn_values<CPL, XF>(rx[i], x + i * CPL);
-            gn_values<CPL, YF>(rg[i], u + i * CPL);
+            if constexpr (GATE) gn_values<CPL, YF>(rg[i], u + i * CPL);
             if constexpr (BWD) gn_values<CPL, YF>(rd[i], dy + i * CPL);
         }
-        const bool here = mine && t < end;
-        if (mine && t + plan.tokens < end) fetch(t + plan.tokens);
+        const bool here = t < end;
+        if (t0 + plan.tokens < end) fetch(t + plan.tokens);
         float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < ITER; ++i)
-#pragma unroll
-            for (int j = 0; j < CPL; ++j) sum += in[i] ? x[i * CPL + j] : 0.f;
+        for (int k = 0; k < N; ++k) sum += x[k];
         const float mean = lanes_sum<P>(sum) * mean_of;
         float squares = 0.f;
 #pragma unroll
-        for (int i = 0; i < ITER; ++i)
+        for (int i = 0; i < ITER; ++i) {
+            const float less = in[i] ? mean : 0.f;
 #pragma unroll
             for (int j = 0; j < CPL; ++j) {
                 float& v = x[i * CPL + j];
-                v = in[i] ? v - mean : 0.f;
+                v -= less;
                 squares = fmaf(v, v, squares);
             }
+        }
         // the square root and the division to the last bit: one each for a row
-        const float rstd = 1.f / sqrtf(fmaf(lanes_sum<P>(squares), mean_of, a.eps));
-        if constexpr (!BWD) {
-#pragma unroll
-            for (int i = 0; i < ITER; ++i) {
-                float y[CPL];
-#pragma unroll
-                for (int j = 0; j < CPL; ++j) {
-                    const int k = i * CPL + j;
-                    const float z = fmaf(x[k] * rstd, w[k], b[k]);
-                    float f, slope;
-                    gn_act<false>(a.gate ? u[k] : z, a.act, f, slope);
-                    y[j] = a.gate ? z * f : f;
-                }
-                if (here && in[i]) gn_store<CPL, YF>(a.y, t * C + c0 + at[i], y);
-            }
-        } else {
+        float rstd = 1.f / sqrtf(fmaf(lanes_sum<P>(squares), mean_of, a.eps));
+        if (!here) rstd = 0.f;  // of a row of zeros it may be infinite
+        auto row = [&](auto with) {  // with an activation, or none
+            constexpr bool ACT = decltype(with)::value;
             float s1 = 0.f, s2 = 0.f;
 #pragma unroll
-            for (int i = 0; i < ITER; ++i) {
-#pragma unroll
-                for (int j = 0; j < CPL; ++j) {
-                    const int k = i * CPL + j;
-                    x[k] *= rstd;
-                    const float z = fmaf(x[k], w[k], b[k]);
-                    float f, slope;
-                    gn_act<true>(a.gate ? u[k] : z, a.act, f, slope);
-                    u[k] = dy[k] * z * slope;                   // the gate's gradient
-                    const float dz = dy[k] * (a.gate ? f : slope);
-                    dw[k] = fmaf(here ? dz : 0.f, x[k], dw[k]);
-                    db[k] += here ? dz : 0.f;
+            for (int k = 0; k < N; ++k) {
+                x[k] *= rstd;
+                const float z = fmaf(x[k], w[k], b[k]), v = GATE ? u[k] : z;
+                float f = v, slope = 1.f;
+                if constexpr (ACT) gn_act<YF, BWD>(v, alone, f, slope);
+                if constexpr (!BWD) {
+                    x[k] = GATE ? z * f : f;
+                } else {
+                    if constexpr (GATE) u[k] = dy[k] * z * slope;  // the gate's gradient
+                    const float dz = dy[k] * (GATE ? f : slope);
+                    dw[k] = fmaf(dz, x[k], dw[k]);
+                    db[k] += dz;
                     dy[k] = dz * w[k];
-                    s1 += in[i] ? dy[k] : 0.f;
-                    s2 = fmaf(in[i] ? dy[k] : 0.f, x[k], s2);
+                    s1 += dy[k];
+                    s2 = fmaf(dy[k], x[k], s2);
                 }
-                if (a.gate && here && in[i]) gn_store<CPL, YF>(a.dgate, t * C + c0 + at[i], u + i * CPL);
             }
-            s1 = lanes_sum<P>(s1) * mean_of;
-            s2 = lanes_sum<P>(s2) * mean_of;
+            if constexpr (BWD) {
+                s1 = lanes_sum<P>(s1) * mean_of;
+                s2 = lanes_sum<P>(s2) * mean_of;
 #pragma unroll
-            for (int i = 0; i < ITER; ++i) {
-                float dx[CPL];
+                for (int k = 0; k < N; ++k) x[k] = rstd * (dy[k] - fmaf(x[k], s2, s1));
+            }
+        };
+        a.act ? row(std::true_type()) : row(std::false_type());
 #pragma unroll
-                for (int j = 0; j < CPL; ++j) {
-                    const int k = i * CPL + j;
-                    dx[j] = rstd * (dy[k] - fmaf(x[k], s2, s1));
-                }
-                if (here && in[i]) gn_store<CPL, XF>(a.dx, t * C + c0 + at[i], dx);
+        for (int i = 0; i < ITER; ++i) {
+            if (!here || !in[i]) continue;
+            if constexpr (BWD) {
+                if constexpr (GATE) gn_store<CPL, YF>(a.dgate, t * C + c0 + at[i], u + i * CPL);
+                gn_store<CPL, XF>(a.dx, t * C + c0 + at[i], x + i * CPL);
+            } else {
+                gn_store<CPL, YF>(a.y, t * C + c0 + at[i], x + i * CPL);
             }
         }
     }
@@ -307,12 +302,21 @@ inline GnPlan gn_plan(const GroupNormArgs& a, int lanes, int64_t places, int64_t
 
 }  // namespace
 
+template <bool XF, bool YF, bool BWD>
+void groupnorm_launch(const GroupNormArgs& a, hipStream_t st) {
+    gn_shape(groupnorm_wide(a), a.width, [&](auto cpl, auto p, auto iter) {
+        constexpr int CPL = decltype(cpl)::value, P = decltype(p)::value, ITER = decltype(iter)::value;
+        int64_t columns;
+        const GnPlan plan = BWD ? gn_plan(a, P, kGnBlocks, kGnBlockTokens, columns) : gn_plan(a, P, 4096, 1, columns);
+        const dim3 grid((unsigned)columns, (unsigned)plan.blocks);
+        if (a.gate) hipLaunchKernelGGL((groupnorm_kernel<XF, YF, CPL, P, ITER, BWD, true>), grid, dim3(kGnThreads), 0, st, a, plan);
+        else hipLaunchKernelGGL((groupnorm_kernel<XF, YF, CPL, P, ITER, BWD, false>), grid, dim3(kGnThreads), 0, st, a, plan);
+        if (BWD && a.dweight) groupnorm_sums(a, plan.blocks, st);
+    });
+}
+
 // Rows up to this wide are held in registers.
 inline bool gn_in_registers(const GroupNormArgs& a) { return a.width <= (groupnorm_wide(a) ? 2048 : 1024); }
-// Blocks of tokens in whose sums the weights' gradients are added up: of 16 tokens at least, so that they are small beside the
-// rows, and at most so many that the workspace stays small.
-constexpr int64_t kGnBlocks = 1024, kGnBlockTokens = 16;
-
 template <bool XF, bool YF>
 void groupnorm_fwd_of(const GroupNormArgs& a, hipStream_t st);
 template <bool XF, bool YF>

@@ -4,9 +4,33 @@
 
 namespace kda {
 
-void groupnorm_sums(const GroupNormArgs& a, int64_t blocks, hipStream_t st);
-
 namespace {
+
+// The sums over the blocks of tokens, 32 columns (of both weights' gradients) a workgroup, so that a row of threads reads a line:
+// 32 rows take every 32nd block each, and are added up in their order.
+__global__ __launch_bounds__(1024) void groupnorm_sums_kernel(const float* part, int64_t blocks, int64_t C, float* dweight,
+                                                              float* dbias) {
+    __shared__ float rows[32][33];
+    const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x % 32;
+    const int r = threadIdx.x / 32;
+    float sum = 0.f;
+    if (c < 2 * C) {
+        constexpr int AHEAD = 8;
+        for (int64_t i = r; i < blocks; i += 32 * AHEAD) {
+            float v[AHEAD];
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) v[k] = i + 32 * k < blocks ? part[(i + 32 * k) * 2 * C + c] : 0.f;
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) sum += v[k];
+        }
+    }
+    rows[r][threadIdx.x % 32] = sum;
+    __syncthreads();
+    if (r || c >= 2 * C) return;
+#pragma unroll
+    for (int i = 1; i < 32; ++i) sum += rows[i][threadIdx.x];
+    (c < C ? dweight : dbias - C)[c] = sum;
+}
 
 __device__ __forceinline__ float block_sum(float x, float* lds) {
     x = lanes_sum<64>(x);
@@ -21,6 +45,13 @@ __device__ __forceinline__ float load1(const void* p, int64_t i) {
     float x[1];
     gn_values<1, XF>(gn_load<1, XF>(p, i), x);
     return x[0];
+}
+
+template <bool YF>
+__device__ __forceinline__ void act_of(float v, int act, float& f, float& slope) {
+    f = v;
+    slope = 1.f;
+    if (act) gn_act<YF, true>(v, act == 2, f, slope);
 }
 
 // A workgroup for a group of a token, an element a thread at a time; the passes after the first find the row in the caches.
@@ -47,7 +78,8 @@ __global__ __launch_bounds__(kGnThreads) void groupnorm_rows_kernel(GroupNormArg
         n = (load1<XF>(a.x, x0 + c) - mean) * rstd;
         w = a.weight ? a.weight[c0 + c] : 1.f;
         z = fmaf(n, w, a.bias ? a.bias[c0 + c] : 0.f);
-        gn_act<true>(a.gate ? load1<YF>(a.gate, g0 + c) : z, a.act, f, slope);
+        const float v = a.gate ? load1<YF>(a.gate, g0 + c) : z;
+        act_of<YF>(v, a.act, f, slope);
     };
     float n, z, w, f, slope;
     if (!a.dy) {
@@ -88,7 +120,7 @@ __global__ __launch_bounds__(kGnThreads) void groupnorm_columns_kernel(GroupNorm
         const float* s = stats + 2 * (t * a.groups + c / a.width);
         const float n = (load1<XF>(a.x, t * a.x_stride + c) - s[0]) * s[1], z = fmaf(n, w, b);
         float f, slope;
-        gn_act<true>(a.gate ? load1<YF>(a.gate, t * a.gate_stride + c) : z, a.act, f, slope);
+        act_of<YF>(a.gate ? load1<YF>(a.gate, t * a.gate_stride + c) : z, a.act, f, slope);
         const float dz = load1<YF>(a.dy, t * C + c) * (a.gate ? f : slope);
         dw = fmaf(dz, n, dw);
         db += dz;
@@ -121,6 +153,12 @@ void by_type(const GroupNormArgs& a, F&& f) {
 }
 
 }  // namespace
+
+void groupnorm_sums(const GroupNormArgs& a, int64_t blocks, hipStream_t st) {
+    const int64_t C = a.groups * a.width;
+    hipLaunchKernelGGL(groupnorm_sums_kernel, dim3((unsigned)((2 * C + 31) / 32)), dim3(1024), 0, st,
+                       static_cast<const float*>(a.ws), blocks, C, a.dweight, a.dbias);
+}
 
 bool groupnorm_wide(const GroupNormArgs& a) { return a.width % 8 == 0 && a.x_stride % 8 == 0 && a.gate_stride % 8 == 0; }
 

@@ -1,0 +1,11 @@
+// Backward pass of the group norm with an activation for bf16 x (kda_groupnorm.h).
+#include "kda_groupnorm.h"
+
+namespace kda {
+
+template <>
+void groupnorm_bwd_of<false, false>(const GroupNormArgs& a, hipStream_t st) { groupnorm_launch<false, false, true>(a, st); }
+template <>
+void groupnorm_bwd_of<false, true>(const GroupNormArgs& a, hipStream_t st) { groupnorm_launch<false, true, true>(a, st); }
+
+}  // namespace kda
