@@ -164,7 +164,7 @@ bool groupnorm_wide(const GroupNormArgs& a) { return a.width % 8 == 0 && a.x_str
 
 int64_t groupnorm_groups(const GroupNormArgs& a) {
     if (!gn_in_registers(a)) return a.tokens * a.groups;
-    return 4096 + a.groups;
+    return 8192 + a.groups;
 }
 
 int64_t groupnorm_bwd_workspace_bytes(int64_t tokens, int64_t groups, int64_t width) {
