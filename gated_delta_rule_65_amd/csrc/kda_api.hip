@@ -373,7 +373,7 @@ kda_status lin_packed(kda::LinArgs& a, const int32_t* cu, int64_t N, int64_t tot
 }
 
 kda_status lin_ws(kda::LinArgs& a, bool backward, void* ws, size_t bytes, const char* what) {
-    if (kda::linattn_groups(a, backward) > kda::kMaxThreads / 256)
+    if (kda::linattn_threads(a, backward) > kda::kMaxThreads)
         return fail(KDA_ERR_BAD_SHAPE, "%s: %lld tokens of %lld sequences and %d heads exceed the grid limit", what,
                     (long long)a.total, (long long)a.N, a.H);
     const int64_t need = kda::linattn_workspace_bytes(a, backward);

@@ -107,7 +107,7 @@ struct LinArgs {
     float* ds0;
 };
 int64_t linattn_workspace_bytes(const LinArgs& a, bool backward);
-int64_t linattn_groups(const LinArgs& a, bool backward);  // workgroups of a call's largest launch
+int64_t linattn_threads(const LinArgs& a, bool backward);  // of a call's largest launch
 hipError_t launch_linattn_fwd(const LinArgs& a, hipStream_t st);
 hipError_t launch_linattn_bwd(const LinArgs& a, hipStream_t st);
 hipError_t launch_linattn_step(const LinArgs& a, const float* s_in, float* s_out, hipStream_t st);
@@ -132,7 +132,7 @@ struct GroupNormArgs {
     void* ws;
 };
 bool groupnorm_wide(const GroupNormArgs& a);  // rows are read 16 bytes at a time
-int64_t groupnorm_groups(const GroupNormArgs& a);  // workgroups of a call's largest launch
+int64_t groupnorm_groups(const GroupNormArgs& a);  // of a call's largest launch
 int64_t groupnorm_bwd_workspace_bytes(int64_t tokens, int64_t groups, int64_t width);
 hipError_t launch_groupnorm_fwd(const GroupNormArgs& a, hipStream_t st);
 hipError_t launch_groupnorm_bwd(const GroupNormArgs& a, hipStream_t st);

@@ -45,7 +45,7 @@ struct Segs {
 
 struct Where {
     int64_t n, begin, end;  // sequence, and the segment's tokens
-    int64_t slot;           // its place among the states
+    int64_t base;           // the sequence's first place among the states
     int64_t j, count;       // segment j of count; count 0: a sequence without tokens
     int64_t tail;           // tokens of the sequence's last segment
 };
@@ -55,38 +55,57 @@ __device__ __forceinline__ int64_t seq_begin(const Segs& s, int64_t n) {
     return x < 0 ? 0 : x > s.total ? s.total : x;
 }
 
-// The segment of a slot; count < 0: there is none.  Packed sequence n takes the slots from floor(begin / L) + n on: no two
-// the same, and one at least for each sequence.  64 sequences are looked at together.
-__device__ __forceinline__ Where where_of(const Segs& s, int64_t slot) {
+// The last packed sequence n whose begin is below what is looked for; 64 sequences are looked at together.
+template <typename Below>
+__device__ __forceinline__ int64_t last_below(const Segs& s, Below below) {
+    int64_t lo = 0, hi = s.N;
+    while (hi - lo > 1) {
+        const int64_t step = (hi - lo + 63) / 64, at = lo + (int64_t)(threadIdx.x & 63) * step;
+        const uint64_t found = __ballot(at < hi && below(seq_begin(s, at < hi ? at : lo), at));
+        if (!found) break;
+        lo += (63 - __builtin_clzll(found)) * step;
+        hi = lo + step < hi ? lo + step : hi;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ Where sequence(const Segs& s, int64_t n) {
     Where w;
-    w.slot = slot;
+    w.n = n;
     if (!s.cu) {
-        w.n = slot / s.per_seq;
-        w.j = slot - w.n * s.per_seq;
-        w.count = (s.T_fixed + s.L - 1) / s.L;
-        w.begin = w.n * s.T_fixed;
+        w.begin = n * s.T_fixed;
         w.end = w.begin + s.T_fixed;
     } else {
-        int64_t lo = 0, hi = s.N;
-        while (hi - lo > 1) {
-            const int64_t step = (hi - lo + 63) / 64, at = lo + (int64_t)(threadIdx.x & 63) * step;
-            const uint64_t below = __ballot(at < hi && seq_begin(s, at < hi ? at : lo) / s.L + at <= slot);
-            if (!below) break;
-            lo += (63 - __builtin_clzll(below)) * step;
-            hi = lo + step < hi ? lo + step : hi;
-        }
-        w.n = lo;
-        w.begin = seq_begin(s, lo);
-        const int64_t e = seq_begin(s, lo + 1);
+        w.begin = seq_begin(s, n);
+        const int64_t e = seq_begin(s, n + 1);
         w.end = e < w.begin ? w.begin : e;
-        w.j = slot - (w.begin / s.L + lo);
-        w.count = (w.end - w.begin + s.L - 1) / s.L;
     }
-    if (w.n >= s.N || w.j < 0 || w.j >= (w.count ? w.count : 1)) {
+    w.j = 0;
+    w.count = (w.end - w.begin + s.L - 1) / s.L;
+    w.tail = w.end - w.begin - (w.count - 1) * s.L;
+    w.base = w.begin / s.L;
+    return w;
+}
+
+// The segment of a slot; count < 0: there is none.  Packed sequence n takes the slots from floor(begin / L) + n on: no two
+// the same, and one at least for each sequence.
+//
+// States are kept between segments only, one fewer than a sequence has segments, from floor(begin / L) on: forward that behind
+// segment j has place j of them, backward that before it place j - 1.  Sequences with one segment need none, and all of them
+// lie below total / L: the next sequence begins behind all but the last segment.
+__device__ __forceinline__ Where where_of(const Segs& s, int64_t slot) {
+    const int64_t n = s.cu ? last_below(s, [&](int64_t begin, int64_t at) { return begin / s.L + at <= slot; }) : slot / s.per_seq;
+    if (n >= s.N) {
+        Where w{};
         w.count = -1;
         return w;
     }
-    w.tail = w.end - w.begin - (w.count - 1) * s.L;
+    Where w = sequence(s, n);
+    w.j = slot - (s.cu ? w.base + n : n * s.per_seq);
+    if (w.j < 0 || w.j >= (w.count ? w.count : 1)) {
+        w.count = -1;
+        return w;
+    }
     w.begin += w.j * s.L;
     if (w.end > w.begin + s.L) w.end = w.begin + s.L;
     return w;
@@ -392,7 +411,7 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
         const float f = before > 0 ? (float)exp(lg * segs.L) : 0.f;
         for (int64_t i = folded ? before - 1 : 0; i < before; ++i) {
             // segments in the order of the recurrence; the first one of it may be the sequence's last, with fewer tokens
-            const float* x = op.states + ((w.slot + (op.back ? before - i : i - before)) * H + h) * (int64_t)DA * DC;
+            const float* x = op.states + ((w.base + (op.back ? w.count - 2 - i : i)) * H + h) * (int64_t)DA * DC;
             const float fi = folded ? 0.f : op.back && i == 0 ? (float)exp(lg * w.tail) : f;
 #pragma unroll
             for (int ct = 0; ct < G::CT; ++ct)
@@ -757,7 +776,7 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
                     for (int j = 0; j < 4; ++j) to[state_row(ct, 4 * grp + j) * DC + state_col<ND>(wave, m, d)] = S[ct][d][j];
         }
     } else {
-        float* to = static_cast<float*>(op.out) + (w.slot * H + h) * (int64_t)DA * DC;
+        float* to = static_cast<float*>(op.out) + ((w.base + w.j - (op.back ? 1 : 0)) * H + h) * (int64_t)DA * DC;
 #pragma unroll
         for (int ct = 0; ct < G::CT; ++ct)
 #pragma unroll
@@ -767,7 +786,8 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
 }
 
 // The states behind (with `back` before) each segment from the segments' own ones, in place, for sequences of many segments:
-// X_j = a^length X_(j-1) + U_j.  A thread holds four values of a head's state through all segments.
+// X_j = a^length X_(j-1) + U_j.  A thread holds four values of a head's state through all segments.  A packed sequence of more
+// than kOwnFold segments holds a token whose number is a multiple of kOwnFold L: its first such token stands for it in the grid.
 struct FoldOp {
     float* states;
     const float* x0;
@@ -777,28 +797,27 @@ template <int DA>
 __global__ __launch_bounds__(kThreads) void linattn_fold_kernel(FoldOp op0, FoldOp op1, Segs segs, const float* g, int DC) {
     const FoldOp op = blockIdx.y ? op1 : op0;
     const int size = DA * DC, per = size / (4 * kThreads);
-    const int64_t nh = blockIdx.x / per, n = nh / segs.H;
-    const int h = nh % segs.H, at = (int)(blockIdx.x % per) * 4 * kThreads + 4 * threadIdx.x;
-    const int64_t slot0 = segs.cu ? seq_begin(segs, n) / segs.L + n : n * segs.per_seq;
-    const Where w = where_of(segs, slot0);
-    if (w.n != n || w.count <= kOwnFold) return;
+    const int64_t sh = blockIdx.x / per, token = sh / segs.H * kOwnFold * segs.L;
+    const int h = sh % segs.H, at = (int)(blockIdx.x % per) * 4 * kThreads + 4 * threadIdx.x;
+    const Where w = sequence(segs, segs.cu ? last_below(segs, [&](int64_t begin, int64_t) { return begin <= token; }) : sh / segs.H);
+    if (w.count <= kOwnFold || (segs.cu && (token < w.begin || token - w.begin >= kOwnFold * segs.L))) return;
     const double lg = log_decay(g[h]);
     const float whole = (float)exp(lg * segs.L), tail = (float)exp(lg * w.tail);
     f32x4_t x = {0.f, 0.f, 0.f, 0.f};
     if (op.x0) {
         const int lane = at / 4 % 64, ct = at / 256 % (DA / 16), c = at / (256 * (DA / 16)) * 16 + lane % 16;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = op.x0[nh * size + state_row(ct, lane / 16 * 4 + j) * DC + c];
+        for (int j = 0; j < 4; ++j) x[j] = op.x0[(w.n * segs.H + h) * size + state_row(ct, lane / 16 * 4 + j) * DC + c];
     }
     const int64_t step = (int64_t)segs.H * size;
-    f32x4_t* p = reinterpret_cast<f32x4_t*>(op.states + (slot0 * segs.H + h) * (int64_t)size + at);
+    f32x4_t* p = reinterpret_cast<f32x4_t*>(op.states + (w.base * segs.H + h) * (int64_t)size + at);
     constexpr int AHEAD = 8;
     for (int64_t j0 = 0; j0 < w.count - 1; j0 += AHEAD) {
         f32x4_t u[AHEAD];
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
             const int64_t j = j0 + i < w.count - 1 ? j0 + i : w.count - 2;
-            u[i] = p[(op.back ? w.count - 1 - j : j) * (step / 4)];
+            u[i] = p[(op.back ? w.count - 2 - j : j) * (step / 4)];
         }
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
@@ -807,7 +826,7 @@ __global__ __launch_bounds__(kThreads) void linattn_fold_kernel(FoldOp op0, Fold
             const float f = op.back && j == 0 ? tail : whole;
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[e] = fmaf(f, x[e], u[i][e]);
-            p[(op.back ? w.count - 1 - j : j) * (step / 4)] = x;
+            p[(op.back ? w.count - 2 - j : j) * (step / 4)] = x;
         }
     }
 }
@@ -907,7 +926,8 @@ void chunks(const LinArgs& a, const Segs& s, std::initializer_list<LinOp> ops, i
 
 void fold(const LinArgs& a, const Segs& s, FoldOp one, const FoldOp* two, hipStream_t st) {
     if ((s.cu ? (s.total + s.L - 1) / s.L : s.per_seq) <= kOwnFold) return;
-    const dim3 grid((unsigned)(a.N * a.H * (a.Dk * a.Dv / (4 * kThreads))), two ? 2 : 1);
+    const int64_t sequences = s.cu ? (s.total - 1) / (kOwnFold * s.L) + 1 : s.N;
+    const dim3 grid((unsigned)(sequences * a.H * (a.Dk * a.Dv / (4 * kThreads))), two ? 2 : 1);
     auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, st, one, two ? *two : one, s, a.g, a.Dv); };
     a.Dk == 64 ? run(linattn_fold_kernel<64>) : run(linattn_fold_kernel<128>);
 }
@@ -918,13 +938,13 @@ void fold(const LinArgs& a, const Segs& s, FoldOp one, const FoldOp* two, hipStr
 int64_t linattn_workspace_bytes(const LinArgs& a, bool backward) {
     const int64_t L = segment_tokens(a.total, a.H, true);
     if (a.total <= L) return 0;
-    return (a.total / L + a.N) * a.H * a.Dk * (int64_t)a.Dv * 4 * (backward ? 2 : 1);
+    return a.total / L * a.H * a.Dk * (int64_t)a.Dv * 4 * (backward ? 2 : 1);
 }
 
-int64_t linattn_groups(const LinArgs& a, bool backward) {
-    const Segs s = segs_of(a);
-    const int64_t chunk = (slots_of(s) * a.H + 8) * (backward ? 3 : 1), folds = a.N * a.H * (a.Dk * a.Dv / (4 * kThreads));
-    return chunk > folds ? chunk : folds;
+// Workgroups of the largest launch, and the threads of one at most.  The fold's are fewer: it has a sequence for 8 segments.
+int64_t linattn_threads(const LinArgs& a, bool backward) {
+    const int64_t D = a.Dk > a.Dv ? a.Dk : a.Dv;
+    return (slots_of(segs_of(a)) * a.H + 8) * (backward ? 3 : 1) * (a.f32 ? 4 * D : 256);
 }
 
 hipError_t launch_linattn_fwd(const LinArgs& a, hipStream_t st) {
@@ -941,7 +961,7 @@ hipError_t launch_linattn_fwd(const LinArgs& a, hipStream_t st) {
 hipError_t launch_linattn_bwd(const LinArgs& a, hipStream_t st) {
     const Segs s = segs_of(a);
     float* states = static_cast<float*>(a.ws);
-    float* grads = states + slots_of(s) * a.H * a.Dk * a.Dv;
+    float* grads = states + s.total / s.L * a.H * a.Dk * a.Dv;
     if (is_split(s)) {
         chunks<false>(a, s, {LinOp{nullptr, a.k, a.v, states, nullptr, nullptr, nullptr, false, false, 1.f, 1.f, false},
                              LinOp{nullptr, a.q, a.d_o, grads, nullptr, nullptr, nullptr, false, true, a.scale, 1.f, false}},

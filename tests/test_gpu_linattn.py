@@ -210,6 +210,38 @@ def test_many_sequences_in_one_call():
         assert float((a.double() - b.double()).norm()) <= 4 * 2 ** -8 * float(b.double().norm())
 
 
+SEGMENTS = [[0, 5000], [0, 40, 3000, 3100, 3101], [0, 2500, 2500, 5100], [0, 63, 1500, 1564, 4000], [0, 640, 1280, 1921, 4000]]
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("dk,dv", [(64, 128), (128, 128)])
+@pytest.mark.parametrize("cu", SEGMENTS, ids=lambda c: "_".join(map(str, c)))
+def test_packed_segments(cu, dk, dv, dtype):
+    """Sequences of one, of up to eight and of more segments in one call, ends inside and at segments; decays that reach far."""
+    q, k, v, d_o, g, s0, d_sf = ref.inputs(cu[-1], (cu[-1],), 2, dk, dv, TYPES[dtype], len(cu) - 1, kinds=[-1e-4, -0.004])
+    cu = torch.tensor(cu, dtype=torch.int32)
+    Q, K, V, G, S0, DO, DS, CU = gpu(q, k, v, g, s0, d_o, d_sf, cu)
+    o, sf = kda.linattn_varlen_fwd(Q, K, V, G, CU, S0, scale=0.125)
+    check_fwd(o, sf, q, k, v, g, s0, cu, 0.125, 600)
+    got = kda.linattn_varlen_bwd(Q, K, V, G, CU, DO, S0, DS, scale=0.125)
+    check_bwd(got, q, k, v, g, d_o, s0, d_sf, cu, 0.125, 600)
+
+
+def test_more_sequences_than_a_fold_would_have_workgroups_for():
+    """Over a million sequences of one token: o = scale (q . k) v, and nothing in the way of the grid."""
+    B, H, D = 70000, 16, 128
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    q, k, v = (torch.randn((B, 1, H, D), generator=gen, device="cuda").bfloat16() for _ in range(3))
+    g = torch.full((H,), -0.1, device="cuda")
+    o, _ = kda.linattn_fwd(q, k, v, g, scale=0.25, output_final_state=False)
+    for at in (slice(0, 500), slice(35000, 35500), slice(B - 500, B)):
+        dots = (q[at].double() * k[at].double()).sum(-1, keepdim=True)
+        want = 0.25 * dots * v[at].double()
+        # half a step of bf16, and 128 products, the scale and the score's planes in 24 and 16 bits
+        allowed = want.abs() * 2 ** -8 + 0.25 * (q[at].double() * k[at].double()).abs().sum(-1, keepdim=True) * v[at].double().abs() * 2 ** -15
+        assert bool(((o[at].double() - want).abs() <= allowed + 1e-30).all())
+
+
 @pytest.mark.parametrize("dtype", list(TYPES))
 def test_differences(dtype):
     """o is linear in q, in k, in v and in s0: central differences of the forward call are the gradients, up to rounding."""

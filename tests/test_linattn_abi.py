@@ -96,6 +96,21 @@ def test_linattn_workspace_sizes():
             assert size(1, 1 << 20, 8, 128, 128, dtype) > 0
 
 
+@pytest.mark.parametrize("N,total,H", [(1, 1 << 20, 8), (4096, 4096 * 64, 16), (65536, 65536, 64), (3, 40011, 16), (1, 999, 1),
+                                       (100000, 3000000, 4)])
+def test_linattn_workspace_is_for_what_lies_between_segments(N, total, H):
+    """768 segments of all heads at most have a state to hand on, however many sequences there are."""
+    for size, ways in ((kda.linattn_workspace_bytes, 1), (kda.linattn_bwd_workspace_bytes, 2)):
+        assert size(N, total, H, 64, 128, torch.bfloat16) <= ways * 768 * 64 * 128 * 4
+
+
+def test_linattn_more_workgroups_than_a_grid_has():
+    grid = dict(T=1, H=1, Dk=128, Dv=128, s0=None)  # one workgroup a sequence: of 256 threads in bf16, of 512 in fp32
+    expect("kda_linattn_fwd", FWD, dict(B=1 << 24, **grid), 2, "grid limit")
+    expect("kda_linattn_fwd", FWD, dict(B=9 << 20, dtype=0, **grid), 2, "grid limit")
+    expect("kda_linattn_bwd", BWD, dict(B=3 << 20, dtype=0, d_sfinal=None, **grid), 2, "grid limit")
+
+
 GN = dict(x=FAKE, x_stride=128, weight=FAKE, bias=FAKE, gate=FAKE, gate_stride=128, y=FAKE, tokens=3, groups=2, width=64,
           form=GroupNormForm(1, 1, 1, 1e-5), stream=None)
 GN_BWD = dict(x=FAKE, x_stride=128, weight=FAKE, bias=FAKE, gate=FAKE, gate_stride=128, dy=FAKE, dx=FAKE, dgate=FAKE,
