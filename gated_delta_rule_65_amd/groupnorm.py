@@ -8,13 +8,12 @@ from __future__ import annotations
 
 import ctypes
 import functools
-import math
 from typing import Optional
 
 import torch
 
-from . import DTYPE, _aligned_grad, _first_order, _need, _ptr, load_library
-from .layer import _float, _launch, _same_device, _token_stride, _ws
+from . import DTYPE, _aligned_grad, _first_order, _ptr, load_library
+from .layer import _expect, _float, _launch, _same_device, _token_stride, _ws
 
 ACT = {"none": 0, "silu": 1, "sigmoid": 2}
 
@@ -48,14 +47,15 @@ def _rows(t, name):
     """Elements from one token to the next of [..., C]."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU (got {t.device})")
-    return _token_stride(t.unsqueeze(-2), name)
+    return t.shape[-1] if t.is_contiguous() else _token_stride(t.unsqueeze(-2), name)
 
 
 def _inputs(x, groups, weight, bias, gate, act, eps, dtype):
     _float(x, "x")
-    if x.dim() < 1:
+    size, device = x.shape, x.device
+    if len(size) < 1:
         raise ValueError("x must be [..., C]")
-    C = x.shape[-1]
+    C = size[-1]
     if groups < 1 or C < 1 or C % groups:
         raise ValueError(f"groups must divide the {C} channels (got {groups})")
     if act not in ACT:
@@ -63,20 +63,20 @@ def _inputs(x, groups, weight, bias, gate, act, eps, dtype):
     x_stride, gate_stride = _rows(x, "x"), 0
     if gate is not None:
         _float(gate, "gate")
-        if gate.shape != x.shape:
-            raise ValueError(f"gate has shape {tuple(gate.shape)}, expected {tuple(x.shape)}")
+        if gate.shape != size:
+            raise ValueError(f"gate has shape {tuple(gate.shape)}, expected {tuple(size)}")
         if dtype is not None and gate.dtype != dtype:
             raise TypeError(f"gate must have the outputs' type {dtype} (got {gate.dtype})")
         dtype, gate_stride = gate.dtype, _rows(gate, "gate")
+        _same_device(device, gate=gate)
     dtype = x.dtype if dtype is None else dtype
     if dtype not in DTYPE:
         raise TypeError(f"dtype must be float32 or bfloat16 (got {dtype})")
     for t, name in ((weight, "weight"), (bias, "bias")):
         if t is not None:
-            _need(t, name, torch.float32, (C,))
-    _same_device(x.device, weight=weight, bias=bias, gate=gate)
+            _expect(t, name, torch.float32, (C,), device)
     args = (_ptr(x), x_stride, _ptr(weight), _ptr(bias), _ptr(gate), gate_stride)
-    return args, math.prod(x.shape[:-1]), C // groups, dtype, _form(x.dtype, dtype, act, float(eps))
+    return args, x.numel() // C, C // groups, dtype, _form(x.dtype, dtype, act, float(eps))
 
 
 def group_norm_act_fwd(x: torch.Tensor, groups: int, *, weight: Optional[torch.Tensor] = None,
@@ -90,7 +90,7 @@ def group_norm_act_fwd(x: torch.Tensor, groups: int, *, weight: Optional[torch.T
     in ``dtype`` (default: x's).  act: ``"silu"``, ``"sigmoid"`` or ``"none"``.
     """
     args, tokens, width, dtype, form = _inputs(x, groups, weight, bias, gate, act, eps, dtype)
-    y = torch.empty(x.shape, dtype=dtype, device=x.device)
+    y = torch.empty_like(x, dtype=dtype, memory_format=torch.contiguous_format)
     _launch(load_library().kda_groupnorm_fwd, x.device, *args, _ptr(y), tokens, groups, width, form)
     return y
 
@@ -103,10 +103,9 @@ def group_norm_act_bwd(x: torch.Tensor, groups: int, dy: torch.Tensor, *, weight
     what was not given."""
     _float(dy, "dy")
     args, tokens, width, dtype, form = _inputs(x, groups, weight, bias, gate, act, eps, dy.dtype)
-    _need(dy, "dy", dtype, x.shape)
-    _same_device(x.device, dy=dy)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    dgate = torch.empty(x.shape, dtype=dtype, device=x.device) if gate is not None else None
+    _expect(dy, "dy", dtype, x.shape, x.device)
+    dx = torch.empty_like(x, memory_format=torch.contiguous_format)
+    dgate = torch.empty_like(dy) if gate is not None else None
     dw = db = None
     ws, ws_bytes = None, 0
     if weight is not None or bias is not None:

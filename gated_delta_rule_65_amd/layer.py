@@ -77,6 +77,14 @@ def _same_device(device, **tensors):
             raise ValueError(f"{name} must be on {device} (got {t.device})")
 
 
+def _expect(t, name, dtype, shape, device):
+    """A contiguous tensor of this type, shape (a torch.Size) and GPU: what is as it should be is told in one look."""
+    if not (isinstance(t, torch.Tensor) and t.get_device() == device.index and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous()):
+        _need(t, name, dtype, shape)
+        _same_device(device, **{name: t})
+
+
 def _float(t, name):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")

@@ -12,7 +12,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import DTYPE, _aligned_grad, _first_order, _need, _ptr, layer, load_library
-from .layer import _launch, _same_device, _seqs, _ws
+from .layer import _expect, _launch, _same_device, _seqs, _ws
 
 
 def declare(L):
@@ -39,37 +39,38 @@ def linattn_bwd_workspace_bytes(N: int, total: int, H: int, Dk: int, Dv: int, dt
     return int(load_library().kda_linattn_bwd_workspace_bytes(N, total, H, Dk, Dv, DTYPE[dtype]))
 
 
-def _inputs(q, k, v, g, states, lead):
-    """Checks q, k, v, g and the named states; returns the leading sizes, H, Dk, Dv."""
-    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+def _inputs(q, k, v, g, lead):
+    """Checks q, k, v and g; returns the leading sizes, H, Dk, Dv."""
+    for t, name in ((q, "q"), (v, "v")):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
-    if q.dim() != lead + 2:
-        raise ValueError(f"q must be [{'B, T, ' if lead == 2 else ''}H, Dk]")
-    if q.dtype not in DTYPE:
-        raise TypeError(f"q, k and v must be float32 or bfloat16 (got {q.dtype})")
-    *front, H, Dk = q.shape
-    if v.dim() != q.dim():
+    dtype, size = q.dtype, q.shape
+    if len(size) != lead + 2:
+        raise ValueError(f"q must be [{'B, T' if lead == 2 else 'B or total'}, H, Dk]")
+    if dtype not in DTYPE:
+        raise TypeError(f"q, k and v must be float32 or bfloat16 (got {dtype})")
+    *front, H, Dk = size
+    if v.dim() != lead + 2:
         raise ValueError(f"v has shape {tuple(v.shape)}, expected {(*front, H)} and its own head size")
-    Dv = v.shape[-1]
-    _need(q, "q", q.dtype)
-    _need(k, "k", q.dtype, (*front, H, Dk))
-    _need(v, "v", q.dtype, (*front, H, Dv))
-    _need(g, "g", torch.float32, (H,))
-    _same_device(q.device, k=k, v=v, g=g, **states)
+    Dv, device = v.shape[-1], q.device
+    _need(q, "q", dtype)
+    _expect(k, "k", dtype, size, device)
+    _expect(v, "v", dtype, size if Dv == Dk else (*front, H, Dv), device)
+    _expect(g, "g", torch.float32, (H,), device)
     return front, H, Dk, Dv
 
 
-def _state_like(t, name, shape):
+def _state_like(t, name, shape, device):
     if t is not None:
-        _need(t, name, torch.float32, shape)
+        _expect(t, name, torch.float32, shape, device)
 
 
 def _fwd(q, k, v, g, cu, s0, scale, output_final_state, workspace):
     packed = cu is not None
-    front, H, Dk, Dv = _inputs(q, k, v, g, {"s0": s0, "cu_seqlens": cu}, 1 if packed else 2)
+    front, H, Dk, Dv = _inputs(q, k, v, g, 1 if packed else 2)
     N, total = (_seqs(cu), front[0]) if packed else (front[0], front[0] * front[1])
-    _state_like(s0, "s0", (N, H, Dk, Dv))
+    _same_device(q.device, cu_seqlens=cu)
+    _state_like(s0, "s0", (N, H, Dk, Dv), q.device)
     o = torch.empty(v.shape, dtype=q.dtype, device=q.device)
     sf = torch.empty((N, H, Dk, Dv), dtype=torch.float32, device=q.device) if output_final_state else None
     ws, ws_bytes = _ws(linattn_workspace_bytes(N, total, H, Dk, Dv, q.dtype), workspace, q.device)
@@ -107,12 +108,12 @@ def linattn_varlen_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: tor
 
 def _bwd(q, k, v, g, cu, d_o, s0, d_sfinal, scale, workspace):
     packed = cu is not None
-    front, H, Dk, Dv = _inputs(q, k, v, g, {"d_o": d_o, "s0": s0, "d_sfinal": d_sfinal, "cu_seqlens": cu},
-                               1 if packed else 2)
+    front, H, Dk, Dv = _inputs(q, k, v, g, 1 if packed else 2)
     N, total = (_seqs(cu), front[0]) if packed else (front[0], front[0] * front[1])
-    _need(d_o, "d_o", q.dtype, v.shape)
-    _state_like(s0, "s0", (N, H, Dk, Dv))
-    _state_like(d_sfinal, "d_sfinal", (N, H, Dk, Dv))
+    _same_device(q.device, cu_seqlens=cu)
+    _expect(d_o, "d_o", q.dtype, v.shape, q.device)
+    _state_like(s0, "s0", (N, H, Dk, Dv), q.device)
+    _state_like(d_sfinal, "d_sfinal", (N, H, Dk, Dv), q.device)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     ds0 = torch.empty((N, H, Dk, Dv), dtype=torch.float32, device=q.device)
     ws, ws_bytes = _ws(linattn_bwd_workspace_bytes(N, total, H, Dk, Dv, q.dtype), workspace, q.device)
@@ -149,8 +150,8 @@ def linattn_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Ten
                  scale: float = 1.0, inplace: bool = False) -> Tuple[torch.Tensor, torch.Tensor]:
     """One token per sequence: q, k [B, H, Dk], v [B, H, Dv], state (fp32) [B, H, Dk, Dv].  Returns o [B, H, Dv] (q's type)
     and the new state (``state`` itself when ``inplace``)."""
-    (B,), H, Dk, Dv = _inputs(q, k, v, g, {"state": state}, 1)
-    _need(state, "state", torch.float32, (B, H, Dk, Dv))
+    (B,), H, Dk, Dv = _inputs(q, k, v, g, 1)
+    _expect(state, "state", torch.float32, (B, H, Dk, Dv), q.device)
     o = torch.empty_like(v)
     out = state if inplace else torch.empty_like(state)
     _launch(load_library().kda_linattn_step, q.device, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state), _ptr(out), _ptr(o),
