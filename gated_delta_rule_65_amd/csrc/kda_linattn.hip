@@ -123,7 +123,6 @@ struct LinOp {
     bool turned;            // states and x0 are taken transposed
     bool back;
     float su, so;           // scales of the state's products, and of the outputs
-    bool stream;            // rows go past the caches
 };
 
 template <bool F32>
@@ -248,14 +247,6 @@ __device__ __forceinline__ int place(int row, int unit) {
 // Four values of one column of a bf16 tile: lane i of 16 gives the place of four values of row i/4, and gets column i.
 __device__ __forceinline__ bf16x4_t read_turned(const char* p) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4bf16((__attribute__((address_space(3))) bf16x4_t*)const_cast<char*>(p));
-}
-
-typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
-template <typename V>
-__device__ __forceinline__ void put(char* p, V v, bool stream) {
-    if (stream) __builtin_nontemporal_store(v, reinterpret_cast<V*>(p));
-    else *reinterpret_cast<V*>(p) = v;
 }
 
 // The count of s_waitcnt that lets `vm` requests of memory be under way, and none of LDS.
@@ -698,11 +689,11 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
             for (int r = 0; r < G::RB; ++r)
                 if (!LAST || 16 * r + m < n) {
                     char* p = to + (int64_t)(16 * r * pitch) + mine;
-                    if constexpr (F32) put(p, O[r][0], op.stream);
+                    if constexpr (F32) *reinterpret_cast<f32x4_t*>(p) = O[r][0];
                     else if constexpr (ND == 2)
-                        put(p, u32x4_t{pack2(O[r][0][0], O[r][0][1]), pack2(O[r][0][2], O[r][0][3]),
-                                       pack2(O[r][1][0], O[r][1][1]), pack2(O[r][1][2], O[r][1][3])}, op.stream);
-                    else put(p, u32x2_t{pack2(O[r][0][0], O[r][0][1]), pack2(O[r][0][2], O[r][0][3])}, op.stream);
+                        *reinterpret_cast<uint4*>(p) = make_uint4(pack2(O[r][0][0], O[r][0][1]), pack2(O[r][0][2], O[r][0][3]),
+                                                                  pack2(O[r][1][0], O[r][1][1]), pack2(O[r][1][2], O[r][1][3]));
+                    else *reinterpret_cast<uint2*>(p) = make_uint2(pack2(O[r][0][0], O[r][0][1]), pack2(O[r][0][2], O[r][0][3]));
                 }
             __asm__ volatile("" ::: "memory");
         } else {
@@ -903,10 +894,6 @@ bool is_split(const Segs& s) { return s.cu ? s.total > s.L : s.per_seq > 1; }
 using I64 = std::integral_constant<int, 64>;
 using I128 = std::integral_constant<int, 128>;
 
-// Outputs past the caches where they and the inputs do not fit there anyway: they then keep what the two passes share (1M tokens
-// of a head in all 406 -> 390 us).
-bool streams(const LinArgs& a) { return a.total * a.H * (a.Dk + a.Dv) * (a.f32 ? 8 : 4) >= 2 * kStreamBytes; }
-
 template <bool ROWS>
 void chunks(const LinArgs& a, const Segs& s, std::initializer_list<LinOp> ops, int DA, int DC, hipStream_t st) {
     LinOp op[3] = {};
@@ -951,10 +938,10 @@ hipError_t launch_linattn_fwd(const LinArgs& a, hipStream_t st) {
     const Segs s = segs_of(a);
     float* states = static_cast<float*>(a.ws);
     if (is_split(s)) {
-        chunks<false>(a, s, {LinOp{nullptr, a.k, a.v, states, nullptr, nullptr, nullptr, false, false, 1.f, 1.f, false}}, a.Dk, a.Dv, st);
+        chunks<false>(a, s, {LinOp{nullptr, a.k, a.v, states, nullptr, nullptr, nullptr, false, false, 1.f, 1.f}}, a.Dk, a.Dv, st);
         fold(a, s, FoldOp{states, a.s0, false}, nullptr, st);
     }
-    chunks<true>(a, s, {LinOp{a.q, a.k, a.v, a.o, a.s0, states, a.s_final, false, false, 1.f, a.scale, streams(a)}}, a.Dk, a.Dv, st);
+    chunks<true>(a, s, {LinOp{a.q, a.k, a.v, a.o, a.s0, states, a.s_final, false, false, 1.f, a.scale}}, a.Dk, a.Dv, st);
     return hipGetLastError();
 }
 
@@ -963,15 +950,15 @@ hipError_t launch_linattn_bwd(const LinArgs& a, hipStream_t st) {
     float* states = static_cast<float*>(a.ws);
     float* grads = states + s.total / s.L * a.H * a.Dk * a.Dv;
     if (is_split(s)) {
-        chunks<false>(a, s, {LinOp{nullptr, a.k, a.v, states, nullptr, nullptr, nullptr, false, false, 1.f, 1.f, false},
-                             LinOp{nullptr, a.q, a.d_o, grads, nullptr, nullptr, nullptr, false, true, a.scale, 1.f, false}},
+        chunks<false>(a, s, {LinOp{nullptr, a.k, a.v, states, nullptr, nullptr, nullptr, false, false, 1.f, 1.f},
+                             LinOp{nullptr, a.q, a.d_o, grads, nullptr, nullptr, nullptr, false, true, a.scale, 1.f}},
                       a.Dk, a.Dv, st);
         const FoldOp two{grads, a.d_sfinal, true};
         fold(a, s, FoldOp{states, a.s0, false}, &two, st);
     }
-    const LinOp dq{a.d_o, a.v, a.k, a.dq, a.s0, states, nullptr, true, false, 1.f, a.scale, streams(a)};
-    const LinOp dk{a.v, a.d_o, a.q, a.dk, a.d_sfinal, grads, nullptr, true, true, a.scale, 1.f, streams(a)};
-    const LinOp dv{a.k, a.q, a.d_o, a.dv, a.d_sfinal, grads, a.ds0, false, true, a.scale, 1.f, streams(a)};
+    const LinOp dq{a.d_o, a.v, a.k, a.dq, a.s0, states, nullptr, true, false, 1.f, a.scale};
+    const LinOp dk{a.v, a.d_o, a.q, a.dk, a.d_sfinal, grads, nullptr, true, true, a.scale, 1.f};
+    const LinOp dv{a.k, a.q, a.d_o, a.dv, a.d_sfinal, grads, a.ds0, false, true, a.scale, 1.f};
     if (a.Dk == a.Dv) {
         chunks<true>(a, s, {dq, dk, dv}, a.Dk, a.Dv, st);
     } else {
