@@ -17,6 +17,7 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
+#define KDA_INLINE __attribute__((always_inline))  // a state that a call is given by reference would lie in memory
 
 // The log of a head's decay: e^-10000 is zero in 32 bits, and has powers where minus infinity has none; a NaN stays one.
 __device__ __forceinline__ float log_decay(float g) { return g > 0.f ? 0.f : g < -1e4f ? -1e4f : g; }
@@ -123,6 +124,7 @@ struct LinOp {
     bool turned;            // states and x0 are taken transposed
     bool back;
     float su, so;           // scales of the state's products, and of the outputs
+    bool whole;             // the state behind the last segment is one in 32 bits
 };
 
 template <bool F32>
@@ -269,7 +271,10 @@ struct LinTile {
     static constexpr int KB = C * UA * 16, VB = C * UC * 16;
     static constexpr int KS = C / 32, RB = C / 16, AS = DA / 32, CT = DA / 16;
     static constexpr int PL = F32 ? 1 : 2;       // planes of scores and of the state
-    static constexpr int VL = F32 ? 1 : 3;       // planes of the weighted values
+    // Planes of the weighted values: three hold all of their 24 bits.  In the outputs' pass two do where no state is given out
+    // behind the segment: outputs of 16 bits do not show what is left out (the state is off by 3e-6 instead of 3e-7), and it is
+    // a sixth of the products (backward of B=4 T=4096 H=16 D=128 204 -> 195 us).
+    static constexpr int VL = F32 ? 1 : 3;
     static constexpr int PB = F32 ? 32 * 128 : 32 * 64 + 32 * 128;  // a plane of scores: rows up to their diagonal's 32 tokens
 };
 
@@ -335,12 +340,12 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
     // caches what that pass reads first.
     const bool back = op.back == ROWS;
     const int64_t row0 = back ? w.end - 1 : w.begin;
-    auto offset_of = [&](auto units) {
+    auto offset_of = [&](auto units) KDA_INLINE {
         constexpr int U = decltype(units)::value;
         const int r = tid / U;
         return (uint32_t)((back ? C - 1 - r : r) * H * U + (tid % U ^ turn<U, F32>(r))) * 16u;
     };
-    auto fetch = [&](const void* from, char* to, int c, auto units, uint32_t offset) {
+    auto fetch = [&](const void* from, char* to, int c, auto units, uint32_t offset) KDA_INLINE {
         constexpr int U = decltype(units)::value, N = C * U / THREADS, STEP = THREADS / U;
         static_assert(N * THREADS == C * U && (STEP % 16 == 0 || (F32 && STEP == 8)), "a row's turn is that of 16 rows before");
         constexpr int other = STEP == 8 ? 8 : 0;
@@ -451,7 +456,7 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
     int at_score = F32 ? place<8, true>(m, 2 * grp) : place<4, false>(m, grp);
     int at_score2 = F32 ? 0 : 2048 + place<8, false>(m, grp);
     int at_power = m, at_far = 16 - 4 * grp;  // of the decay's powers
-    auto frag = [&](const char* tile, int r, int s) {
+    auto frag = [&](const char* tile, int r, int s) KDA_INLINE {
         LFrag<F32> f;
         if constexpr (F32) {
             const f32x4_t x = *reinterpret_cast<const f32x4_t*>(tile + (at_row ^ (128 * s)) + 16 * RA * r);
@@ -464,7 +469,7 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
         return f;
     };
     // the channels of a tile of the state over 32 tokens: group g holds tokens 4g .. +3 and 16 + 4g .. +3
-    auto frag_bt = [&](const char* tile, int ct, int ks) {
+    auto frag_bt = [&](const char* tile, int ct, int ks) KDA_INLINE {
         LFrag<F32> f;
         if constexpr (F32) {
 #pragma unroll
@@ -477,7 +482,7 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
         }
         return f;
     };
-    auto frag_ct = [&](const char* tile, int d, int ks) {
+    auto frag_ct = [&](const char* tile, int d, int ks) KDA_INLINE {
         LFrag<F32> f;
         if constexpr (F32) {
 #pragma unroll
@@ -490,9 +495,11 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
         return f;
     };
 
+    const bool three = op.whole && last;
+
     // One chunk with its keys in K; those of the next one go to Kn, if there is one: only the last chunk may have fewer tokens
     // than C.  Which requests are under way is the same on every path, so that the compiler sees what has been waited for.
-    auto chunk = [&](int c, char* K, char* Kn, char* V, char* Vn, auto ends) {
+    auto chunk = [&](int c, char* K, char* Kn, char* V, char* Vn, auto ends) KDA_INLINE {
         constexpr bool LAST = decltype(ends)::value;
         const int n = LAST ? tokens - c * C : C;
         // the places of a chunk's fragments are made again from these few: kept, they would take most of the registers
@@ -520,7 +527,7 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
         }
 
         LFrag<F32> vf[G::KS * ND];
-        auto read_values = [&]() {
+        auto read_values = [&]() KDA_INLINE {
 #pragma unroll
             for (int ks = 0; ks < G::KS; ++ks)
 #pragma unroll
@@ -532,7 +539,7 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
             // The scores are the first waves' (every SIMD has one of them), with the products of the state where all waves are.
             constexpr bool TOGETHER = G::WAVES == G::RB;
             f32x4_t O[G::RB][ND], P[G::RB];
-            auto scores = [&]() {
+            auto scores = [&]() KDA_INLINE {
                 // Of row 16r + m against token 16i + 4 grp + j with i = wave: a^(16(r-i)-4 grp-j) a^m above the diagonal's tile; in
                 // it a^(m-4 grp-j) and nothing above the diagonal; rows of the products' 32 tokens behind it: zeros.
                 float part = sp * powers[at_power];
@@ -701,7 +708,7 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
         }
 
         __builtin_amdgcn_s_setprio(0);
-        // the weighted values as sums of three bf16 values, which hold all of their 24 bits
+        // the weighted values as sums of two or three bf16 values
 #pragma unroll
         for (int ks = 0; ks < G::KS; ++ks) {
             f32x4_t w0 = *reinterpret_cast<const f32x4_t*>(weights[LAST] + 32 * ks + 4 * grp);
@@ -710,7 +717,8 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
 #pragma unroll
                 for (int j = 0; j < 4; ++j) w0[j] *= left, w1[j] *= left;
             constexpr int TOGETHER = F32 ? 2 : 4;  // tiles of the state: as many as the registers hold
-            LFrag<F32> vb[ND][G::VL], kt[TOGETHER];
+            constexpr int VL = ROWS && !F32 ? 2 : G::VL;
+            LFrag<F32> vb[ND][VL], rest[ND], kt[TOGETHER];
 #pragma unroll
             for (int ct = 0; ct < TOGETHER; ++ct) kt[ct] = frag_bt(K, ct, ks);
 #pragma unroll
@@ -719,7 +727,17 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
                 values(vf[ks * ND + d], x);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) x[j] *= w0[j], x[4 + j] *= w1[j];
-                split<G::VL>(x, vb[d], ones);
+                split<VL>(x, vb[d], ones);
+                if constexpr (VL < G::VL)
+                    if (three) {
+                        const uint4 a = __builtin_bit_cast(uint4, vb[d][0].v), b = __builtin_bit_cast(uint4, vb[d][1].v);
+                        uint4 u;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            (&u.x)[j] = pack2(less_low(less_low(x[2 * j], (&a.x)[j], ones), (&b.x)[j], ones),
+                                              less_high(less_high(x[2 * j + 1], (&a.x)[j], ones), (&b.x)[j], ones));
+                        rest[d].v = __builtin_bit_cast(bf16x8_t, u);
+                    }
             }
 #pragma unroll
             for (int first = 0; first < G::CT; first += TOGETHER) {
@@ -727,11 +745,18 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
 #pragma unroll
                     for (int ct = 0; ct < TOGETHER; ++ct) kt[ct] = frag_bt(K, first + ct, ks);
 #pragma unroll
-                for (int p = 0; p < G::VL; ++p)
+                for (int p = 0; p < VL; ++p)
 #pragma unroll
                     for (int ct = 0; ct < TOGETHER; ++ct)
 #pragma unroll
                         for (int d = 0; d < ND; ++d) S[first + ct][d] = mma(kt[ct], vb[d][p], S[first + ct][d]);
+                if constexpr (VL < G::VL)
+                    if (three) {
+#pragma unroll
+                        for (int ct = 0; ct < TOGETHER; ++ct)
+#pragma unroll
+                            for (int d = 0; d < ND; ++d) S[first + ct][d] = mma(kt[ct], rest[d], S[first + ct][d]);
+                    }
             }
         }
         if (ROWS && marked) {
@@ -746,8 +771,8 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
     };
 
     char* const ldsVn = ROWS ? ldsV0 : ldsV1;
-    int c = 0;
     __builtin_amdgcn_s_waitcnt(waitcnt(0));
+    int c = 0;
     while (true) {
         if (c + 1 >= chunks) break;
         chunk(c++, ldsK0, ldsK1, ldsV0, ldsVn, std::false_type());
@@ -938,10 +963,10 @@ hipError_t launch_linattn_fwd(const LinArgs& a, hipStream_t st) {
     const Segs s = segs_of(a);
     float* states = static_cast<float*>(a.ws);
     if (is_split(s)) {
-        chunks<false>(a, s, {LinOp{nullptr, a.k, a.v, states, nullptr, nullptr, nullptr, false, false, 1.f, 1.f}}, a.Dk, a.Dv, st);
+        chunks<false>(a, s, {LinOp{nullptr, a.k, a.v, states, nullptr, nullptr, nullptr, false, false, 1.f, 1.f, false}}, a.Dk, a.Dv, st);
         fold(a, s, FoldOp{states, a.s0, false}, nullptr, st);
     }
-    chunks<true>(a, s, {LinOp{a.q, a.k, a.v, a.o, a.s0, states, a.s_final, false, false, 1.f, a.scale}}, a.Dk, a.Dv, st);
+    chunks<true>(a, s, {LinOp{a.q, a.k, a.v, a.o, a.s0, states, a.s_final, false, false, 1.f, a.scale, true}}, a.Dk, a.Dv, st);
     return hipGetLastError();
 }
 
@@ -950,15 +975,15 @@ hipError_t launch_linattn_bwd(const LinArgs& a, hipStream_t st) {
     float* states = static_cast<float*>(a.ws);
     float* grads = states + s.total / s.L * a.H * a.Dk * a.Dv;
     if (is_split(s)) {
-        chunks<false>(a, s, {LinOp{nullptr, a.k, a.v, states, nullptr, nullptr, nullptr, false, false, 1.f, 1.f},
-                             LinOp{nullptr, a.q, a.d_o, grads, nullptr, nullptr, nullptr, false, true, a.scale, 1.f}},
+        chunks<false>(a, s, {LinOp{nullptr, a.k, a.v, states, nullptr, nullptr, nullptr, false, false, 1.f, 1.f, false},
+                             LinOp{nullptr, a.q, a.d_o, grads, nullptr, nullptr, nullptr, false, true, a.scale, 1.f, false}},
                       a.Dk, a.Dv, st);
         const FoldOp two{grads, a.d_sfinal, true};
         fold(a, s, FoldOp{states, a.s0, false}, &two, st);
     }
-    const LinOp dq{a.d_o, a.v, a.k, a.dq, a.s0, states, nullptr, true, false, 1.f, a.scale};
-    const LinOp dk{a.v, a.d_o, a.q, a.dk, a.d_sfinal, grads, nullptr, true, true, a.scale, 1.f};
-    const LinOp dv{a.k, a.q, a.d_o, a.dv, a.d_sfinal, grads, a.ds0, false, true, a.scale, 1.f};
+    const LinOp dq{a.d_o, a.v, a.k, a.dq, a.s0, states, nullptr, true, false, 1.f, a.scale, false};
+    const LinOp dk{a.v, a.d_o, a.q, a.dk, a.d_sfinal, grads, nullptr, true, true, a.scale, 1.f, false};
+    const LinOp dv{a.k, a.q, a.d_o, a.dv, a.d_sfinal, grads, a.ds0, false, true, a.scale, 1.f, true};
     if (a.Dk == a.Dv) {
         chunks<true>(a, s, {dq, dk, dv}, a.Dk, a.Dv, st);
     } else {
