@@ -4,6 +4,9 @@
 // A group of a token goes to P lanes of ITER pieces of CPL channels each, held in registers between the mean, the sum of
 // squares around it and the outputs, so that memory is read and written once.  A thread keeps its channels over the tokens
 // of its workgroup: weights are read once, and the weights' gradients are sums in registers until the workgroup's end.
+//
+// Memory bounds it: 32768 x 16 x 128 with weights and a gate, from fp32 to bf16 in 92 us (5.8 TB/s; a copy of as many bytes
+// takes 86), in bf16 62 us forward (6.4 TB/s) and 117 backward (5.7 TB/s).
 #pragma once
 #include <type_traits>
 

@@ -68,8 +68,8 @@ def magnitude(f, *tensors, **kw):
 def bound(dtype, ref, size, steps):
     """How far a result of `dtype` may be off: half a step of its own rounding, and of the sums before it one rounding of 32
     bits for each of at most `steps` additions on the way of a term, which has at most the magnitude `size`.  Products of
-    16-bit operands take both as pairs of 16-bit numbers, off by at most half a step of half a step (2^-16) each: of the
-    scores, and of the state."""
+    16-bit operands take both as pairs of 16-bit numbers, off by at most half a step of half a step (2^-16) each: a term goes
+    through its score, or through its weighted value and the state, two at most."""
     own = HALF[dtype] * ref.abs()
     return own + (steps * 2.0 ** -24 + (2 * 2.0 ** -16 if dtype == torch.bfloat16 else 0.0)) * size * (1 + HALF[dtype]) + 1e-37
 
