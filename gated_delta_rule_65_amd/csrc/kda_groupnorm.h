@@ -15,10 +15,10 @@
 
 namespace kda {
 
-// Blocks of tokens in whose sums the weights' gradients are added up: of 16 tokens at least, so that they are small beside the
-// rows, and two workgroups for a CU where there is one for each (32768 x 16 x 128 in bf16, backward: 122 us with 512, 156 with
+// Blocks of tokens in whose sums the weights' gradients are added up: of 8 tokens at least, so that they are small beside the
+// rows (4099 x 12 x 90 fp32, backward: 15.4 us with 8, 18.8 with 16, 15.4 with 4), and two workgroups for a CU where there is one for each (32768 x 16 x 128 in bf16, backward: 122 us with 512, 156 with
 // 256, 131 with 768 and 148 with 1024).
-constexpr int64_t kGnBlocks = 512, kGnBlockTokens = 16;
+constexpr int64_t kGnBlocks = 512, kGnBlockTokens = 8;
 // the sums of the workspace's blocks
 void groupnorm_sums(const GroupNormArgs& a, int64_t blocks, hipStream_t st);
 
@@ -47,10 +47,15 @@ __device__ __forceinline__ void gn_put(void* p, V v, bool stream) {
     }
 }
 
+typedef __bf16 gn_bf16x2 __attribute__((ext_vector_type(2)));
+typedef float gn_f32x2 __attribute__((ext_vector_type(2)));
+
 template <int N, bool F32>
 struct GnRaw {
-    using Word = std::conditional_t<N * (F32 ? 4 : 2) >= 16, uint4, std::conditional_t<F32, uint32_t, uint16_t>>;
-    Word w[N * (F32 ? 4 : 2) >= 16 ? N * (F32 ? 4 : 2) / 16 : N];
+    static constexpr int BYTES = N * (F32 ? 4 : 2);
+    using Word = std::conditional_t<BYTES >= 16, uint4,
+                                    std::conditional_t<BYTES == 8, uint2, std::conditional_t<BYTES == 4, uint32_t, uint16_t>>>;
+    Word w[BYTES >= 16 ? BYTES / 16 : 1];
 };
 template <int N, bool F32>
 __device__ __forceinline__ GnRaw<N, F32> gn_load(const void* p, int64_t at) {
@@ -65,6 +70,9 @@ template <int N, bool F32>
 __device__ __forceinline__ void gn_values(const GnRaw<N, F32>& r, float x[N]) {
     if constexpr (N == 1) {
         x[0] = F32 ? __uint_as_float(r.w[0]) : __uint_as_float((uint32_t)r.w[0] << 16);
+    } else if constexpr (N == 2 && !F32) {
+        x[0] = __uint_as_float(r.w[0] << 16);
+        x[1] = __uint_as_float(r.w[0] & 0xffff0000u);
     } else {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
@@ -73,14 +81,15 @@ __device__ __forceinline__ void gn_values(const GnRaw<N, F32>& r, float x[N]) {
         }
     }
 }
-typedef __bf16 gn_bf16x2 __attribute__((ext_vector_type(2)));
-typedef float gn_f32x2 __attribute__((ext_vector_type(2)));
 template <int N, bool F32>
 __device__ __forceinline__ void gn_store(void* p, int64_t at, const float x[N], bool stream = false) {
     char* q = static_cast<char*>(p) + at * (F32 ? 4 : 2);
     if constexpr (N == 1) {
         if constexpr (F32) *reinterpret_cast<float*>(q) = x[0];
         else *reinterpret_cast<__bf16*>(q) = (__bf16)x[0];
+    } else if constexpr (N == 2) {
+        if constexpr (F32) *reinterpret_cast<gn_f32x2*>(q) = gn_f32x2{x[0], x[1]};
+        else *reinterpret_cast<gn_bf16x2*>(q) = __builtin_convertvector(gn_f32x2{x[0], x[1]}, gn_bf16x2);
     } else if constexpr (F32) {
 #pragma unroll
         for (int i = 0; i < N / 4; ++i) gn_put(q + 16 * i, f32x4_t{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]}, stream);
@@ -274,20 +283,40 @@ __global__ __launch_bounds__(kGnThreads) void groupnorm_kernel(GroupNormArgs a, 
     }
 }
 
+// Channels that are read at a time: 8 where the call's form promises them, else 2 where they lie so (4099 x 12 x 90 fp32:
+// forward 11.7 -> 10.4 us, backward 19.3 -> 18.6), else one.
+inline int gn_piece(const GroupNormArgs& a) {
+    if (groupnorm_wide(a)) return 8;
+    auto odd = [](const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes; };
+    const int xb = a.x_f32 ? 8 : 4, yb = a.y_f32 ? 8 : 4;
+    return a.width % 2 || a.x_stride % 2 || a.gate_stride % 2 || odd(a.x, xb) || odd(a.dx, xb) || odd(a.gate, yb) || odd(a.y, yb) ||
+                   odd(a.dy, yb) || odd(a.dgate, yb) || odd(a.weight, 8) || odd(a.bias, 8)
+               ? 1
+               : 2;
+}
+
 // Lanes and pieces of a row: the fewest lanes that hold it.
 template <typename F>
-void gn_shape(bool wide, int64_t width, F&& f) {
+void gn_shape(int piece, int64_t width, F&& f) {
     auto run = [&](auto cpl, auto p, auto iter) { f(cpl, p, iter); };
     auto i = [](auto v) { return v; };
 #define KDA_GN(CPL, P, ITER) \
     run(i(std::integral_constant<int, CPL>()), i(std::integral_constant<int, P>()), i(std::integral_constant<int, ITER>()))
-    if (wide) {
+    if (piece == 8) {
         if (width <= 64) KDA_GN(8, 8, 1);
         else if (width <= 128) KDA_GN(8, 16, 1);
         else if (width <= 256) KDA_GN(8, 32, 1);
         else if (width <= 512) KDA_GN(8, 64, 1);
         else if (width <= 1024) KDA_GN(8, 64, 2);
         else KDA_GN(8, 64, 4);
+    } else if (piece == 2) {
+        if (width <= 32) KDA_GN(2, 16, 1);
+        else if (width <= 64) KDA_GN(2, 32, 1);
+        else if (width <= 96) KDA_GN(2, 16, 3);
+        else if (width <= 128) KDA_GN(2, 32, 2);
+        else if (width <= 256) KDA_GN(2, 32, 4);
+        else if (width <= 512) KDA_GN(2, 64, 4);
+        else KDA_GN(2, 64, 8);
     } else {
         if (width <= 16) KDA_GN(1, 16, 1);
         else if (width <= 32) KDA_GN(1, 32, 1);
@@ -324,16 +353,17 @@ inline GnPlan gn_plan(const GroupNormArgs& a, int lanes, int64_t places, int64_t
 }  // namespace
 
 // Workgroups of a forward pass: rows of fp32 have twice the bytes (32768 x 16 x 128, to bf16: 94 us with 8192, 98 with 4096 from fp32,
-// 65 and 62 from bf16).
+// 65 and 62 from bf16).  Of two tokens each, the second one's loads beside the first one's work (4099 x 12 x 90 fp32: 10.5 -> 9.4 us),
+// where one each would not fit on the chip at once anyway.
 template <bool XF>
 constexpr int64_t kGnForward = XF ? 8192 : 4096;
 
 template <bool XF, bool YF, bool BWD>
 void groupnorm_launch(const GroupNormArgs& a, hipStream_t st) {
-    gn_shape(groupnorm_wide(a), a.width, [&](auto cpl, auto p, auto iter) {
+    gn_shape(gn_piece(a), a.width, [&](auto cpl, auto p, auto iter) {
         constexpr int CPL = decltype(cpl)::value, P = decltype(p)::value, ITER = decltype(iter)::value;
         int64_t columns;
-        const GnPlan plan = BWD ? gn_plan(a, P, kGnBlocks, kGnBlockTokens, columns) : gn_plan(a, P, kGnForward<XF>, 1, columns);
+        const GnPlan plan = BWD ? gn_plan(a, P, kGnBlocks, kGnBlockTokens, columns) : gn_plan(a, P, kGnForward<XF>, a.tokens < 1024 ? 1 : 2, columns);
         const dim3 grid((unsigned)columns, (unsigned)plan.blocks);
         if (a.gate) hipLaunchKernelGGL((groupnorm_kernel<XF, YF, CPL, P, ITER, BWD, true>), grid, dim3(kGnThreads), 0, st, a, plan);
         else hipLaunchKernelGGL((groupnorm_kernel<XF, YF, CPL, P, ITER, BWD, false>), grid, dim3(kGnThreads), 0, st, a, plan);

@@ -136,6 +136,20 @@ def test_leading_dimensions_and_starts():
     check_bwd(got, x, 2, dy, w, b, gate, "silu", 1e-5)
 
 
+@pytest.mark.parametrize("width", [2, 30, 34, 62, 66, 94, 98, 126, 130, 254, 258, 510, 514, 1022, 1026])
+@pytest.mark.parametrize("xt,yt", [("bf16", "bf16"), ("f32", "bf16"), ("f32", "f32")])
+def test_even_widths(width, xt, yt):
+    """Read two channels at a time, or one where a tensor begins at an odd one: to the same bounds."""
+    x, w, b, gate, dy = make(width, 21, 3, width, xt, yt)
+    run(x, 3, w, b, gate, dy, "silu", 1e-5)
+    off = lambda t: torch.cat([t.new_zeros(1), t.flatten()]).cuda()[1:].view(t.shape)  # noqa: E731
+    one = [t.cuda() for t in (x, w, b, gate, dy)]
+    for i in range(5):
+        X, W, Bi, G, DY = (off(t) if i == j else t for j, t in enumerate(one))
+        check_fwd(kda.group_norm_act_fwd(X, 3, weight=W, bias=Bi, gate=G), x, 3, w, b, gate, "silu", 1e-5)
+        check_bwd(kda.group_norm_act_bwd(X, 3, DY, weight=W, bias=Bi, gate=G), x, 3, dy, w, b, gate, "silu", 1e-5)
+
+
 def test_far_means():
     """A mean far from zero against the deviation: the variance is of the centred values."""
     x, w, b, gate, dy = make(10, 60, 2, 128, "f32", "f32")
