@@ -311,6 +311,16 @@ __device__ __forceinline__ int state_at(int row, int c) {
 // of 64 KB make dearer than a kernel for it beyond.
 constexpr int kOwnFold = 8;
 
+// Two of a lane's values and two of another's as a matrix, transposed: a lane of the upper half gives its first value for the other's
+// second.  CTRL: where the other lane is, of four.
+template <int CTRL>
+__device__ __forceinline__ void across(float& a, float& b, bool upper) {
+    const float give = upper ? a : b;
+    const float take = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(give), CTRL, 0xf, 0xf, true));
+    if (upper) a = take;
+    else b = take;
+}
+
 template <int DC, bool F32>
 constexpr int kLinThreads = !F32 && DC == 128 ? 256 : 4 * DC;
 
@@ -396,6 +406,7 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
     const float whole32 = (float)whole, rest = whole > 0 ? (float)((whole - (double)whole32) / whole) : 0.f;
 
     // The state before the segment: what there is before the sequence, and the segments' before this one, or these folded already.
+    // Turned states are summed as they lie, four lanes with each other's columns, and change places in the end.
     f32x4_t S[G::CT][ND];
 #pragma unroll
     for (int ct = 0; ct < G::CT; ++ct)
@@ -404,41 +415,41 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
     if constexpr (ROWS) {
         const int64_t before = op.back ? w.count - 1 - w.j : w.j;
         const bool folded = before > 0 && w.count > kOwnFold;
-        if (op.x0 && !folded) {
-            const float* x = op.x0 + (w.n * H + h) * (int64_t)DA * DC;
+        auto each = [&](auto f) KDA_INLINE {
 #pragma unroll
             for (int ct = 0; ct < G::CT; ++ct)
 #pragma unroll
-                for (int d = 0; d < ND; ++d) {
-                    const int r = state_row(ct, 4 * grp), c = state_col<ND>(wave, m, d);
-                    if (op.turned) S[ct][d] = *reinterpret_cast<const f32x4_t*>(x + (int64_t)c * DA + r);
-                    else
+                for (int d = 0; d < ND; ++d) f(S[ct][d], state_row(ct, 4 * grp), state_col<ND>(wave, m, d));
+        };
+        if (op.x0 && !folded) {
+            const float* x = op.x0 + (w.n * H + h) * (int64_t)DA * DC;
+            each([&](f32x4_t& to, int r, int c) KDA_INLINE {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) S[ct][d][j] = x[(r + j) * DC + c];
-                }
+                for (int j = 0; j < 4; ++j) to[j] = op.turned ? x[((c & ~3) + j) * DA + r + (c & 3)] : x[(r + j) * DC + c];
+            });
         }
         const float f = before > 0 ? (float)exp(lg * segs.L) : 0.f;
         for (int64_t i = folded ? before - 1 : 0; i < before; ++i) {
             // segments in the order of the recurrence; the first one of it may be the sequence's last, with fewer tokens
             const float* x = op.states + ((w.base + (op.back ? w.count - 2 - i : i)) * H + h) * (int64_t)DA * DC;
             const float fi = folded ? 0.f : op.back && i == 0 ? (float)exp(lg * w.tail) : f;
+            auto add = [&](f32x4_t& to, const float* from) KDA_INLINE {
+                const f32x4_t u = *reinterpret_cast<const f32x4_t*>(from);
 #pragma unroll
-            for (int ct = 0; ct < G::CT; ++ct)
-#pragma unroll
-                for (int d = 0; d < ND; ++d) {
-                    const int r = state_row(ct, 4 * grp), c = state_col<ND>(wave, m, d);
-                    f32x4_t u;
-                    if (op.turned) {
-                        const float* from = x + state_at<DC>(c & ~3, r) + (c & 3);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) u[j] = from[4 * j];
-                    } else {
-                        u = *reinterpret_cast<const f32x4_t*>(x + state_at<DA>(r, c));
-                    }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) S[ct][d][j] = folded ? u[j] : fmaf(fi, S[ct][d][j], u[j]);
-                }
+                for (int j = 0; j < 4; ++j) to[j] = folded ? u[j] : fmaf(fi, to[j], u[j]);
+            };
+            if (op.turned) each([&](f32x4_t& to, int r, int c) KDA_INLINE { add(to, x + state_at<DC>(c & ~3, r + (c & 3))); });
+            else each([&](f32x4_t& to, int r, int c) KDA_INLINE { add(to, x + state_at<DA>(r, c)); });
         }
+        if (op.turned)
+            each([&](f32x4_t& to, int, int) KDA_INLINE {
+                float u[4] = {to[0], to[1], to[2], to[3]};
+                across<0xb1>(u[0], u[1], m & 1);  // the neighbour's
+                across<0xb1>(u[2], u[3], m & 1);
+                across<0x4e>(u[0], u[2], m & 2);  // the other pair's
+                across<0x4e>(u[1], u[3], m & 2);
+                to = f32x4_t{u[0], u[1], u[2], u[3]};
+            });
     }
 
     __syncthreads();
