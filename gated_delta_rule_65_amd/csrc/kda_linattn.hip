@@ -308,7 +308,8 @@ __device__ __forceinline__ int state_at(int row, int c) {
 }
 
 // Sequences of up to so many segments: a segment's workgroup folds those before it by itself, which the last one's seven states
-// of 64 KB make dearer than a kernel for it beyond.
+// of 64 KB make dearer than a kernel for it beyond (8 segments each: prefill of B=4 T=8192 H=16 D=128 138 us against 131 and 12
+// for the kernel, dq, dk, dv of T=4096 184 against 165 and 22).
 constexpr int kOwnFold = 8;
 
 // Two of a lane's values and two of another's as a matrix, transposed: a lane of the upper half gives its first value for the other's
