@@ -921,18 +921,27 @@ __global__ __launch_bounds__(256) void linattn_step_kernel(const void* q, const 
 
 // ------------------------------------------------------------------------------------------------ launches
 
-// Tokens of a segment.  Two workgroups fit on a CU: with 512 segments every place has one.  Packed sequences end anywhere, so
-// that half of the segments are shorter: with 768 of them the places even out (40011 tokens of 16 heads in 32 sequences 214 ->
-// 196 us, 206 -> 240 for equal lengths).  A segment's state is written and read, several times its size, which 256 tokens
-// outweigh; fewer only where every CU has no segment otherwise.
-int64_t segment_tokens(int64_t total, int H, bool packed) {
+// Tokens of a segment, about `many`.  A segment's state is written and read, several times its size, which 256 tokens outweigh; fewer
+// only where every CU has no segment otherwise.
+int64_t segment_tokens(int64_t many, int64_t total, int H) {
     auto whole = [](int64_t x) { return (x + 63) / 64 * 64; };
-    const int64_t places = packed ? 768 : 512, many = whole((total * H + places - 1) / places), one = whole((total * H + 255) / 256);
+    const int64_t one = whole((total * H + 255) / 256);
+    many = whole(many);
     return many > 256 ? many : one < 64 ? 64 : one < 256 ? one : 256;
+}
+// Packed sequences end anywhere, so that half of the segments are shorter: with 768 of them the 512 places, two on a CU, even out
+// (40011 tokens of 16 heads in 32 sequences 214 -> 196 us).
+int64_t packed_segment(const LinArgs& a) { return segment_tokens((a.total * a.H + 767) / 768, a.total, a.H); }
+// Equal lengths are cut in equal parts, as many as there are places for (with 768: 206 -> 240 us), and not at all where that is one
+// part: the first pass costs more than empty places (B=30 T=1500 H=16 D=128 bf16 in two unequal parts 386 us, whole 228; fp32 1385
+// and 538; B=10 T=3000 in unequal parts 243, in equal ones 174).
+int64_t equal_segment(const LinArgs& a) {
+    const int64_t parts = a.N * a.H >= 512 ? 1 : 512 / (a.N * a.H);
+    return segment_tokens((a.T_fixed + parts - 1) / parts, a.total, a.H);
 }
 
 Segs segs_of(const LinArgs& a) {
-    Segs s{a.cu, a.T_fixed, a.N, a.total, segment_tokens(a.total, a.H, a.cu), 1, a.H};
+    Segs s{a.cu, a.T_fixed, a.N, a.total, a.cu ? packed_segment(a) : equal_segment(a), 1, a.H};
     if (!a.cu && a.T_fixed > s.L) s.per_seq = (a.T_fixed + s.L - 1) / s.L;
     return s;
 }
@@ -972,9 +981,10 @@ void fold(const LinArgs& a, const Segs& s, FoldOp one, const FoldOp* two, hipStr
 
 }  // namespace
 
-// For either way of giving the sequences: packed ones have the shorter segments.
+// For either way of giving the sequences: packed ones have the shorter segments, since a part of an equal length has a 512th of
+// all tokens at least.
 int64_t linattn_workspace_bytes(const LinArgs& a, bool backward) {
-    const int64_t L = segment_tokens(a.total, a.H, true);
+    const int64_t L = packed_segment(a);
     if (a.total <= L) return 0;
     return a.total / L * a.H * a.Dk * (int64_t)a.Dv * 4 * (backward ? 2 : 1);
 }

@@ -62,6 +62,29 @@ def test_offsets_past_32_bits():
     check_end(o, sf, T - 300, "packed")
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("B,T,H", [(3, 1100, 40), (1, 1300, 171), (2, 1100, 129), (1, 600, 511), (2, 600, 256), (3, 400, 200)])
+def test_parts_of_equal_lengths(B, T, H, dtype):
+    """Lengths cut in four, two, one part for the places there are; some heads are checked, each is its own."""
+    q, k, v, d_o, g, s0, d_sf = ref.inputs(T + H, (B, T), H, 64, 64, TYPES[dtype], B, kinds=[-0.003, -0.2, 0.0, -1e-4, -30.0])
+    Q, K, V, DO, G, S0, DS = (t.cuda() for t in (q, k, v, d_o, g, s0, d_sf))
+    heads = [0, 1, H // 2, H - 1]
+    of = lambda t: t[:, :, heads].contiguous()  # noqa: E731
+    args, s, ds = [of(t) for t in (q, k, v)] + [g[heads]], s0[:, heads], d_sf[:, heads]
+    o, end = kda.linattn_fwd(Q, K, V, G, S0, scale=0.125)
+    want, last = ref.attend(*args, s, None, 0.125)
+    size, last_size = ref.magnitude(ref.attend, *args, s0=s, scale=0.125)
+    steps = 400  # chunks of 64 tokens, within one, and segments
+    near(of(o), want, ref.bound(q.dtype, want, size, steps), "o")
+    near(end[:, heads], last, ref.state_bound(last, last_size, steps), "s_final")
+    got = kda.linattn_bwd(Q, K, V, G, DO, S0, DS, scale=0.125)
+    want = ref.attend_grads(*args, of(d_o), s, ds, None, 0.125)
+    size = ref.magnitude(ref.attend_grads, *args, d_o=of(d_o), s0=s, d_sf=ds, scale=0.125)
+    for name, x, w, m in zip(("dq", "dk", "dv"), got, want, size):
+        near(of(x), w, ref.bound(q.dtype, w, m, steps), name)
+    near(got[3][:, heads], want[3], ref.state_bound(want[3], size[3], steps), "ds0")
+
+
 @pytest.mark.parametrize("backward", [False, True])
 def test_workspaces_of_the_caller(backward):
     q, k, v, d_o, g, s0, d_sf = (t.cuda() for t in ref.inputs(1, (1, 3000), 4, 64, 128, torch.bfloat16, 1))
