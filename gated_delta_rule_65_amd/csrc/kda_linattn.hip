@@ -101,25 +101,29 @@ __device__ __forceinline__ Where sequence(const Segs& s, int64_t n) {
     return w;
 }
 
-// The segment of a slot; count < 0: there is none.  Packed sequence n takes the slots from floor(begin / L) + n on: no two
-// the same, and one at least for each sequence.
+// The segment of a slot; count < 0: there is none.  For the outputs packed sequence n takes the slots from floor(begin / L) + n
+// on: no two the same, and one at least for each sequence.
 //
 // States are kept between segments only, one fewer than a sequence has segments, from floor(begin / L) on: forward that behind
 // segment j has place j of them, backward that before it place j - 1.  Sequences with one segment need none, and all of them
-// lie below total / L: the next sequence begins behind all but the last segment.
-__device__ __forceinline__ Where where_of(const Segs& s, int64_t slot) {
-    const int64_t n = s.cu ? last_below(s, [&](int64_t begin, int64_t at) { return begin / s.L + at <= slot; }) : slot / s.per_seq;
+// lie below total / L: the next sequence begins behind all but the last segment.  The pass for the segments' states has these
+// places for slots, so that many short sequences cost it nothing.
+template <bool ROWS>
+__device__ __forceinline__ Where where_of(const Segs& s, int64_t slot, bool back) {
+    const int64_t each = s.per_seq - (ROWS ? 0 : 1);
+    const int64_t n = s.cu ? last_below(s, [&](int64_t begin, int64_t at) { return begin / s.L + (ROWS ? at : 0) <= slot; }) : slot / each;
     if (n >= s.N) {
         Where w{};
         w.count = -1;
         return w;
     }
     Where w = sequence(s, n);
-    w.j = slot - (s.cu ? w.base + n : n * s.per_seq);
-    if (w.j < 0 || w.j >= (w.count ? w.count : 1)) {
+    w.j = slot - (s.cu ? w.base + (ROWS ? n : 0) : n * each);
+    if (w.j < 0 || w.j >= (ROWS ? (w.count ? w.count : 1) : w.count - 1)) {
         w.count = -1;
         return w;
     }
+    if (!ROWS && back) ++w.j;
     w.begin += w.j * s.L;
     if (w.end > w.begin + s.L) w.end = w.begin + s.L;
     return w;
@@ -344,18 +348,17 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
     const int which = blockIdx.x / 8 % ops;
     const LinOp op = which == 0 ? op0 : which == 1 ? op1 : op2;
     const int H = segs.H, h = id % H;
-    const Where w = where_of(segs, id / H);
+    const Where w = where_of<ROWS>(segs, id / H, op.back);
     if (w.count < 0) return;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, m = lane & 15, grp = lane >> 4;
     const bool last = op.back ? w.j == 0 : w.j + 1 >= w.count;
     if (w.count == 0) {
-        if (ROWS && op.fin) {
+        if (op.fin) {
             const int64_t at = (w.n * H + h) * (int64_t)DA * DC;
             for (int i = tid; i < DA * DC; i += THREADS) op.fin[at + i] = op.x0 ? op.x0[at + i] : 0.f;
         }
         return;
     }
-    if (!ROWS && last) return;
 
     const int tokens = (int)(w.end - w.begin), chunks = (tokens + C - 1) / C;
     // Rows of a chunk, in the order of the recurrence, to LDS, 64 units a wave at a time: for a whole chunk, a lane's offset from
@@ -946,7 +949,9 @@ Segs segs_of(const LinArgs& a) {
     return s;
 }
 
-int64_t slots_of(const Segs& s) { return s.cu ? s.total / s.L + s.N : s.N * s.per_seq; }
+int64_t slots_of(const Segs& s, bool rows) {
+    return s.cu ? s.total / s.L + (rows ? s.N : 0) : s.N * (s.per_seq - (rows ? 0 : 1));
+}
 
 // Whether a sequence may have more than one segment.
 bool is_split(const Segs& s) { return s.cu ? s.total > s.L : s.per_seq > 1; }
@@ -959,7 +964,7 @@ void chunks(const LinArgs& a, const Segs& s, std::initializer_list<LinOp> ops, i
     LinOp op[3] = {};
     int count = 0;
     for (const LinOp& o : ops) op[count++] = o;
-    const int64_t each = (slots_of(s) * a.H + 7) / 8 * 8;  // workgroups behind the last segment find none
+    const int64_t each = (slots_of(s, ROWS) * a.H + 7) / 8 * 8;  // workgroups behind the last segment find none
     auto run = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, dim3((unsigned)(each * count)), dim3(a.f32 || DC == 64 ? 4 * DC : 256), 0, st, op[0], op[1], op[2], count, s, a.g);
     };
@@ -992,7 +997,7 @@ int64_t linattn_workspace_bytes(const LinArgs& a, bool backward) {
 // Workgroups of the largest launch, and the threads of one at most.  The fold's are fewer: it has a sequence for 8 segments.
 int64_t linattn_threads(const LinArgs& a, bool backward) {
     const int64_t D = a.Dk > a.Dv ? a.Dk : a.Dv;
-    return (slots_of(segs_of(a)) * a.H + 8) * (backward ? 3 : 1) * (a.f32 ? 4 * D : 256);
+    return (slots_of(segs_of(a), true) * a.H + 8) * (backward ? 3 : 1) * (a.f32 ? 4 * D : 256);
 }
 
 hipError_t launch_linattn_fwd(const LinArgs& a, hipStream_t st) {
