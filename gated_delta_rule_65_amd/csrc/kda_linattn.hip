@@ -10,13 +10,13 @@
 //
 // Two passes over a sequence's segments: the first makes what each segment adds to the state (reads k and v), the second
 // starts every segment from the state before it.  One pass from begin to end would read k and v once, but has one workgroup
-// for a sequence and head, 64 for B=4 H=16: 534 us where two passes take 195.
+// for a sequence and head, 64 for B=4 H=16: 534 us where two passes take 216.
 //
-// bf16: products of bf16 on the matrix units, with what is not bf16 split into sums of bf16 values: the state and the scores
-// in two (16 bits: outputs are as far off as their own rounding, 1.7e-3 of their norm; with one the error is 1.41 times that
-// and the call a fifth faster), the weighted values in two or three.  fp32: products of fp32 (16x16x4).
+// bf16: products of bf16 on the matrix units, with what is not bf16 (the state, the scores, the weighted values) as the sum of three
+// bf16 values, which hold all of its 24 bits: a result that is small beside its terms is as exact as in fp32.  Two planes, 16 bits,
+// would take 198 us instead of 216, with errors of 2^-17 of the terms.  fp32: products of fp32 (16x16x4).
 //
-// B=4 T=8192 H=16 D=128 bf16: 59 us for the segments' states and 135 for the outputs, 195 in all; reading q, k, v and writing o
+// B=4 T=8192 H=16 D=128 bf16: 59 us for the segments' states and 155 for the outputs, 216 in all; reading q, k, v and writing o
 // once takes 86 at a copy's rate, k and v twice 129.  What bounds the outputs' pass is that vector and matrix instructions
 // of a SIMD's two waves do not overlap well: the vector units are busy for 44% of the time, the matrix units for 36%
 // (one product and four vector instructions take 26 to 29 cycles together, 17.5 and 18.6 alone).
@@ -141,7 +141,6 @@ struct LinOp {
     bool turned;            // states and x0 are taken transposed
     bool back;
     float su, so;           // scales of the state's products, and of the outputs
-    bool whole;             // the state behind the last segment is one in 32 bits
 };
 
 template <bool F32>
@@ -287,17 +286,22 @@ struct LinTile {
     static constexpr int UA = DA * ES / 16, UC = DC * ES / 16;  // units of a row
     static constexpr int KB = C * UA * 16, VB = C * UC * 16;
     static constexpr int KS = C / 32, RB = C / 16, AS = DA / 32, CT = DA / 16;
-    static constexpr int PL = F32 ? 1 : 2;       // planes of scores and of the state
-    // Planes of the weighted values: three hold all of their 24 bits.  In the outputs' pass two do where no state is given out
-    // behind the segment: outputs of 16 bits do not show what is left out (the state is off by 3e-6 instead of 3e-7), and it is
-    // a sixth of the products (backward of B=4 T=4096 H=16 D=128 204 -> 195 us).
-    static constexpr int VL = F32 ? 1 : 3;
-    static constexpr int PB = F32 ? 32 * 128 : 32 * 64 + 32 * 128;  // a plane of scores: rows up to their diagonal's 32 tokens
+    // Planes of the state, of the scores and of the weighted values: three bf16 hold all 24 bits of each.
+    static constexpr int PL = F32 ? 1 : 3;
+    static constexpr int PB = F32 ? 32 * 128 : 5120;  // a plane of scores: rows up to their diagonal's tile
 };
 
 // The state's rows are dealt over tiles of 16 so that a lane's rows of two tiles' products are eight side by side: what the next
 // product contracts lies in a row of `a` as it is.  Row i of tile ct:
 __host__ __device__ constexpr int state_row(int ct, int i) { return 32 * (ct >> 1) + 8 * (i >> 2) + 4 * (ct & 1) + (i & 3); }
+// Scores of 16 rows against 32 tokens in a plane: a block of 64 bytes a row, or of 32 where the second 16 tokens lie above the
+// diagonal (half_block), which are zeros and not kept: with three whole planes two workgroups would not fit on a CU.
+__host__ __device__ constexpr int score_block(int r, int ks) { return r == 0 ? 0 : 1024 * (r + ks) - (r < 3 ? 512 : 0); }
+__host__ __device__ constexpr bool half_block(int r, int ks) { return r == 2 * ks; }
+static_assert(score_block(1, 0) == score_block(0, 0) + 512 && score_block(2, 0) == score_block(1, 0) + 1024 &&
+                  score_block(2, 1) == score_block(2, 0) + 1024 && score_block(3, 0) == score_block(2, 1) + 512 &&
+                  score_block(3, 1) == score_block(3, 0) + 1024 && score_block(3, 1) + 1024 == 5120,
+              "blocks lie one behind another");
 // A wave's columns likewise, for what is stored in a row of the outputs: column i of its tile d.
 template <int ND>
 __host__ __device__ constexpr int state_col(int wave, int i, int d) {
@@ -480,9 +484,9 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
         at_col = ND == 2 ? place<UC, false>(4 * grp + (m >> 2), 4 * wave + (m & 3))
                          : place<UC, false>(4 * grp + (m >> 2), 2 * wave + (m >> 1 & 1)) + 8 * (m & 1);
     }
-    // scores, read by row: 32 rows of 32 tokens, and behind them 32 of 64; in fp32 one tile of 32
+    // scores, read by row: a lane's place in a whole block and in a half one; in fp32 one tile of 32
     int at_score = F32 ? place<8, true>(m, 2 * grp) : place<4, false>(m, grp);
-    int at_score2 = F32 ? 0 : 2048 + place<8, false>(m, grp);
+    int at_half = F32 ? 0 : 32 * m + 8 * grp;
     int at_power = m, at_far = 16 - 4 * grp;  // of the decay's powers
     auto frag = [&](const char* tile, int r, int s) KDA_INLINE {
         LFrag<F32> f;
@@ -523,15 +527,13 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
         return f;
     };
 
-    const bool three = op.whole && last;
-
     // One chunk with its keys in K; those of the next one go to Kn, if there is one: only the last chunk may have fewer tokens
     // than C.  Which requests are under way is the same on every path, so that the compiler sees what has been waited for.
     auto chunk = [&](int c, char* K, char* Kn, char* V, char* Vn, auto ends) KDA_INLINE {
         constexpr bool LAST = decltype(ends)::value;
         const int n = LAST ? tokens - c * C : C;
         // the places of a chunk's fragments are made again from these few: kept, they would take most of the registers
-        __asm__ volatile("" : "+v"(ones.low), "+v"(ones.high), "+v"(at_row), "+v"(at_turned), "+v"(at_col), "+v"(at_score), "+v"(at_score2),
+        __asm__ volatile("" : "+v"(ones.low), "+v"(ones.high), "+v"(at_row), "+v"(at_turned), "+v"(at_col), "+v"(at_score), "+v"(at_half),
                          "+v"(at_power), "+v"(at_far));
         // Of two workgroups on a CU one goes first in these products and the other in the state's, else the elder in all of them
         // (packed 40011 tokens 138 -> 129 us, prefill batch 142 -> 139).
@@ -574,7 +576,7 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
                 const float step16 = powers[16];
 #pragma unroll
                 for (int r = 0; r < G::RB; ++r) {
-                    if (wave > (r | 1)) continue;
+                    if (wave > (F32 ? r | 1 : r)) continue;
                     float x[4];
                     if (wave == r) {
 #pragma unroll
@@ -593,12 +595,17 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
                     if constexpr (F32) {
                         *reinterpret_cast<f32x4_t*>(ldsP + (at_score ^ (16 * wave)) + 2048 * r) = f32x4_t{x[0], x[1], x[2], x[3]};
                     } else {
-                        const uint32_t h0 = pack2(x[0], x[1]), h1 = pack2(x[2], x[3]);
-                        char* to = ldsP + (r < 2 ? at_score + 1024 * r : (at_score2 ^ (64 * (wave >> 1))) + 2048 * (r - 2)) + 8 * (wave & 1);
-                        *reinterpret_cast<uint2*>(to) = make_uint2(h0, h1);
-                        *reinterpret_cast<uint2*>(to + G::PB) =
-                            make_uint2(pack2(less_low(x[0], h0, ones), less_high(x[1], h0, ones)),
-                                       pack2(less_low(x[2], h1, ones), less_high(x[3], h1, ones)));
+                        char* to = ldsP + (wave == r && r % 2 == 0 ? score_block(r, r / 2) + at_half
+                                                                   : score_block(r, wave >> 1) + at_score + 8 * (wave & 1));
+#pragma unroll
+                        for (int p = 0; p < G::PL; ++p) {
+                            const uint32_t h0 = pack2(x[0], x[1]), h1 = pack2(x[2], x[3]);
+                            *reinterpret_cast<uint2*>(to + p * G::PB) = make_uint2(h0, h1);
+                            if (p + 1 < G::PL) {
+                                x[0] = less_low(x[0], h0, ones), x[1] = less_high(x[1], h0, ones);
+                                x[2] = less_low(x[2], h1, ones), x[3] = less_high(x[3], h1, ones);
+                            }
+                        }
                     }
                 }
             };
@@ -674,8 +681,11 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
 #pragma unroll
                             for (int j = 0; j < 4; ++j) f.v[j] = x[j], f.v[4 + j] = y[j];
                         } else {
-                            f.v = *reinterpret_cast<const bf16x8_t*>(
-                                ldsP + p * G::PB + (r < 2 ? at_score + 1024 * r : (at_score2 ^ (64 * ks)) + 2048 * (r - 2)));
+                            const char* from = ldsP + p * G::PB + score_block(r, ks);
+                            if (half_block(r, ks))
+                                f.v = __builtin_shufflevector(*reinterpret_cast<const bf16x4_t*>(from + at_half), bf16x4_t{},
+                                                              0, 1, 2, 3, 4, 5, 6, 7);
+                            else f.v = *reinterpret_cast<const bf16x8_t*>(from + at_score);
                         }
                     }
             // A value that is not finite must not meet the zeros of earlier rows: such values are left out of the products, and
@@ -736,7 +746,6 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
         }
 
         __builtin_amdgcn_s_setprio(0);
-        // the weighted values as sums of two or three bf16 values
 #pragma unroll
         for (int ks = 0; ks < G::KS; ++ks) {
             f32x4_t w0 = *reinterpret_cast<const f32x4_t*>(weights[LAST] + 32 * ks + 4 * grp);
@@ -745,8 +754,7 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
 #pragma unroll
                 for (int j = 0; j < 4; ++j) w0[j] *= left, w1[j] *= left;
             constexpr int TOGETHER = F32 ? 2 : 4;  // tiles of the state: as many as the registers hold
-            constexpr int VL = ROWS && !F32 ? 2 : G::VL;
-            LFrag<F32> vb[ND][VL], rest[ND], kt[TOGETHER];
+            LFrag<F32> vb[ND][G::PL], kt[TOGETHER];
 #pragma unroll
             for (int ct = 0; ct < TOGETHER; ++ct) kt[ct] = frag_bt(K, ct, ks);
 #pragma unroll
@@ -755,17 +763,7 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
                 values(vf[ks * ND + d], x);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) x[j] *= w0[j], x[4 + j] *= w1[j];
-                split<VL>(x, vb[d], ones);
-                if constexpr (VL < G::VL)
-                    if (three) {
-                        const uint4 a = __builtin_bit_cast(uint4, vb[d][0].v), b = __builtin_bit_cast(uint4, vb[d][1].v);
-                        uint4 u;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            (&u.x)[j] = pack2(less_low(less_low(x[2 * j], (&a.x)[j], ones), (&b.x)[j], ones),
-                                              less_high(less_high(x[2 * j + 1], (&a.x)[j], ones), (&b.x)[j], ones));
-                        rest[d].v = __builtin_bit_cast(bf16x8_t, u);
-                    }
+                split<G::PL>(x, vb[d], ones);
             }
 #pragma unroll
             for (int first = 0; first < G::CT; first += TOGETHER) {
@@ -773,18 +771,11 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
 #pragma unroll
                     for (int ct = 0; ct < TOGETHER; ++ct) kt[ct] = frag_bt(K, first + ct, ks);
 #pragma unroll
-                for (int p = 0; p < VL; ++p)
+                for (int p = 0; p < G::PL; ++p)
 #pragma unroll
                     for (int ct = 0; ct < TOGETHER; ++ct)
 #pragma unroll
                         for (int d = 0; d < ND; ++d) S[first + ct][d] = mma(kt[ct], vb[d][p], S[first + ct][d]);
-                if constexpr (VL < G::VL)
-                    if (three) {
-#pragma unroll
-                        for (int ct = 0; ct < TOGETHER; ++ct)
-#pragma unroll
-                            for (int d = 0; d < ND; ++d) S[first + ct][d] = mma(kt[ct], rest[d], S[first + ct][d]);
-                    }
             }
         }
         if (ROWS && marked) {
@@ -1004,10 +995,10 @@ hipError_t launch_linattn_fwd(const LinArgs& a, hipStream_t st) {
     const Segs s = segs_of(a);
     float* states = static_cast<float*>(a.ws);
     if (is_split(s)) {
-        chunks<false>(a, s, {LinOp{nullptr, a.k, a.v, states, nullptr, nullptr, nullptr, false, false, 1.f, 1.f, false}}, a.Dk, a.Dv, st);
+        chunks<false>(a, s, {LinOp{nullptr, a.k, a.v, states, nullptr, nullptr, nullptr, false, false, 1.f, 1.f}}, a.Dk, a.Dv, st);
         fold(a, s, FoldOp{states, a.s0, false}, nullptr, st);
     }
-    chunks<true>(a, s, {LinOp{a.q, a.k, a.v, a.o, a.s0, states, a.s_final, false, false, 1.f, a.scale, true}}, a.Dk, a.Dv, st);
+    chunks<true>(a, s, {LinOp{a.q, a.k, a.v, a.o, a.s0, states, a.s_final, false, false, 1.f, a.scale}}, a.Dk, a.Dv, st);
     return hipGetLastError();
 }
 
@@ -1016,15 +1007,15 @@ hipError_t launch_linattn_bwd(const LinArgs& a, hipStream_t st) {
     float* states = static_cast<float*>(a.ws);
     float* grads = states + s.total / s.L * a.H * a.Dk * a.Dv;
     if (is_split(s)) {
-        chunks<false>(a, s, {LinOp{nullptr, a.k, a.v, states, nullptr, nullptr, nullptr, false, false, 1.f, 1.f, false},
-                             LinOp{nullptr, a.q, a.d_o, grads, nullptr, nullptr, nullptr, false, true, a.scale, 1.f, false}},
+        chunks<false>(a, s, {LinOp{nullptr, a.k, a.v, states, nullptr, nullptr, nullptr, false, false, 1.f, 1.f},
+                             LinOp{nullptr, a.q, a.d_o, grads, nullptr, nullptr, nullptr, false, true, a.scale, 1.f}},
                       a.Dk, a.Dv, st);
         const FoldOp two{grads, a.d_sfinal, true};
         fold(a, s, FoldOp{states, a.s0, false}, &two, st);
     }
-    const LinOp dq{a.d_o, a.v, a.k, a.dq, a.s0, states, nullptr, true, false, 1.f, a.scale, false};
-    const LinOp dk{a.v, a.d_o, a.q, a.dk, a.d_sfinal, grads, nullptr, true, true, a.scale, 1.f, false};
-    const LinOp dv{a.k, a.q, a.d_o, a.dv, a.d_sfinal, grads, a.ds0, false, true, a.scale, 1.f, true};
+    const LinOp dq{a.d_o, a.v, a.k, a.dq, a.s0, states, nullptr, true, false, 1.f, a.scale};
+    const LinOp dk{a.v, a.d_o, a.q, a.dk, a.d_sfinal, grads, nullptr, true, true, a.scale, 1.f};
+    const LinOp dv{a.k, a.q, a.d_o, a.dv, a.d_sfinal, grads, a.ds0, false, true, a.scale, 1.f};
     if (a.Dk == a.Dv) {
         chunks<true>(a, s, {dq, dk, dv}, a.Dk, a.Dv, st);
     } else {
