@@ -122,15 +122,15 @@ __device__ __forceinline__ float lanes_sum(float x) {
 }
 
 // 1 / (1 + e^-u).  CLOSE: e^-u from the product's two halves, so that it keeps 32 bits' accuracy far from zero (the product alone is
-// off by |u| 2^-24, which 16-bit results do not show).  Beyond +-100 e^-u is 0 or infinite in 32 bits anyway.  Of a NaN, some
-// number.
+// off by |u| 2^-24, which 16-bit results do not show); where the product is infinite already the rest is of a finite factor, which leaves
+// it so.  Beyond +-100 e^-u is 0 or infinite in 32 bits anyway.  Of a NaN, some number.
 template <bool CLOSE>
 __device__ __forceinline__ float gn_sigmoid(float u) {
     constexpr float l2e = 1.44269502162933349609375f, l2e_rest = 1.925963033500011e-8f, ln2 = 0.693147182464599609375f;
     const float t = __builtin_amdgcn_fmed3f(-u, -100.f, 100.f), hi = t * l2e, e = __builtin_amdgcn_exp2f(hi);
     if constexpr (!CLOSE) return __builtin_amdgcn_rcpf(1.f + e);
     const float lo = fmaf(t, l2e_rest, fmaf(t, l2e, -hi));
-    return __builtin_amdgcn_rcpf(1.f + fmaf(e, lo * ln2, e));
+    return __builtin_amdgcn_rcpf(1.f + fmaf(fminf(e, 3e38f), lo * ln2, e));
 }
 
 // act(u) and its slope; u times the sigmoid, or the sigmoid alone, by selection and not by branches between the values.

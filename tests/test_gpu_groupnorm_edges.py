@@ -1,0 +1,85 @@
+"""The group norm's activation on the GPU far from zero, where e^-u leaves the range of 32 bits, and how exact it is."""
+import pytest
+import torch
+
+import gated_delta_rule_65_amd as kda
+from tests.test_gpu_groupnorm import E, TYPES, near
+
+pytestmark = pytest.mark.gpu
+FLOOR = 128 * 2.0 ** -126  # a sigmoid below the smallest normal number may be zero; |u| is below 128
+
+
+def parts(u, act):
+    s = torch.sigmoid(u.double())
+    return (s, s * (1 - s), s) if act == "sigmoid" else (u.double() * s, s + u.double() * s * (1 - s), s)
+
+
+def rows(tokens, groups, width):
+    """Rows of +1 and -1, as many of either: their own norm exactly."""
+    return torch.tensor([1.0, -1.0]).repeat(tokens, groups * width // 2)
+
+
+def sweep(values, C, dtype=torch.float32):
+    """[rows, C], the last row filled up with what lies in the middle."""
+    n = -(-values.numel() // C) * C
+    return torch.cat([values, values[:1].expand(n - values.numel())]).view(-1, C).to(dtype)
+
+
+FAR = torch.cat([torch.linspace(-104, -80, 20001), torch.linspace(80, 104, 2001),
+                 torch.tensor([-3e38, -1e4, -200.0, -100.0, -88.75, -88.5, 3e38 ** 0.5, 1e4])])
+WIDTHS = [(2, 64), (3, 50), (2, 3000), (1, 4098)]  # in registers, 16 bytes and an element or two at a time; too wide for them
+
+
+@pytest.mark.parametrize("act", ["silu", "sigmoid"])
+@pytest.mark.parametrize("groups,width", WIDTHS)
+def test_far_gates(groups, width, act):
+    """Every step as in 64 bits: sigmoids to 12 half steps of 32 bits (the exponential's and the reciprocal's whole steps, four
+    roundings) or to the smallest normal number."""
+    C = groups * width
+    gate = sweep(FAR[FAR.abs() < 1e4], C)
+    x, dy = rows(gate.shape[0], groups, width), torch.ones_like(gate)
+    w = torch.ones(C)
+    kw = {"weight": w.cuda(), "bias": torch.zeros(C).cuda(), "gate": gate.cuda(), "act": act, "eps": 0.0}
+    f, slope, s = parts(gate, act)
+    y = kda.group_norm_act_fwd(x.cuda(), groups, **kw)
+    near(y, x * f, 12 * E * f.abs() + FLOOR, "y")
+    dx, dw, db, dgate = kda.group_norm_act_bwd(x.cuda(), groups, dy.cuda(), **kw)
+    near(dgate, x * slope, 16 * E * (f.abs() + s) + FLOOR, "dgate")
+    many = lambda t: t.unflatten(-1, (groups, width))  # noqa: E731
+    mean = many(f).mean(-1, keepdim=True)
+    along = (many(f) * many(x.double())).mean(-1, keepdim=True)
+    most = many(f).abs().amax(-1, keepdim=True)
+    near(many(dx), many(f) - mean - many(x.double()) * along, (3 * (width / 8 + 16) + 12) * E * most + 4 * FLOOR, "dx")
+    size = f.abs().sum(0)
+    near(dw, (f * x).sum(0), (gate.shape[0] + 12) * E * size + gate.shape[0] * FLOOR, "dweight")
+    near(db, f.sum(0), (gate.shape[0] + 12) * E * size + gate.shape[0] * FLOOR, "dbias")
+
+
+@pytest.mark.parametrize("act", ["silu", "sigmoid"])
+@pytest.mark.parametrize("groups,width", WIDTHS)
+def test_far_values(groups, width, act):
+    """The same of the normed values themselves: a weight of zero leaves the bias."""
+    C = groups * width
+    for bias in sweep(FAR[FAR.abs() < 1e4], C)[:40]:
+        x = rows(1, groups, width)
+        kw = {"weight": torch.zeros(C).cuda(), "bias": bias.cuda(), "act": act, "eps": 0.0}
+        f, slope, s = parts(bias, act)
+        near(kda.group_norm_act_fwd(x.cuda(), groups, **kw)[0], f, 12 * E * f.abs() + FLOOR, "y")
+        dx, dw, db, _ = kda.group_norm_act_bwd(x.cuda(), groups, torch.ones(1, C).cuda(), **kw)
+        assert not bool(dx.any())
+        near(dw, slope * x[0], 16 * E * (f.abs() + s) + FLOOR, "dweight")
+        near(db, slope, 16 * E * (f.abs() + s) + FLOOR, "dbias")
+
+
+@pytest.mark.parametrize("act", ["silu", "sigmoid"])
+@pytest.mark.parametrize("groups,width", WIDTHS)
+def test_largest_gates_leave_gradients_finite(groups, width, act):
+    """Gates to the end of float32's range: y, dx, dgate and the weights' gradients are numbers wherever the formula's are."""
+    C = groups * width
+    gate = sweep(FAR, C)
+    gate[-1, -2:] = torch.tensor([-3.4e38, 1e18])
+    x, dy = rows(gate.shape[0], groups, width), torch.ones_like(gate)
+    kw = {"weight": torch.ones(C).cuda(), "bias": torch.zeros(C).cuda(), "gate": gate.cuda(), "act": act, "eps": 0.0}
+    assert bool(torch.isfinite(kda.group_norm_act_fwd(x.cuda(), groups, **kw)).all())
+    for name, t in zip(("dx", "dw", "db", "dgate"), kda.group_norm_act_bwd(x.cuda(), groups, dy.cuda(), **kw)):
+        assert bool(torch.isfinite(t).all()), name
