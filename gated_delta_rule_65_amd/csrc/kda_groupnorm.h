@@ -122,7 +122,7 @@ __device__ __forceinline__ float lanes_sum(float x) {
 }
 
 // 1 / (1 + e^-u).  CLOSE: e^-u from the product's two halves, so that it keeps 32 bits' accuracy far from zero (the product alone is
-// off by |u| 2^-24, which 16-bit results do not show); where the product is infinite already the rest is of a finite factor, which leaves
+// off by |u| 2^-24, which 16-bit outputs do not show; of a backward pass the weights' gradients are always of 32 bits); where the product is infinite already the rest is of a finite factor, which leaves
 // it so.  Beyond +-100 e^-u is 0 or infinite in 32 bits anyway.  Of a NaN, some number.
 template <bool CLOSE>
 __device__ __forceinline__ float gn_sigmoid(float u) {
@@ -220,7 +220,7 @@ __global__ __launch_bounds__(kGnThreads) void groupnorm_kernel(GroupNormArgs a, 
                 x[k] *= rstd;
                 const float z = fmaf(x[k], w[k], b[k]), v = GATE ? u[k] : z;
                 float f = v, slope = 1.f;
-                if constexpr (ACT) gn_act<YF, BWD>(v, alone, f, slope);
+                if constexpr (ACT) gn_act<YF || BWD, BWD>(v, alone, f, slope);
                 if constexpr (!BWD) {
                     x[k] = GATE ? z * f : f;
                 } else {

@@ -47,11 +47,10 @@ __device__ __forceinline__ float load1(const void* p, int64_t i) {
     return x[0];
 }
 
-template <bool YF>
 __device__ __forceinline__ void act_of(float v, int act, float& f, float& slope) {
     f = v;
     slope = 1.f;
-    if (act) gn_act<YF, true>(v, act == 2, f, slope);
+    if (act) gn_act<true, true>(v, act == 2, f, slope);
 }
 
 // A workgroup for a group of a token, an element a thread at a time; the passes after the first find the row in the caches.
@@ -79,7 +78,7 @@ __global__ __launch_bounds__(kGnThreads) void groupnorm_rows_kernel(GroupNormArg
         w = a.weight ? a.weight[c0 + c] : 1.f;
         z = fmaf(n, w, a.bias ? a.bias[c0 + c] : 0.f);
         const float v = a.gate ? load1<YF>(a.gate, g0 + c) : z;
-        act_of<YF>(v, a.act, f, slope);
+        act_of(v, a.act, f, slope);
     };
     float n, z, w, f, slope;
     if (!a.dy) {
@@ -120,7 +119,7 @@ __global__ __launch_bounds__(kGnThreads) void groupnorm_columns_kernel(GroupNorm
         const float* s = stats + 2 * (t * a.groups + c / a.width);
         const float n = (load1<XF>(a.x, t * a.x_stride + c) - s[0]) * s[1], z = fmaf(n, w, b);
         float f, slope;
-        act_of<YF>(a.gate ? load1<YF>(a.gate, t * a.gate_stride + c) : z, a.act, f, slope);
+        act_of(a.gate ? load1<YF>(a.gate, t * a.gate_stride + c) : z, a.act, f, slope);
         const float dz = load1<YF>(a.dy, t * C + c) * (a.gate ? f : slope);
         dw = fmaf(dz, n, dw);
         db += dz;

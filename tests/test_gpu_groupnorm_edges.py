@@ -83,3 +83,20 @@ def test_largest_gates_leave_gradients_finite(groups, width, act):
     assert bool(torch.isfinite(kda.group_norm_act_fwd(x.cuda(), groups, **kw)).all())
     for name, t in zip(("dx", "dw", "db", "dgate"), kda.group_norm_act_bwd(x.cuda(), groups, dy.cuda(), **kw)):
         assert bool(torch.isfinite(t).all()), name
+
+
+@pytest.mark.parametrize("act", ["silu", "sigmoid"])
+@pytest.mark.parametrize("xt", list(TYPES))
+@pytest.mark.parametrize("groups,width", WIDTHS)
+def test_gates_of_16_bits_have_gradients_of_32(groups, width, xt, act):
+    """With gates and outputs in bf16 the weights' gradients are as exact as with float32 ones: one token, so that each sum is one
+    term."""
+    C = groups * width
+    gate = torch.linspace(-86.0, -20.0, C).bfloat16()[None]
+    x, dy = rows(1, groups, width).to(TYPES[xt]), torch.ones(1, C, dtype=torch.bfloat16)
+    kw = {"weight": torch.ones(C).cuda(), "bias": torch.zeros(C).cuda(), "gate": gate.cuda(), "act": act, "eps": 0.0}
+    f, slope, s = parts(gate, act)
+    dx, dw, db, dgate = kda.group_norm_act_bwd(x.cuda(), groups, dy.cuda(), **kw)
+    near(dw, (f * x)[0], 12 * E * f[0].abs() + FLOOR, "dweight")
+    near(db, f[0], 12 * E * f[0].abs() + FLOOR, "dbias")
+    near(dgate, x * slope, 2.0 ** -8 * slope.abs() * (1 + 16 * E) + 16 * E * (f.abs() + s) + FLOOR, "dgate")
