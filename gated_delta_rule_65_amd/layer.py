@@ -85,6 +85,11 @@ def _expect(t, name, dtype, shape, device):
         _same_device(device, **{name: t})
 
 
+def _wanted(ctx, index):
+    """Whether an argument, which may have been left out, wants a gradient."""
+    return any(ctx.needs_input_grad[index:index + 1])
+
+
 def _float(t, name):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")

@@ -12,7 +12,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import DTYPE, _aligned_grad, _first_order, _need, _ptr, layer, load_library
-from .layer import _expect, _launch, _same_device, _seqs, _ws
+from .layer import _expect, _launch, _same_device, _seqs, _wanted, _ws
 
 
 def declare(L):
@@ -106,7 +106,7 @@ def linattn_varlen_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: tor
     return _fwd(q, k, v, g, cu_seqlens, s0, scale, output_final_state, workspace)
 
 
-def _bwd(q, k, v, g, cu, d_o, s0, d_sfinal, scale, workspace):
+def _bwd(q, k, v, g, cu, d_o, s0, d_sfinal, scale, output_ds0, workspace):
     packed = cu is not None
     front, H, Dk, Dv = _inputs(q, k, v, g, 1 if packed else 2)
     N, total = (_seqs(cu), front[0]) if packed else (front[0], front[0] * front[1])
@@ -115,7 +115,7 @@ def _bwd(q, k, v, g, cu, d_o, s0, d_sfinal, scale, workspace):
     _state_like(s0, "s0", (N, H, Dk, Dv), q.device)
     _state_like(d_sfinal, "d_sfinal", (N, H, Dk, Dv), q.device)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    ds0 = torch.empty((N, H, Dk, Dv), dtype=torch.float32, device=q.device)
+    ds0 = torch.empty((N, H, Dk, Dv), dtype=torch.float32, device=q.device) if output_ds0 else None
     ws, ws_bytes = _ws(linattn_bwd_workspace_bytes(N, total, H, Dk, Dv, q.dtype), workspace, q.device)
     tail = (H, Dk, Dv, scale, DTYPE[q.dtype], _ptr(ws), ws_bytes)
     outs = (_ptr(d_o), _ptr(d_sfinal), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ds0))
@@ -130,20 +130,20 @@ def _bwd(q, k, v, g, cu, d_o, s0, d_sfinal, scale, workspace):
 
 def linattn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, d_o: torch.Tensor,
                 s0: Optional[torch.Tensor] = None, d_sfinal: Optional[torch.Tensor] = None, *, scale: float = 1.0,
-                workspace: Optional[torch.Tensor] = None):
+                output_ds0: bool = True, workspace: Optional[torch.Tensor] = None):
     """Gradients of :func:`linattn_fwd` for dL/do = d_o (q's type) and dL/dS_T = d_sfinal (fp32, None = 0).  Returns dq, dk,
-    dv (q's type) and ds0 (fp32)."""
-    return _bwd(q, k, v, g, None, d_o, s0, d_sfinal, scale, workspace)
+    dv (q's type) and ds0 (fp32, or None)."""
+    return _bwd(q, k, v, g, None, d_o, s0, d_sfinal, scale, output_ds0, workspace)
 
 
 def linattn_varlen_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, cu_seqlens: torch.Tensor,
                        d_o: torch.Tensor, s0: Optional[torch.Tensor] = None, d_sfinal: Optional[torch.Tensor] = None, *,
-                       scale: float = 1.0, workspace: Optional[torch.Tensor] = None):
+                       scale: float = 1.0, output_ds0: bool = True, workspace: Optional[torch.Tensor] = None):
     """Gradients of :func:`linattn_varlen_fwd`; arguments and results as for :func:`linattn_bwd`.  Rows behind the last
     sequence are left unwritten."""
     if cu_seqlens is None:
         raise ValueError("cu_seqlens is needed")
-    return _bwd(q, k, v, g, cu_seqlens, d_o, s0, d_sfinal, scale, workspace)
+    return _bwd(q, k, v, g, cu_seqlens, d_o, s0, d_sfinal, scale, output_ds0, workspace)
 
 
 def linattn_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, state: torch.Tensor, *,
@@ -164,13 +164,18 @@ def _constant(ctx, index):
         raise ValueError("g has no gradient here, the decays are constants: pass it detached")
 
 
+def _state_grad(d_sf):
+    return None if d_sf is None else _aligned_grad(d_sf, torch.float32)
+
+
 class LinearAttention(torch.autograd.Function):
-    """Autograd wrapper: ``o, s_final = LinearAttention.apply(q, k, v, g, s0, scale)``; s0 may be None.  The decays are
-    constants; gradients of gradients are refused."""
+    """Autograd wrapper: ``o, s_final = LinearAttention.apply(q, k, v, g, s0, scale, output_final_state)``; s0 may be None.  Without
+    ``output_final_state`` s_final is None, and no state is written forward nor read as its gradient: 64 KB each for a sequence and
+    head of 128 channels.  The decays are constants; gradients of gradients are refused."""
 
     @staticmethod
-    def forward(ctx, q, k, v, g, s0=None, scale=1.0):
-        o, sf = linattn_fwd(q, k, v, g, s0, scale=scale)
+    def forward(ctx, q, k, v, g, s0=None, scale=1.0, output_final_state=True):
+        o, sf = linattn_fwd(q, k, v, g, s0, scale=scale, output_final_state=output_final_state)
         ctx.scale = scale
         ctx.save_for_backward(q, k, v, g, s0)
         return o, sf
@@ -180,18 +185,19 @@ class LinearAttention(torch.autograd.Function):
     def backward(ctx, d_o, d_sf):
         _constant(ctx, 3)
         q, k, v, g, s0 = ctx.saved_tensors
-        dq, dk, dv, ds0 = linattn_bwd(q, k, v, g, _aligned_grad(d_o, q.dtype), s0, _aligned_grad(d_sf, torch.float32),
-                                      scale=ctx.scale)
-        return dq, dk, dv, None, (ds0 if s0 is not None else None), None
+        wanted = _wanted(ctx, 4)
+        dq, dk, dv, ds0 = linattn_bwd(q, k, v, g, _aligned_grad(d_o, q.dtype), s0, _state_grad(d_sf), scale=ctx.scale,
+                                      output_ds0=wanted)
+        return dq, dk, dv, None, (ds0 if wanted else None), None, None
 
 
 class VarlenLinearAttention(torch.autograd.Function):
     """:class:`LinearAttention` over packed sequences: ``o, s_final = VarlenLinearAttention.apply(q, k, v, g, cu_seqlens, s0,
-    scale)``.  Rows behind the last sequence, where q is longer, are zeros in o and have zero gradients."""
+    scale, output_final_state)``.  Rows behind the last sequence, where q is longer, are zeros in o and have zero gradients."""
 
     @staticmethod
-    def forward(ctx, q, k, v, g, cu_seqlens, s0=None, scale=1.0):
-        o, sf = linattn_varlen_fwd(q, k, v, g, cu_seqlens, s0, scale=scale)
+    def forward(ctx, q, k, v, g, cu_seqlens, s0=None, scale=1.0, output_final_state=True):
+        o, sf = linattn_varlen_fwd(q, k, v, g, cu_seqlens, s0, scale=scale, output_final_state=output_final_state)
         layer._zero_behind(cu_seqlens, o)
         ctx.scale = scale
         ctx.save_for_backward(q, k, v, g, cu_seqlens, s0)
@@ -202,8 +208,9 @@ class VarlenLinearAttention(torch.autograd.Function):
     def backward(ctx, d_o, d_sf):
         _constant(ctx, 3)
         q, k, v, g, cu, s0 = ctx.saved_tensors
-        dq, dk, dv, ds0 = linattn_varlen_bwd(q, k, v, g, cu, _aligned_grad(d_o, q.dtype), s0,
-                                             _aligned_grad(d_sf, torch.float32), scale=ctx.scale)
+        wanted = _wanted(ctx, 5)
+        dq, dk, dv, ds0 = linattn_varlen_bwd(q, k, v, g, cu, _aligned_grad(d_o, q.dtype), s0, _state_grad(d_sf), scale=ctx.scale,
+                                             output_ds0=wanted)
         layer._zero_behind(cu, dq, dk)
         layer._zero_behind(cu, dv)
-        return dq, dk, dv, None, None, (ds0 if s0 is not None else None), None
+        return dq, dk, dv, None, None, (ds0 if wanted else None), None, None
