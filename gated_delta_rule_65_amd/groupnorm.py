@@ -13,7 +13,7 @@ from typing import Optional
 import torch
 
 from . import DTYPE, _aligned_grad, _first_order, _ptr, load_library
-from .layer import _expect, _float, _launch, _same_device, _token_stride, _ws
+from .layer import _expect, _float, _launch, _same_device, _token_stride, _wanted, _ws
 
 ACT = {"none": 0, "silu": 1, "sigmoid": 2}
 
@@ -97,10 +97,10 @@ def group_norm_act_fwd(x: torch.Tensor, groups: int, *, weight: Optional[torch.T
 
 def group_norm_act_bwd(x: torch.Tensor, groups: int, dy: torch.Tensor, *, weight: Optional[torch.Tensor] = None,
                        bias: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None, act: str = "silu",
-                       eps: float = 1e-5, workspace: Optional[torch.Tensor] = None):
+                       eps: float = 1e-5, output_dweights: bool = True, workspace: Optional[torch.Tensor] = None):
     """Gradients of :func:`group_norm_act_fwd` for dL/dy = dy (contiguous, the outputs' type).  Returns dx (contiguous, x's
-    type), dweight and dbias (fp32, summed over tokens in a fixed order) and dgate (contiguous, the gate's type); None for
-    what was not given."""
+    type), dweight and dbias (fp32, summed over tokens in a fixed order; None without ``output_dweights``) and dgate
+    (contiguous, the gate's type); None for what was not given."""
     _float(dy, "dy")
     args, tokens, width, dtype, form = _inputs(x, groups, weight, bias, gate, act, eps, dy.dtype)
     _expect(dy, "dy", dtype, x.shape, x.device)
@@ -108,7 +108,7 @@ def group_norm_act_bwd(x: torch.Tensor, groups: int, dy: torch.Tensor, *, weight
     dgate = torch.empty_like(dy) if gate is not None else None
     dw = db = None
     ws, ws_bytes = None, 0
-    if weight is not None or bias is not None:
+    if output_dweights and (weight is not None or bias is not None):
         dw, db = (torch.empty(groups * width, dtype=torch.float32, device=x.device) for _ in range(2))
         ws, ws_bytes = _ws(group_norm_act_workspace_bytes(tokens, groups, width), workspace, x.device)
     _launch(load_library().kda_groupnorm_bwd, x.device, *args, _ptr(dy), _ptr(dx), _ptr(dgate), _ptr(dw), _ptr(db), tokens,
@@ -132,5 +132,5 @@ class GroupNormAct(torch.autograd.Function):
     def backward(ctx, dy):
         x, weight, bias, gate = ctx.saved_tensors
         dx, dw, db, dgate = group_norm_act_bwd(x, ctx.groups, _aligned_grad(dy, ctx.y_dtype), weight=weight, bias=bias,
-                                               gate=gate, **ctx.form)
+                                               gate=gate, output_dweights=_wanted(ctx, 2) or _wanted(ctx, 3), **ctx.form)
         return dx, None, dw, db, dgate, None, None, None

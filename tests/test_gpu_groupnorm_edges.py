@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import gated_delta_rule_65_amd as kda
-from tests.test_gpu_groupnorm import E, TYPES, near
+from tests.test_gpu_groupnorm import E, TYPES, make, near
 
 pytestmark = pytest.mark.gpu
 FLOOR = 128 * 2.0 ** -126  # a sigmoid below the smallest normal number may be zero; |u| is below 128
@@ -100,3 +100,14 @@ def test_gates_of_16_bits_have_gradients_of_32(groups, width, xt, act):
     near(dw, (f * x)[0], 12 * E * f[0].abs() + FLOOR, "dweight")
     near(db, f[0], 12 * E * f[0].abs() + FLOOR, "dbias")
     near(dgate, x * slope, 2.0 ** -8 * slope.abs() * (1 + 16 * E) + 16 * E * (f.abs() + s) + FLOOR, "dgate")
+
+
+@pytest.mark.parametrize("width", [64, 50, 3000])
+def test_gradients_without_the_weights(width):
+    """dx and dgate are the same bits with the weights' sums and without."""
+    x, w, b, gate, dy = (t.cuda() for t in make(3, 70, 2, width, "bf16", "bf16"))
+    kw = {"weight": w, "bias": b, "gate": gate}
+    dx, dw, db, dgate = kda.group_norm_act_bwd(x, 2, dy, **kw)
+    some = kda.group_norm_act_bwd(x, 2, dy, output_dweights=False, **kw)
+    assert some[1] is None and some[2] is None and dw is not None and db is not None
+    assert torch.equal(some[0], dx) and torch.equal(some[3], dgate)

@@ -72,3 +72,24 @@ def test_a_final_state_is_there_unless_it_is_left_out(asked, packed):
     (o.sum() + 2 * s.sum()).backward()
     assert asked[tag + "_fwd"] == {"final": True} and asked[tag + "_bwd"]["ds0"]
     assert torch.equal(asked[tag + "_bwd"]["d_sfinal"], torch.full((1, 2, 4, 4), 2.0)) and s0.grad is not None
+
+
+@pytest.mark.parametrize("weight,bias", [(False, False), (True, False), (False, True)])
+def test_weights_that_want_no_gradient(stand_ins, monkeypatch, weight, bias):  # noqa: F811
+    """The sums over tokens are made only where the weight or the bias wants one."""
+    from gated_delta_rule_65_amd import groupnorm
+    whole, seen = groupnorm.group_norm_act_bwd, {}
+
+    def bwd(*args, output_dweights=True, **kw):
+        seen["sums"] = output_dweights
+        dx, dw, db, dgate = whole(*args, **kw)
+        return (dx, dw, db, dgate) if output_dweights else (dx, None, None, dgate)
+
+    monkeypatch.setattr(groupnorm, "group_norm_act_bwd", bwd)
+    x, w, b = torch.randn(3, 8).requires_grad_(), torch.randn(8), torch.randn(8)
+    kda.GroupNormAct.apply(x, 2, w.requires_grad_(weight), b.requires_grad_(bias), None, "silu").sum().backward()
+    assert seen["sums"] == (weight or bias) and (w.grad is not None) == weight and (b.grad is not None) == bias
+    want = ref.group_norm_grads(x.detach(), 2, torch.ones(3, 8), w.detach(), b.detach(), None, "silu", 1e-5)
+    assert torch.allclose(x.grad.double(), want["dx"], rtol=1e-5, atol=1e-5)
+    for leaf, name in ((w, "dw"), (b, "db")):
+        assert leaf.grad is None or torch.allclose(leaf.grad.double(), want[name], rtol=1e-5, atol=1e-5)
