@@ -484,13 +484,14 @@ kda_status gn_inputs(kda::GroupNormArgs& a, const void* x, int64_t x_stride, con
     a.y_f32 = f->y_dtype == KDA_F32;
     a.act = f->act;
     a.eps = f->eps;
-    const bool wide = kda::groupnorm_wide(a);
-    const int xa = wide ? 16 : a.x_f32 ? 4 : 2, ya = wide ? 16 : a.y_f32 ? 4 : 2;
-    if ((st = check_ptrs({{x, "x", tokens > 0, xa}, {gate, "gate", false, ya}, {weight, "weight", false, wide ? 16 : 4},
-                          {bias, "bias", false, wide ? 16 : 4}})) != KDA_OK)
-        return st;
+    return check_ptrs({{x, "x", tokens > 0, a.x_f32 ? 4 : 2}, {gate, "gate", false, a.y_f32 ? 4 : 2}, {weight, "weight", false, 4},
+                       {bias, "bias", false, 4}});
+}
+
+// With all of the call's pointers, which decide on its kernel.
+kda_status gn_grid(const kda::GroupNormArgs& a) {
     if (kda::groupnorm_groups(a) > kda::kMaxThreads / 256)
-        return fail(KDA_ERR_BAD_SHAPE, "%lld tokens of %lld groups exceed the grid limit", (long long)tokens, (long long)groups);
+        return fail(KDA_ERR_BAD_SHAPE, "%lld tokens of %lld groups exceed the grid limit", (long long)a.tokens, (long long)a.groups);
     return KDA_OK;
 }
 
@@ -987,10 +988,10 @@ kda_status kda_groupnorm_fwd(const void* x, int64_t x_stride, const float* weigh
     kda_status st;
     kda::GroupNormArgs a{};
     if ((st = gn_inputs(a, x, x_stride, weight, bias, gate, gate_stride, tokens, groups, width, form)) != KDA_OK) return st;
-    const int ya = kda::groupnorm_wide(a) ? 16 : a.y_f32 ? 4 : 2;
-    if ((st = check_ptrs({{y, "y", tokens > 0, ya}})) != KDA_OK) return st;
+    if ((st = check_ptrs({{y, "y", tokens > 0, a.y_f32 ? 4 : 2}})) != KDA_OK) return st;
     if (tokens == 0) return ok();
     a.y = y;
+    if ((st = gn_grid(a)) != KDA_OK) return st;
     return launched(kda::launch_groupnorm_fwd(a, static_cast<hipStream_t>(stream)), "kda_groupnorm_fwd");
 }
 
@@ -1001,8 +1002,8 @@ kda_status kda_groupnorm_bwd(const void* x, int64_t x_stride, const float* weigh
     kda_status st;
     kda::GroupNormArgs a{};
     if ((st = gn_inputs(a, x, x_stride, weight, bias, gate, gate_stride, tokens, groups, width, form)) != KDA_OK) return st;
-    const bool any = tokens > 0, wide = kda::groupnorm_wide(a), sums = dweight || dbias;
-    const int xa = wide ? 16 : a.x_f32 ? 4 : 2, ya = wide ? 16 : a.y_f32 ? 4 : 2;
+    const bool any = tokens > 0, sums = dweight || dbias;
+    const int xa = a.x_f32 ? 4 : 2, ya = a.y_f32 ? 4 : 2;
     if ((st = check_ptrs({{dy, "dy", any, ya}, {dx, "dx", any, xa}, {dgate, "dgate", any && gate, ya},
                           {dweight, "dweight", sums}, {dbias, "dbias", sums}, {workspace, "workspace", false}})) != KDA_OK)
         return st;
@@ -1020,6 +1021,7 @@ kda_status kda_groupnorm_bwd(const void* x, int64_t x_stride, const float* weigh
     a.dweight = dweight;
     a.dbias = dbias;
     a.ws = workspace;
+    if ((st = gn_grid(a)) != KDA_OK) return st;
     return launched(kda::launch_groupnorm_bwd(a, static_cast<hipStream_t>(stream)), "kda_groupnorm_bwd");
 }
 

@@ -159,7 +159,13 @@ void groupnorm_sums(const GroupNormArgs& a, int64_t blocks, hipStream_t st) {
                        static_cast<const float*>(a.ws), blocks, C, a.dweight, a.dbias);
 }
 
-bool groupnorm_wide(const GroupNormArgs& a) { return a.width % 8 == 0 && a.x_stride % 8 == 0 && a.gate_stride % 8 == 0; }
+bool groupnorm_wide(const GroupNormArgs& a) {
+    uintptr_t starts = 0;
+    for (const void* p : {a.x, a.gate, a.dy, static_cast<const void*>(a.weight), static_cast<const void*>(a.bias),
+                          static_cast<const void*>(a.y), static_cast<const void*>(a.dx), static_cast<const void*>(a.dgate)})
+        starts |= reinterpret_cast<uintptr_t>(p);
+    return a.width % 8 == 0 && a.x_stride % 8 == 0 && a.gate_stride % 8 == 0 && starts % 16 == 0;
+}
 
 int64_t groupnorm_groups(const GroupNormArgs& a) {
     if (!gn_in_registers(a)) return a.tokens * a.groups;

@@ -220,8 +220,8 @@ size_t kda_linattn_bwd_workspace_bytes(int64_t N, int64_t total, int H, int Dk, 
  * act: the value itself, x / (1 + e^-x) or 1 / (1 + e^-x).  x [tokens, groups * width] x_dtype, gate and y as many of
  * y_dtype; x_stride, gate_stride: elements from one token to the next (at least groups * width), so that they may be columns
  * of wider rows; y is contiguous.  weight, bias [groups * width] float32, each may be NULL (ones, zeros).  All of it is
- * computed in float32 and rounded once.  Where width and the strides are multiples of 8, rows are read 16 bytes at a time
- * and x, gate and y have to be 16-byte aligned; else an element or two at a time, and they may begin at any (weight and bias too).
+ * computed in float32 and rounded once.  x, gate and y, their gradients, weight and bias may begin at any element; where all of
+ * them begin at 16 bytes and width and the strides are multiples of 8, rows are read 16 bytes at a time, else an element or two.
  * width up to 2^16.
  */
 enum { KDA_ACT_NONE = 0, KDA_ACT_SILU = 1, KDA_ACT_SIGMOID = 2 };

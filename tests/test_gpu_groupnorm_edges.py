@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import gated_delta_rule_65_amd as kda
-from tests.test_gpu_groupnorm import E, TYPES, make, near
+from tests.test_gpu_groupnorm import E, TYPES, check_bwd, check_fwd, make, near
 
 pytestmark = pytest.mark.gpu
 FLOOR = 128 * 2.0 ** -126  # a sigmoid below the smallest normal number may be zero; |u| is below 128
@@ -111,3 +111,24 @@ def test_gradients_without_the_weights(width):
     some = kda.group_norm_act_bwd(x, 2, dy, output_dweights=False, **kw)
     assert some[1] is None and some[2] is None and dw is not None and db is not None
     assert torch.equal(some[0], dx) and torch.equal(some[3], dgate)
+
+
+@pytest.mark.parametrize("xt,yt", [("bf16", "bf16"), ("f32", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("width", [64, 256, 1536, 2048])
+@pytest.mark.parametrize("skip", [1, 2, 4])
+def test_starts_that_are_not_aligned(skip, width, xt, yt):
+    """Widths and strides that wide loads divide, and each tensor in turn at another place: to the same bounds."""
+    x, w, b, gate, dy = make(skip + width, 19, 2, width, xt, yt)
+
+    def off(t):
+        return torch.cat([t.new_zeros(skip), t.flatten()]).cuda()[skip:].view(t.shape)
+
+    def columns(t):
+        wide = t.new_zeros(19, 2 * width + 16)
+        wide[:, skip:skip + 2 * width] = t
+        return wide.cuda()[:, skip:skip + 2 * width]
+
+    for i, moved in [(i, off) for i in range(5)] + [(0, columns), (3, columns)]:
+        X, W, B, G, D = (moved(t) if i == j else t.cuda() for j, t in enumerate((x, w, b, gate, dy)))
+        check_fwd(kda.group_norm_act_fwd(X, 2, weight=W, bias=B, gate=G), x, 2, w, b, gate, "silu", 1e-5)
+        check_bwd(kda.group_norm_act_bwd(X, 2, D, weight=W, bias=B, gate=G), x, 2, dy, w, b, gate, "silu", 1e-5)
