@@ -286,6 +286,7 @@ struct LinTile {
     static constexpr int UA = DA * ES / 16, UC = DC * ES / 16;  // units of a row
     static constexpr int KB = C * UA * 16, VB = C * UC * 16;
     static constexpr int KS = C / 32, RB = C / 16, AS = DA / 32, CT = DA / 16;
+    static constexpr int STORES = RB;            // that a wave makes at least at the end of a whole chunk, behind its loads
     // Planes of the state, of the scores and of the weighted values: three bf16 hold all 24 bits of each.
     static constexpr int PL = F32 ? 1 : 3;
     static constexpr int PB = F32 ? 32 * 128 : 5120;  // a plane of scores: rows up to their diagonal's tile
@@ -540,7 +541,7 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
         __builtin_amdgcn_s_setprio(1);
         // The chunk's rows have come.  Requests end in the order in which they were made, and the last ones are the stores of the
         // chunk before: they are not waited for.
-        __builtin_amdgcn_s_waitcnt(waitcnt(ROWS ? G::RB : 0));
+        __builtin_amdgcn_s_waitcnt(waitcnt(ROWS ? G::STORES : 0));
         __asm__ volatile("s_barrier" ::: "memory");
         if constexpr (!LAST) {
             fetch(op.b, Kn, c + 1, UnitsA(), offset_a);
@@ -730,6 +731,7 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
             char* to = static_cast<char*>(op.out) + ((row0 + (op.back ? -c * C : c * C)) * H + h) * (int64_t)(DC * G::ES);
             const int pitch = (op.back ? -H : H) * DC * G::ES, mine = m * pitch + state_col<ND>(wave, 4 * grp, 0) * G::ES;
             __asm__ volatile("" ::: "memory");  // behind the chunk's loads, all of them
+            static_assert(G::STORES == G::RB && 4 * ND * G::ES <= 16, "one store for each of a lane's rows");
 #pragma unroll
             for (int r = 0; r < G::RB; ++r)
                 if (!LAST || 16 * r + m < n) {
@@ -967,10 +969,16 @@ void chunks(const LinArgs& a, const Segs& s, std::initializer_list<LinOp> ops, i
     else DC == 64 ? types(I128(), I64()) : types(I128(), I128());
 }
 
+// Workgroups of the fold for one operation; 0: no sequence can have so many segments.
+int64_t fold_groups(const LinArgs& a, const Segs& s) {
+    if ((s.cu ? (s.total + s.L - 1) / s.L : s.per_seq) <= kOwnFold) return 0;
+    return (s.cu ? (s.total - 1) / (kOwnFold * s.L) + 1 : s.N) * a.H * (a.Dk * a.Dv / (4 * kThreads));
+}
+
 void fold(const LinArgs& a, const Segs& s, FoldOp one, const FoldOp* two, hipStream_t st) {
-    if ((s.cu ? (s.total + s.L - 1) / s.L : s.per_seq) <= kOwnFold) return;
-    const int64_t sequences = s.cu ? (s.total - 1) / (kOwnFold * s.L) + 1 : s.N;
-    const dim3 grid((unsigned)(sequences * a.H * (a.Dk * a.Dv / (4 * kThreads))), two ? 2 : 1);
+    const int64_t groups = fold_groups(a, s);
+    if (groups == 0) return;
+    const dim3 grid((unsigned)groups, two ? 2 : 1);
     auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, st, one, two ? *two : one, s, a.g, a.Dv); };
     a.Dk == 64 ? run(linattn_fold_kernel<64>) : run(linattn_fold_kernel<128>);
 }
@@ -985,10 +993,13 @@ int64_t linattn_workspace_bytes(const LinArgs& a, bool backward) {
     return a.total / L * a.H * a.Dk * (int64_t)a.Dv * 4 * (backward ? 2 : 1);
 }
 
-// Workgroups of the largest launch, and the threads of one at most.  The fold's are fewer: it has a sequence for 8 segments.
+// Of the outputs' launch, or of the fold's where that has more: 16 workgroups for 8 segments of 128 x 128, twice in a backward call
+// (a sequence of 768 segments and one head: 1536 against 769, 3072 against 2307).
 int64_t linattn_threads(const LinArgs& a, bool backward) {
-    const int64_t D = a.Dk > a.Dv ? a.Dk : a.Dv;
-    return (slots_of(segs_of(a), true) * a.H + 8) * (backward ? 3 : 1) * (a.f32 ? 4 * D : 256);
+    const Segs s = segs_of(a);
+    const int64_t D = a.Dk > a.Dv ? a.Dk : a.Dv, rows = (slots_of(s, true) * a.H + 8) * (backward ? 3 : 1) * (a.f32 ? 4 * D : 256);
+    const int64_t folds = fold_groups(a, s) * kThreads * (backward ? 2 : 1);
+    return rows > folds ? rows : folds;
 }
 
 hipError_t launch_linattn_fwd(const LinArgs& a, hipStream_t st) {
