@@ -17,9 +17,10 @@ def steps(T):
     return 12 + 3 * (T // 32 + 1)
 
 
-def allowed(dtype, want, size, T):
+def allowed(dtype, want, size, T, more=0):
+    """A result's own rounding, and a half step of 32 bits of its terms for each rounding; `more`: of the sums of many terms."""
     half = ref.HALF[dtype]
-    return half * want.abs() + steps(T) * 2.0 ** -24 * size * (1 + half) + 1e-37
+    return half * want.abs() + (steps(T) + more) * 2.0 ** -24 * size * (1 + half) + 1e-37
 
 
 def inputs(seed, T, H, dk, dv, dtype):
