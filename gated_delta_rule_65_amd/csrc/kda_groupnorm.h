@@ -295,7 +295,11 @@ inline int gn_piece(const GroupNormArgs& a) {
                : 2;
 }
 
-// Lanes and pieces of a row: the fewest lanes that hold it.
+// Lanes and pieces of a row.  Pieces of 8: a lane for each.  Smaller ones: the fewest lanes, 16 at least, that hold the row in four
+// pieces each, so that a lane has several loads under way and a row's sums few steps; beyond 64 lanes more pieces.  Against twice the
+// lanes of half the pieces, forward and backward of 4.4 million fp32 values four times over: 12 x 42 channels 39 and 70 us for 48 and
+// 107, 12 x 90 24 and 47 for 33 and 74, 12 x 126 24 and 43 for 26 and 54; three pieces for four: 12 x 130 31 and 62 for 36 and 70,
+// 12 x 258 26 and 50 for 29 and 58; one channel at a time, 12 x 41: 32 and 66 for 47 and 114.
 template <typename F>
 void gn_shape(int piece, int64_t width, F&& f) {
     auto run = [&](auto cpl, auto p, auto iter) { f(cpl, p, iter); };
@@ -311,18 +315,22 @@ void gn_shape(int piece, int64_t width, F&& f) {
         else KDA_GN(8, 64, 4);
     } else if (piece == 2) {
         if (width <= 32) KDA_GN(2, 16, 1);
-        else if (width <= 64) KDA_GN(2, 32, 1);
+        else if (width <= 64) KDA_GN(2, 16, 2);
         else if (width <= 96) KDA_GN(2, 16, 3);
-        else if (width <= 128) KDA_GN(2, 32, 2);
+        else if (width <= 128) KDA_GN(2, 16, 4);
+        else if (width <= 192) KDA_GN(2, 32, 3);
         else if (width <= 256) KDA_GN(2, 32, 4);
+        else if (width <= 384) KDA_GN(2, 64, 3);
         else if (width <= 512) KDA_GN(2, 64, 4);
         else KDA_GN(2, 64, 8);
     } else {
         if (width <= 16) KDA_GN(1, 16, 1);
-        else if (width <= 32) KDA_GN(1, 32, 1);
-        else if (width <= 64) KDA_GN(1, 32, 2);
+        else if (width <= 32) KDA_GN(1, 16, 2);
+        else if (width <= 48) KDA_GN(1, 16, 3);
+        else if (width <= 64) KDA_GN(1, 16, 4);
         else if (width <= 96) KDA_GN(1, 32, 3);
         else if (width <= 128) KDA_GN(1, 32, 4);
+        else if (width <= 192) KDA_GN(1, 64, 3);
         else if (width <= 256) KDA_GN(1, 64, 4);
         else if (width <= 512) KDA_GN(1, 64, 8);
         else KDA_GN(1, 64, 16);
@@ -330,14 +338,19 @@ void gn_shape(int piece, int64_t width, F&& f) {
 #undef KDA_GN
 }
 
-// Workgroups of all groups' columns; tokens in blocks, as many workgroups in all as `places`, none of fewer than `least` tokens.
-inline GnPlan gn_plan(const GroupNormArgs& a, int lanes, int64_t places, int64_t least, int64_t& columns) {
+// Workgroups of all groups' columns; tokens in blocks, as many workgroups in all as `places`.  A block has kGnBlockTokens at least in a
+// backward pass; in a forward one two where workgroups of one each would not fit on the chip at once anyway, so that the second
+// one's loads are beside the first one's work (4099 x 12 x 90 fp32: 10.5 -> 9.4 us; 2048 x 16 x 128 fp32, which fit: 8.2 with two, 7.4).
+template <bool BWD>
+GnPlan gn_plan(const GroupNormArgs& a, int lanes, int64_t places, int64_t& columns) {
     GnPlan p;
     const int64_t fit = kGnThreads / lanes;
     p.groups = (int)(a.groups < fit ? a.groups : fit);
     p.tokens = (int)(fit / p.groups);
     columns = (a.groups + p.groups - 1) / p.groups;
     int64_t blocks = (places + columns - 1) / columns;
+    const int64_t at_once = 8 * 256;  // workgroups of 256 threads on 256 CUs
+    const int64_t least = BWD ? kGnBlockTokens : columns * ((a.tokens + p.tokens - 1) / p.tokens) > at_once ? 2 : 1;
     const int64_t most = (a.tokens + least - 1) / least;
     if (blocks > most) blocks = most;
     if (blocks < 1) blocks = 1;
@@ -353,8 +366,7 @@ inline GnPlan gn_plan(const GroupNormArgs& a, int lanes, int64_t places, int64_t
 }  // namespace
 
 // Workgroups of a forward pass: rows of fp32 have twice the bytes (32768 x 16 x 128, to bf16: 94 us with 8192, 98 with 4096 from fp32,
-// 65 and 62 from bf16).  Of two tokens each, the second one's loads beside the first one's work (4099 x 12 x 90 fp32: 10.5 -> 9.4 us),
-// where one each would not fit on the chip at once anyway.
+// 65 and 62 from bf16).
 template <bool XF>
 constexpr int64_t kGnForward = XF ? 8192 : 4096;
 
@@ -363,7 +375,7 @@ void groupnorm_launch(const GroupNormArgs& a, hipStream_t st) {
     gn_shape(gn_piece(a), a.width, [&](auto cpl, auto p, auto iter) {
         constexpr int CPL = decltype(cpl)::value, P = decltype(p)::value, ITER = decltype(iter)::value;
         int64_t columns;
-        const GnPlan plan = BWD ? gn_plan(a, P, kGnBlocks, kGnBlockTokens, columns) : gn_plan(a, P, kGnForward<XF>, a.tokens < 1024 ? 1 : 2, columns);
+        const GnPlan plan = gn_plan<BWD>(a, P, BWD ? kGnBlocks : kGnForward<XF>, columns);
         const dim3 grid((unsigned)columns, (unsigned)plan.blocks);
         if (a.gate) hipLaunchKernelGGL((groupnorm_kernel<XF, YF, CPL, P, ITER, BWD, true>), grid, dim3(kGnThreads), 0, st, a, plan);
         else hipLaunchKernelGGL((groupnorm_kernel<XF, YF, CPL, P, ITER, BWD, false>), grid, dim3(kGnThreads), 0, st, a, plan);
