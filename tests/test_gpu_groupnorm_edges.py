@@ -132,3 +132,16 @@ def test_starts_that_are_not_aligned(skip, width, xt, yt):
         X, W, B, G, D = (moved(t) if i == j else t.cuda() for j, t in enumerate((x, w, b, gate, dy)))
         check_fwd(kda.group_norm_act_fwd(X, 2, weight=W, bias=B, gate=G), x, 2, w, b, gate, "silu", 1e-5)
         check_bwd(kda.group_norm_act_bwd(X, 2, D, weight=W, bias=B, gate=G), x, 2, dy, w, b, gate, "silu", 1e-5)
+
+
+@pytest.mark.parametrize("width", [17, 33, 48, 49, 65, 97, 129, 192, 193, 257, 384, 386, 513])
+@pytest.mark.parametrize("gated", [False, True])
+def test_widths_around_every_shape(width, gated):
+    """The first and last widths of each number of lanes and pieces, groups that fill a workgroup and one more."""
+    for groups, tokens, xt, yt in ((1, 40, "f32", "f32"), (17, 9, "bf16", "bf16"), (5, 23, "f32", "bf16")):
+        x, w, b, gate, dy = make(width + groups, tokens, groups, width, xt, yt)
+        gate = gate if gated else None
+        c = lambda t: None if t is None else t.cuda()  # noqa: E731
+        kw = {"weight": w.cuda(), "bias": b.cuda(), "gate": c(gate)}
+        check_fwd(kda.group_norm_act_fwd(x.cuda(), groups, dtype=dy.dtype, **kw), x, groups, w, b, gate, "silu", 1e-5)
+        check_bwd(kda.group_norm_act_bwd(x.cuda(), groups, dy.cuda(), **kw), x, groups, dy, w, b, gate, "silu", 1e-5)
