@@ -92,7 +92,8 @@ __device__ __forceinline__ void gn_store(void* p, int64_t at, const float x[N], 
         else *reinterpret_cast<gn_bf16x2*>(q) = __builtin_convertvector(gn_f32x2{x[0], x[1]}, gn_bf16x2);
     } else if constexpr (F32) {
 #pragma unroll
-        for (int i = 0; i < N / 4; ++i) gn_put(q + 16 * i, f32x4_t{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]}, stream);
+        for (int i = 0; i < N / 4; ++i)
+            *reinterpret_cast<f32x4_t*>(q + 16 * i) = f32x4_t{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]};
     } else {
 #pragma unroll
         for (int i = 0; i < N / 8; ++i) {
@@ -357,8 +358,9 @@ GnPlan gn_plan(const GroupNormArgs& a, int lanes, int64_t places, int64_t& colum
     p.block = (a.tokens + blocks - 1) / blocks;
     p.block = (p.block + p.tokens - 1) / p.tokens * p.tokens;
     p.blocks = (a.tokens + p.block - 1) / p.block;
-    // rows that do not stay in the caches anyway (32768 x 16 x 128: forward from bf16 77 -> 62 us, from fp32 96 -> 92, backward
-    // 127 -> 117)
+    // 16-bit rows that do not stay in the caches anyway: a store of a wave is whole lines (32768 x 16 x 128: forward from bf16 75 -> 61
+    // us, from fp32 95 -> 92).  fp32 rows take two stores of 16 of every 32 bytes, which the caches have to make lines of (the same
+    // in fp32, past them and through them: forward 183 and 142, backward 361 and 270).
     p.stream = a.tokens * a.groups * a.width * ((a.x_f32 ? 4 : 2) + (a.y_f32 ? 4 : 2)) >= kStreamBytes;
     return p;
 }
