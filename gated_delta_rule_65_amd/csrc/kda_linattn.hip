@@ -995,7 +995,7 @@ int64_t linattn_workspace_bytes(const LinArgs& a, bool backward) {
 }
 
 // Of the outputs' launch, or of the fold's where that has more: 16 workgroups for 8 segments of 128 x 128, twice in a backward call
-// (a sequence of 768 segments and one head: 1536 against 769, 3072 against 2307).
+// (forward, a sequence of 768 segments and one head: 1536 against 769).
 int64_t linattn_threads(const LinArgs& a, bool backward) {
     const Segs s = segs_of(a);
     const int64_t D = a.Dk > a.Dv ? a.Dk : a.Dv, rows = (slots_of(s, true) * a.H + 8) * (backward ? 3 : 1) * (a.f32 ? 4 * D : 256);
